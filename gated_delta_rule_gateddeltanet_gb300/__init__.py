@@ -10,6 +10,9 @@ missing or cannot be loaded, importing the entry points raises.
 Entry points (same names as the C ABI):
     gdn_forward(...)        -> (output, final_state, state_update)
     gdn_replay_prefix(...)  -> state_banks (updated in place)
+
+The softmax-attention operators (rotary positions, paged key-value cache,
+attention over it) are in ``attention.py`` and exported from here.
 """
 from __future__ import annotations
 
@@ -22,12 +25,15 @@ from .build import LIB as LIB_PATH
 
 __all__ = ["gdn_forward", "ForwardCall", "gdn_forward_dense", "state_transpose", "gdn_forward_no_alloc", "gdn_replay_prefix", "varlen_causal_conv_with_state",
            "causal_conv_replay_prefix", "GdnError", "load_library", "capsule_width",
-           "STATUS", "DEVERR", "PLAN"]
+           "STATUS", "DEVERR", "PLAN", "rotary_table", "rotary", "RotaryCall", "PagedKVCache", "kv_cache_write",
+           "KVCacheWriteCall", "kv_cache_read", "KVCacheReadCall", "paged_attention", "PagedAttentionCall",
+           "paged_attention_workspace"]
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_DTYPE", 3: "GDN_ERR_SHAPE", 4: "GDN_ERR_ALIGN",
           5: "GDN_ERR_WORKSPACE", 6: "GDN_ERR_CUDA", 7: "GDN_ERR_UNSUPPORTED", 8: "GDN_ERR_ARG"}
 DEVERR = {"cu_seqlens": 0x1, "state_slot": 0x2, "accept_len": 0x4, "replay_slot": 0x8, "timeout": 0x10,
-          "capture_count": 0x20, "dup_slot": 0x40}
+          "capture_count": 0x20, "dup_slot": 0x40, "position": 0x80, "cache_slot": 0x100, "page": 0x200,
+          "kv_len": 0x400}
 ACTIVATION = {"none": 0, "silu": 1}
 PLAN = {"auto": 0, "recurrent": 1, "chunked": 2, "chunked_split": 3}
 DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -103,6 +109,7 @@ def load_library(path: str | None = None):
     lib.gdn_state_transpose.argtypes = [P, P, ctypes.c_int64, i32, i32, P]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_status_string.argtypes = [i32]
+    attention.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -506,3 +513,9 @@ def causal_conv_replay_prefix(conv_states, src_slots, dst_slots, state_update, a
     if rc != 0:
         raise GdnError(rc, "causal_conv_replay_prefix")
     return conv_states
+
+
+from . import attention  # noqa: E402  (it uses this module's checks)
+from .attention import (KVCacheReadCall, KVCacheWriteCall, PagedAttentionCall, PagedKVCache, RotaryCall,  # noqa: E402
+                        kv_cache_read, kv_cache_write, paged_attention, paged_attention_workspace, rotary,
+                        rotary_table)

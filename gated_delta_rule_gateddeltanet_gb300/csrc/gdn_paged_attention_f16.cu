@@ -1,0 +1,6 @@
+// Paged attention over FP16 caches (see gdn_paged_attention.cuh).
+#include "gdn_paged_attention.cuh"
+
+namespace gdn {
+template cudaError_t launch_paged_attention<GDN_F16>(const PagedAttnParams &p, cudaStream_t stream);
+}

@@ -52,7 +52,8 @@ typedef struct CUstream_st *gdn_stream_t;
 typedef enum gdn_status {
     GDN_OK = 0,
     GDN_ERR_NULL = 1,        /* a required pointer is NULL */
-    GDN_ERR_DTYPE = 2,       /* unsupported I/O dtype; BF16 is always rejected */
+    GDN_ERR_DTYPE = 2,       /* unsupported I/O dtype; the gated delta rule and the convolution always
+                                reject BF16 */
     GDN_ERR_SHAPE = 3,       /* inconsistent or unsupported sizes */
     GDN_ERR_ALIGN = 4,       /* a state pointer is not 16-byte aligned */
     GDN_ERR_WORKSPACE = 5,   /* workspace missing or smaller than gdn_forward_workspace_size */
@@ -62,8 +63,10 @@ typedef enum gdn_status {
                                 invalid for the call (see each entry point) */
 } gdn_status;
 
-/* I/O dtypes of q, k, v and output.  Gates and states are always FP32. */
-enum { GDN_F32 = 0, GDN_F16 = 1, GDN_BF16 = 2 /* rejected */ };
+/* I/O dtypes of q, k, v and output.  Gates and states are always FP32.  The gated
+ * delta rule and the convolution reject BF16; the softmax-attention operators
+ * below accept it.  The 8-bit types are element types of a paged cache only. */
+enum { GDN_F32 = 0, GDN_F16 = 1, GDN_BF16 = 2, GDN_FP8_E4M3 = 3, GDN_INT8 = 4 };
 
 /* How the `a` and `b` inputs are read. */
 enum {
@@ -107,6 +110,10 @@ enum {
                                       write the same state slot, or a replay writes a slot that
                                       another request of the call reads; the release build does
                                       not check this precondition (results are then undefined) */
+#define GDN_DEVERR_POSITION 0x80  /* positions[t] outside [0, max_positions) (the token is not written) */
+#define GDN_DEVERR_CACHE_SLOT 0x100 /* a cache slot outside the pool (the token is not written) */
+#define GDN_DEVERR_PAGE 0x200     /* a block-table entry outside [0, num_pages) (read as zero rows) */
+#define GDN_DEVERR_KV_LEN 0x400   /* kv_lens[b] negative or past the block table's row (the sequence is skipped) */
 
 /*
  * Arguments of gdn_forward.
@@ -447,6 +454,240 @@ gdn_status causal_conv_replay_prefix(void *conv_states, int32_t num_slots, int32
                                      int32_t kernel_size, int32_t io_dtype, const int32_t *src_slots,
                                      const int32_t *dst_slots, const void *state_update, int32_t capacity,
                                      const int32_t *accept_len, int32_t *status, gdn_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Softmax attention over a paged key-value cache.
+ *
+ * Hybrid decoders interleave the gated-delta-rule layers above with layers of
+ * softmax attention.  The entry points below are what such a layer needs
+ * between its projections: rotary positions, a paged cache of keys and values
+ * (kept as they are or quantised to 8 bits as they are written) and attention
+ * of new tokens over that cache.  Argument and data errors, streams and
+ * launches follow the rules at the top of this file; unlike the operators
+ * above, these accept FP32, FP16 and BF16.  Arithmetic is FP32 throughout and
+ * each result is rounded once, when it is stored.
+ * ------------------------------------------------------------------------ */
+
+/* How the angles of a rotary table are scaled for contexts longer than the
+ * model was trained on; f_i = base^(-2i/rotary_dim) for pair i, `factor` = s,
+ * original_positions = P0.  beta_fast > beta_slow are numbers of turns. */
+enum {
+    GDN_ROPE_NONE = 0,     /* f_i */
+    GDN_ROPE_LINEAR = 1,   /* f_i / s (positions interpolated) */
+    GDN_ROPE_NTK = 2,      /* base stretched to base * s^(rotary_dim / (rotary_dim - 2)); needs rotary_dim > 2 */
+    GDN_ROPE_BY_PARTS = 3, /* f_i (w + (1 - w) / s) with w rising from 0 to 1 as the turns
+                              P0 f_i / (2 pi) that pair i makes over the trained length
+                              rise from beta_slow to beta_fast */
+    GDN_ROPE_YARN = 4      /* f_i (w + (1 - w) / s) with w falling from 1 to 0 over the pair
+                              indices [lo, hi], lo = floor(t(beta_fast)), hi = ceil(t(beta_slow)),
+                              t(b) = rotary_dim ln(P0 / (2 pi b)) / (2 ln base), clamped to
+                              [0, rotary_dim - 1]; cos and sin times 0.1 ln s + 1 unless
+                              attention_factor says otherwise */
+};
+
+/*
+ * Arguments of gdn_rotary_table: the table of cosines and sines that
+ * gdn_rotary and gdn_kv_cache_write read.
+ *   table  device [max_positions, rotary_dim] FP32: row p is
+ *          [m cos(p w_i) for each pair i | m sin(p w_i) for each pair i] with
+ *          w_i the scaled frequency above.  Angles, cosines and sines are
+ *          evaluated in 64 bits, so a row is exact to FP32 rounding at any position.
+ *   m      attention_factor; 0 means 1 (GDN_ROPE_YARN with factor > 1: 0.1 ln(factor) + 1)
+ */
+typedef struct gdn_rotary_table_args {
+    int32_t max_positions;       /* P >= 0 */
+    int32_t rotary_dim;          /* even, >= 2 */
+    int32_t scaling;             /* GDN_ROPE_* */
+    int32_t original_positions;  /* P0 >= 1; GDN_ROPE_BY_PARTS and GDN_ROPE_YARN only */
+    double base;                 /* > 1 */
+    double factor;               /* s >= 1; ignored by GDN_ROPE_NONE */
+    double beta_fast, beta_slow; /* BY_PARTS and YARN: beta_fast > beta_slow > 0 */
+    double attention_factor;     /* >= 0 */
+    float *table;
+} gdn_rotary_table_args;
+
+gdn_status gdn_rotary_table(const gdn_rotary_table_args *args, gdn_stream_t stream);
+
+/*
+ * Arguments of gdn_rotary: rotates the first rotary_dim channels of every head
+ * of q and k by their token's position; the other channels are copied.
+ * For a pair (x1, x2) of channels, with (c, s) the table's entry for the pair:
+ *   y1 = x1 c - x2 s,  y2 = x2 c + x1 s
+ * Pair i is channels (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved.
+ * inverse = 1 turns by the negative angle: with dy the gradient of a rotated
+ * tensor, the inverse rotation of dy is the gradient of its input (the
+ * rotation is linear; a factor m in the table belongs in both directions).
+ *   q, k          device [T, heads, head_dim] io_dtype, heads and channels
+ *                 contiguous inside a token; q_stride / k_stride elements
+ *                 between tokens (0 = heads * head_dim).  Either may be NULL
+ *                 with its head count 0.
+ *   q_out, k_out  device, same layout with their own strides; may equal the
+ *                 input (in place, with the same stride), must not overlap it otherwise
+ *   positions     device [T] int32
+ *   table         device [max_positions, rotary_dim] FP32, 16-byte aligned
+ * Any even head_dim and rotary_dim <= head_dim are valid; 16-byte aligned rows
+ * whose halves are whole 16-byte groups take the vector kernel.
+ */
+typedef struct gdn_rotary_args {
+    int32_t total_tokens;
+    int32_t num_q_heads;
+    int32_t num_k_heads;
+    int32_t head_dim;
+    int32_t rotary_dim;
+    int32_t max_positions;
+    int32_t io_dtype;     /* GDN_F32, GDN_F16 or GDN_BF16 */
+    int32_t interleaved;  /* 0 or 1 */
+    int32_t inverse;      /* 0 or 1 */
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    const void *q, *k;
+    void *q_out, *k_out;
+    const int32_t *positions;
+    const float *table;
+    int32_t *status;
+} gdn_rotary_args;
+
+gdn_status gdn_rotary(const gdn_rotary_args *args, gdn_stream_t stream);
+
+/*
+ * A paged cache of keys and values.  Token t of a sequence lives in page
+ * block_table[b, t / page_size] at offset t % page_size; its "slot" is
+ * page * page_size + offset.  Any order of pages, offsets and heads in memory
+ * is described by three strides, the same for k and v:
+ *   k, v              device; element (page, offset, head, channel) at
+ *                     page * page_stride + offset * token_stride +
+ *                     head * head_stride + channel.  Strides 0, 0, 0 mean
+ *                     [num_pages, page_size, num_kv_heads, head_dim] without gaps.
+ *                     16-byte aligned, strides whole multiples of 16 bytes.
+ *   k_scale, v_scale  device FP32, one per (page, offset, head), by the three
+ *                     scale strides (0, 0, 0: [num_pages, page_size, num_kv_heads]).
+ *                     8-bit caches only; NULL otherwise.
+ * An 8-bit row holds channels x as q * scale:
+ *   GDN_FP8_E4M3  scale = the smallest power of two (at least 2^-120) with
+ *                 max|x| <= 448 scale; q = x / scale rounded to e4m3.  A power
+ *                 of two loses nothing against max|x| / 448, since e4m3 is itself
+ *                 a floating format, and makes x / scale exact.
+ *   GDN_INT8      scale = max|x| / 127; q = x / scale rounded to nearest even
+ * A row of zeros has scale 1; a row with an infinity or NaN has scale NaN, so
+ * that it reads back as NaN.
+ */
+typedef struct gdn_kv_cache {
+    int32_t num_pages;    /* num_pages * page_size < 2^31 */
+    int32_t page_size;    /* >= 1 */
+    int32_t num_kv_heads;
+    int32_t head_dim;     /* 64, 128 or 256 */
+    int32_t cache_dtype;  /* GDN_F32, GDN_F16, GDN_BF16, GDN_FP8_E4M3 or GDN_INT8 */
+    int64_t page_stride, token_stride, head_stride;                    /* elements */
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride;  /* elements */
+    void *k, *v;
+    float *k_scale, *v_scale;
+} gdn_kv_cache;
+
+/*
+ * Arguments of gdn_kv_cache_write: new tokens' keys and values into the cache,
+ * the keys (and, if given, queries) rotated first when a table is given.
+ *   k, v      device [T, num_kv_heads, head_dim] io_dtype, token strides
+ *             k_stride, v_stride elements (0 = no gap)
+ *   slots     device [T] int32: each token's slot; -1 = not stored (padding),
+ *             which is not an error (its query is still rotated).  Distinct.
+ *   table     device [max_positions, rotary_dim] FP32 or NULL (no rotation);
+ *             rotary_dim a multiple of 16, <= head_dim; pairs as in gdn_rotary
+ *   positions device [T] int32 (with a table)
+ *   q, q_out  device [T, num_q_heads, head_dim] or NULL with num_q_heads = 0;
+ *             rotated queries (needs a table); q_out may equal q
+ * A cache of 16 or 32 bits has the I/O type; an 8-bit cache takes any.
+ * k, v, q, q_out: 16-byte aligned, strides whole multiples of 16 bytes.
+ */
+typedef struct gdn_kv_write_args {
+    gdn_kv_cache cache;
+    int32_t total_tokens;
+    int32_t num_q_heads;
+    int32_t rotary_dim;
+    int32_t max_positions;
+    int32_t io_dtype;
+    int32_t interleaved;
+    int64_t k_stride, v_stride, q_stride, q_out_stride;
+    const void *k, *v, *q;
+    void *q_out;
+    const int32_t *slots, *positions;
+    const float *table;
+    int32_t *status;
+} gdn_kv_write_args;
+
+gdn_status gdn_kv_cache_write(const gdn_kv_write_args *args, gdn_stream_t stream);
+
+/*
+ * Arguments of gdn_kv_cache_read: the first cu_seqlens[b+1] - cu_seqlens[b]
+ * cached tokens of every sequence, packed, in io_dtype (dequantised and
+ * rounded; any cache type to any I/O type).
+ *   block_table   device [B, pages_per_seq] int32, rows block_table_stride apart (0 = no gap)
+ *   k_out, v_out  device [T, num_kv_heads, head_dim] io_dtype, contiguous, 16-byte aligned
+ */
+typedef struct gdn_kv_read_args {
+    gdn_kv_cache cache;
+    int32_t num_seqs;
+    int32_t total_tokens;
+    int32_t pages_per_seq;
+    int32_t io_dtype;
+    int64_t block_table_stride;
+    const int32_t *block_table, *cu_seqlens;
+    void *k_out, *v_out;
+    int32_t *status;
+} gdn_kv_read_args;
+
+gdn_status gdn_kv_cache_read(const gdn_kv_read_args *args, gdn_stream_t stream);
+
+/*
+ * Arguments of gdn_paged_attention: attention of each sequence's newest tokens
+ * over its cached keys and values, its own among them.  Query token i of the n
+ * that sequence b has in this call stands at position p = kv_lens[b] - n + i
+ * and sees cache positions (p - window, p] (window = 0: [0, p]):
+ *   o = sum_t softmax_t(scale q k_t) v_t
+ * for every query head, whose key head is head / (num_q_heads / num_kv_heads).
+ * A query that sees nothing (p < 0) gives zeros and a log-sum-exp of -inf.
+ * One token a sequence is decode; a few are the verification of a draft.  Long
+ * spans are valid but reread the cache for every 8 to 64 query rows.
+ *   q            device [T, num_q_heads, head_dim] io_dtype, 16-byte aligned, token
+ *                stride q_stride elements (0 = no gap; whole multiples of 16 bytes)
+ *   block_table  device [B, pages_per_seq] int32, rows block_table_stride apart (0 = no gap);
+ *                entries past a sequence's last page are not read
+ *   kv_lens      device [B] int32: cached tokens of each sequence, new ones included
+ *   cu_seqlens   device [B+1] int32, or NULL: one query token per sequence (T = B)
+ *   output       device [T, num_q_heads, head_dim] io_dtype, contiguous
+ *   lse          device [T, num_q_heads] FP32 or NULL: ln sum_t exp(scale q k_t)
+ * What the cache holds in slots that no query may see (uninitialised memory,
+ * NaN) does not reach the results.  io_dtype is the cache's type, or FP16 or
+ * BF16 over an 8-bit cache.
+ * The work is split over sequences, heads and cache length by the lengths on
+ * the device, so a captured graph stays balanced as they change; pieces of one
+ * sequence are joined in a fixed order (the same call gives the same bits).
+ *   workspace    device scratch of gdn_paged_attention_workspace_size bytes, 16-byte aligned:
+ *                its first 16 KiB must be zero before the first call that uses it and
+ *                are zero again after every call.  Not shared by calls that overlap.
+ */
+typedef struct gdn_paged_attention_args {
+    gdn_kv_cache cache;
+    int32_t num_seqs;       /* B, at most 65535 */
+    int32_t total_tokens;   /* T */
+    int32_t num_q_heads;    /* a multiple of num_kv_heads */
+    int32_t pages_per_seq;
+    int32_t window;         /* 0 = unlimited */
+    int32_t max_seqlen;     /* most query tokens of one sequence, 0 = unknown; a hint as in gdn_forward */
+    int32_t io_dtype;
+    float scale;            /* 0 means 1/sqrt(head_dim) */
+    int64_t block_table_stride, q_stride;
+    const void *q;
+    const int32_t *block_table, *kv_lens, *cu_seqlens;
+    void *output;
+    float *lse;
+    int32_t *status;
+    void *workspace;
+    size_t workspace_bytes;
+} gdn_paged_attention_args;
+
+/* Bytes of workspace for these sizes on the current device (pointers are not read). */
+gdn_status gdn_paged_attention_workspace_size(const gdn_paged_attention_args *args, size_t *bytes);
+
+gdn_status gdn_paged_attention(const gdn_paged_attention_args *args, gdn_stream_t stream);
 
 /* A static, human-readable name for a status code. */
 const char *gdn_status_string(gdn_status status);
