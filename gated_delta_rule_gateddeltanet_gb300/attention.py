@@ -404,7 +404,7 @@ class PagedAttentionCall(_Call):
         a.q, a.block_table, a.kv_lens, a.cu_seqlens = _ptr(q), _ptr(block_table), _ptr(kv_lens), _ptr(cu_seqlens)
         a.output, a.lse, a.status = _ptr(output), _ptr(lse), _ptr(status)
         if workspace is None:
-            workspace = torch.zeros(_workspace_size(a), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(_workspace_size(a), dtype=torch.uint8, device=dev)
         _check(workspace, "workspace", device=dev)
         a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
         self._resolve("gdn_paged_attention", a, (output, lse) if return_lse or lse is not None else output,
@@ -420,14 +420,14 @@ def _workspace_size(args):
 
 
 def paged_attention_workspace(cache, num_q_heads, *, dtype=torch.float16, max_seqlen=1):
-    """A zeroed workspace for calls over ``cache`` with these query heads and at
-    most ``max_seqlen`` query tokens a sequence; every call leaves it ready for
-    the next, so one serves any number of calls that do not overlap."""
+    """A workspace for calls over ``cache`` with these query heads and at most
+    ``max_seqlen`` query tokens a sequence; one serves any number of calls that
+    do not overlap."""
     a = PagedAttentionArgs()
     a.cache = cache.args
     a.num_seqs = a.total_tokens = 1
     a.num_q_heads, a.max_seqlen, a.io_dtype = int(num_q_heads), int(max_seqlen), DTYPE[dtype]
-    return torch.zeros(_workspace_size(a), dtype=torch.uint8, device=cache.device)
+    return torch.empty(_workspace_size(a), dtype=torch.uint8, device=cache.device)
 
 
 def paged_attention(q, cache, block_table, kv_lens, **kw):

@@ -72,16 +72,23 @@ struct PagedAttnParams {
     void *out;
     float *lse;
     int32_t *status;
-    int32_t *counters;  // ATTN_COUNTERS zeroed int32
     float *partials;
+    int page_shift;  // log2(page_size), -1 if it is not a power of two
 };
-
-constexpr int ATTN_COUNTERS = 4096;  // at the start of the attention workspace
 
 cudaError_t launch_rotary_table(const RotaryTableParams &p, cudaStream_t stream);
 cudaError_t launch_rotary(const RotaryParams &p, int io_dtype, cudaStream_t stream);
 cudaError_t launch_kv_write(const KvWriteParams &p, int io_dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadParams &p, int io_dtype, int cache_dtype, cudaStream_t stream);
+
+// Tensor map over one half of a paged cache, strides in elements: rows are cut
+// into spans of 128 bytes (a row, if that is less), dimensions are (element of
+// a span, token, span, head, page).  A box of box_tokens tokens and box_spans
+// spans lands in shared memory as box_spans tiles of box_tokens spans each,
+// with the 16-byte pieces swizzled: piece x of the r-th span of a tile that
+// starts on a 1024-byte boundary at x ^ (r % 8), for 64-byte spans at x ^ (r / 2 % 4).
+bool encode_cache_rows(CUtensorMap *map, const void *base, int elem_bytes, int d, int heads, int page_size, int pages,
+                       long long head_stride, long long token_stride, long long page_stride, int box_tokens, int box_spans);
 
 // Attention kernels are instantiated per cache type, one translation unit each.
 template <int CacheDtype>
@@ -95,13 +102,11 @@ inline int row_tiles(bool f32, int d, int rows) {
     return rows <= 8 || most == 1 ? 1 : rows <= 16 || most == 2 ? 2 : 4;
 }
 // One CTA per SM: its ring of copies takes the whole shared memory.
-inline int attention_ctas() {
-    const int n = current_device_sms();
-    return n < ATTN_COUNTERS ? n : ATTN_COUNTERS;
-}
-// Two unnormalised parts a CTA: rows x d outputs, and each row's maximum and sum.
-inline size_t attention_partial_floats(bool f32, int d, int rows) {
-    return (size_t)2 * attention_ctas() * 8 * row_tiles(f32, d, rows) * (d + 2);
+inline int attention_ctas() { return current_device_sms(); }
+// A CTA's record of a split unit (8 int32), and two unnormalised parts: rows x d
+// outputs and each row's maximum and sum.
+inline size_t attention_workspace_floats(bool f32, int d, int rows) {
+    return (size_t)attention_ctas() * (8 + 2 * 8 * row_tiles(f32, d, rows) * (d + 2));
 }
 
 // ---------------------------------------------------------------- device helpers

@@ -38,8 +38,11 @@ gdn_status resolve_cache(const gdn_kv_cache &c, gdn::PagedCache *out) {
     p.head_stride = packed ? c.head_dim : c.head_stride;
     p.token_stride = packed ? (int64_t)c.num_kv_heads * c.head_dim : c.token_stride;
     p.page_stride = packed ? (int64_t)c.page_size * p.token_stride : c.page_stride;
-    if (p.head_stride < 0 || p.token_stride < 0 || p.page_stride < 0) return GDN_ERR_SHAPE;
     const size_t esz = cache_bytes(c.cache_dtype);
+    const int64_t most = (INT64_C(1) << 40) / (int64_t)esz - 1;  // what a tensor map takes
+    auto bad = [&](int extent, int64_t stride) { return stride < 0 || (extent > 1 && (stride == 0 || stride > most)); };
+    if (bad(c.num_kv_heads, p.head_stride) || bad(c.page_size, p.token_stride) || bad(c.num_pages, p.page_stride))
+        return GDN_ERR_SHAPE;
     if (!aligned16(c.k) || !aligned16(c.v) || (p.head_stride * esz) % 16 || (p.token_stride * esz) % 16 ||
         (p.page_stride * esz) % 16)
         return GDN_ERR_ALIGN;
@@ -82,8 +85,7 @@ int rows_hint(const gdn_paged_attention_args *a) {
 }
 
 size_t attention_bytes(const gdn_paged_attention_args *a) {
-    return 4 * ((size_t)gdn::ATTN_COUNTERS + gdn::attention_partial_floats(a->cache.cache_dtype == GDN_F32,
-                                                                           a->cache.head_dim, rows_hint(a)));
+    return 4 * gdn::attention_workspace_floats(a->cache.cache_dtype == GDN_F32, a->cache.head_dim, rows_hint(a));
 }
 
 cudaStream_t cuda_stream(gdn_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -282,8 +284,10 @@ gdn_status gdn_paged_attention(const gdn_paged_attention_args *a, gdn_stream_t s
     p.out = a->output;
     p.lse = a->lse;
     p.status = a->status;
-    p.counters = static_cast<int32_t *>(a->workspace);
-    p.partials = static_cast<float *>(a->workspace) + gdn::ATTN_COUNTERS;
+    p.partials = static_cast<float *>(a->workspace);
+    p.page_shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (p.c.page_size == 1 << s) p.page_shift = s;
     cudaError_t e;
     switch (a->cache.cache_dtype) {
         case GDN_F16: e = gdn::launch_paged_attention<GDN_F16>(p, cuda_stream(stream)); break;

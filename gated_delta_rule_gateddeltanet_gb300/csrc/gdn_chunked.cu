@@ -48,6 +48,7 @@
 #include <mutex>
 
 #include "chunk_tiles.cuh"
+#include "attn_internal.cuh"
 #include "gdn_internal.cuh"
 #include "ptx.cuh"
 
@@ -774,6 +775,27 @@ bool encode_rows_f32(CUtensorMap *map, const float *base, long long row_elems, l
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_cache_rows(CUtensorMap *map, const void *base, int elem_bytes, int d, int heads, int page_size, int pages,
+                       long long head_stride, long long token_stride, long long page_stride, int box_tokens, int box_spans) {
+    auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    const int row = d * elem_bytes, span = row < 128 ? row : 128;
+    // (the stride of an extent of one is never used, but has to be a valid one)
+    auto stride = [&](int extent, long long elems) { return (cuuint64_t)(extent > 1 ? elems * elem_bytes : row); };
+    const cuuint64_t dims[5] = {(cuuint64_t)(span / elem_bytes), (cuuint64_t)page_size, (cuuint64_t)(row / span),
+                                (cuuint64_t)heads, (cuuint64_t)pages};
+    const cuuint64_t strides[4] = {stride(page_size, token_stride), (cuuint64_t)span, stride(heads, head_stride),
+                                   stride(pages, page_stride)};
+    const cuuint32_t box[5] = {(cuuint32_t)(span / elem_bytes), (cuuint32_t)box_tokens, (cuuint32_t)box_spans, 1, 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    const CUtensorMapDataType type = elem_bytes == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return encode(map, type, 5, const_cast<void *>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_state_tiles(CUtensorMap *map, const float *base, int d, long long rows, int box_rows) {

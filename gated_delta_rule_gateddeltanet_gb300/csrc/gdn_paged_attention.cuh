@@ -26,12 +26,18 @@
 // FIFO per lane, with no barrier, no bank conflict and no swizzle, and each
 // of the CTA's warps streams on its own (tiles of 16 or 32 tokens).
 //
+// Roles.  Each consumer warp feeds itself: it owns a ring of slots, its tensor
+// copies run a ring ahead of its products (also across the ends of sequences),
+// and it looks its next 32 tiles' pages up in one load.  Nothing is shared
+// between consumers while they stream.  Joiner warps fetch queries ahead and add
+// the consumers' parts of a finished piece while these go on with the next, so
+// that memory never idles for a table lookup, a softmax or a join.
+//
 // Work split.  The lengths are on the device, so the split is made there: all
-// (sequence, key head, group of query rows) units are cut into chunks of
-// W tiles, laid end to end, and CTA c of G takes chunks [c total / G, (c + 1)
-// total / G).  A unit that spans several CTAs leaves unnormalised partial
-// results with their maxima and sums, and the last of its CTAs to finish joins
-// them in CTA order.  Copies run ahead across unit boundaries.
+// (sequence, key head, group of query rows) units are cut into chunks of W
+// tiles, laid end to end, and dealt to the CTAs in equal runs.  A unit that
+// spans several CTAs leaves unnormalised parts with their maxima and sums in
+// the workspace, and a second kernel, a row to a CTA, joins them in order.
 //
 // Numerics.  Scores, maxima, sums and outputs are FP32.  The weights P are
 // 32-bit numbers that go to the tensor cores as two 16-bit parts (hi + lo, about
@@ -62,18 +68,17 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int sr
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(src_bytes)
                      : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <int N>  // N 32-bit words (1, 2 or 4)
-__device__ __forceinline__ void lds(uint32_t (&w)[N], uint32_t addr) {
-    if constexpr (N == 4)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
-    else if constexpr (N == 2)
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-    else
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+template <int N>  // N 32-bit words (2 or 4) of shared memory
+__device__ __forceinline__ void lds(uint32_t (&w)[N], const uint8_t *p) {
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    }
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -90,7 +95,7 @@ __device__ __forceinline__ float log2_fast(float x) {
 // 8 x 8 matrix of 16-bit values, one packed pair a lane, transposed across the warp.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -98,19 +103,19 @@ template <bool BF16>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
     if constexpr (BF16)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
@@ -171,6 +176,9 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t &p01, uint32_t &p23) 
     }
 }
 
+struct Yes { __device__ constexpr bool operator()() const { return true; } };
+struct No { __device__ constexpr bool operator()() const { return false; } };
+
 // Whether a 32-bit word of cache elements holds an infinity or NaN.
 template <int CT>
 __device__ __forceinline__ bool non_finite(uint32_t w) {
@@ -186,8 +194,6 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
 // ---------------------------------------------------------------- configuration
 
 constexpr int SMEM_LIMIT = 232448;
-constexpr int ITEMS = 64;          // output channels joined at a time
-constexpr int BUF_ROW = ITEMS + 4;  // floats a row of the join buffer
 
 template <int CT, int D_, int NT_>
 struct Cfg {
@@ -202,20 +208,33 @@ struct Cfg {
     static constexpr int CPL = CHV / ESZ;               // channels of a value piece
     static constexpr int MT = D / 16;                   // 16-channel output tiles
     static constexpr int MPV = MT / VB;                 // of them per value piece (CPL / 2)
-    static constexpr int TS = 32 * RB <= 4096 ? 2 : 1;  // 16-token subtiles a tile
+    static constexpr int TS = 32 * RB <= 4096 || NT == 4 ? 2 : 1;  // 16-token subtiles a tile
     static constexpr int TT = 16 * TS;
-    static constexpr int SLOT = TT * RB + (Q8 ? TT * 8 : 0);  // half a tile (its keys or its values), scales after the rows
-    static constexpr int join_bytes(int w) { return w * ROWS * BUF_ROW * 4; }
-    static constexpr int ml_bytes(int w) { return 2 * (w + 1) * ROWS * 2 * 4; }
-    static constexpr int slots(int w) { return (SMEM_LIMIT - 1024 - join_bytes(w) - ml_bytes(w)) / (w * SLOT); }
-    static constexpr int W = slots(8) >= 3 ? 8 : 4;     // warps
-    static constexpr int S = slots(W) < 8 ? slots(W) : 8;  // ring slots a warp
-    static constexpr int SMEM = 1024 + join_bytes(W) + ml_bytes(W) + W * S * SLOT;
+    static constexpr int HALF = TT * RB;                // a tile's keys; its values
+    static constexpr int SPAN = RB < 128 ? RB : 128;    // row bytes a tensor copy takes
+    static constexpr int BOXES = RB / SPAN;             // spans a row; each half is [BOXES][TT][SPAN]
     static constexpr int QR = F32 ? D / 4 : D / 8;      // query registers per 8 rows
-    static constexpr int THREADS = 32 * W;
+    // A ring slot holds a tile (keys, values, scales of 8-bit rows) or a
+    // consumer's part of a finished segment (rows and their statistics).
+    static constexpr int OROW = D + 4;                  // floats a row of a part
+    static constexpr int TILE = 2 * HALF + (Q8 ? TT * 8 : 0), PART = ROWS * (OROW + 2) * 4;
+    static constexpr int SLOT = ((TILE > PART ? TILE : PART) + 1023) / 1024 * 1024;
+    static constexpr int QROW = D * (F32 ? 4 : 2) + 16;  // bytes a staged query row
+    static constexpr int QUERIES = 2 * ROWS * QROW;
+    static constexpr int HEAD = 2048;                    // scan, flags and barriers
+    // Warps: W consumers and NJ joiners; 12 have 168 registers a thread, 8
+    // (where queries and outputs alone take 64 or more) have 255.
+    static constexpr int HELD = NT * (D / 4 + QR);
+    static constexpr int FACTORS = 8 * ROWS * 4 + ROWS * 8;
+    static constexpr int ROOM = (SMEM_LIMIT - 1024 - HEAD - QUERIES - FACTORS) / SLOT;  // slots that fit
+    static constexpr int W = HELD < 64 && ROOM >= 16 ? 8 : ROOM >= 12 ? 6 : ROOM >= 8 ? 4 : 3;
+    static constexpr int NJ = W == 8 ? 4 : 2;
+    static constexpr int THREADS = 32 * (W + NJ);
+    static constexpr int S = ROOM / W < 8 ? ROOM / W : 8;  // ring slots a consumer
+    static constexpr int SMEM = 1024 + HEAD + QUERIES + FACTORS + W * S * SLOT;  // (1024: the ring's alignment)
     static constexpr float BIAS = CT == GDN_F16 || Q8 ? 6.f : -8.f;  // weights are 2^(s - m + BIAS)
     static constexpr float HEADROOM = 8.f;  // a score may exceed the maximum by this: FP16 weights stay below 2^14
-    static_assert(S >= 2, "a ring needs two slots");
+    static_assert(S >= 2 && 512 + W * S * 8 + 64 <= HEAD && HALF % 1024 == 0, "ring and barriers");
 };
 
 // One sequence as the kernel sees it.
@@ -253,19 +272,19 @@ struct Walk {
     Seq s;
     int unit, chunk;     // the current segment's unit and first chunk
     int seg_chunks;
-    long long left;      // chunks of this CTA not yet behind the walk, this segment's included
+    int left;            // chunks of this CTA not yet behind the walk, this segment's included
     int tile, tile_end;  // the warp's next tile and the segment's end
 };
 
 template <class C>
-__device__ __forceinline__ void open_segment(Walk &w, int warp) {
-    w.seg_chunks = (int)min((long long)(w.s.chunks - w.chunk), w.left);
-    w.tile = w.chunk * C::W + warp;
+__device__ __forceinline__ void open_segment(Walk &w, int first) {
+    w.seg_chunks = min(w.s.chunks - w.chunk, w.left);
+    w.tile = w.chunk * C::W + first;
     w.tile_end = min((w.chunk + w.seg_chunks) * C::W, w.s.tiles);
 }
 
 template <class C>
-__device__ __forceinline__ void next_segment(Walk &w, const PagedAttnParams &p, int warp) {
+__device__ __forceinline__ void next_segment(Walk &w, const PagedAttnParams &p, int first) {
     w.left -= w.seg_chunks;
     if (w.left <= 0) return;
     w.chunk = 0;
@@ -280,22 +299,95 @@ __device__ __forceinline__ void next_segment(Walk &w, const PagedAttnParams &p, 
         } while (w.s.units == 0);
         w.unit = 0;
     }
-    open_segment<C>(w, warp);
+    open_segment<C>(w, first);
 }
+
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The first `rem` CTAs take one chunk more than the others.
+struct Shares {
+    long long each, rem;
+    __device__ __forceinline__ long long begin(int cta) const { return cta * each + min((long long)cta, rem); }
+    __device__ __forceinline__ int owner(long long chunk) const {
+        const long long big = rem * (each + 1);
+        return (int)(chunk < big ? divide(chunk, each + 1) : rem + divide(chunk - big, each));
+    }
+};
+
+// Waits for a ring barrier's phase.  A wait that runs out (WAIT_LIMIT cycles;
+// it never does while the other side runs) marks the CTA dead: no wait of it
+// blocks any more and it writes no results.
+constexpr long long WAIT_LIMIT = 4000000000LL;
+__device__ __forceinline__ void ring_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*dead) return;
+        if (clock64() - t0 > WAIT_LIMIT) *dead = 1;
+    }
+}
+
+// The barrier receives this lane's arrival when all its copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// What a CTA leaves for the join: the unit whose head it holds but not its end.
+struct Split {
+    int parts;  // CTAs that hold parts of it, from this one on; 0: there is none
+    int rows, row0, head, cu0, pos0;
+    int pad[2];  // 32 bytes, so that what follows the records is aligned
+};
+
+// A part without a maximum has zeros (or the NaN that its scores are).
+__device__ __forceinline__ float part_factor(float part, float all) {
+    return part == __int_as_float(0xff800000) ? 1.f : exp2_fast(part - all);
+}
+
+// Four channels of joined row r of a unit, x unnormalised, st = (maximum, sum).
+template <int CT, class C>
+__device__ __forceinline__ void store_row(const PagedAttnParams &p, int row, int head, int cu0, int pos0, int ch, float4 x,
+                                          float2 st) {
+    const int i = (int)((uint32_t)row / (uint32_t)p.G), hq = row - i * p.G;
+    const bool any = pos0 + i >= 0;  // a query at a position before the cache sees nothing
+    const float inv = any ? 1.f / st.y : 0.f;
+    const long long at = (long long)(cu0 + i) * p.Hq + (long long)head * p.G + hq;
+    const float4 y = any ? make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (C::F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at * C::D + ch) = y;
+    } else {
+        const bool bf = C::BF16 || (C::Q8 && p.io_bf16);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at * C::D + ch) =
+            bf ? make_uint2(pack2<true>(y.x, y.y), pack2<true>(y.z, y.w)) : make_uint2(pack2<false>(y.x, y.y), pack2<false>(y.z, y.w));
+    }
+    if (p.lse && ch == 0)
+        p.lse[at] = any ? (st.x - C::BIAS + log2f(st.y)) * 0.6931471805599453f : __int_as_float(0xff800000);
+}
+
+// The workspace: a Split per CTA, then two parts a CTA (0: the end or middle of
+// a unit that another CTA began, 1: the head of one): (maximum, sum) of each
+// row, and the rows.
+template <class C>
+struct Parts {
+    Split *split;
+    float2 *ml;
+    float *o;
+    __device__ __forceinline__ Parts(float *base, int ctas) {
+        split = reinterpret_cast<Split *>(base);
+        ml = reinterpret_cast<float2 *>(base + (size_t)ctas * (sizeof(Split) / 4));
+        o = base + (size_t)ctas * (sizeof(Split) / 4 + 4 * C::ROWS);
+    }
+};
 
 // ---------------------------------------------------------------- the kernel
 
-// Refills the ring slot that was just used: S copies are always in flight or
-// waiting, keys and values in turn, so the next copy is of the kind just used
-// when S is even and of the other kind when it is odd.
-template <int S, class K, class V>
-__device__ __forceinline__ void refill(K &issue_k, V &issue_v, bool used_k) {
-    if (used_k == (S % 2 == 0)) issue_k();
-    else issue_v();
-}
-
 template <int CT, class C>
-__global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedAttnParams p,
+                                                                        const __grid_constant__ CUtensorMap k_map,
+                                                                        const __grid_constant__ CUtensorMap v_map, int box_tokens) {
     constexpr int NT = C::NT, ROWS = C::ROWS, D = C::D, TS = C::TS, TT = C::TT, W = C::W, S = C::S;
     constexpr int KB = C::KB, VB = C::VB, MT = C::MT, MPV = C::MPV, QR = C::QR;
     constexpr bool Q8 = C::Q8, F32 = C::F32, BF16 = C::BF16;
@@ -303,17 +395,36 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     const float NEG_INF = __int_as_float(0xff800000);
 
     extern __shared__ __align__(1024) uint8_t smem[];
-    long long *scan = reinterpret_cast<long long *>(smem);             // [W] warp sums
-    int *found = reinterpret_cast<int *>(smem + 512);                  // sequence, then the last-CTA flag
-    long long *found_off = reinterpret_cast<long long *>(smem + 528);  // chunk offset in that sequence
-    float *buf = reinterpret_cast<float *>(smem + 1024);               // [W][ROWS][BUF_ROW]
-    float2 *ml = reinterpret_cast<float2 *>(smem + 1024 + C::join_bytes(W));  // [2][W + 1][ROWS]; row W: joined
-    uint8_t *ring = smem + 1024 + C::join_bytes(W) + C::ml_bytes(W);
+    long long *scan = reinterpret_cast<long long *>(smem);               // [warps] sums
+    long long *found_off = reinterpret_cast<long long *>(smem + 256);    // chunk offset in the first sequence
+    int *found = reinterpret_cast<int *>(smem + 264);                    // that sequence
+    volatile int *dead = reinterpret_cast<volatile int *>(smem + 272);   // a wait ran out
+    int *part_slot = reinterpret_cast<int *>(smem + 288);                // [W] where a consumer left its part
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + 512);           // [W][S] a slot's tile has landed
+    uint64_t *q_full = full + W * S, *q_empty = q_full + 2;              // [2] a segment's queries
+    uint64_t *j_full = q_empty + 2, *j_empty = j_full + 1;               // the consumers' parts of a segment
+    uint8_t *queries = smem + C::HEAD;                                   // [2][ROWS][QROW]
+    float2 *joined = reinterpret_cast<float2 *>(queries + C::QUERIES);   // [ROWS] maxima and sums
+    float *factor = reinterpret_cast<float *>(joined + ROWS);            // [W][ROWS]
+    uint8_t *ring = smem + (C::SMEM - W * S * C::SLOT - 1024);           // [W][S][SLOT], on a 1024-byte boundary
+    ring += (1024 - (ptx::smem_u32(ring) & 1023)) & 1023;
 
-    dependent_prologue();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    if (tid < W * S) ptx::mbar_init(full + tid, Q8 ? 33 : 1);  // the tensor copies, and each lane's copies of scales
+    if (tid < 2) {
+        ptx::mbar_init(q_full + tid, 32);
+        ptx::mbar_init(q_empty + tid, W);
+    }
+    if (tid == 0) {
+        ptx::mbar_init(j_full, W);
+        ptx::mbar_init(j_empty, 1);
+        *dead = 0;
+    }
+    ptx::fence_mbar_init();
+    dependent_prologue();
 
     // ---- this CTA's share of the chunks
+    Shares shares;
     long long total, start;
     {
         const int per = (p.B + C::THREADS - 1) / C::THREADS;
@@ -334,13 +445,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         long long before = 0;
         total = 0;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
+        for (int i = 0; i < C::THREADS / 32; ++i) {
             if (i < warp) before += scan[i];
             total += scan[i];
         }
-        const long long ctas = min((long long)gridDim.x, total);
-        if ((long long)blockIdx.x >= ctas) return;
-        start = total * blockIdx.x / ctas;
+        const int ctas = (int)min((long long)gridDim.x, total);  // those with work
+        if (blockIdx.x >= ctas) {
+            if (tid == 0) Parts<C>(p.partials, gridDim.x).split[blockIdx.x].parts = 0;
+            return;
+        }
+        shares.each = divide(total, ctas);
+        shares.rem = total - shares.each * ctas;
+        start = shares.begin(blockIdx.x);
         long long excl = before + incl - sum;
         if (start >= excl && start < excl + sum) {
             for (int b = b0;; ++b) {
@@ -356,159 +472,301 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         }
         __syncthreads();
     }
-    const long long ctas = min((long long)gridDim.x, total);  // those with work
-    Walk use;  // what the products are at
+    const long long end = shares.begin(blockIdx.x + 1);
+    Walk use;  // what the warp is at
     use.s = load_seq<C>(p, *found, false);
-    use.unit = (int)(*found_off / use.s.chunks);
+    use.unit = (int)divide(*found_off, use.s.chunks);
     use.chunk = (int)(*found_off - (long long)use.unit * use.s.chunks);
-    use.left = total * (blockIdx.x + 1) / ctas - start;
-    open_segment<C>(use, warp);
-    Walk get = use;  // what the copies are at, some tiles ahead
+    use.left = (int)(end - start);
 
-    // ---- copies
-    const uint32_t ring0 = ptx::smem_u32(ring) + warp * (S * C::SLOT);
-    const uint8_t *kbase = static_cast<const uint8_t *>(p.c.k), *vbase = static_cast<const uint8_t *>(p.c.v);
-    bool wanted = false;         // whether this lane's token of the tile at `get` is read at all
-    int page = 0, in_page = 0;   // where it is
-    long long row = -1;          // its byte offset in the cache (head included), -1: not read
-    uint32_t put = 0, take = 0;  // ring positions in bytes
-
-    auto look_up = [&]() {  // one tile ahead of its use, so that the table's latency is hidden
-        while (get.left > 0 && get.tile >= get.tile_end) next_segment<C>(get, p, warp);
-        wanted = false;
-        if (get.left > 0) {
-            const int t = get.s.t0 + get.tile * TT + (lane & (TT - 1));
-            if (t >= get.s.first && t < get.s.len) {
-                const int i = t / p.c.page_size;
-                in_page = t - i * p.c.page_size;
-                page = p.block_table[get.s.b * p.bt_stride + i];
-                wanted = true;
+    // ---- joiners: fetch the queries of the segments and add the consumers' parts of them
+    if (warp >= W) {
+        constexpr int THREADS = 32 * C::NJ;
+        const int j = tid - 32 * W;
+        const Parts<C> parts(p.partials, gridDim.x);
+        int split_parts = 0;
+        open_segment<C>(use, 0);
+        auto fetch = [&](const Walk &w, int segment) {  // by the first joiner warp
+            if (j >= 32 || w.left <= 0) return;
+            const int b = segment & 1;
+            ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead);
+            const int head = (int)((uint32_t)w.unit / (uint32_t)w.s.row_groups);
+            const int row0 = (w.unit - head * w.s.row_groups) * ROWS;
+            const int rows = min(ROWS, w.s.n * p.G - row0);
+            constexpr int PIECES = D * (F32 ? 4 : 2) / 16;
+            for (int i = lane; i < ROWS * PIECES; i += 32) {
+                const int r = i / PIECES, x = i % PIECES;
+                const int row = row0 + min(r, rows - 1);
+                const int token = (int)((uint32_t)row / (uint32_t)p.G), hq = row - token * p.G;
+                const uint8_t *src = static_cast<const uint8_t *>(p.q) +
+                                     ((long long)(w.s.cu0 + token) * p.q_stride + ((long long)head * p.G + hq) * D) * (F32 ? 4 : 2);
+                copy_async<16>(ptx::smem_u32(queries + (b * ROWS + r) * C::QROW + x * 16), src + x * 16, r < rows ? 16 : 0);
             }
-        }
-    };
-    auto issue_k = [&]() {
-        if (get.left > 0) {
-            row = -1;
-            const int head = get.unit / get.s.row_groups;
-            if (wanted) {
-                if (page >= 0 && page < p.c.num_pages)
-                    row = (page * p.c.page_stride + in_page * p.c.token_stride + head * p.c.head_stride) * C::ESZ;
-                else
-                    flag_error(p.status, GDN_DEVERR_PAGE);
-            }
-            const uint32_t dst = ring0 + put + lane * C::CHK;
+            copy_arrive(q_full + b);
+        };
+        fetch(use, 0);
+        for (int segment = 0; use.left > 0; ++segment) {
+            Walk next = use;
+            next_segment<C>(next, p, 0);
+            fetch(next, segment + 1);
+            const int head = (int)((uint32_t)use.unit / (uint32_t)use.s.row_groups);
+            const int row0 = (use.unit - head * use.s.row_groups) * ROWS;
+            const int rows = min(ROWS, use.s.n * p.G - row0);
+            const int pos0 = use.s.len - use.s.n;
+            const bool whole = use.seg_chunks == use.s.chunks;
+            ring_wait(j_full, segment & 1, dead);
+            const float *part[W];  // [ROWS][OROW], then the rows' (maximum, sum)
 #pragma unroll
-            for (int r = 0; r < 2 * TS; ++r) {
-                const long long o = __shfl_sync(FULL, row, r * 8 + g);
-                const uint8_t *src = kbase + (o < 0 ? 0 : o) + c * C::CHK;
+            for (int w = 0; w < W; ++w) part[w] = reinterpret_cast<const float *>(ring + (w * S + part_slot[w]) * C::SLOT);
+            for (int r = j; r < ROWS; r += THREADS) {
+                float2 st[W];
+                float mm = NEG_INF, ll = 0.f;
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-                    copy_async<C::CHK>(dst + (r * KB + kb) * 32 * C::CHK, src + kb * 4 * C::CHK, o < 0 ? 0 : C::CHK);
+                for (int w = 0; w < W; ++w) {
+                    st[w] = reinterpret_cast<const float2 *>(part[w] + ROWS * C::OROW)[r];
+                    mm = fmaxf(mm, st[w].x);
+                }
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float f = part_factor(st[w].x, mm);
+                    factor[w * ROWS + r] = f;
+                    ll += st[w].y * f;
+                }
+                joined[r] = make_float2(mm, ll);
             }
-            if constexpr (Q8) {
-                // lanes' tokens: TS == 2 one each, TS == 1 lanes 0-15 fetch key scales and 16-31 value scales
-                const long long so = row < 0 ? 0
-                                             : page * p.c.s_page_stride + in_page * p.c.s_token_stride +
-                                                   head * p.c.s_head_stride;
-                const uint32_t sdst = ring0 + put + TT * C::RB;
-                const int bytes = row < 0 ? 0 : 4;
-                if constexpr (TS == 2) {
-                    copy_async<4>(sdst + lane * 4, p.c.k_scale + so, bytes);
-                    copy_async<4>(sdst + 128 + lane * 4, p.c.v_scale + so, bytes);
+            named_sync(1, THREADS);
+            const long long slot = 2LL * blockIdx.x + (use.chunk == 0 ? 1 : 0);
+            for (int i = j; i < rows * (D / 4); i += THREADS) {
+                const int r = i / (D / 4), ch = i % (D / 4) * 4;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float4 x = *reinterpret_cast<const float4 *>(part[w] + r * C::OROW + ch);
+                    const float f = factor[w * ROWS + r];
+                    sum.x += f * x.x, sum.y += f * x.y, sum.z += f * x.z, sum.w += f * x.w;
+                }
+                if (*dead) continue;
+                if (whole) {
+                    store_row<CT, C>(p, row0 + r, head, use.s.cu0, pos0, ch, sum, joined[r]);
                 } else {
-                    copy_async<4>(sdst + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + so, bytes);
+                    *reinterpret_cast<float4 *>(parts.o + (slot * ROWS + r) * D + ch) = sum;
+                    if (ch == 0) parts.ml[slot * ROWS + r] = joined[r];
                 }
             }
-        }
-        copy_commit();
-        put = put + C::SLOT == S * C::SLOT ? 0 : put + C::SLOT;
-    };
-    auto issue_v = [&]() {
-        if (get.left > 0) {
-            const uint32_t dst = ring0 + put + lane * C::CHV;
-#pragma unroll
-            for (int r = 0; r < 4 * TS; ++r) {
-                const int tk = r & 3;
-                const int token = (r >> 2) * 16 + (F32 ? c + 4 * tk : 2 * c + (tk & 1) + 8 * (tk >> 1));
-                const long long o = __shfl_sync(FULL, row, token);
-                const uint8_t *src = vbase + (o < 0 ? 0 : o) + g * C::CHV;
-#pragma unroll
-                for (int vb = 0; vb < VB; ++vb)
-                    copy_async<C::CHV>(dst + (r * VB + vb) * 32 * C::CHV, src + vb * 8 * C::CHV, o < 0 ? 0 : C::CHV);
+            ptx::fence_proxy_async_smem();  // tensor copies will overwrite what the consumers stored
+            named_sync(1, THREADS);
+            if (j == 0) {
+                ptx::mbar_arrive(j_empty);
+                if (!whole && use.chunk == 0) {  // the head of a unit that goes on: this CTA's last segment
+                    split_parts = shares.owner(end - use.left + use.s.chunks - 1) - (int)blockIdx.x + 1;
+                    parts.split[blockIdx.x] = {split_parts, rows, row0, head, use.s.cu0, pos0, {0, 0}};
+                }
             }
-            get.tile += W;
-            look_up();
+            use = next;
         }
-        copy_commit();
-        put = put + C::SLOT == S * C::SLOT ? 0 : put + C::SLOT;
-    };
-    look_up();
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        if (i % 2 == 0) issue_k();
-        else issue_v();
+        if (j == 0) {
+            if (split_parts == 0) parts.split[blockIdx.x].parts = 0;
+            if (*dead) flag_error(p.status, GDN_DEVERR_TIMEOUT);
+        }
+        copy_wait_all();
+        return;
     }
 
-    // ---- one segment after another
-    int parity = 0;
-    while (true) {
-        const int head = use.unit / use.s.row_groups;
-        const int row0 = (use.unit - head * use.s.row_groups) * ROWS;   // first query row of the unit
-        const int rows = min(ROWS, use.s.n * p.G - row0);               // query rows it has
-        const int pos0 = use.s.len - use.s.n;                           // the first query's position
+    // ---- consumers: warp w multiplies tiles w, w + W, ... of each segment
+    open_segment<C>(use, warp);
+    uint8_t *slots = ring + warp * (S * C::SLOT);  // this warp's
+    uint64_t *landed = full + warp * S;
+    int at = 0;          // the slot that is used next
+    uint32_t phase = 0;  // bit i: the parity of slot i's next landing
+    // A tile's keys (values) are `subs` boxes of box_tokens tokens, each within a page.  Lane i looks up box
+    // i % subs of the warp's (i / subs)-th next tile of the segment that copies are at.
+    const int subs = TT / box_tokens, batch = 32 / subs;
+    Walk get = use;              // get.tile: the batch's first tile
+    int page = 0, in_page = 0;   // where the lane's box is
+    bool wanted = false;         // whether it is read at all
+    int taken = 0;               // tiles of the batch that have been copied
+    int put = 0, free_slots = S; // the slot that is filled next, and how many may be
+    auto look_up = [&]() {
+        taken = 0;
+        wanted = false;
+        if (get.left <= 0) return;
+        const int tile = get.tile + lane / subs * W;
+        const int t = get.s.t0 + tile * TT + lane % subs * box_tokens;
+        wanted = tile < get.tile_end && t < get.s.len && t + box_tokens > get.s.first;
+        if (wanted) {
+            const int i = p.page_shift >= 0 ? t >> p.page_shift : (int)((uint32_t)t / (uint32_t)p.c.page_size);
+            in_page = t - i * p.c.page_size;
+            page = p.block_table[get.s.b * p.bt_stride + i];
+        }
+    };
+    // Fills free slots in the order of use: the tiles of a segment, then one that is left for the warp's part of
+    // it.  A slot that holds a part is free once the joiners are done with that segment; `block` waits for them.
+    int part_at = -1, part_segment = 0;  // the last part's slot, until it is known to be free
+    auto pump = [&](bool block) {
+        while (free_slots > 0 && get.left > 0) {
+            if (put == part_at) {
+                if (block) ring_wait(j_empty, part_segment & 1, dead);
+                else if (!__all_sync(FULL, ptx::mbar_test_wait(j_empty, part_segment & 1))) return;
+                part_at = -1;
+            }
+            const int tile = get.tile + taken * W;
+            if (tile >= get.tile_end) {
+                next_segment<C>(get, p, warp);
+                look_up();
+            } else {
+                const int box0 = taken * subs;
+                const int head = (int)((uint32_t)get.unit / (uint32_t)get.s.row_groups);
+                const uint32_t mine = __ballot_sync(FULL, wanted) >> box0 & (subs == 32 ? FULL : (1u << subs) - 1);
+                // 64-byte rows of pages with an odd number of tokens: a tensor copy's destination is a multiple
+                // of 128 bytes, so such rows are copied in 16-byte pieces instead
+                const bool by_rows = C::SPAN == 64 && box_tokens == 1;
+                uint8_t *dst = slots + put * C::SLOT;
+                uint64_t *bar = landed + put;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, by_rows ? 0 : 2 * __popc(mine) * box_tokens * C::RB);
+                // (a page outside the pool reads as zeros: it is outside the map)
+                auto box_page = [&](int b) {
+                    const int pg = __shfl_sync(FULL, page, box0 + b);
+                    const bool bad = (mine >> b & 1) && (pg < 0 || pg >= p.c.num_pages);
+                    if (bad && lane == 0) flag_error(p.status, GDN_DEVERR_PAGE);
+                    return bad ? p.c.num_pages : pg;
+                };
+                if (C::SPAN == 64 && by_rows) {
+#pragma unroll 1
+                    for (int k = lane; k < TT * 8; k += 32) {
+                        const int half = k >= TT * 4, token = k >> 2 & (TT - 1), x = k & 3;
+                        const int pg = __shfl_sync(FULL, page, box0 + token), off = __shfl_sync(FULL, in_page, box0 + token);
+                        const bool ok = (mine >> token & 1) && pg >= 0 && pg < p.c.num_pages;
+                        if ((mine >> token & 1) && !ok) flag_error(p.status, GDN_DEVERR_PAGE);
+                        const uint8_t *src = static_cast<const uint8_t *>(half ? p.c.v : p.c.k);
+                        if (ok) src += (pg * p.c.page_stride + off * p.c.token_stride + head * p.c.head_stride) * C::ESZ + x * 16;
+                        copy_async<16>(ptx::smem_u32(dst + half * C::HALF + token * 64 + ((x ^ (token >> 1 & 3)) << 4)), src,
+                                       ok ? 16 : 0);
+                    }
+                } else if (subs == 1) {  // all spans at once
+                    const int pg = box_page(0), off = __shfl_sync(FULL, in_page, box0);
+                    if (lane == 0) {
+                        ptx::tma_load_5d(dst, &k_map, 0, off, 0, head, pg, bar);
+                        ptx::tma_load_5d(dst + C::HALF, &v_map, 0, off, 0, head, pg, bar);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int b = 0; b < subs; ++b) {
+                        const int pg = box_page(b), off = __shfl_sync(FULL, in_page, box0 + b);
+                        if (lane != 0 || !(mine >> b & 1)) continue;
+                        uint8_t *to = dst + b * box_tokens * C::SPAN;
+#pragma unroll
+                        for (int x = 0; x < C::BOXES; ++x) {
+                            ptx::tma_load_5d(to + x * TT * C::SPAN, &k_map, 0, off, x, head, pg, bar);
+                            ptx::tma_load_5d(to + C::HALF + x * TT * C::SPAN, &v_map, 0, off, x, head, pg, bar);
+                        }
+                    }
+                }
+                if constexpr (Q8) {
+                    // TS == 2: a token a lane; 16 tokens: the upper lanes repeat them for the value scales
+                    const int token = lane & (TT - 1), sub = token / box_tokens;
+                    const int pg = __shfl_sync(FULL, page, box0 + sub);
+                    const int off = __shfl_sync(FULL, in_page, box0 + sub) + token - sub * box_tokens;
+                    const int t = get.s.t0 + tile * TT + token;
+                    const bool ok = (mine >> sub & 1) && pg >= 0 && pg < p.c.num_pages && t >= get.s.first && t < get.s.len;
+                    const long long o = ok ? pg * p.c.s_page_stride + off * p.c.s_token_stride + head * p.c.s_head_stride : 0;
+                    const uint32_t to = ptx::smem_u32(dst + 2 * C::HALF + 4 * lane);
+                    if constexpr (TS == 2) {
+                        copy_async<4>(to, p.c.k_scale + o, ok ? 4 : 0);
+                        copy_async<4>(to + 4 * TT, p.c.v_scale + o, ok ? 4 : 0);
+                    } else {
+                        copy_async<4>(to, (lane < 16 ? p.c.k_scale : p.c.v_scale) + o, ok ? 4 : 0);
+                    }
+                    copy_arrive(bar);
+                }
+                if (++taken == batch) {
+                    get.tile += batch * W;
+                    look_up();
+                }
+            }
+            // (a slot for the part of a segment is taken like one for a tile)
+            put = put + 1 == S ? 0 : put + 1;
+            --free_slots;
+        }
+    };
+    auto filled = [&]() {
+        if (free_slots == S) pump(true);
+        ring_wait(landed + at, phase >> at & 1, dead);
+        phase ^= 1u << at;
+    };
+    // Frees the slot at `at`, all of whose readers are behind, and refills.
+    auto release = [&]() {
+        __syncwarp();
+        at = at + 1 == S ? 0 : at + 1;
+        ++free_slots;
+        pump(false);
+    };
+    look_up();
+    pump(false);
+
+    // Where the lane's pieces are in a slot: key row g (and g + 8), piece c (odd steps: + 4); value rows
+    // 2 c, 2 c + 1 (and + 8), its piece g.  Swizzled as the tensor copies leave them.
+    constexpr bool HALF_LINE = C::SPAN == 64;
+    const int k_at = g * C::SPAN + ((c ^ (HALF_LINE ? g >> 1 : g)) << 4);
+    const int v_at0 = 2 * c * C::SPAN + (HALF_LINE ? ((g >> 1 ^ c) << 4) + (g & 1) * 8 : (g ^ 2 * c) << 4);
+    const int v_at1 = (2 * c + 1) * C::SPAN + (HALF_LINE ? ((g >> 1 ^ c) << 4) + (g & 1) * 8 : (g ^ (2 * c + 1)) << 4);
+
+    for (int segment = 0; use.left > 0; ++segment) {
+        const int head = (int)((uint32_t)use.unit / (uint32_t)use.s.row_groups);
+        const int row0 = (use.unit - head * use.s.row_groups) * ROWS;  // first query row of the unit
+        const int rows = min(ROWS, use.s.n * p.G - row0);              // query rows it has
+        const int pos0 = use.s.len - use.s.n;                          // the first query's position
 
         // queries: lane (g, c) holds, of row 8 nt + g, the channels that its key pieces have
         uint32_t q[NT][QR];
         float col_scale[NT][2];  // scores' factor of the lane's two columns
+        ring_wait(q_full + (segment & 1), segment >> 1 & 1, dead);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + g;
-            const int i = (row0 + r) / p.G, hq = (row0 + r) - i * p.G;
-            const uint8_t *src = static_cast<const uint8_t *>(p.q) +
-                                 ((long long)(use.s.cu0 + i) * p.q_stride + ((long long)head * p.G + hq) * D) * (F32 ? 4 : 2);
-            const bool real = r < rows;
-            if constexpr (Q8) {
-                // 16 channels a piece; scaled so that the row's largest magnitude is in [1, 2)
-                uint32_t raw[KB][8];
-                float top = 0.f;
+            const uint8_t *src = queries + ((segment & 1) * ROWS + nt * 8 + g) * C::QROW;
+            col_scale[nt][0] = col_scale[nt][1] = p.scale_log2;
+            if constexpr (!Q8) {
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    const uint4 *s4 = reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32);
-                    const uint4 x = real ? s4[0] : make_uint4(0, 0, 0, 0), y = real ? s4[1] : make_uint4(0, 0, 0, 0);
-                    raw[kb][0] = x.x, raw[kb][1] = x.y, raw[kb][2] = x.z, raw[kb][3] = x.w;
-                    raw[kb][4] = y.x, raw[kb][5] = y.y, raw[kb][6] = y.z, raw[kb][7] = y.w;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 f = p.io_bf16 ? unpack2<true>(raw[kb][j]) : unpack2<false>(raw[kb][j]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-                }
-                top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-                // the exponent of top, kept in a range where both powers of two are normal
-                int e = ((__float_as_uint(top) >> 23) & 255) - 127;
-                e = top > 0.f && top <= 3.402823466e38f ? max(e, -100) : 0;
-                const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 f = p.io_bf16 ? unpack2<true>(raw[kb][j]) : unpack2<false>(raw[kb][j]);
-                        q[nt][kb * 8 + j] = pack2<false>(f.x * down, f.y * down);
-                    }
-                col_scale[nt][0] = p.scale_log2 * __shfl_sync(FULL, up, 8 * c);
-                col_scale[nt][1] = p.scale_log2 * __shfl_sync(FULL, up, 8 * c + 4);
-            } else {
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    const uint4 x = real ? *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 16) : make_uint4(0, 0, 0, 0);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 16);
                     q[nt][kb * 4] = x.x, q[nt][kb * 4 + 1] = x.y, q[nt][kb * 4 + 2] = x.z, q[nt][kb * 4 + 3] = x.w;
                 }
-                col_scale[nt][0] = col_scale[nt][1] = p.scale_log2;
+            } else {  // 16 channels a piece
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32 + 16);
+                    q[nt][kb * 8] = x.x, q[nt][kb * 8 + 1] = x.y, q[nt][kb * 8 + 2] = x.z, q[nt][kb * 8 + 3] = x.w;
+                    q[nt][kb * 8 + 4] = y.x, q[nt][kb * 8 + 5] = y.y, q[nt][kb * 8 + 6] = y.z, q[nt][kb * 8 + 7] = y.w;
+                }
+                if (p.io_bf16) {
+                    // to FP16, scaled by a power of two so that the row's largest magnitude is in [1, 2)
+                    float top = 0.f;
+#pragma unroll
+                    for (int j = 0; j < QR; ++j) {
+                        const float2 f = unpack2<true>(q[nt][j]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+                    // the exponent of top, kept where both powers of two are normal
+                    int e = (int)(__float_as_uint(top) >> 23 & 255) - 127;
+                    e = top > 0.f && top <= 3.402823466e38f ? max(e, -100) : 0;
+                    e = min(e, 126);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                    for (int j = 0; j < QR; ++j) {
+                        const float2 f = unpack2<true>(q[nt][j]);
+                        q[nt][j] = pack2<false>(f.x * down, f.y * down);
+                    }
+                    col_scale[nt][0] *= __shfl_sync(FULL, up, 8 * c);
+                    col_scale[nt][1] *= __shfl_sync(FULL, up, 8 * c + 4);
+                }
             }
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(q_empty + (segment & 1));
         // positions that every query row of the unit sees: [all_lo, all_hi)
-        const int all_hi = pos0 + row0 / p.G + 1;
+        const int all_hi = pos0 + (int)((uint32_t)row0 / (uint32_t)p.G) + 1;
         const int all_lo = p.window > 0 ? max(0, pos0 + (row0 + rows - 1) / p.G - p.window + 1) : 0;
         auto seen = [&](int r, int t) {  // whether row r of the unit sees position t
             const int pos = pos0 + (row0 + min(r, rows - 1)) / p.G;
@@ -529,7 +787,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             const bool edge = tile_t < all_lo || tile_t + TT > all_hi;
 
             // ---- scores: S^T = K Q^T
-            copy_wait<S - 1>();
+            filled();
             float sc[TS][NT][4], sc2[TS][NT][4];
 #pragma unroll
             for (int ts = 0; ts < TS; ++ts)
@@ -537,14 +795,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[ts][nt][e] = sc2[ts][nt][e] = 0.f;
-            const uint32_t ks = ring0 + take + lane * C::CHK;
+            const uint8_t *ks = slots + at * C::SLOT;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int ts = 0; ts < TS; ++ts) {
                     uint32_t x[4], y[4];
-                    lds<4>(x, ks + ((2 * ts) * KB + kb) * 32 * C::CHK);
-                    lds<4>(y, ks + ((2 * ts + 1) * KB + kb) * 32 * C::CHK);
+                    const uint8_t *piece = ks + (kb / 2) * TT * C::SPAN + ts * 16 * C::SPAN + (kb % 2 ? k_at ^ 64 : k_at);
+                    lds<4>(x, piece);
+                    lds<4>(y, piece + 8 * C::SPAN);
                     if constexpr (Q8) {
                         uint32_t u[8], v[8];
 #pragma unroll
@@ -582,8 +841,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             // the lane's tokens are rows g and g + 8 of each subtile
             float vs[TS][2], lv[TS][2], ksc[TS][2];
             if constexpr (Q8) {
-                __syncwarp();  // the scales were copied by other lanes
-                const float *kscale = reinterpret_cast<const float *>(ring + warp * (S * C::SLOT) + take + TT * C::RB);
+                const float *kscale = reinterpret_cast<const float *>(slots + at * C::SLOT + 2 * C::HALF);
 #pragma unroll
                 for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
@@ -593,7 +851,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         vs[ts][e] = kscale[TT + i];
                         lv[ts][e] = log2_fast(fmaxf(fabsf(vs[ts][e]), 1e-30f));  // (rows of zeros may have scale 0)
                     }
-                __syncwarp();
             }
             float top[NT][2];
 #pragma unroll
@@ -612,8 +869,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         if constexpr (Q8) y = x == NEG_INF ? x : x + lv[ts][e >> 1];
                         top[nt][e & 1] = fmaxf(top[nt][e & 1], y);
                     }
-            refill<S>(issue_k, issue_v, true);
-            take = take + C::SLOT == S * C::SLOT ? 0 : take + C::SLOT;
 
             // ---- raise the maxima where a score exceeds them by more than the headroom
             bool raise = false;
@@ -658,14 +913,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         else w[e] = x;
                     }
                     if constexpr (F32) {
-                        // token c (+4, +8, +12) of column g: from the lane that holds that token's row
-                        const int src = c * 4 + (g >> 1);
+                        // k-slots c and c + 4 are tokens 2 c and 2 c + 1 (+ 8): from the lanes that hold their rows, column g
+                        const int src = c * 8 + (g >> 1);
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const float a = __shfl_sync(FULL, w[2 * k], src + 16 * j);
-                                const float b = __shfl_sync(FULL, w[2 * k + 1], src + 16 * j);
+                                const float a = __shfl_sync(FULL, w[2 * k], src + 4 * j);
+                                const float b = __shfl_sync(FULL, w[2 * k + 1], src + 4 * j);
                                 split_tf32(__float_as_uint(g & 1 ? b : a), fh[ts][nt][k][j], fl[ts][nt][k][j]);
                             }
                     } else {
@@ -681,11 +936,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 }
 
             // ---- O^T += V^T P^T
-            copy_wait<S - 1>();
-            const uint32_t vsm = ring0 + take + lane * C::CHV;
+            const uint8_t *vsm = slots + at * C::SLOT + C::HALF;
             constexpr int VW = C::CHV / 4;  // words of a value piece
-            // `only`: -1, or the single query row to add, with values that it does not see left out
-            auto add_values = [&](int only) {
+            // `only`: -1, or the single query row to add, with values that it does not see left out.  A tile
+            // at an end of what is cached holds other tokens' rows too, which count as zeros.
+            auto add_values = [&](int only, auto careful) {
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb)
 #pragma unroll
@@ -693,10 +948,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         uint32_t v[4][VW];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            lds<VW>(v[k], vsm + ((ts * 4 + k) * VB + vb) * 32 * C::CHV);
-                            if (only >= 0) {
-                                const int t = tile_t + ts * 16 + (F32 ? c + 4 * k : 2 * c + (k & 1) + 8 * (k >> 1));
-                                if (!seen(only, t)) {
+                            lds<VW>(v[k], vsm + vb * TT * C::SPAN + (ts * 16 + 8 * (k >> 1)) * C::SPAN + ((k & 1) ? v_at1 : v_at0));
+                            if constexpr (careful()) {
+                                const int t = tile_t + ts * 16 + 2 * c + (k & 1) + 8 * (k >> 1);
+                                if (t < use.s.first || t >= use.s.len || (only >= 0 && !seen(only, t))) {
 #pragma unroll
                                     for (int j = 0; j < VW; ++j) v[k][j] = 0u;
                                 }
@@ -750,27 +1005,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             };
             // A value that some rows of the tile see and others do not would reach the others as
             // 0 * inf if it is not finite: such a tile is added row by row.
-            bool rough = false;
-            if (CT != GDN_INT8 && edge && use.s.n > 1) {
-                uint32_t x[VW];
-                for (int i = 0; i < 4 * TS * VB; ++i) {
-                    lds<VW>(x, vsm + i * 32 * C::CHV);
-#pragma unroll
-                    for (int j = 0; j < VW; ++j) rough |= non_finite<CT>(x[j]);
+            if (edge) {
+                bool rough = false;
+                if (CT != GDN_INT8 && use.s.n > 1) {
+                    for (int i = lane * 4; i < C::HALF; i += 128) {  // (any order: rows of the tile, SPAN bytes each)
+                        const int t = tile_t + i / C::SPAN % TT;
+                        rough |= t >= use.s.first && t < use.s.len && non_finite<CT>(*reinterpret_cast<const uint32_t *>(vsm + i));
+                    }
+                    rough = __any_sync(FULL, rough);
                 }
-                rough = __any_sync(FULL, rough);
-            }
-            if (rough) {
-                for (int r = 0; r < rows; ++r) add_values(r);
+                for (int r = rough ? 0 : -1; r < (rough ? rows : 0); ++r) add_values(r, Yes());
             } else {
-                add_values(-1);
+                add_values(-1, No());
             }
-            refill<S>(issue_k, issue_v, false);
-            take = take + C::SLOT == S * C::SLOT ? 0 : take + C::SLOT;
+            release();
         }
 
-        // ---- join the warps
-        float2 *mlp = ml + parity * (W + 1) * ROWS;
+        // ---- this warp's part of the segment, for the joiners
+        if (free_slots == S) pump(true);
+        if (segment > 0) ring_wait(j_empty, (segment - 1) & 1, dead);  // the joiners take one segment at a time
+        float *part = reinterpret_cast<float *>(slots + at * C::SLOT);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -779,138 +1033,94 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 x += __shfl_xor_sync(FULL, x, 4);
                 x += __shfl_xor_sync(FULL, x, 8);
                 x += __shfl_xor_sync(FULL, x, 16);
-                if (g == 0) mlp[warp * ROWS + nt * 8 + 2 * c + e] = make_float2(m[nt][e], x);
-            }
-        __syncthreads();
-        // a part without a maximum has zeros (or the NaN that its scores are)
-        auto part_factor = [&](float part, float all) { return part == NEG_INF ? 1.f : exp2_fast(part - all); };
-        if (tid < ROWS) {
-            float mm = NEG_INF, ll = 0.f;
+                const int r = nt * 8 + 2 * c + e;
+                if (g == 0) reinterpret_cast<float2 *>(part + ROWS * C::OROW)[r] = make_float2(m[nt][e], x);
+                float *dst = part + r * C::OROW + g * C::CPL;
 #pragma unroll
-            for (int w = 0; w < W; ++w) mm = fmaxf(mm, mlp[w * ROWS + tid].x);
+                for (int vb = 0; vb < VB; ++vb)
 #pragma unroll
-            for (int w = 0; w < W; ++w) ll += mlp[w * ROWS + tid].y * part_factor(mlp[w * ROWS + tid].x, mm);
-            mlp[W * ROWS + tid] = make_float2(mm, ll);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mm = NEG_INF;
-#pragma unroll
-                for (int w = 0; w < W; ++w) mm = fmaxf(mm, mlp[w * ROWS + nt * 8 + 2 * c + e].x);
-                const float f = part_factor(m[nt][e], mm);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    o[nt][i][e] *= f;
-                    o[nt][i][e + 2] *= f;
-                }
-            }
-        const bool whole = use.seg_chunks == use.s.chunks;
-        // owner(x): the CTA whose share holds chunk x
-        const long long unit0 = start + (total * (blockIdx.x + 1) / ctas - start - use.left) - use.chunk;  // the unit's first chunk
-        const int c0 = (int)(((unit0 + 1) * ctas - 1) / total);
-        const int c1 = (int)(((unit0 + use.s.chunks) * ctas - 1) / total);
-        auto store_row = [&](int r, int ch, float4 x, float2 st) {  // joined, unnormalised
-            const int i = (row0 + r) / p.G, hq = (row0 + r) - i * p.G;
-            const long long token = use.s.cu0 + i;
-            const bool any = pos0 + i >= 0;  // a query at a position before the cache sees nothing
-            const float inv = any ? 1.f / st.y : 0.f;
-            const long long at = (token * p.Hq + (long long)head * p.G + hq);
-            const float y[4] = {any ? x.x * inv : 0.f, any ? x.y * inv : 0.f, any ? x.z * inv : 0.f, any ? x.w * inv : 0.f};
-            if constexpr (F32) {
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at * D + ch) = make_float4(y[0], y[1], y[2], y[3]);
-            } else {
-                const bool bf = BF16 || (Q8 && p.io_bf16);
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at * D + ch) =
-                    bf ? make_uint2(pack2<true>(y[0], y[1]), pack2<true>(y[2], y[3]))
-                       : make_uint2(pack2<false>(y[0], y[1]), pack2<false>(y[2], y[3]));
-            }
-            if (p.lse && ch == 0) p.lse[at] = any ? (st.x - C::BIAS + log2f(st.y)) * 0.6931471805599453f : NEG_INF;
-        };
-        const long long my_slot = 2LL * blockIdx.x + (blockIdx.x == c0 ? 1 : 0);
-        float2 *part_ml = reinterpret_cast<float2 *>(p.partials);
-        float *part_o = p.partials + 4LL * gridDim.x * ROWS;
-#pragma unroll
-        for (int ph_ = 0; ph_ < D / ITEMS; ++ph_) {
-            if (ph_ > 0) __syncthreads();
-            // four output tiles: 8 values a lane and row
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float4 *dst = reinterpret_cast<float4 *>(buf + (warp * ROWS + nt * 8 + 2 * c + e) * BUF_ROW + g * 8);
-                    const int i = ph_ * 4;
-                    dst[0] = make_float4(o[nt][i][e], o[nt][i][e + 2], o[nt][i + 1][e], o[nt][i + 1][e + 2]);
-                    dst[1] = make_float4(o[nt][i + 2][e], o[nt][i + 2][e + 2], o[nt][i + 3][e], o[nt][i + 3][e + 2]);
-                }
-            __syncthreads();
-            for (int i = tid; i < rows * (ITEMS / 4); i += C::THREADS) {
-                const int r = i / (ITEMS / 4), x4 = i % (ITEMS / 4);
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const float4 x = *reinterpret_cast<const float4 *>(buf + (w * ROWS + r) * BUF_ROW + x4 * 4);
-                    sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
-                }
-                // value 4 x4 of the phase: lane group x4 / 2, output tiles ph_ * 4 + (x4 & 1) * 2 and the next
-                const int mt = ph_ * 4 + (x4 & 1) * 2;
-                const int ch = (mt / MPV * 8 + x4 / 2) * C::CPL + 2 * (mt % MPV);
-                if (whole) {
-                    store_row(r, ch, sum, mlp[W * ROWS + r]);
-                } else {
-                    *reinterpret_cast<float4 *>(part_o + (my_slot * ROWS + r) * D + ch) = sum;
-                    if (ch == 0) part_ml[my_slot * ROWS + r] = mlp[W * ROWS + r];
-                }
-            }
-        }
-        // ---- join the CTAs: the last one to arrive adds all parts, in CTA order
-        if (!whole) {
-            __threadfence();
-            __syncthreads();
-            const int parts = c1 - c0 + 1;
-            if (tid == 0) *found = atomicAdd(&p.counters[c0], 1) == parts - 1;
-            __syncthreads();
-            if (*found) {
-                __threadfence();
-                float *fac = buf;  // [parts][ROWS]
-                for (int r = warp; r < rows; r += W) {
-                    float mm = NEG_INF, ll = 0.f;
-                    for (int i = lane; i < parts; i += 32)
-                        mm = fmaxf(mm, __ldcg(&part_ml[(2LL * (c0 + i) + (i == 0)) * ROWS + r]).x);
-#pragma unroll
-                    for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, s));
-                    for (int i = lane; i < parts; i += 32) {
-                        const float2 x = __ldcg(&part_ml[(2LL * (c0 + i) + (i == 0)) * ROWS + r]);
-                        const float f = part_factor(x.x, mm);
-                        fac[i * ROWS + r] = f;
-                        ll += x.y * f;
+                    for (int i = 0; i < MPV; i += 2) {
+                        const float(&a)[4] = o[nt][vb * MPV + i], (&b)[4] = o[nt][vb * MPV + i + 1];
+                        *reinterpret_cast<float4 *>(dst + vb * 8 * C::CPL + 2 * i) = make_float4(a[e], a[e + 2], b[e], b[e + 2]);
                     }
-                    ll = warp_sum(ll);
-                    if (lane == 0) mlp[W * ROWS + r] = make_float2(mm, ll);
-                }
-                __syncthreads();
-                for (int i = tid; i < rows * (D / 4); i += C::THREADS) {
-                    const int r = i / (D / 4), ch = i % (D / 4) * 4;
-                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int k = 0; k < parts; ++k) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(
-                            part_o + ((2LL * (c0 + k) + (k == 0)) * ROWS + r) * D + ch));
-                        const float f = fac[k * ROWS + r];
-                        sum.x += f * x.x, sum.y += f * x.y, sum.z += f * x.z, sum.w += f * x.w;
-                    }
-                    store_row(r, ch, sum, mlp[W * ROWS + r]);
-                }
-                if (tid == 0) p.counters[c0] = 0;
-                __syncthreads();
             }
-        }
-        parity ^= 1;
+        if (lane == 0) part_slot[warp] = at;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(j_full);
+        part_at = at;
+        part_segment = segment;
+        at = at + 1 == S ? 0 : at + 1;
+        ++free_slots;
         next_segment<C>(use, p, warp);
-        if (use.left <= 0) break;
+        pump(false);
     }
-    copy_wait<0>();
+}
+
+// ---------------------------------------------------------------- joining split units
+
+constexpr int JOIN_THREADS = 256;
+
+// CTA (i, r): row r of the unit whose head CTA i of the attention kernel holds.
+// Groups of D / 4 threads take every GROUPS-th part, eight loads in flight.
+template <int CT, class C>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ PagedAttnParams p) {
+    constexpr int D = C::D, ROWS = C::ROWS, LANES = D / 4, GROUPS = JOIN_THREADS / LANES, BATCH = 8;
+    __shared__ float4 sums[GROUPS][LANES];
+    __shared__ float2 stats[GROUPS];
+    dependent_prologue();
+    const float NEG_INF = __int_as_float(0xff800000);
+    const Parts<C> parts(p.partials, gridDim.x);
+    const int i = blockIdx.x, r = blockIdx.y;
+    const Split s = parts.split[i];
+    if (r >= s.rows || s.parts == 0) return;
+    const int x = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float2 all = make_float2(NEG_INF, 0.f);
+    auto add = [&](const float2 (&st)[BATCH], const float4 (&v)[BATCH]) {
+        float mm = all.x;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) mm = fmaxf(mm, st[k].x);
+        const float f0 = part_factor(all.x, mm);
+        sum.x *= f0, sum.y *= f0, sum.z *= f0, sum.w *= f0;
+        all = make_float2(mm, all.y * f0);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const float f = part_factor(st[k].x, mm);
+            sum.x += f * v[k].x, sum.y += f * v[k].y, sum.z += f * v[k].z, sum.w += f * v[k].w;
+            all.y += f * st[k].y;
+        }
+    };
+    for (int k0 = grp; k0 < s.parts; k0 += BATCH * GROUPS) {
+        float2 st[BATCH];
+        float4 v[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int part = k0 + k * GROUPS;
+            st[k] = make_float2(NEG_INF, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (part < s.parts) {
+                const long long slot = 2LL * (i + part) + (part == 0);
+                st[k] = parts.ml[slot * ROWS + r];
+                v[k] = *reinterpret_cast<const float4 *>(parts.o + (slot * ROWS + r) * D + x * 4);
+            }
+        }
+        add(st, v);
+    }
+    sums[grp][x] = sum;
+    if (x == 0) stats[grp] = all;
+    __syncthreads();
+    if (grp != 0) return;
+    for (int k0 = 1; k0 < GROUPS; k0 += BATCH) {
+        float2 st[BATCH];
+        float4 v[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            st[k] = k0 + k < GROUPS ? stats[k0 + k] : make_float2(NEG_INF, 0.f);
+            v[k] = k0 + k < GROUPS ? sums[k0 + k][x] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        add(st, v);
+    }
+    store_row<CT, C>(p, s.row0 + r, s.head, s.cu0, s.pos0, x * 4, sum, all);
 }
 
 template <int CT, int D, int NT>
@@ -919,7 +1129,22 @@ cudaError_t launch_sized(const PagedAttnParams &p, cudaStream_t stream) {
     auto kernel = paged_attention_kernel<CT, C>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3((unsigned)attention_ctas()), dim3(C::THREADS), C::SMEM, stream, p);
+    // the largest power of two of tokens, up to a tile, that never crosses a page
+    int box_tokens = C::TT;
+    while (p.c.page_size % box_tokens) box_tokens >>= 1;
+    const int spans = box_tokens == C::TT ? C::BOXES : 1;  // whole tiles land in one copy
+    CUtensorMap k_map, v_map;
+    if (!encode_cache_rows(&k_map, p.c.k, C::ESZ, D, p.c.H, p.c.page_size, p.c.num_pages, p.c.head_stride, p.c.token_stride,
+                           p.c.page_stride, box_tokens, spans) ||
+        !encode_cache_rows(&v_map, p.c.v, C::ESZ, D, p.c.H, p.c.page_size, p.c.num_pages, p.c.head_stride, p.c.token_stride,
+                           p.c.page_stride, box_tokens, spans))
+        return cudaErrorInvalidValue;
+    const unsigned ctas = (unsigned)attention_ctas();
+    const cudaError_t e2 =
+        launch_dependent(kernel, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, p, k_map, v_map, box_tokens);
+    // a unit of one chunk is never split
+    if (e2 != cudaSuccess || (long long)p.pages_per_seq * p.c.page_size <= C::W * C::TT) return e2;
+    return launch_dependent(join_kernel<CT, C>, dim3(ctas, C::ROWS), dim3(JOIN_THREADS), 0, stream, p);
 }
 
 // Query rows a pass: as few groups of 8 as hold the rows of one key head

@@ -660,9 +660,8 @@ gdn_status gdn_kv_cache_read(const gdn_kv_read_args *args, gdn_stream_t stream);
  * The work is split over sequences, heads and cache length by the lengths on
  * the device, so a captured graph stays balanced as they change; pieces of one
  * sequence are joined in a fixed order (the same call gives the same bits).
- *   workspace    device scratch of gdn_paged_attention_workspace_size bytes, 16-byte aligned:
- *                its first 16 KiB must be zero before the first call that uses it and
- *                are zero again after every call.  Not shared by calls that overlap.
+ *   workspace    device scratch of gdn_paged_attention_workspace_size bytes, 16-byte aligned;
+ *                its contents need not be kept or set.  Not shared by calls that overlap.
  */
 typedef struct gdn_paged_attention_args {
     gdn_kv_cache cache;
