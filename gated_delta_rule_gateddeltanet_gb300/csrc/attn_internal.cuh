@@ -74,6 +74,7 @@ struct PagedAttnParams {
     int32_t *status;
     float *partials;
     int page_shift;  // log2(page_size), -1 if it is not a power of two
+    int s_page_stride32, s_token_stride32, s_head_stride32;  // the scale strides of the cache
 };
 
 cudaError_t launch_rotary_table(const RotaryTableParams &p, cudaStream_t stream);

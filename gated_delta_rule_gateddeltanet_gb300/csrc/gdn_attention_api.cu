@@ -51,7 +51,9 @@ gdn_status resolve_cache(const gdn_kv_cache &c, gdn::PagedCache *out) {
         p.s_head_stride = spacked ? 1 : c.scale_head_stride;
         p.s_token_stride = spacked ? c.num_kv_heads : c.scale_token_stride;
         p.s_page_stride = spacked ? (int64_t)c.page_size * c.num_kv_heads : c.scale_page_stride;
-        if (p.s_head_stride < 0 || p.s_token_stride < 0 || p.s_page_stride < 0) return GDN_ERR_SHAPE;
+        if (p.s_head_stride < 0 || p.s_token_stride < 0 || p.s_page_stride < 0 || p.s_head_stride > INT32_MAX ||
+            p.s_token_stride > INT32_MAX || p.s_page_stride > INT32_MAX)
+            return GDN_ERR_SHAPE;
         p.k_scale = c.k_scale;
         p.v_scale = c.v_scale;
     }
@@ -285,6 +287,9 @@ gdn_status gdn_paged_attention(const gdn_paged_attention_args *a, gdn_stream_t s
     p.lse = a->lse;
     p.status = a->status;
     p.partials = static_cast<float *>(a->workspace);
+    p.s_page_stride32 = (int)p.c.s_page_stride;
+    p.s_token_stride32 = (int)p.c.s_token_stride;
+    p.s_head_stride32 = (int)p.c.s_head_stride;
     p.page_shift = -1;
     for (int s = 0; s < 31; ++s)
         if (p.c.page_size == 1 << s) p.page_shift = s;

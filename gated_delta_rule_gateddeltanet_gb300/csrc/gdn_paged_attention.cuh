@@ -271,6 +271,7 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams &p, int b, bool fl
 struct Walk {
     Seq s;
     int unit, chunk;     // the current segment's unit and first chunk
+    int head, row0;      // the unit's key head and first query row
     int seg_chunks;
     int left;            // chunks of this CTA not yet behind the walk, this segment's included
     int tile, tile_end;  // the warp's next tile and the segment's end
@@ -278,6 +279,8 @@ struct Walk {
 
 template <class C>
 __device__ __forceinline__ void open_segment(Walk &w, int first) {
+    w.head = w.s.row_groups == 1 ? w.unit : (int)((uint32_t)w.unit / (uint32_t)w.s.row_groups);
+    w.row0 = (w.unit - w.head * w.s.row_groups) * C::ROWS;
     w.seg_chunks = min(w.s.chunks - w.chunk, w.left);
     w.tile = w.chunk * C::W + first;
     w.tile_end = min((w.chunk + w.seg_chunks) * C::W, w.s.tiles);
@@ -387,7 +390,7 @@ struct Parts {
 template <int CT, class C>
 __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedAttnParams p,
                                                                         const __grid_constant__ CUtensorMap k_map,
-                                                                        const __grid_constant__ CUtensorMap v_map, int box_tokens) {
+                                                                        const __grid_constant__ CUtensorMap v_map, int box_shift) {
     constexpr int NT = C::NT, ROWS = C::ROWS, D = C::D, TS = C::TS, TT = C::TT, W = C::W, S = C::S;
     constexpr int KB = C::KB, VB = C::VB, MT = C::MT, MPV = C::MPV, QR = C::QR;
     constexpr bool Q8 = C::Q8, F32 = C::F32, BF16 = C::BF16;
@@ -396,8 +399,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
 
     extern __shared__ __align__(1024) uint8_t smem[];
     long long *scan = reinterpret_cast<long long *>(smem);               // [warps] sums
-    long long *found_off = reinterpret_cast<long long *>(smem + 256);    // chunk offset in the first sequence
-    int *found = reinterpret_cast<int *>(smem + 264);                    // that sequence
+    Walk *first = reinterpret_cast<Walk *>(smem + 128);                  // where this CTA's share begins
     volatile int *dead = reinterpret_cast<volatile int *>(smem + 272);   // a wait ran out
     int *part_slot = reinterpret_cast<int *>(smem + 288);                // [W] where a consumer left its part
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + 512);           // [W][S] a slot's tile has landed
@@ -419,6 +421,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         ptx::mbar_init(j_full, W);
         ptx::mbar_init(j_empty, 1);
         *dead = 0;
+    }
+    if (tid == 32) {
+        ptx::prefetch_tensor_map(&k_map);
+        ptx::prefetch_tensor_map(&v_map);
     }
     ptx::fence_mbar_init();
     dependent_prologue();
@@ -463,8 +469,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 const Seq s = load_seq<C>(p, b, false);
                 const long long here = (long long)s.units * s.chunks;
                 if (start < excl + here) {
-                    *found = b;
-                    *found_off = start - excl;
+                    Walk w;
+                    w.s = s;
+                    w.unit = (int)divide(start - excl, s.chunks);
+                    w.chunk = (int)(start - excl - (long long)w.unit * s.chunks);
+                    w.left = (int)(shares.begin(blockIdx.x + 1) - start);
+                    *first = w;
                     break;
                 }
                 excl += here;
@@ -472,12 +482,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         }
         __syncthreads();
     }
-    const long long end = shares.begin(blockIdx.x + 1);
-    Walk use;  // what the warp is at
-    use.s = load_seq<C>(p, *found, false);
-    use.unit = (int)divide(*found_off, use.s.chunks);
-    use.chunk = (int)(*found_off - (long long)use.unit * use.s.chunks);
-    use.left = (int)(end - start);
+    Walk use = *first;  // what the warp is at
 
     // ---- joiners: fetch the queries of the segments and add the consumers' parts of them
     if (warp >= W) {
@@ -490,16 +495,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             if (j >= 32 || w.left <= 0) return;
             const int b = segment & 1;
             ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead);
-            const int head = (int)((uint32_t)w.unit / (uint32_t)w.s.row_groups);
-            const int row0 = (w.unit - head * w.s.row_groups) * ROWS;
-            const int rows = min(ROWS, w.s.n * p.G - row0);
+            const int rows = min(ROWS, w.s.n * p.G - w.row0);
             constexpr int PIECES = D * (F32 ? 4 : 2) / 16;
+            const int group = lane < ROWS ? w.row0 + min(lane, rows - 1) : 0;  // lane r: where row r is
+            const int token = w.s.n == 1 ? 0 : (int)((uint32_t)group / (uint32_t)p.G);
+            const long long row = ((long long)(w.s.cu0 + token) * p.q_stride + (w.head * p.G + group - token * p.G) * D) * (F32 ? 4 : 2);
+#pragma unroll
             for (int i = lane; i < ROWS * PIECES; i += 32) {
                 const int r = i / PIECES, x = i % PIECES;
-                const int row = row0 + min(r, rows - 1);
-                const int token = (int)((uint32_t)row / (uint32_t)p.G), hq = row - token * p.G;
-                const uint8_t *src = static_cast<const uint8_t *>(p.q) +
-                                     ((long long)(w.s.cu0 + token) * p.q_stride + ((long long)head * p.G + hq) * D) * (F32 ? 4 : 2);
+                const uint8_t *src = static_cast<const uint8_t *>(p.q) + __shfl_sync(FULL, row, r);
                 copy_async<16>(ptx::smem_u32(queries + (b * ROWS + r) * C::QROW + x * 16), src + x * 16, r < rows ? 16 : 0);
             }
             copy_arrive(q_full + b);
@@ -509,9 +513,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             Walk next = use;
             next_segment<C>(next, p, 0);
             fetch(next, segment + 1);
-            const int head = (int)((uint32_t)use.unit / (uint32_t)use.s.row_groups);
-            const int row0 = (use.unit - head * use.s.row_groups) * ROWS;
-            const int rows = min(ROWS, use.s.n * p.G - row0);
+            const int head = use.head, row0 = use.row0, rows = min(ROWS, use.s.n * p.G - row0);
             const int pos0 = use.s.len - use.s.n;
             const bool whole = use.seg_chunks == use.s.chunks;
             ring_wait(j_full, segment & 1, dead);
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             if (j == 0) {
                 ptx::mbar_arrive(j_empty);
                 if (!whole && use.chunk == 0) {  // the head of a unit that goes on: this CTA's last segment
-                    split_parts = shares.owner(end - use.left + use.s.chunks - 1) - (int)blockIdx.x + 1;
+                    split_parts = shares.owner(shares.begin(blockIdx.x + 1) - use.left + use.s.chunks - 1) - (int)blockIdx.x + 1;
                     parts.split[blockIdx.x] = {split_parts, rows, row0, head, use.s.cu0, pos0, {0, 0}};
                 }
             }
@@ -580,24 +582,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     uint32_t phase = 0;  // bit i: the parity of slot i's next landing
     // A tile's keys (values) are `subs` boxes of box_tokens tokens, each within a page.  Lane i looks up box
     // i % subs of the warp's (i / subs)-th next tile of the segment that copies are at.
-    const int subs = TT / box_tokens, batch = 32 / subs;
+    const int box_tokens = 1 << box_shift, subs = TT >> box_shift, batch = 32 / subs;
     Walk get = use;              // get.tile: the batch's first tile
     int page = 0, in_page = 0;   // where the lane's box is
-    bool wanted = false;         // whether it is read at all
+    uint32_t boxes = 0;          // the lanes with boxes that are
     int taken = 0;               // tiles of the batch that have been copied
     int put = 0, free_slots = S; // the slot that is filled next, and how many may be
     auto look_up = [&]() {
         taken = 0;
-        wanted = false;
+        boxes = 0;
         if (get.left <= 0) return;
-        const int tile = get.tile + lane / subs * W;
-        const int t = get.s.t0 + tile * TT + lane % subs * box_tokens;
-        wanted = tile < get.tile_end && t < get.s.len && t + box_tokens > get.s.first;
+        const int box = lane << box_shift;  // in tokens
+        const int tile = get.tile + box / TT * W;
+        const int t = get.s.t0 + tile * TT + box % TT;
+        const bool wanted = tile < get.tile_end && t < get.s.len && t + box_tokens > get.s.first;
         if (wanted) {
             const int i = p.page_shift >= 0 ? t >> p.page_shift : (int)((uint32_t)t / (uint32_t)p.c.page_size);
             in_page = t - i * p.c.page_size;
             page = p.block_table[get.s.b * p.bt_stride + i];
         }
+        boxes = __ballot_sync(FULL, wanted);
     };
     // Fills free slots in the order of use: the tiles of a segment, then one that is left for the warp's part of
     // it.  A slot that holds a part is free once the joiners are done with that segment; `block` waits for them.
@@ -615,14 +619,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 look_up();
             } else {
                 const int box0 = taken * subs;
-                const int head = (int)((uint32_t)get.unit / (uint32_t)get.s.row_groups);
-                const uint32_t mine = __ballot_sync(FULL, wanted) >> box0 & (subs == 32 ? FULL : (1u << subs) - 1);
+                const int head = get.head;
+                const uint32_t mine = boxes >> box0 & (FULL >> (32 - subs));
                 // 64-byte rows of pages with an odd number of tokens: a tensor copy's destination is a multiple
                 // of 128 bytes, so such rows are copied in 16-byte pieces instead
                 const bool by_rows = C::SPAN == 64 && box_tokens == 1;
                 uint8_t *dst = slots + put * C::SLOT;
                 uint64_t *bar = landed + put;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, by_rows ? 0 : 2 * __popc(mine) * box_tokens * C::RB);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, by_rows ? 0 : __popc(mine) * (2 * C::RB) << box_shift);
                 // (a page outside the pool reads as zeros: it is outside the map)
                 auto box_page = [&](int b) {
                     const int pg = __shfl_sync(FULL, page, box0 + b);
@@ -653,7 +657,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     for (int b = 0; b < subs; ++b) {
                         const int pg = box_page(b), off = __shfl_sync(FULL, in_page, box0 + b);
                         if (lane != 0 || !(mine >> b & 1)) continue;
-                        uint8_t *to = dst + b * box_tokens * C::SPAN;
+                        uint8_t *to = dst + (b << box_shift) * C::SPAN;
 #pragma unroll
                         for (int x = 0; x < C::BOXES; ++x) {
                             ptx::tma_load_5d(to + x * TT * C::SPAN, &k_map, 0, off, x, head, pg, bar);
@@ -663,12 +667,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 }
                 if constexpr (Q8) {
                     // TS == 2: a token a lane; 16 tokens: the upper lanes repeat them for the value scales
-                    const int token = lane & (TT - 1), sub = token / box_tokens;
+                    const int token = lane & (TT - 1), sub = token >> box_shift;
                     const int pg = __shfl_sync(FULL, page, box0 + sub);
-                    const int off = __shfl_sync(FULL, in_page, box0 + sub) + token - sub * box_tokens;
+                    const int off = __shfl_sync(FULL, in_page, box0 + sub) + (token & (box_tokens - 1));
                     const int t = get.s.t0 + tile * TT + token;
                     const bool ok = (mine >> sub & 1) && pg >= 0 && pg < p.c.num_pages && t >= get.s.first && t < get.s.len;
-                    const long long o = ok ? pg * p.c.s_page_stride + off * p.c.s_token_stride + head * p.c.s_head_stride : 0;
+                    const long long o = ok ? (long long)pg * p.s_page_stride32 + (long long)off * p.s_token_stride32 +
+                                                 (long long)head * p.s_head_stride32
+                                           : 0;
                     const uint32_t to = ptx::smem_u32(dst + 2 * C::HALF + 4 * lane);
                     if constexpr (TS == 2) {
                         copy_async<4>(to, p.c.k_scale + o, ok ? 4 : 0);
@@ -688,20 +694,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             --free_slots;
         }
     };
-    auto filled = [&]() {
-        if (free_slots == S) pump(true);
-        ring_wait(landed + at, phase >> at & 1, dead);
-        phase ^= 1u << at;
-    };
-    // Frees the slot at `at`, all of whose readers are behind, and refills.
-    auto release = [&]() {
-        __syncwarp();
-        at = at + 1 == S ? 0 : at + 1;
-        ++free_slots;
-        pump(false);
-    };
     look_up();
-    pump(false);
 
     // Where the lane's pieces are in a slot: key row g (and g + 8), piece c (odd steps: + 4); value rows
     // 2 c, 2 c + 1 (and + 8), its piece g.  Swizzled as the tensor copies leave them.
@@ -710,84 +703,92 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     const int v_at0 = 2 * c * C::SPAN + (HALF_LINE ? ((g >> 1 ^ c) << 4) + (g & 1) * 8 : (g ^ 2 * c) << 4);
     const int v_at1 = (2 * c + 1) * C::SPAN + (HALF_LINE ? ((g >> 1 ^ c) << 4) + (g & 1) * 8 : (g ^ (2 * c + 1)) << 4);
 
-    for (int segment = 0; use.left > 0; ++segment) {
-        const int head = (int)((uint32_t)use.unit / (uint32_t)use.s.row_groups);
-        const int row0 = (use.unit - head * use.s.row_groups) * ROWS;  // first query row of the unit
-        const int rows = min(ROWS, use.s.n * p.G - row0);              // query rows it has
-        const int pos0 = use.s.len - use.s.n;                          // the first query's position
-
-        // queries: lane (g, c) holds, of row 8 nt + g, the channels that its key pieces have
-        uint32_t q[NT][QR];
-        float col_scale[NT][2];  // scores' factor of the lane's two columns
-        ring_wait(q_full + (segment & 1), segment >> 1 & 1, dead);
+    uint32_t q[NT][QR];
+    float col_scale[NT][2];  // scores' factor of the lane's two columns
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+    int rows = 0;                // query rows of the unit
+    int at_pos[NT][2];           // the positions of the queries of the lane's two columns
+    int all_lo = 0, all_hi = 0;  // positions that every query row of the unit sees: [all_lo, all_hi)
+    auto sees = [&](int pos, int t) { return t <= pos && (p.window == 0 || t > pos - p.window); };
+    bool fresh = true;
+    for (int segment = 0; use.left > 0;) {
+        pump(free_slots == S);
+        if (fresh) {  // a new segment
+            fresh = false;
+            rows = min(ROWS, use.s.n * p.G - use.row0);
+            const int pos0 = use.s.len - use.s.n;  // the first query's position
+            auto position = [&](int r) {           // of row r's query (rows past the last repeat it)
+                return use.s.n == 1 ? pos0 : pos0 + (int)((uint32_t)(use.row0 + min(r, rows - 1)) / (uint32_t)p.G);
+            };
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const uint8_t *src = queries + ((segment & 1) * ROWS + nt * 8 + g) * C::QROW;
-            col_scale[nt][0] = col_scale[nt][1] = p.scale_log2;
-            if constexpr (!Q8) {
+            for (int nt = 0; nt < NT; ++nt) {
+                at_pos[nt][0] = position(nt * 8 + 2 * c);
+                at_pos[nt][1] = position(nt * 8 + 2 * c + 1);
+            }
+            all_hi = position(0) + 1;
+            all_lo = p.window > 0 ? max(0, position(rows - 1) - p.window + 1) : 0;
+            // queries: lane (g, c) holds, of row 8 nt + g, the channels that its key pieces have
+            ring_wait(q_full + (segment & 1), segment >> 1 & 1, dead);
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 16);
-                    q[nt][kb * 4] = x.x, q[nt][kb * 4 + 1] = x.y, q[nt][kb * 4 + 2] = x.z, q[nt][kb * 4 + 3] = x.w;
-                }
-            } else {  // 16 channels a piece
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint8_t *src = queries + ((segment & 1) * ROWS + nt * 8 + g) * C::QROW;
+                col_scale[nt][0] = col_scale[nt][1] = p.scale_log2;
+                if constexpr (!Q8) {
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32 + 16);
-                    q[nt][kb * 8] = x.x, q[nt][kb * 8 + 1] = x.y, q[nt][kb * 8 + 2] = x.z, q[nt][kb * 8 + 3] = x.w;
-                    q[nt][kb * 8 + 4] = y.x, q[nt][kb * 8 + 5] = y.y, q[nt][kb * 8 + 6] = y.z, q[nt][kb * 8 + 7] = y.w;
-                }
-                if (p.io_bf16) {
-                    // to FP16, scaled by a power of two so that the row's largest magnitude is in [1, 2)
-                    float top = 0.f;
-#pragma unroll
-                    for (int j = 0; j < QR; ++j) {
-                        const float2 f = unpack2<true>(q[nt][j]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int kb = 0; kb < KB; ++kb) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 16);
+                        q[nt][kb * 4] = x.x, q[nt][kb * 4 + 1] = x.y, q[nt][kb * 4 + 2] = x.z, q[nt][kb * 4 + 3] = x.w;
                     }
-                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-                    // the exponent of top, kept where both powers of two are normal
-                    int e = (int)(__float_as_uint(top) >> 23 & 255) - 127;
-                    e = top > 0.f && top <= 3.402823466e38f ? max(e, -100) : 0;
-                    e = min(e, 126);
-                    const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+                } else {  // 16 channels a piece
 #pragma unroll
-                    for (int j = 0; j < QR; ++j) {
-                        const float2 f = unpack2<true>(q[nt][j]);
-                        q[nt][j] = pack2<false>(f.x * down, f.y * down);
+                    for (int kb = 0; kb < KB; ++kb) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32);
+                        const uint4 y = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32 + 16);
+                        q[nt][kb * 8] = x.x, q[nt][kb * 8 + 1] = x.y, q[nt][kb * 8 + 2] = x.z, q[nt][kb * 8 + 3] = x.w;
+                        q[nt][kb * 8 + 4] = y.x, q[nt][kb * 8 + 5] = y.y, q[nt][kb * 8 + 6] = y.z, q[nt][kb * 8 + 7] = y.w;
                     }
-                    col_scale[nt][0] *= __shfl_sync(FULL, up, 8 * c);
-                    col_scale[nt][1] *= __shfl_sync(FULL, up, 8 * c + 4);
+                    if (p.io_bf16) {
+                        // to FP16, scaled by a power of two so that the row's largest magnitude is in [1, 2)
+                        float top = 0.f;
+#pragma unroll
+                        for (int j = 0; j < QR; ++j) {
+                            const float2 f = unpack2<true>(q[nt][j]);
+                            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+                        // the exponent of top, kept where both powers of two are normal
+                        int e = (int)(__float_as_uint(top) >> 23 & 255) - 127;
+                        e = top > 0.f && top <= 3.402823466e38f ? max(e, -100) : 0;
+                        e = min(e, 126);
+                        const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                        for (int j = 0; j < QR; ++j) {
+                            const float2 f = unpack2<true>(q[nt][j]);
+                            q[nt][j] = pack2<false>(f.x * down, f.y * down);
+                        }
+                        col_scale[nt][0] *= __shfl_sync(FULL, up, 8 * c);
+                        col_scale[nt][1] *= __shfl_sync(FULL, up, 8 * c + 4);
+                    }
                 }
             }
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(q_empty + (segment & 1));
-        // positions that every query row of the unit sees: [all_lo, all_hi)
-        const int all_hi = pos0 + (int)((uint32_t)row0 / (uint32_t)p.G) + 1;
-        const int all_lo = p.window > 0 ? max(0, pos0 + (row0 + rows - 1) / p.G - p.window + 1) : 0;
-        auto seen = [&](int r, int t) {  // whether row r of the unit sees position t
-            const int pos = pos0 + (row0 + min(r, rows - 1)) / p.G;
-            return t <= pos && (p.window == 0 || t > pos - p.window);
-        };
-
-        float o[NT][MT][4], m[NT][2], l[NT][2];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(q_empty + (segment & 1));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = NEG_INF;
-            l[nt][0] = l[nt][1] = 0.f;
+            for (int nt = 0; nt < NT; ++nt) {
+                m[nt][0] = m[nt][1] = NEG_INF;
+                l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+                for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+            }
         }
-
-        for (; use.tile < use.tile_end; use.tile += W) {
+        if (use.tile < use.tile_end) {
             const int tile_t = use.s.t0 + use.tile * TT;
             const bool edge = tile_t < all_lo || tile_t + TT > all_hi;
 
             // ---- scores: S^T = K Q^T
-            filled();
+            ring_wait(landed + at, phase >> at & 1, dead);
+            phase ^= 1u << at;
             float sc[TS][NT][4], sc2[TS][NT][4];
 #pragma unroll
             for (int ts = 0; ts < TS; ++ts)
@@ -863,7 +864,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     for (int e = 0; e < 4; ++e) {
                         float x = (sc[ts][nt][e] + sc2[ts][nt][e]) * col_scale[nt][e & 1];
                         if constexpr (Q8) x *= ksc[ts][e >> 1];
-                        if (edge && !seen(nt * 8 + 2 * c + (e & 1), tile_t + ts * 16 + g + 8 * (e >> 1))) x = NEG_INF;
+                        if (edge && !sees(at_pos[nt][e & 1], tile_t + ts * 16 + g + 8 * (e >> 1))) x = NEG_INF;
                         sc[ts][nt][e] = x;
                         float y = x;
                         if constexpr (Q8) y = x == NEG_INF ? x : x + lv[ts][e >> 1];
@@ -940,7 +941,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             constexpr int VW = C::CHV / 4;  // words of a value piece
             // `only`: -1, or the single query row to add, with values that it does not see left out.  A tile
             // at an end of what is cached holds other tokens' rows too, which count as zeros.
-            auto add_values = [&](int only, auto careful) {
+            auto add_values = [&](int only, int only_pos, auto careful) {
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb)
 #pragma unroll
@@ -951,7 +952,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                             lds<VW>(v[k], vsm + vb * TT * C::SPAN + (ts * 16 + 8 * (k >> 1)) * C::SPAN + ((k & 1) ? v_at1 : v_at0));
                             if constexpr (careful()) {
                                 const int t = tile_t + ts * 16 + 2 * c + (k & 1) + 8 * (k >> 1);
-                                if (t < use.s.first || t >= use.s.len || (only >= 0 && !seen(only, t))) {
+                                if (t < use.s.first || t >= use.s.len || (only >= 0 && !sees(only_pos, t))) {
 #pragma unroll
                                     for (int j = 0; j < VW; ++j) v[k][j] = 0u;
                                 }
@@ -1014,45 +1015,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     }
                     rough = __any_sync(FULL, rough);
                 }
-                for (int r = rough ? 0 : -1; r < (rough ? rows : 0); ++r) add_values(r, Yes());
+                for (int r = rough ? 0 : -1; r < (rough ? rows : 0); ++r)
+                    add_values(r, use.s.len - use.s.n + (use.row0 + max(r, 0)) / p.G, Yes());
             } else {
-                add_values(-1, No());
+                add_values(-1, 0, No());
             }
-            release();
+            __syncwarp();  // all of its readers are behind
+            use.tile += W;
+        } else {
+            // ---- this warp's part of the segment, for the joiners
+            if (segment > 0) ring_wait(j_empty, (segment - 1) & 1, dead);  // the joiners take one segment at a time
+            float *part = reinterpret_cast<float *>(slots + at * C::SLOT);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[nt][e];
+                    x += __shfl_xor_sync(FULL, x, 4);
+                    x += __shfl_xor_sync(FULL, x, 8);
+                    x += __shfl_xor_sync(FULL, x, 16);
+                    const int r = nt * 8 + 2 * c + e;
+                    if (g == 0) reinterpret_cast<float2 *>(part + ROWS * C::OROW)[r] = make_float2(m[nt][e], x);
+                    float *dst = part + r * C::OROW + g * C::CPL;
+#pragma unroll
+                    for (int vb = 0; vb < VB; ++vb)
+#pragma unroll
+                        for (int i = 0; i < MPV; i += 2) {
+                            const float(&a)[4] = o[nt][vb * MPV + i], (&b)[4] = o[nt][vb * MPV + i + 1];
+                            *reinterpret_cast<float4 *>(dst + vb * 8 * C::CPL + 2 * i) = make_float4(a[e], a[e + 2], b[e], b[e + 2]);
+                        }
+                }
+            if (lane == 0) part_slot[warp] = at;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(j_full);
+            part_at = at;
+            part_segment = segment++;
+            next_segment<C>(use, p, warp);
+            fresh = true;
         }
-
-        // ---- this warp's part of the segment, for the joiners
-        if (free_slots == S) pump(true);
-        if (segment > 0) ring_wait(j_empty, (segment - 1) & 1, dead);  // the joiners take one segment at a time
-        float *part = reinterpret_cast<float *>(slots + at * C::SLOT);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = l[nt][e];
-                x += __shfl_xor_sync(FULL, x, 4);
-                x += __shfl_xor_sync(FULL, x, 8);
-                x += __shfl_xor_sync(FULL, x, 16);
-                const int r = nt * 8 + 2 * c + e;
-                if (g == 0) reinterpret_cast<float2 *>(part + ROWS * C::OROW)[r] = make_float2(m[nt][e], x);
-                float *dst = part + r * C::OROW + g * C::CPL;
-#pragma unroll
-                for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                    for (int i = 0; i < MPV; i += 2) {
-                        const float(&a)[4] = o[nt][vb * MPV + i], (&b)[4] = o[nt][vb * MPV + i + 1];
-                        *reinterpret_cast<float4 *>(dst + vb * 8 * C::CPL + 2 * i) = make_float4(a[e], a[e + 2], b[e], b[e + 2]);
-                    }
-            }
-        if (lane == 0) part_slot[warp] = at;
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(j_full);
-        part_at = at;
-        part_segment = segment;
         at = at + 1 == S ? 0 : at + 1;
         ++free_slots;
-        next_segment<C>(use, p, warp);
-        pump(false);
     }
 }
 
@@ -1130,8 +1132,8 @@ cudaError_t launch_sized(const PagedAttnParams &p, cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     // the largest power of two of tokens, up to a tile, that never crosses a page
-    int box_tokens = C::TT;
-    while (p.c.page_size % box_tokens) box_tokens >>= 1;
+    int box_tokens = C::TT, box_shift = C::TS == 2 ? 5 : 4;
+    while (p.c.page_size % box_tokens) box_tokens >>= 1, --box_shift;
     const int spans = box_tokens == C::TT ? C::BOXES : 1;  // whole tiles land in one copy
     CUtensorMap k_map, v_map;
     if (!encode_cache_rows(&k_map, p.c.k, C::ESZ, D, p.c.H, p.c.page_size, p.c.num_pages, p.c.head_stride, p.c.token_stride,
@@ -1141,7 +1143,7 @@ cudaError_t launch_sized(const PagedAttnParams &p, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const unsigned ctas = (unsigned)attention_ctas();
     const cudaError_t e2 =
-        launch_dependent(kernel, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, p, k_map, v_map, box_tokens);
+        launch_dependent(kernel, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, p, k_map, v_map, box_shift);
     // a unit of one chunk is never split
     if (e2 != cudaSuccess || (long long)p.pages_per_seq * p.c.page_size <= C::W * C::TT) return e2;
     return launch_dependent(join_kernel<CT, C>, dim3(ctas, C::ROWS), dim3(JOIN_THREADS), 0, stream, p);

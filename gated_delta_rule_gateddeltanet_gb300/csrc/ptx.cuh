@@ -113,6 +113,11 @@ __device__ __forceinline__ void tma_load_5d(void *dst_smem, const void *tensor_m
         : "memory");
 }
 
+// Fetches a tensor map (a __grid_constant__ kernel parameter) ahead of its first use.
+__device__ __forceinline__ void prefetch_tensor_map(const void *tensor_map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tensor_map) : "memory");
+}
+
 // Shared -> global 2-D tensor store of one box from a tensor map, tracked by
 // the issuing thread's bulk async-groups (coordinates must not be negative).
 __device__ __forceinline__ void tma_store_2d(const void *tensor_map, const void *src_smem, int x, int y) {
