@@ -97,7 +97,7 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p, cudaStream_t stream
 
 // Groups of 8 query rows that a kernel's registers hold (queries and outputs of
 // every row: NT * D * 3/4 registers, FP32 NT * D).
-constexpr int max_row_tiles(bool f32, int d) { return d == 64 ? 4 : d == 128 ? (f32 ? 2 : 4) : (f32 ? 1 : 2); }
+constexpr int max_row_tiles(bool f32, int d) { return d == 64 ? 4 : d == 128 ? (f32 ? 1 : 2) : (f32 ? 1 : 2); }
 inline int row_tiles(bool f32, int d, int rows) {
     const int most = max_row_tiles(f32, d);
     return rows <= 8 || most == 1 ? 1 : rows <= 16 || most == 2 ? 2 : 4;

@@ -193,6 +193,24 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
 
 // ---------------------------------------------------------------- configuration
 
+// One sequence as the kernel sees it.
+struct Seq {
+    int b, len, n, cu0;
+    int first;  // first cache position any query sees
+    int t0;     // `first` rounded down to a tile
+    int tiles, chunks, row_groups, units;
+};
+
+// A walk over a CTA's chunks, one segment (part of one unit) at a time.
+struct Walk {
+    Seq s;
+    int unit, chunk;     // the current segment's unit and first chunk
+    int head, row0;      // the unit's key head and first query row
+    int seg_chunks;
+    int left;            // chunks of this CTA not yet behind the walk, this segment's included
+    int tile, tile_end;  // the warp's next tile and the segment's end
+};
+
 constexpr int SMEM_LIMIT = 232448;
 
 template <int CT, int D_, int NT_>
@@ -221,7 +239,7 @@ struct Cfg {
     static constexpr int SLOT = ((TILE > PART ? TILE : PART) + 1023) / 1024 * 1024;
     static constexpr int QROW = D * (F32 ? 4 : 2) + 16;  // bytes a staged query row
     static constexpr int QUERIES = 2 * ROWS * QROW;
-    static constexpr int HEAD = 2048;                    // scan, flags and barriers
+    static constexpr int HEAD = 3072;                    // scan, flags, barriers and walks
     // Warps: W consumers and NJ joiners; 12 have 168 registers a thread, 8
     // (where queries and outputs alone take 64 or more) have 255.
     static constexpr int HELD = NT * (D / 4 + QR);
@@ -232,17 +250,12 @@ struct Cfg {
     static constexpr int THREADS = 32 * (W + NJ);
     static constexpr int S = ROOM / W < 8 ? ROOM / W : 8;  // ring slots a consumer
     static constexpr int SMEM = 1024 + HEAD + QUERIES + FACTORS + W * S * SLOT;  // (1024: the ring's alignment)
+    // Weights of 8-bit values are single FP16 numbers: next to values of 8 bits, 11 are plenty, and the
+    // second product would cost what these kernels are bound by.
+    static constexpr bool SPLIT_P = !Q8;
     static constexpr float BIAS = CT == GDN_F16 || Q8 ? 6.f : -8.f;  // weights are 2^(s - m + BIAS)
     static constexpr float HEADROOM = 8.f;  // a score may exceed the maximum by this: FP16 weights stay below 2^14
-    static_assert(S >= 2 && 512 + W * S * 8 + 64 <= HEAD && HALF % 1024 == 0, "ring and barriers");
-};
-
-// One sequence as the kernel sees it.
-struct Seq {
-    int b, len, n, cu0;
-    int first;  // first cache position any query sees
-    int t0;     // `first` rounded down to a tile
-    int tiles, chunks, row_groups, units;
+    static_assert(S >= 2 && 512 + W * S * 8 + 64 <= 1280 && 1280 + 2 * W * (int)sizeof(Walk) <= HEAD && HALF % 1024 == 0, "ring and barriers");
 };
 
 template <class C>
@@ -266,16 +279,6 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams &p, int b, bool fl
     s.units = p.c.H * s.row_groups;
     return s;
 }
-
-// A walk over a CTA's chunks, one segment (part of one unit) at a time.
-struct Walk {
-    Seq s;
-    int unit, chunk;     // the current segment's unit and first chunk
-    int head, row0;      // the unit's key head and first query row
-    int seg_chunks;
-    int left;            // chunks of this CTA not yet behind the walk, this segment's included
-    int tile, tile_end;  // the warp's next tile and the segment's end
-};
 
 template <class C>
 __device__ __forceinline__ void open_segment(Walk &w, int first) {
@@ -326,7 +329,7 @@ constexpr long long WAIT_LIMIT = 4000000000LL;
 __device__ __forceinline__ void ring_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
     if (ptx::mbar_try_wait(bar, parity)) return;
     const long long t0 = clock64();
-    while (!ptx::mbar_try_wait(bar, parity)) {
+    while (!ptx::mbar_try_wait_for(bar, parity, 20000)) {
         if (*dead) return;
         if (clock64() - t0 > WAIT_LIMIT) *dead = 1;
     }
@@ -387,7 +390,8 @@ struct Parts {
 
 // ---------------------------------------------------------------- the kernel
 
-template <int CT, class C>
+// BY_ROWS: pages are not a multiple of 8 tokens, rows are copied one by one (see launch_sized).
+template <int CT, class C, bool BY_ROWS>
 __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedAttnParams p,
                                                                         const __grid_constant__ CUtensorMap k_map,
                                                                         const __grid_constant__ CUtensorMap v_map, int box_shift) {
@@ -405,6 +409,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + 512);           // [W][S] a slot's tile has landed
     uint64_t *q_full = full + W * S, *q_empty = q_full + 2;              // [2] a segment's queries
     uint64_t *j_full = q_empty + 2, *j_empty = j_full + 1;               // the consumers' parts of a segment
+    Walk *walks = reinterpret_cast<Walk *>(smem + 1280);                 // [W][2] where a consumer's products and copies are
     uint8_t *queries = smem + C::HEAD;                                   // [2][ROWS][QROW]
     float2 *joined = reinterpret_cast<float2 *>(queries + C::QUERIES);   // [ROWS] maxima and sums
     float *factor = reinterpret_cast<float *>(joined + ROWS);            // [W][ROWS]
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     ring += (1024 - (ptx::smem_u32(ring) & 1023)) & 1023;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    if (tid < W * S) ptx::mbar_init(full + tid, Q8 ? 33 : 1);  // the tensor copies, and each lane's copies of scales
+    if (tid < W * S) ptx::mbar_init(full + tid, Q8 || BY_ROWS ? 33 : 1);  // tensor copies, and each lane's other copies
     if (tid < 2) {
         ptx::mbar_init(q_full + tid, 32);
         ptx::mbar_init(q_empty + tid, W);
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         ptx::mbar_init(j_empty, 1);
         *dead = 0;
     }
-    if (tid == 32) {
+    if (!BY_ROWS && tid == 32) {
         ptx::prefetch_tensor_map(&k_map);
         ptx::prefetch_tensor_map(&v_map);
     }
@@ -575,123 +580,141 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     }
 
     // ---- consumers: warp w multiplies tiles w, w + W, ... of each segment
+    // Both walks are in shared memory, changed by lane 0; what every tile needs of them is in registers.
+    Walk &at_use = walks[2 * warp], &at_get = walks[2 * warp + 1];
     open_segment<C>(use, warp);
+    if (lane == 0) at_use = at_get = use;
+    __syncwarp();
+    int use_left = use.left, use_tile = use.tile, use_end = use.tile_end, use_t0 = use.s.t0;
+    int get_left = use.left, get_tile = use.tile, get_end = use.tile_end, get_head = use.head;
     uint8_t *slots = ring + warp * (S * C::SLOT);  // this warp's
     uint64_t *landed = full + warp * S;
     int at = 0;          // the slot that is used next
     uint32_t phase = 0;  // bit i: the parity of slot i's next landing
     // A tile's keys (values) are `subs` boxes of box_tokens tokens, each within a page.  Lane i looks up box
-    // i % subs of the warp's (i / subs)-th next tile of the segment that copies are at.
+    // i % subs of the warp's (i / subs)-th next tile of the segment that copies are at, as soon as the last
+    // tile before has been copied, so that the table's latency passes behind the products.
     const int box_tokens = 1 << box_shift, subs = TT >> box_shift, batch = 32 / subs;
-    Walk get = use;              // get.tile: the batch's first tile
     int page = 0, in_page = 0;   // where the lane's box is
     uint32_t boxes = 0;          // the lanes with boxes that are
     int taken = 0;               // tiles of the batch that have been copied
+    bool owed = false;           // the slot for the part of the segment before comes first
     int put = 0, free_slots = S; // the slot that is filled next, and how many may be
     auto look_up = [&]() {
         taken = 0;
         boxes = 0;
-        if (get.left <= 0) return;
+        if (get_left <= 0) return;
         const int box = lane << box_shift;  // in tokens
-        const int tile = get.tile + box / TT * W;
-        const int t = get.s.t0 + tile * TT + box % TT;
-        const bool wanted = tile < get.tile_end && t < get.s.len && t + box_tokens > get.s.first;
+        const int tile = get_tile + box / TT * W;
+        const int t = at_get.s.t0 + tile * TT + box % TT;
+        const bool wanted = tile < get_end && t < at_get.s.len && t + box_tokens > at_get.s.first;
         if (wanted) {
             const int i = p.page_shift >= 0 ? t >> p.page_shift : (int)((uint32_t)t / (uint32_t)p.c.page_size);
             in_page = t - i * p.c.page_size;
-            page = p.block_table[get.s.b * p.bt_stride + i];
+            page = p.block_table[at_get.s.b * p.bt_stride + i];
         }
         boxes = __ballot_sync(FULL, wanted);
+    };
+    // To the next segment once the warp's tiles of the current one are copied.
+    auto advance = [&]() {
+        if (get_tile + taken * W < get_end) {
+            if (taken == batch) {
+                get_tile += batch * W;
+                look_up();
+            }
+            return;
+        }
+        owed = true;
+        __syncwarp();
+        if (lane == 0) next_segment<C>(at_get, p, warp);
+        __syncwarp();
+        get_left = at_get.left, get_tile = at_get.tile, get_end = at_get.tile_end, get_head = at_get.head;
+        look_up();
     };
     // Fills free slots in the order of use: the tiles of a segment, then one that is left for the warp's part of
     // it.  A slot that holds a part is free once the joiners are done with that segment; `block` waits for them.
     int part_at = -1, part_segment = 0;  // the last part's slot, until it is known to be free
     auto pump = [&](bool block) {
-        while (free_slots > 0 && get.left > 0) {
+        while (free_slots > 0 && (owed || get_left > 0)) {
             if (put == part_at) {
                 if (block) ring_wait(j_empty, part_segment & 1, dead);
                 else if (!__all_sync(FULL, ptx::mbar_test_wait(j_empty, part_segment & 1))) return;
                 part_at = -1;
             }
-            const int tile = get.tile + taken * W;
-            if (tile >= get.tile_end) {
-                next_segment<C>(get, p, warp);
-                look_up();
-            } else {
-                const int box0 = taken * subs;
-                const int head = get.head;
+            const bool is_part = owed, is_tile = !owed && get_tile + taken * W < get_end;
+            owed = false;
+            if (is_tile) {
+                const int box0 = taken * subs, head = get_head;
                 const uint32_t mine = boxes >> box0 & (FULL >> (32 - subs));
-                // 64-byte rows of pages with an odd number of tokens: a tensor copy's destination is a multiple
-                // of 128 bytes, so such rows are copied in 16-byte pieces instead
-                const bool by_rows = C::SPAN == 64 && box_tokens == 1;
                 uint8_t *dst = slots + put * C::SLOT;
                 uint64_t *bar = landed + put;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, by_rows ? 0 : __popc(mine) * (2 * C::RB) << box_shift);
-                // (a page outside the pool reads as zeros: it is outside the map)
-                auto box_page = [&](int b) {
-                    const int pg = __shfl_sync(FULL, page, box0 + b);
-                    const bool bad = (mine >> b & 1) && (pg < 0 || pg >= p.c.num_pages);
-                    if (bad && lane == 0) flag_error(p.status, GDN_DEVERR_PAGE);
-                    return bad ? p.c.num_pages : pg;
-                };
-                if (C::SPAN == 64 && by_rows) {
-#pragma unroll 1
-                    for (int k = lane; k < TT * 8; k += 32) {
-                        const int half = k >= TT * 4, token = k >> 2 & (TT - 1), x = k & 3;
-                        const int pg = __shfl_sync(FULL, page, box0 + token), off = __shfl_sync(FULL, in_page, box0 + token);
-                        const bool ok = (mine >> token & 1) && pg >= 0 && pg < p.c.num_pages;
-                        if ((mine >> token & 1) && !ok) flag_error(p.status, GDN_DEVERR_PAGE);
-                        const uint8_t *src = static_cast<const uint8_t *>(half ? p.c.v : p.c.k);
-                        if (ok) src += (pg * p.c.page_stride + off * p.c.token_stride + head * p.c.head_stride) * C::ESZ + x * 16;
-                        copy_async<16>(ptx::smem_u32(dst + half * C::HALF + token * 64 + ((x ^ (token >> 1 & 3)) << 4)), src,
-                                       ok ? 16 : 0);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, BY_ROWS ? 0 : __popc(mine) * (2 * C::RB) << box_shift);
+                if constexpr (BY_ROWS) {
+                    // lane box0 + i looked up token i: its row's byte offset, -1 if it is not read
+                    long long row = -1;
+                    if (boxes >> lane & 1) {
+                        if (page >= 0 && page < p.c.num_pages)
+                            row = (page * p.c.page_stride + in_page * p.c.token_stride + head * p.c.head_stride) * C::ESZ;
+                        else
+                            flag_error(p.status, GDN_DEVERR_PAGE);
                     }
-                } else if (subs == 1) {  // all spans at once
-                    const int pg = box_page(0), off = __shfl_sync(FULL, in_page, box0);
-                    if (lane == 0) {
-                        ptx::tma_load_5d(dst, &k_map, 0, off, 0, head, pg, bar);
-                        ptx::tma_load_5d(dst + C::HALF, &v_map, 0, off, 0, head, pg, bar);
+                    constexpr int PIECES = C::RB / 16, PER_SPAN = C::SPAN / 16;
+                    const uint32_t to = ptx::smem_u32(dst);
+#pragma unroll 4
+                    for (int k = lane; k < TT * PIECES; k += 32) {
+                        const int token = k / PIECES, x = k % PIECES, y = x % PER_SPAN;
+                        const long long o = __shfl_sync(FULL, row, box0 + token);
+                        const uint32_t at = to + (x / PER_SPAN) * TT * C::SPAN + token * C::SPAN +
+                                            ((y ^ (C::SPAN == 64 ? token >> 1 & 3 : token & 7)) << 4);
+                        const long long src = o < 0 ? 0 : o + x * 16;
+                        copy_async<16>(at, static_cast<const uint8_t *>(p.c.k) + src, o < 0 ? 0 : 16);
+                        copy_async<16>(at + C::HALF, static_cast<const uint8_t *>(p.c.v) + src, o < 0 ? 0 : 16);
                     }
                 } else {
 #pragma unroll 1
                     for (int b = 0; b < subs; ++b) {
-                        const int pg = box_page(b), off = __shfl_sync(FULL, in_page, box0 + b);
+                        int pg = __shfl_sync(FULL, page, box0 + b);
+                        const int off = __shfl_sync(FULL, in_page, box0 + b);
                         if (lane != 0 || !(mine >> b & 1)) continue;
+                        if (pg < 0 || pg >= p.c.num_pages) {
+                            flag_error(p.status, GDN_DEVERR_PAGE);
+                            pg = p.c.num_pages;  // outside the map: reads as zeros
+                        }
                         uint8_t *to = dst + (b << box_shift) * C::SPAN;
-#pragma unroll
-                        for (int x = 0; x < C::BOXES; ++x) {
-                            ptx::tma_load_5d(to + x * TT * C::SPAN, &k_map, 0, off, x, head, pg, bar);
-                            ptx::tma_load_5d(to + C::HALF + x * TT * C::SPAN, &v_map, 0, off, x, head, pg, bar);
+                        if (subs == 1) {  // all spans at once
+                            ptx::tma_load_5d(to, &k_map, 0, off, 0, head, pg, bar);
+                            ptx::tma_load_5d(to + C::HALF, &v_map, 0, off, 0, head, pg, bar);
+                        } else {
+#pragma unroll 1
+                            for (int x = 0; x < C::BOXES; ++x) {
+                                ptx::tma_load_5d(to + x * TT * C::SPAN, &k_map, 0, off, x, head, pg, bar);
+                                ptx::tma_load_5d(to + C::HALF + x * TT * C::SPAN, &v_map, 0, off, x, head, pg, bar);
+                            }
                         }
                     }
                 }
                 if constexpr (Q8) {
-                    // TS == 2: a token a lane; 16 tokens: the upper lanes repeat them for the value scales
+                    // TS == 2: a token a lane; 16 tokens: the upper lanes fetch the value scales.  (Those of tokens
+                    // past the end are of the same page, and masked like their scores.)
                     const int token = lane & (TT - 1), sub = token >> box_shift;
                     const int pg = __shfl_sync(FULL, page, box0 + sub);
                     const int off = __shfl_sync(FULL, in_page, box0 + sub) + (token & (box_tokens - 1));
-                    const int t = get.s.t0 + tile * TT + token;
-                    const bool ok = (mine >> sub & 1) && pg >= 0 && pg < p.c.num_pages && t >= get.s.first && t < get.s.len;
-                    const long long o = ok ? (long long)pg * p.s_page_stride32 + (long long)off * p.s_token_stride32 +
-                                                 (long long)head * p.s_head_stride32
-                                           : 0;
+                    const int ok = (mine >> sub & 1) && pg >= 0 && pg < p.c.num_pages ? 4 : 0;
+                    const long long at = ok ? (long long)pg * p.s_page_stride32 + (long long)off * p.s_token_stride32 +
+                                                  (long long)head * p.s_head_stride32
+                                            : 0;
                     const uint32_t to = ptx::smem_u32(dst + 2 * C::HALF + 4 * lane);
-                    if constexpr (TS == 2) {
-                        copy_async<4>(to, p.c.k_scale + o, ok ? 4 : 0);
-                        copy_async<4>(to + 4 * TT, p.c.v_scale + o, ok ? 4 : 0);
-                    } else {
-                        copy_async<4>(to, (lane < 16 ? p.c.k_scale : p.c.v_scale) + o, ok ? 4 : 0);
-                    }
-                    copy_arrive(bar);
+                    copy_async<4>(to, (TS == 2 || lane < 16 ? p.c.k_scale : p.c.v_scale) + at, ok);
+                    if (TS == 2) copy_async<4>(to + 4 * TT, p.c.v_scale + at, ok);
                 }
-                if (++taken == batch) {
-                    get.tile += batch * W;
-                    look_up();
-                }
+                if (Q8 || BY_ROWS) copy_arrive(bar);
+                ++taken;
             }
-            // (a slot for the part of a segment is taken like one for a tile)
-            put = put + 1 == S ? 0 : put + 1;
-            --free_slots;
+            if (get_left > 0) advance();
+            if (is_tile || is_part) {
+                put = put + 1 == S ? 0 : put + 1;
+                --free_slots;
+            }
         }
     };
     look_up();
@@ -711,14 +734,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     int all_lo = 0, all_hi = 0;  // positions that every query row of the unit sees: [all_lo, all_hi)
     auto sees = [&](int pos, int t) { return t <= pos && (p.window == 0 || t > pos - p.window); };
     bool fresh = true;
-    for (int segment = 0; use.left > 0;) {
+    for (int segment = 0; use_left > 0;) {
         pump(free_slots == S);
         if (fresh) {  // a new segment
             fresh = false;
-            rows = min(ROWS, use.s.n * p.G - use.row0);
-            const int pos0 = use.s.len - use.s.n;  // the first query's position
+            rows = min(ROWS, at_use.s.n * p.G - at_use.row0);
+            const int pos0 = at_use.s.len - at_use.s.n;  // the first query's position
             auto position = [&](int r) {           // of row r's query (rows past the last repeat it)
-                return use.s.n == 1 ? pos0 : pos0 + (int)((uint32_t)(use.row0 + min(r, rows - 1)) / (uint32_t)p.G);
+                return at_use.s.n == 1 ? pos0 : pos0 + (int)((uint32_t)(at_use.row0 + min(r, rows - 1)) / (uint32_t)p.G);
             };
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -782,8 +805,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
             }
         }
-        if (use.tile < use.tile_end) {
-            const int tile_t = use.s.t0 + use.tile * TT;
+        if (use_tile < use_end) {
+            const int tile_t = use_t0 + use_tile * TT;
             const bool edge = tile_t < all_lo || tile_t + TT > all_hi;
 
             // ---- scores: S^T = K Q^T
@@ -928,10 +951,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const uint32_t hi = pack2<BF16>(w[2 * k], w[2 * k + 1]);
-                            const float2 back = unpack2<BF16>(hi);
-                            const uint32_t lo = pack2<BF16>(w[2 * k] - back.x, w[2 * k + 1] - back.y);
                             ph[ts][nt][k] = transpose8x8(hi);
-                            pl[ts][nt][k] = transpose8x8(lo);
+                            if constexpr (C::SPLIT_P) {
+                                const float2 back = unpack2<BF16>(hi);
+                                pl[ts][nt][k] = transpose8x8(pack2<BF16>(w[2 * k] - back.x, w[2 * k + 1] - back.y));
+                            }
                         }
                     }
                 }
@@ -939,8 +963,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             // ---- O^T += V^T P^T
             const uint8_t *vsm = slots + at * C::SLOT + C::HALF;
             constexpr int VW = C::CHV / 4;  // words of a value piece
-            // `only`: -1, or the single query row to add, with values that it does not see left out.  A tile
-            // at an end of what is cached holds other tokens' rows too, which count as zeros.
+            // `only` (careful): the single query row to add, with values that it does not see left out
             auto add_values = [&](int only, int only_pos, auto careful) {
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb)
@@ -952,13 +975,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                             lds<VW>(v[k], vsm + vb * TT * C::SPAN + (ts * 16 + 8 * (k >> 1)) * C::SPAN + ((k & 1) ? v_at1 : v_at0));
                             if constexpr (careful()) {
                                 const int t = tile_t + ts * 16 + 2 * c + (k & 1) + 8 * (k >> 1);
-                                if (t < use.s.first || t >= use.s.len || (only >= 0 && !sees(only_pos, t))) {
+                                if (!sees(only_pos, t)) {
 #pragma unroll
                                     for (int j = 0; j < VW; ++j) v[k][j] = 0u;
                                 }
                             }
                         }
-                        auto mine = [&](uint32_t x, int nt) { return only < 0 || only == nt * 8 + g ? x : 0u; };
+                        auto mine = [&](uint32_t x, int nt) { return !careful() || only == nt * 8 + g ? x : 0u; };
                         if constexpr (F32) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
@@ -996,32 +1019,43 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                             for (int j = 0; j < MPV; ++j)
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-                                    mma16<BF16>(o[nt][vb * MPV + j], a[j][0], a[j][1], a[j][2], a[j][3],
-                                                mine(pl[ts][nt][0], nt), mine(pl[ts][nt][1], nt));
+                                    if constexpr (C::SPLIT_P)
+                                        mma16<BF16>(o[nt][vb * MPV + j], a[j][0], a[j][1], a[j][2], a[j][3],
+                                                    mine(pl[ts][nt][0], nt), mine(pl[ts][nt][1], nt));
                                     mma16<BF16>(o[nt][vb * MPV + j], a[j][0], a[j][1], a[j][2], a[j][3],
                                                 mine(ph[ts][nt][0], nt), mine(ph[ts][nt][1], nt));
                                 }
                         }
                     }
             };
-            // A value that some rows of the tile see and others do not would reach the others as
-            // 0 * inf if it is not finite: such a tile is added row by row.
-            if (edge) {
-                bool rough = false;
-                if (CT != GDN_INT8 && use.s.n > 1) {
-                    for (int i = lane * 4; i < C::HALF; i += 128) {  // (any order: rows of the tile, SPAN bytes each)
-                        const int t = tile_t + i / C::SPAN % TT;
-                        rough |= t >= use.s.first && t < use.s.len && non_finite<CT>(*reinterpret_cast<const uint32_t *>(vsm + i));
-                    }
-                    rough = __any_sync(FULL, rough);
+            // A tile at an end of what is cached holds other rows too (of other tokens, or never written): their
+            // values are zeroed.  A value that some query rows see and others do not would reach the others as 0 *
+            // inf if it is not finite: such a tile is added row by row.
+            bool rough = false;
+            if (__builtin_expect(edge, 0)) {
+                const int first = at_use.s.first, len = at_use.s.len;
+                const bool several = CT != GDN_INT8 && at_use.s.n > 1;
+#pragma unroll 1
+                for (int i = lane * 16; i < C::HALF; i += 512) {  // [BOXES][TT][SPAN] bytes
+                    const int t = tile_t + i / C::SPAN % TT;
+                    uint4 *x = reinterpret_cast<uint4 *>(slots + at * C::SLOT + C::HALF + i);
+                    if (t < first || t >= len)
+                        *x = make_uint4(0, 0, 0, 0);
+                    else if (several)
+                        rough |= non_finite<CT>(x->x) || non_finite<CT>(x->y) || non_finite<CT>(x->z) || non_finite<CT>(x->w);
                 }
-                for (int r = rough ? 0 : -1; r < (rough ? rows : 0); ++r)
-                    add_values(r, use.s.len - use.s.n + (use.row0 + max(r, 0)) / p.G, Yes());
+                ptx::fence_proxy_async_smem();  // (a later tensor copy overwrites the zeros)
+                rough = __any_sync(FULL, rough);
+                __syncwarp();
+            }
+            if (__builtin_expect(rough, 0)) {
+#pragma unroll 1
+                for (int r = 0; r < rows; ++r) add_values(r, at_use.s.len - at_use.s.n + (at_use.row0 + r) / p.G, Yes());
             } else {
-                add_values(-1, 0, No());
+                add_values(0, 0, No());
             }
             __syncwarp();  // all of its readers are behind
-            use.tile += W;
+            use_tile += W;
         } else {
             // ---- this warp's part of the segment, for the joiners
             if (segment > 0) ring_wait(j_empty, (segment - 1) & 1, dead);  // the joiners take one segment at a time
@@ -1050,7 +1084,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             if (lane == 0) ptx::mbar_arrive(j_full);
             part_at = at;
             part_segment = segment++;
-            next_segment<C>(use, p, warp);
+            if (lane == 0) next_segment<C>(at_use, p, warp);
+            __syncwarp();
+            use_left = at_use.left, use_tile = at_use.tile, use_end = at_use.tile_end, use_t0 = at_use.s.t0;
             fresh = true;
         }
         at = at + 1 == S ? 0 : at + 1;
@@ -1128,18 +1164,23 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
 template <int CT, int D, int NT>
 cudaError_t launch_sized(const PagedAttnParams &p, cudaStream_t stream) {
     using C = Cfg<CT, D, NT>;
-    auto kernel = paged_attention_kernel<CT, C>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    // the largest power of two of tokens, up to a tile, that never crosses a page
+    // Tensor copies of the largest power of two of tokens, up to a tile, that never crosses a page; below 8
+    // tokens they are so many (a lane issues them one by one) that 16-byte copies of single rows by all lanes
+    // are faster: pages of 7 tokens, 8 x 4099 x 8 heads of 64, FP32, 28 us against 56 us.
     int box_tokens = C::TT, box_shift = C::TS == 2 ? 5 : 4;
     while (p.c.page_size % box_tokens) box_tokens >>= 1, --box_shift;
+    const bool by_rows = box_tokens < 8;
+    if (by_rows) box_tokens = 1, box_shift = 0;
+    auto kernel = by_rows ? paged_attention_kernel<CT, C, true> : paged_attention_kernel<CT, C, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
     const int spans = box_tokens == C::TT ? C::BOXES : 1;  // whole tiles land in one copy
-    CUtensorMap k_map, v_map;
-    if (!encode_cache_rows(&k_map, p.c.k, C::ESZ, D, p.c.H, p.c.page_size, p.c.num_pages, p.c.head_stride, p.c.token_stride,
-                           p.c.page_stride, box_tokens, spans) ||
-        !encode_cache_rows(&v_map, p.c.v, C::ESZ, D, p.c.H, p.c.page_size, p.c.num_pages, p.c.head_stride, p.c.token_stride,
-                           p.c.page_stride, box_tokens, spans))
+    CUtensorMap k_map{}, v_map{};
+    if (!by_rows &&
+        (!encode_cache_rows(&k_map, p.c.k, C::ESZ, D, p.c.H, p.c.page_size, p.c.num_pages, p.c.head_stride, p.c.token_stride,
+                            p.c.page_stride, box_tokens, spans) ||
+         !encode_cache_rows(&v_map, p.c.v, C::ESZ, D, p.c.H, p.c.page_size, p.c.num_pages, p.c.head_stride, p.c.token_stride,
+                            p.c.page_stride, box_tokens, spans)))
         return cudaErrorInvalidValue;
     const unsigned ctas = (unsigned)attention_ctas();
     const cudaError_t e2 =
