@@ -121,12 +121,14 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// x = hi + lo with hi a TF32 number (10 fraction bits kept).  A non-finite x stays in hi alone.
+// x = hi + lo with hi rounded to TF32 (to nearest in magnitude, so that lo and
+// the dropped lo lo products have no sign in common; in integers: the convert
+// instruction ran 64 x 4096 x 128 FP32 at half the rate).  The tensor cores drop lo's bits
+// past TF32, which leaves 21 bits.  A non-finite x stays in hi alone.
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
-    hi = x & 0xffffe000u;
+    hi = (x + 0x1000u) & 0xffffe000u;
     const float l = __uint_as_float(x) - __uint_as_float(hi);
-    lo = (x & 0x7f800000u) == 0x7f800000u ? 0u : __float_as_uint(l);
-    if ((x & 0x7f800000u) == 0x7f800000u) hi = x;
+    lo = l == l ? __float_as_uint(l) : 0u;
 }
 // D += A B for FP32 operands
 __device__ __forceinline__ void mma_f32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&bh)[2],
@@ -173,6 +175,19 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t &p01, uint32_t &p23) 
         const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), bias);
         p01 = *reinterpret_cast<const uint32_t *>(&x);
         p23 = *reinterpret_cast<const uint32_t *>(&y);
+    }
+}
+
+// The same for keys, where int8 may stay biased: pairs of 1152 + x, to which
+// the scores' bias of -1152 sum(q) belongs.
+template <int CT>
+__device__ __forceinline__ void widen_keys(uint32_t w, uint32_t &p01, uint32_t &p23) {
+    if constexpr (CT == GDN_INT8) {
+        const uint32_t u = w ^ 0x80808080u;
+        p01 = __byte_perm(u, 0x64646464u, 0x4140);
+        p23 = __byte_perm(u, 0x64646464u, 0x4342);
+    } else {
+        widen<CT>(w, p01, p23);
     }
 }
 
@@ -231,21 +246,21 @@ struct Cfg {
     static constexpr int HALF = TT * RB;                // a tile's keys; its values
     static constexpr int SPAN = RB < 128 ? RB : 128;    // row bytes a tensor copy takes
     static constexpr int BOXES = RB / SPAN;             // spans a row; each half is [BOXES][TT][SPAN]
-    static constexpr int QR = F32 ? D / 4 : D / 8;      // query registers per 8 rows
     // A ring slot holds a tile (keys, values, scales of 8-bit rows) or a
     // consumer's part of a finished segment (rows and their statistics).
     static constexpr int OROW = D + 4;                  // floats a row of a part
     static constexpr int TILE = 2 * HALF + (Q8 ? TT * 8 : 0), PART = ROWS * (OROW + 2) * 4;
     static constexpr int SLOT = ((TILE > PART ? TILE : PART) + 1023) / 1024 * 1024;
-    static constexpr int QROW = D * (F32 ? 4 : 2) + 16;  // bytes a staged query row
-    static constexpr int QUERIES = 2 * ROWS * QROW;
+    // Bytes a staged query row; the padding keeps the lanes' reads of 8 rows free of bank conflicts.
+    static constexpr int QROW = D * (F32 ? 4 : 2) + (Q8 ? 16 : 64);
+    static constexpr int QUERIES = 2 * ROWS * (QROW + 8);  // and each row's (scale, bias)
     static constexpr int HEAD = 3072;                    // scan, flags, barriers and walks
-    // Warps: W consumers and NJ joiners; 12 have 168 registers a thread, 8
-    // (where queries and outputs alone take 64 or more) have 255.
-    static constexpr int HELD = NT * (D / 4 + QR);
+    // Warps: W consumers and NJ joiners; 12 have 168 registers a thread, 8 (where a consumer's outputs alone
+    // take more than 64, or the ring has no room for more) have 255.
+    static constexpr int HELD = NT * D / 4;
     static constexpr int FACTORS = 8 * ROWS * 4 + ROWS * 8;
     static constexpr int ROOM = (SMEM_LIMIT - 1024 - HEAD - QUERIES - FACTORS) / SLOT;  // slots that fit
-    static constexpr int W = HELD < 64 && ROOM >= 16 ? 8 : ROOM >= 12 ? 6 : ROOM >= 8 ? 4 : 3;
+    static constexpr int W = HELD <= 64 && NT < 4 && ROOM >= 16 ? 8 : ROOM >= 12 ? 6 : ROOM >= 8 ? 4 : 3;
     static constexpr int NJ = W == 8 ? 4 : 2;
     static constexpr int THREADS = 32 * (W + NJ);
     static constexpr int S = ROOM / W < 8 ? ROOM / W : 8;  // ring slots a consumer
@@ -348,10 +363,8 @@ struct Split {
     int pad[2];  // 32 bytes, so that what follows the records is aligned
 };
 
-// A part without a maximum has zeros (or the NaN that its scores are).
-__device__ __forceinline__ float part_factor(float part, float all) {
-    return part == __int_as_float(0xff800000) ? 1.f : exp2_fast(part - all);
-}
+// What a part's sums count for when its maximum is `part` and that of all parts `all`.
+__device__ __forceinline__ float part_factor(float part, float all) { return exp2_fast(part - all); }
 
 // Four channels of joined row r of a unit, x unnormalised, st = (maximum, sum).
 template <int CT, class C>
@@ -396,10 +409,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                                                                         const __grid_constant__ CUtensorMap k_map,
                                                                         const __grid_constant__ CUtensorMap v_map, int box_shift) {
     constexpr int NT = C::NT, ROWS = C::ROWS, D = C::D, TS = C::TS, TT = C::TT, W = C::W, S = C::S;
-    constexpr int KB = C::KB, VB = C::VB, MT = C::MT, MPV = C::MPV, QR = C::QR;
+    constexpr int KB = C::KB, VB = C::VB, MT = C::MT, MPV = C::MPV;
     constexpr bool Q8 = C::Q8, F32 = C::F32, BF16 = C::BF16;
     constexpr uint32_t FULL = 0xffffffffu;
     const float NEG_INF = __int_as_float(0xff800000);
+    constexpr float NONE = -1e30f;  // the maximum before any score: finite, so that 2^(-inf - NONE) is 0
 
     extern __shared__ __align__(1024) uint8_t smem[];
     long long *scan = reinterpret_cast<long long *>(smem);               // [warps] sums
@@ -411,6 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     uint64_t *j_full = q_empty + 2, *j_empty = j_full + 1;               // the consumers' parts of a segment
     Walk *walks = reinterpret_cast<Walk *>(smem + 1280);                 // [W][2] where a consumer's products and copies are
     uint8_t *queries = smem + C::HEAD;                                   // [2][ROWS][QROW]
+    float2 *q_stat = reinterpret_cast<float2 *>(queries + 2 * ROWS * C::QROW);  // [2][ROWS] scores' (scale, bias)
     float2 *joined = reinterpret_cast<float2 *>(queries + C::QUERIES);   // [ROWS] maxima and sums
     float *factor = reinterpret_cast<float *>(joined + ROWS);            // [W][ROWS]
     uint8_t *ring = smem + (C::SMEM - W * S * C::SLOT - 1024);           // [W][S][SLOT], on a 1024-byte boundary
@@ -496,22 +511,83 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         const Parts<C> parts(p.partials, gridDim.x);
         int split_parts = 0;
         open_segment<C>(use, 0);
-        auto fetch = [&](const Walk &w, int segment) {  // by the first joiner warp
+        // The queries of a segment into shared memory, by the first joiner warp.  Scores are (K q + bias) scale:
+        // queries over 8-bit rows go as FP16, BF16 ones scaled by a power of two that brings the row's largest
+        // magnitude to [1, 2), and int8 keys are multiplied as 1152 + k (see widen_keys).
+        auto fetch = [&](const Walk &w, int segment) {
             if (j >= 32 || w.left <= 0) return;
-            const int b = segment & 1;
-            ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead);
-            const int rows = min(ROWS, w.s.n * p.G - w.row0);
-            constexpr int PIECES = D * (F32 ? 4 : 2) / 16;
+            const int b = segment & 1, rows = min(ROWS, w.s.n * p.G - w.row0);
+            constexpr int EB = F32 ? 4 : 2, LANE = D * EB / 32;  // bytes a lane takes of a row: 4 to 32
+            constexpr int WORDS = LANE / 4, BATCH = ROWS < 8 ? ROWS : 8;
             const int group = lane < ROWS ? w.row0 + min(lane, rows - 1) : 0;  // lane r: where row r is
             const int token = w.s.n == 1 ? 0 : (int)((uint32_t)group / (uint32_t)p.G);
-            const long long row = ((long long)(w.s.cu0 + token) * p.q_stride + (w.head * p.G + group - token * p.G) * D) * (F32 ? 4 : 2);
+            const long long row = ((long long)(w.s.cu0 + token) * p.q_stride + (w.head * p.G + group - token * p.G) * D) * EB;
+            bool free = false;
+#pragma unroll 1
+            for (int r0 = 0; r0 < ROWS; r0 += BATCH) {
+                uint32_t x[BATCH][WORDS];
 #pragma unroll
-            for (int i = lane; i < ROWS * PIECES; i += 32) {
-                const int r = i / PIECES, x = i % PIECES;
-                const uint8_t *src = static_cast<const uint8_t *>(p.q) + __shfl_sync(FULL, row, r);
-                copy_async<16>(ptx::smem_u32(queries + (b * ROWS + r) * C::QROW + x * 16), src + x * 16, r < rows ? 16 : 0);
+                for (int r = 0; r < BATCH; ++r) {
+                    const uint8_t *src = static_cast<const uint8_t *>(p.q) + __shfl_sync(FULL, row, r0 + r) + lane * LANE;
+#pragma unroll
+                    for (int i = 0; i < WORDS; ++i) x[r][i] = 0u;
+                    if (r0 + r < rows) {
+                        if constexpr (WORDS == 1) x[r][0] = *reinterpret_cast<const uint32_t *>(src);
+                        if constexpr (WORDS == 2) lds<2>(x[r], src);
+                        if constexpr (WORDS == 4) lds<4>(x[r], src);
+                        if constexpr (WORDS == 8) {
+                            lds<4>(reinterpret_cast<uint32_t(&)[4]>(x[r][0]), src);
+                            lds<4>(reinterpret_cast<uint32_t(&)[4]>(x[r][4]), src + 16);
+                        }
+                    }
+                }
+                if (!free) ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead);
+                free = true;
+#pragma unroll
+                for (int r = 0; r < BATCH; ++r) {
+                    float scale = p.scale_log2, sum = 0.f;
+                    if constexpr (Q8) {
+                        if (p.io_bf16) {
+                            float top = 0.f;
+#pragma unroll
+                            for (int i = 0; i < WORDS; ++i) {
+                                const float2 f = unpack2<true>(x[r][i]);
+                                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                            }
+#pragma unroll
+                            for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+                            // the exponent of top, kept where both powers of two are normal
+                            int e = (int)(__float_as_uint(top) >> 23 & 255) - 127;
+                            e = top > 0.f && top <= 3.402823466e38f ? min(max(e, -100), 126) : 0;
+                            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                            scale *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                            for (int i = 0; i < WORDS; ++i) {
+                                const float2 f = unpack2<true>(x[r][i]);
+                                x[r][i] = pack2<false>(f.x * down, f.y * down);
+                            }
+                        }
+                        if constexpr (CT == GDN_INT8) {
+#pragma unroll
+                            for (int i = 0; i < WORDS; ++i) {
+                                const float2 f = unpack2<false>(x[r][i]);
+                                sum += f.x + f.y;
+                            }
+                            sum = warp_sum(sum);
+                        }
+                    }
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(queries + (b * ROWS + r0 + r) * C::QROW + lane * LANE);
+                    if constexpr (WORDS == 1) dst[0] = x[r][0];
+                    if constexpr (WORDS == 2) *reinterpret_cast<uint2 *>(dst) = make_uint2(x[r][0], x[r][1]);
+                    if constexpr (WORDS >= 4) {
+#pragma unroll
+                        for (int i = 0; i < WORDS; i += 4)
+                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(x[r][i], x[r][i + 1], x[r][i + 2], x[r][i + 3]);
+                    }
+                    if (lane == 0) q_stat[b * ROWS + r0 + r] = make_float2(scale, -1152.f * sum);
+                }
             }
-            copy_arrive(q_full + b);
+            ptx::mbar_arrive(q_full + b);
         };
         fetch(use, 0);
         for (int segment = 0; use.left > 0; ++segment) {
@@ -527,7 +603,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             for (int w = 0; w < W; ++w) part[w] = reinterpret_cast<const float *>(ring + (w * S + part_slot[w]) * C::SLOT);
             for (int r = j; r < ROWS; r += THREADS) {
                 float2 st[W];
-                float mm = NEG_INF, ll = 0.f;
+                float mm = NONE, ll = 0.f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     st[w] = reinterpret_cast<const float2 *>(part[w] + ROWS * C::OROW)[r];
@@ -726,8 +802,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     const int v_at0 = 2 * c * C::SPAN + (HALF_LINE ? ((g >> 1 ^ c) << 4) + (g & 1) * 8 : (g ^ 2 * c) << 4);
     const int v_at1 = (2 * c + 1) * C::SPAN + (HALF_LINE ? ((g >> 1 ^ c) << 4) + (g & 1) * 8 : (g ^ (2 * c + 1)) << 4);
 
-    uint32_t q[NT][QR];
-    float col_scale[NT][2];  // scores' factor of the lane's two columns
+    float2 col[NT][2];  // the scores' (scale, bias) of the lane's two columns
     float o[NT][MT][4], m[NT][2], l[NT][2];
     int rows = 0;                // query rows of the unit
     int at_pos[NT][2];           // the positions of the queries of the lane's two columns
@@ -754,52 +829,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             ring_wait(q_full + (segment & 1), segment >> 1 & 1, dead);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const uint8_t *src = queries + ((segment & 1) * ROWS + nt * 8 + g) * C::QROW;
-                col_scale[nt][0] = col_scale[nt][1] = p.scale_log2;
-                if constexpr (!Q8) {
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 16);
-                        q[nt][kb * 4] = x.x, q[nt][kb * 4 + 1] = x.y, q[nt][kb * 4 + 2] = x.z, q[nt][kb * 4 + 3] = x.w;
-                    }
-                } else {  // 16 channels a piece
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32);
-                        const uint4 y = *reinterpret_cast<const uint4 *>(src + (kb * 4 + c) * 32 + 16);
-                        q[nt][kb * 8] = x.x, q[nt][kb * 8 + 1] = x.y, q[nt][kb * 8 + 2] = x.z, q[nt][kb * 8 + 3] = x.w;
-                        q[nt][kb * 8 + 4] = y.x, q[nt][kb * 8 + 5] = y.y, q[nt][kb * 8 + 6] = y.z, q[nt][kb * 8 + 7] = y.w;
-                    }
-                    if (p.io_bf16) {
-                        // to FP16, scaled by a power of two so that the row's largest magnitude is in [1, 2)
-                        float top = 0.f;
-#pragma unroll
-                        for (int j = 0; j < QR; ++j) {
-                            const float2 f = unpack2<true>(q[nt][j]);
-                            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                        }
-                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-                        // the exponent of top, kept where both powers of two are normal
-                        int e = (int)(__float_as_uint(top) >> 23 & 255) - 127;
-                        e = top > 0.f && top <= 3.402823466e38f ? max(e, -100) : 0;
-                        e = min(e, 126);
-                        const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                        for (int j = 0; j < QR; ++j) {
-                            const float2 f = unpack2<true>(q[nt][j]);
-                            q[nt][j] = pack2<false>(f.x * down, f.y * down);
-                        }
-                        col_scale[nt][0] *= __shfl_sync(FULL, up, 8 * c);
-                        col_scale[nt][1] *= __shfl_sync(FULL, up, 8 * c + 4);
-                    }
-                }
+                col[nt][0] = q_stat[(segment & 1) * ROWS + nt * 8 + 2 * c];
+                col[nt][1] = q_stat[(segment & 1) * ROWS + nt * 8 + 2 * c + 1];
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(q_empty + (segment & 1));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                m[nt][0] = m[nt][1] = NEG_INF;
+                m[nt][0] = m[nt][1] = NONE;
                 l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
@@ -820,8 +855,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[ts][nt][e] = sc2[ts][nt][e] = 0.f;
             const uint8_t *ks = slots + at * C::SLOT;
+            // lane (g, c) holds, of query row 8 nt + g, the channels that its key pieces have
+            const uint8_t *qs = queries + ((segment & 1) * ROWS + g) * C::QROW + c * (Q8 ? 32 : 16);
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+            for (int kb = 0; kb < KB; ++kb) {
+                uint32_t q[NT][Q8 ? 8 : 4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint8_t *src = qs + nt * 8 * C::QROW + kb * (Q8 ? 128 : 64);
+                    lds<4>(reinterpret_cast<uint32_t(&)[4]>(q[nt][0]), src);
+                    if constexpr (Q8) lds<4>(reinterpret_cast<uint32_t(&)[4]>(q[nt][4]), src + 16);
+                }
 #pragma unroll
                 for (int ts = 0; ts < TS; ++ts) {
                     uint32_t x[4], y[4];
@@ -832,15 +876,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         uint32_t u[8], v[8];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            widen<CT>(x[j], u[2 * j], u[2 * j + 1]);
-                            widen<CT>(y[j], v[2 * j], v[2 * j + 1]);
+                            widen_keys<CT>(x[j], u[2 * j], u[2 * j + 1]);
+                            widen_keys<CT>(y[j], v[2 * j], v[2 * j + 1]);
                         }
 #pragma unroll
                         for (int j = 0; j < 8; j += 2)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16<false>((j & 2) ? sc2[ts][nt] : sc[ts][nt], u[j], v[j], u[j + 1], v[j + 1],
-                                             q[nt][kb * 8 + j], q[nt][kb * 8 + j + 1]);
+                                mma16<false>((j & 2) ? sc2[ts][nt] : sc[ts][nt], u[j], v[j], u[j + 1], v[j + 1], q[nt][j],
+                                             q[nt][j + 1]);
                     } else if constexpr (F32) {
 #pragma unroll
                         for (int j = 0; j < 4; j += 2) {
@@ -848,8 +892,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 uint32_t bh[2], bl[2];
-                                split_tf32(q[nt][kb * 4 + j], bh[0], bl[0]);
-                                split_tf32(q[nt][kb * 4 + j + 1], bh[1], bl[1]);
+                                split_tf32(q[nt][j], bh[0], bl[0]);
+                                split_tf32(q[nt][j + 1], bh[1], bl[1]);
                                 mma_f32(j ? sc2[ts][nt] : sc[ts][nt], a, bh, bl);
                             }
                         }
@@ -858,41 +902,53 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         for (int j = 0; j < 4; j += 2)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16<BF16>(j ? sc2[ts][nt] : sc[ts][nt], x[j], y[j], x[j + 1], y[j + 1],
-                                            q[nt][kb * 4 + j], q[nt][kb * 4 + j + 1]);
+                                mma16<BF16>(j ? sc2[ts][nt] : sc[ts][nt], x[j], y[j], x[j + 1], y[j + 1], q[nt][j], q[nt][j + 1]);
                     }
                 }
-            // the lane's tokens are rows g and g + 8 of each subtile
-            float vs[TS][2], lv[TS][2], ksc[TS][2];
-            if constexpr (Q8) {
-                const float *kscale = reinterpret_cast<const float *>(slots + at * C::SLOT + 2 * C::HALF);
-#pragma unroll
-                for (int ts = 0; ts < TS; ++ts)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int i = ts * 16 + g + 8 * e;
-                        ksc[ts][e] = kscale[i];
-                        vs[ts][e] = kscale[TT + i];
-                        lv[ts][e] = log2_fast(fmaxf(fabsf(vs[ts][e]), 1e-30f));  // (rows of zeros may have scale 0)
-                    }
             }
+            // the lane's tokens are rows g and g + 8 of each subtile
+            float vs[TS][2], lv[TS][2];
             float top[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = NEG_INF;
+            const float *scales = reinterpret_cast<const float *>(slots + at * C::SLOT + 2 * C::HALF);
+#pragma unroll
+            for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float ksc = 1.f;
+                    if constexpr (Q8) {
+                        const int i = ts * 16 + g + 8 * h;
+                        ksc = scales[i];
+                        vs[ts][h] = scales[TT + i];
+                        lv[ts][h] = log2_fast(fmaxf(fabsf(vs[ts][h]), 1e-30f));  // (rows of zeros may have scale 0)
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float &x = sc[ts][nt][2 * h + e];
+                            x += sc2[ts][nt][2 * h + e];
+                            if constexpr (CT == GDN_INT8) x += col[nt][e].y;
+                            x *= Q8 ? col[nt][e].x * ksc : col[nt][e].x;
+                        }
+                }
+            if (__builtin_expect(edge, 0)) {
+#pragma unroll
+                for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!sees(at_pos[nt][e & 1], tile_t + ts * 16 + g + 8 * (e >> 1))) sc[ts][nt][e] = NEG_INF;
+            }
 #pragma unroll
             for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = (sc[ts][nt][e] + sc2[ts][nt][e]) * col_scale[nt][e & 1];
-                        if constexpr (Q8) x *= ksc[ts][e >> 1];
-                        if (edge && !sees(at_pos[nt][e & 1], tile_t + ts * 16 + g + 8 * (e >> 1))) x = NEG_INF;
-                        sc[ts][nt][e] = x;
-                        float y = x;
-                        if constexpr (Q8) y = x == NEG_INF ? x : x + lv[ts][e >> 1];
-                        top[nt][e & 1] = fmaxf(top[nt][e & 1], y);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        top[nt][e & 1] = fmaxf(top[nt][e & 1], Q8 ? sc[ts][nt][e] + lv[ts][e >> 1] : sc[ts][nt][e]);
 
             // ---- raise the maxima where a score exceeds them by more than the headroom
             bool raise = false;
@@ -930,11 +986,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     float w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float base = m[nt][e & 1] == NEG_INF ? 0.f : m[nt][e & 1] - C::BIAS;
-                        const float x = exp2_fast(sc[ts][nt][e] - base);
+                        const float x = exp2_fast(sc[ts][nt][e] - (m[nt][e & 1] - C::BIAS));
                         l[nt][e & 1] += x;
-                        if constexpr (Q8) w[e] = sc[ts][nt][e] == NEG_INF ? 0.f : x * vs[ts][e >> 1];
-                        else w[e] = x;
+                        w[e] = Q8 ? x * vs[ts][e >> 1] : x;
+                    }
+                    if (Q8 && __builtin_expect(edge, 0)) {  // (the scale of a masked row may be anything)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (sc[ts][nt][e] == NEG_INF) w[e] = 0.f;
                     }
                     if constexpr (F32) {
                         // k-slots c and c + 4 are tokens 2 c and 2 c + 1 (+ 8): from the lanes that hold their rows, column g
@@ -1081,7 +1140,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 }
             if (lane == 0) part_slot[warp] = at;
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(j_full);
+            if (lane == 0) {
+                ptx::mbar_arrive(j_full);
+                ptx::mbar_arrive(q_empty + (segment & 1));
+            }
             part_at = at;
             part_segment = segment++;
             if (lane == 0) next_segment<C>(at_use, p, warp);
@@ -1106,14 +1168,14 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     __shared__ float4 sums[GROUPS][LANES];
     __shared__ float2 stats[GROUPS];
     dependent_prologue();
-    const float NEG_INF = __int_as_float(0xff800000);
+    constexpr float NONE = -1e30f;
     const Parts<C> parts(p.partials, gridDim.x);
     const int i = blockIdx.x, r = blockIdx.y;
     const Split s = parts.split[i];
     if (r >= s.rows || s.parts == 0) return;
     const int x = threadIdx.x % LANES, grp = threadIdx.x / LANES;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float2 all = make_float2(NEG_INF, 0.f);
+    float2 all = make_float2(NONE, 0.f);
     auto add = [&](const float2 (&st)[BATCH], const float4 (&v)[BATCH]) {
         float mm = all.x;
 #pragma unroll
@@ -1134,7 +1196,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const int part = k0 + k * GROUPS;
-            st[k] = make_float2(NEG_INF, 0.f);
+            st[k] = make_float2(NONE, 0.f);
             v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (part < s.parts) {
                 const long long slot = 2LL * (i + part) + (part == 0);
@@ -1153,7 +1215,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
         float4 v[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            st[k] = k0 + k < GROUPS ? stats[k0 + k] : make_float2(NEG_INF, 0.f);
+            st[k] = k0 + k < GROUPS ? stats[k0 + k] : make_float2(NONE, 0.f);
             v[k] = k0 + k < GROUPS ? sums[k0 + k][x] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         add(st, v);
