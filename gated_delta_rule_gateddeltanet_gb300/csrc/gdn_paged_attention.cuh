@@ -219,10 +219,10 @@ struct Seq {
 // A walk over a CTA's chunks, one segment (part of one unit) at a time.
 struct Walk {
     Seq s;
-    int unit, chunk;     // the current segment's unit and first chunk
-    int head, row0;      // the unit's key head and first query row
-    int seg_chunks;
-    int left;            // chunks of this CTA not yet behind the walk, this segment's included
+    int unit, pos;           // the current segment's unit and where in its share of the work it starts
+    int chunk, seg_chunks;   // the segment's chunks
+    int head, row0;          // the unit's key head and first query row
+    int seg_work, left;      // the work of the segment, and of this CTA from there on
     int tile, tile_end;  // the warp's next tile and the segment's end
 };
 
@@ -262,6 +262,9 @@ struct Cfg {
     static constexpr int ROOM = (SMEM_LIMIT - 1024 - HEAD - QUERIES - FACTORS) / SLOT;  // slots that fit
     static constexpr int W = HELD <= 64 && NT < 4 && ROOM >= 16 ? 8 : ROOM >= 12 ? 6 : ROOM >= 8 ? 4 : 3;
     static constexpr int NJ = W == 8 ? 4 : 2;
+    // What a unit costs besides its chunks (fetching queries, joining), in chunks: with 0 the CTAs with many
+    // short units are late (256 requests of up to 1024 tokens: 59 us against 55 us; a decode step of 64 x 128 to 2048: 65 against 57).
+    static constexpr int UNIT_WORK = 2;
     static constexpr int THREADS = 32 * (W + NJ);
     static constexpr int S = ROOM / W < 8 ? ROOM / W : 8;  // ring slots a consumer
     static constexpr int SMEM = 1024 + HEAD + QUERIES + FACTORS + W * S * SLOT;  // (1024: the ring's alignment)
@@ -299,16 +302,19 @@ template <class C>
 __device__ __forceinline__ void open_segment(Walk &w, int first) {
     w.head = w.s.row_groups == 1 ? w.unit : (int)((uint32_t)w.unit / (uint32_t)w.s.row_groups);
     w.row0 = (w.unit - w.head * w.s.row_groups) * C::ROWS;
-    w.seg_chunks = min(w.s.chunks - w.chunk, w.left);
+    w.seg_work = min(w.s.chunks + C::UNIT_WORK - w.pos, w.left);
+    w.chunk = max(0, w.pos - C::UNIT_WORK);
+    w.seg_chunks = max(0, w.pos + w.seg_work - C::UNIT_WORK) - w.chunk;
+    if (w.seg_chunks == 0) w.left = 0;  // only a unit's fixed work is left: the next CTA, which has its chunks, does it
     w.tile = w.chunk * C::W + first;
     w.tile_end = min((w.chunk + w.seg_chunks) * C::W, w.s.tiles);
 }
 
 template <class C>
 __device__ __forceinline__ void next_segment(Walk &w, const PagedAttnParams &p, int first) {
-    w.left -= w.seg_chunks;
+    w.left -= w.seg_work;
     if (w.left <= 0) return;
-    w.chunk = 0;
+    w.pos = 0;
     if (++w.unit == w.s.units) {
         int b = w.s.b;
         do {
@@ -327,13 +333,13 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
     return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The first `rem` CTAs take one chunk more than the others.
+// The first `rem` CTAs take one unit of work more than the others.
 struct Shares {
     long long each, rem;
     __device__ __forceinline__ long long begin(int cta) const { return cta * each + min((long long)cta, rem); }
-    __device__ __forceinline__ int owner(long long chunk) const {
+    __device__ __forceinline__ int owner(long long x) const {
         const long long big = rem * (each + 1);
-        return (int)(chunk < big ? divide(chunk, each + 1) : rem + divide(chunk - big, each));
+        return (int)(x < big ? divide(x, each + 1) : rem + divide(x - big, each));
     }
 };
 
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     ptx::fence_mbar_init();
     dependent_prologue();
 
-    // ---- this CTA's share of the chunks
+    // ---- this CTA's share of the work
     Shares shares;
     long long total, start;
     {
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         long long sum = 0;
         for (int b = b0; b < b1; ++b) {
             const Seq s = load_seq<C>(p, b, blockIdx.x == 0);
-            sum += (long long)s.units * s.chunks;
+            sum += (long long)s.units * (s.chunks + C::UNIT_WORK);
         }
         long long incl = sum;
 #pragma unroll
@@ -487,12 +493,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         if (start >= excl && start < excl + sum) {
             for (int b = b0;; ++b) {
                 const Seq s = load_seq<C>(p, b, false);
-                const long long here = (long long)s.units * s.chunks;
+                const long long here = (long long)s.units * (s.chunks + C::UNIT_WORK);
                 if (start < excl + here) {
                     Walk w;
                     w.s = s;
-                    w.unit = (int)divide(start - excl, s.chunks);
-                    w.chunk = (int)(start - excl - (long long)w.unit * s.chunks);
+                    w.unit = (int)divide(start - excl, s.chunks + C::UNIT_WORK);
+                    w.pos = (int)(start - excl - (long long)w.unit * (s.chunks + C::UNIT_WORK));
                     w.left = (int)(shares.begin(blockIdx.x + 1) - start);
                     *first = w;
                     break;
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             if (j == 0) {
                 ptx::mbar_arrive(j_empty);
                 if (!whole && use.chunk == 0) {  // the head of a unit that goes on: this CTA's last segment
-                    split_parts = shares.owner(shares.begin(blockIdx.x + 1) - use.left + use.s.chunks - 1) - (int)blockIdx.x + 1;
+                    split_parts = shares.owner(shares.begin(blockIdx.x + 1) - use.left - use.pos + C::UNIT_WORK + use.s.chunks - 1) - (int)blockIdx.x + 1;
                     parts.split[blockIdx.x] = {split_parts, rows, row0, head, use.s.cu0, pos0, {0, 0}};
                 }
             }
@@ -677,9 +683,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     bool owed = false;           // the slot for the part of the segment before comes first
     int put = 0, free_slots = S; // the slot that is filled next, and how many may be
     auto look_up = [&]() {
+        // (a page outside the pool reads as zeros; flagged here, when the entries have long arrived)
+        if ((boxes >> lane & 1) && (uint32_t)page >= (uint32_t)p.c.num_pages) flag_error(p.status, GDN_DEVERR_PAGE);
         taken = 0;
         boxes = 0;
-        if (get_left <= 0) return;
+        if (get_left <= 0) return;  // (also after the last segment: its pages have been checked above)
         const int box = lane << box_shift;  // in tokens
         const int tile = get_tile + box / TT * W;
         const int t = at_get.s.t0 + tile * TT + box % TT;
@@ -724,16 +732,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 const uint32_t mine = boxes >> box0 & (FULL >> (32 - subs));
                 uint8_t *dst = slots + put * C::SLOT;
                 uint64_t *bar = landed + put;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, BY_ROWS ? 0 : __popc(mine) * (2 * C::RB) << box_shift);
                 if constexpr (BY_ROWS) {
+                    if (lane == 0) ptx::mbar_arrive(bar);
                     // lane box0 + i looked up token i: its row's byte offset, -1 if it is not read
                     long long row = -1;
-                    if (boxes >> lane & 1) {
-                        if (page >= 0 && page < p.c.num_pages)
-                            row = (page * p.c.page_stride + in_page * p.c.token_stride + head * p.c.head_stride) * C::ESZ;
-                        else
-                            flag_error(p.status, GDN_DEVERR_PAGE);
-                    }
+                    if ((boxes >> lane & 1) && (uint32_t)page < (uint32_t)p.c.num_pages)
+                        row = (page * p.c.page_stride + in_page * p.c.token_stride + head * p.c.head_stride) * C::ESZ;
                     constexpr int PIECES = C::RB / 16, PER_SPAN = C::SPAN / 16;
                     const uint32_t to = ptx::smem_u32(dst);
 #pragma unroll 4
@@ -747,27 +751,34 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         copy_async<16>(at + C::HALF, static_cast<const uint8_t *>(p.c.v) + src, o < 0 ? 0 : 16);
                     }
                 } else {
-#pragma unroll 1
-                    for (int b = 0; b < subs; ++b) {
-                        int pg = __shfl_sync(FULL, page, box0 + b);
-                        const int off = __shfl_sync(FULL, in_page, box0 + b);
-                        if (lane != 0 || !(mine >> b & 1)) continue;
-                        if (pg < 0 || pg >= p.c.num_pages) {
-                            flag_error(p.status, GDN_DEVERR_PAGE);
-                            pg = p.c.num_pages;  // outside the map: reads as zeros
-                        }
-                        uint8_t *to = dst + (b << box_shift) * C::SPAN;
+                    constexpr int MOST = TT / 8;  // boxes of 8 tokens or more
+                    int pg[MOST], off[MOST];
+#pragma unroll
+                    for (int b = 0; b < MOST; ++b) {
+                        if (b > 0 && b >= subs) break;
+                        // (num_pages is outside the map, which reads as zeros)
+                        pg[b] = (int)min((uint32_t)__shfl_sync(FULL, page, box0 + b), (uint32_t)p.c.num_pages);
+                        off[b] = __shfl_sync(FULL, in_page, box0 + b);
+                    }
+                    if (ptx::elect_one()) {
+                        ptx::mbar_arrive_expect_tx(bar, __popc(mine) * (2 * C::RB) << box_shift);
                         if (subs == 1) {  // all spans at once
-                            ptx::tma_load_5d(to, &k_map, 0, off, 0, head, pg, bar);
-                            ptx::tma_load_5d(to + C::HALF, &v_map, 0, off, 0, head, pg, bar);
+                            ptx::tma_load_5d(dst, &k_map, 0, off[0], 0, head, pg[0], bar);
+                            ptx::tma_load_5d(dst + C::HALF, &v_map, 0, off[0], 0, head, pg[0], bar);
                         } else {
+#pragma unroll
+                            for (int b = 0; b < MOST; ++b) {
+                                if (!(mine >> b & 1)) continue;
+                                uint8_t *to = dst + (b << box_shift) * C::SPAN;
 #pragma unroll 1
-                            for (int x = 0; x < C::BOXES; ++x) {
-                                ptx::tma_load_5d(to + x * TT * C::SPAN, &k_map, 0, off, x, head, pg, bar);
-                                ptx::tma_load_5d(to + C::HALF + x * TT * C::SPAN, &v_map, 0, off, x, head, pg, bar);
+                                for (int x = 0; x < C::BOXES; ++x) {
+                                    ptx::tma_load_5d(to + x * TT * C::SPAN, &k_map, 0, off[b], x, head, pg[b], bar);
+                                    ptx::tma_load_5d(to + C::HALF + x * TT * C::SPAN, &v_map, 0, off[b], x, head, pg[b], bar);
+                                }
                             }
                         }
                     }
+                    __syncwarp();
                 }
                 if constexpr (Q8) {
                     // TS == 2: a token a lane; 16 tokens: the upper lanes fetch the value scales.  (Those of tokens
@@ -775,7 +786,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     const int token = lane & (TT - 1), sub = token >> box_shift;
                     const int pg = __shfl_sync(FULL, page, box0 + sub);
                     const int off = __shfl_sync(FULL, in_page, box0 + sub) + (token & (box_tokens - 1));
-                    const int ok = (mine >> sub & 1) && pg >= 0 && pg < p.c.num_pages ? 4 : 0;
+                    const int ok = (mine >> sub & 1) && (uint32_t)pg < (uint32_t)p.c.num_pages ? 4 : 0;
                     const long long at = ok ? (long long)pg * p.s_page_stride32 + (long long)off * p.s_token_stride32 +
                                                   (long long)head * p.s_head_stride32
                                             : 0;

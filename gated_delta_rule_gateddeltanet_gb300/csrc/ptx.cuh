@@ -127,6 +127,20 @@ __device__ __forceinline__ void tma_load_5d(void *dst_smem, const void *tensor_m
         : "memory");
 }
 
+// True in one lane of a converged warp.  The compiler knows that a branch on it
+// has one active lane, which spares the copies inside a loop over lanes each.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        :
+        : "memory");
+    return ok != 0;
+}
+
 // Fetches a tensor map (a __grid_constant__ kernel parameter) ahead of its first use.
 __device__ __forceinline__ void prefetch_tensor_map(const void *tensor_map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tensor_map) : "memory");
