@@ -241,7 +241,7 @@ struct Cfg {
     static constexpr int CPL = CHV / ESZ;               // channels of a value piece
     static constexpr int MT = D / 16;                   // 16-channel output tiles
     static constexpr int MPV = MT / VB;                 // of them per value piece (CPL / 2)
-    static constexpr int TS = 32 * RB <= 4096 || NT == 4 ? 2 : 1;  // 16-token subtiles a tile
+    static constexpr int TS = 32 * RB <= 4096 ? 2 : 1;  // 16-token subtiles a tile
     static constexpr int TT = 16 * TS;
     static constexpr int HALF = TT * RB;                // a tile's keys; its values
     static constexpr int SPAN = RB < 128 ? RB : 128;    // row bytes a tensor copy takes
@@ -260,7 +260,7 @@ struct Cfg {
     static constexpr int HELD = NT * D / 4;
     static constexpr int FACTORS = 8 * ROWS * 4 + ROWS * 8;
     static constexpr int ROOM = (SMEM_LIMIT - 1024 - HEAD - QUERIES - FACTORS) / SLOT;  // slots that fit
-    static constexpr int W = HELD <= 64 && NT < 4 && ROOM >= 16 ? 8 : ROOM >= 12 ? 6 : ROOM >= 8 ? 4 : 3;
+    static constexpr int W = HELD <= 64 && ROOM >= 16 ? 8 : ROOM >= 12 ? 6 : ROOM >= 8 ? 4 : 3;
     static constexpr int NJ = W == 8 ? 4 : 2;
     // What a unit costs besides its chunks (fetching queries, joining), in chunks: with 0 the CTAs with many
     // short units are late (256 requests of up to 1024 tokens: 59 us against 55 us; a decode step of 64 x 128 to 2048: 65 against 57).
@@ -1263,14 +1263,12 @@ cudaError_t launch_sized(const PagedAttnParams &p, cudaStream_t stream) {
     return launch_dependent(join_kernel<CT, C>, dim3(ctas, C::ROWS), dim3(JOIN_THREADS), 0, stream, p);
 }
 
-// Query rows a pass: as few groups of 8 as hold the rows of one key head
-// (fewer idle columns), at most what the registers hold.
+// Query rows a pass: 8 where one key head has no more, else 16 (fewer idle columns
+// against fewer passes over the cache).
 template <int CT, int D>
 cudaError_t launch_dim(const PagedAttnParams &p, cudaStream_t stream) {
     constexpr int MAX = max_row_tiles(CT == GDN_F32, D);
     const int nt = row_tiles(CT == GDN_F32, D, p.rows_hint);
-    if constexpr (MAX >= 4)
-        if (nt == 4) return launch_sized<CT, D, 4>(p, stream);
     if constexpr (MAX >= 2)
         if (nt == 2) return launch_sized<CT, D, 2>(p, stream);
     return launch_sized<CT, D, 1>(p, stream);

@@ -645,7 +645,7 @@ gdn_status gdn_kv_cache_read(const gdn_kv_read_args *args, gdn_stream_t stream);
  * for every query head, whose key head is head / (num_q_heads / num_kv_heads).
  * A query that sees nothing (p < 0) gives zeros and a log-sum-exp of -inf.
  * One token a sequence is decode; a few are the verification of a draft.  Long
- * spans are valid but reread the cache for every 8 to 64 query rows.
+ * spans are valid but reread the cache for every 8 or 16 query rows.
  *   q            device [T, num_q_heads, head_dim] io_dtype, 16-byte aligned, token
  *                stride q_stride elements (0 = no gap; whole multiples of 16 bytes)
  *   block_table  device [B, pages_per_seq] int32, rows block_table_stride apart (0 = no gap);
