@@ -178,14 +178,15 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t &p01, uint32_t &p23) 
     }
 }
 
-// The same for keys, where int8 may stay biased: pairs of 1152 + x, to which
-// the scores' bias of -1152 sum(q) belongs.
+// The same for keys, where int8 may stay biased: a byte x + 128 as the low half of an FP16
+// number is the subnormal (x + 128) 2^-24, exactly.  The scores' bias of -128 2^-24 sum(q)
+// and scale of 2^24 belong to it.  (1152 + x, as above, would lose four more bits of a score to its bias.)
 template <int CT>
 __device__ __forceinline__ void widen_keys(uint32_t w, uint32_t &p01, uint32_t &p23) {
     if constexpr (CT == GDN_INT8) {
         const uint32_t u = w ^ 0x80808080u;
-        p01 = __byte_perm(u, 0x64646464u, 0x4140);
-        p23 = __byte_perm(u, 0x64646464u, 0x4342);
+        p01 = __byte_perm(u, 0u, 0x4140);
+        p23 = __byte_perm(u, 0u, 0x4342);
     } else {
         widen<CT>(w, p01, p23);
     }
@@ -194,16 +195,20 @@ __device__ __forceinline__ void widen_keys(uint32_t w, uint32_t &p01, uint32_t &
 struct Yes { __device__ constexpr bool operator()() const { return true; } };
 struct No { __device__ constexpr bool operator()() const { return false; } };
 
-// Whether a 32-bit word of cache elements holds an infinity or NaN.
+// Whether a 32-bit word of 16- or 32-bit cache elements holds an infinity or NaN.
 template <int CT>
 __device__ __forceinline__ bool non_finite(uint32_t w) {
     if constexpr (CT == GDN_F32) return (w & 0x7f800000u) == 0x7f800000u;
     if constexpr (CT == GDN_F16) return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
     if constexpr (CT == GDN_BF16) return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-    if constexpr (CT == GDN_FP8_E4M3)
-        return (w & 0x7fu) == 0x7fu || (w & 0x7f00u) == 0x7f00u || (w & 0x7f0000u) == 0x7f0000u ||
-               (w & 0x7f000000u) == 0x7f000000u;
     return false;
+}
+// A word of e4m3 values with zeros for its NaN (0x7f and 0xff).
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        if ((w >> i & 0x7fu) == 0x7fu) w &= ~(0xffu << i);
+    return w;
 }
 
 // ---------------------------------------------------------------- configuration
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         open_segment<C>(use, 0);
         // The queries of a segment into shared memory, by the first joiner warp.  Scores are (K q + bias) scale:
         // queries over 8-bit rows go as FP16, BF16 ones scaled by a power of two that brings the row's largest
-        // magnitude to [1, 2), and int8 keys are multiplied as 1152 + k (see widen_keys).
+        // magnitude to [1, 2), and int8 keys are multiplied as (128 + k) 2^-24 (see widen_keys).
         auto fetch = [&](const Walk &w, int segment) {
             if (j >= 32 || w.left <= 0) return;
             const int b = segment & 1, rows = min(ROWS, w.s.n * p.G - w.row0);
@@ -580,6 +585,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                                 sum += f.x + f.y;
                             }
                             sum = warp_sum(sum);
+                            scale *= 16777216.f;
                         }
                     }
                     uint32_t *dst = reinterpret_cast<uint32_t *>(queries + (b * ROWS + r0 + r) * C::QROW + lane * LANE);
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         for (int i = 0; i < WORDS; i += 4)
                             *reinterpret_cast<uint4 *>(dst + i) = make_uint4(x[r][i], x[r][i + 1], x[r][i + 2], x[r][i + 3]);
                     }
-                    if (lane == 0) q_stat[b * ROWS + r0 + r] = make_float2(scale, -1152.f * sum);
+                    if (lane == 0) q_stat[b * ROWS + r0 + r] = make_float2(scale, -128.f / 16777216.f * sum);
                 }
             }
             ptx::mbar_arrive(q_full + b);
@@ -1033,7 +1039,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             // ---- O^T += V^T P^T
             const uint8_t *vsm = slots + at * C::SLOT + C::HALF;
             constexpr int VW = C::CHV / 4;  // words of a value piece
-            // `only` (careful): the single query row to add, with values that it does not see left out
+            // `only` (careful): the single query row to add to, with values that it does not see left out
             auto add_values = [&](int only, int only_pos, auto careful) {
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb)
@@ -1051,7 +1057,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                                 }
                             }
                         }
-                        auto mine = [&](uint32_t x, int nt) { return !careful() || only == nt * 8 + g ? x : 0u; };
+                        // acc += a product, in the lane's columns that are meant (the others may have seen 0 * inf)
+                        auto into = [&](float(&acc)[4], int nt, auto product) {
+                            if constexpr (careful()) {
+                                float t[4] = {acc[0], acc[1], acc[2], acc[3]};
+                                product(t);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (only == nt * 8 + 2 * c + (e & 1)) acc[e] = t[e];
+                            } else {
+                                product(acc);
+                            }
+                        };
                         if constexpr (F32) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
@@ -1059,11 +1076,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                                 for (int j = 0; j < VW; j += 2) {
                                     const uint32_t a[4] = {v[2 * k][j], v[2 * k][j + 1], v[2 * k + 1][j], v[2 * k + 1][j + 1]};
 #pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        const uint32_t bh[2] = {mine(fh[ts][nt][k][0], nt), mine(fh[ts][nt][k][1], nt)};
-                                        const uint32_t bl[2] = {mine(fl[ts][nt][k][0], nt), mine(fl[ts][nt][k][1], nt)};
-                                        mma_f32(o[nt][vb * MPV + j / 2], a, bh, bl);
-                                    }
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        into(o[nt][vb * MPV + j / 2], nt,
+                                             [&](float(&acc)[4]) { mma_f32(acc, a, fh[ts][nt][k], fl[ts][nt][k]); });
                                 }
                         } else {
                             uint32_t a[MPV][4];
@@ -1088,37 +1103,39 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
 #pragma unroll
                             for (int j = 0; j < MPV; ++j)
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    if constexpr (C::SPLIT_P)
-                                        mma16<BF16>(o[nt][vb * MPV + j], a[j][0], a[j][1], a[j][2], a[j][3],
-                                                    mine(pl[ts][nt][0], nt), mine(pl[ts][nt][1], nt));
-                                    mma16<BF16>(o[nt][vb * MPV + j], a[j][0], a[j][1], a[j][2], a[j][3],
-                                                mine(ph[ts][nt][0], nt), mine(ph[ts][nt][1], nt));
-                                }
+                                for (int nt = 0; nt < NT; ++nt)
+                                    into(o[nt][vb * MPV + j], nt, [&](float(&acc)[4]) {
+                                        if constexpr (C::SPLIT_P)
+                                            mma16<BF16>(acc, a[j][0], a[j][1], a[j][2], a[j][3], pl[ts][nt][0], pl[ts][nt][1]);
+                                        mma16<BF16>(acc, a[j][0], a[j][1], a[j][2], a[j][3], ph[ts][nt][0], ph[ts][nt][1]);
+                                    });
                         }
                     }
             };
             // A tile at an end of what is cached holds other rows too (of other tokens, or never written): their
             // values are zeroed.  A value that some query rows see and others do not would reach the others as 0 *
-            // inf if it is not finite: such a tile is added row by row.
+            // inf if it is not finite: such a tile is added row by row.  (A row of 8-bit values that is not finite
+            // has a NaN scale, which masks with its weight; its NaN bytes are zeroed.)
             bool rough = false;
             if (__builtin_expect(edge, 0)) {
                 const int first = at_use.s.first, len = at_use.s.len;
-                const bool several = CT != GDN_INT8 && at_use.s.n > 1;
+                const bool several = at_use.s.n > 1;
 #pragma unroll 1
                 for (int i = lane * 16; i < C::HALF; i += 512) {  // [BOXES][TT][SPAN] bytes
                     const int t = tile_t + i / C::SPAN % TT;
                     uint4 *x = reinterpret_cast<uint4 *>(slots + at * C::SLOT + C::HALF + i);
                     if (t < first || t >= len)
                         *x = make_uint4(0, 0, 0, 0);
-                    else if (several)
+                    else if (!Q8 && several)
                         rough |= non_finite<CT>(x->x) || non_finite<CT>(x->y) || non_finite<CT>(x->z) || non_finite<CT>(x->w);
+                    else if (CT == GDN_FP8_E4M3 && several)
+                        *x = make_uint4(without_nan(x->x), without_nan(x->y), without_nan(x->z), without_nan(x->w));
                 }
-                ptx::fence_proxy_async_smem();  // (a later tensor copy overwrites the zeros)
-                rough = __any_sync(FULL, rough);
+                ptx::fence_proxy_async_smem();  // (a later tensor copy overwrites what was stored here)
+                if (!Q8) rough = __any_sync(FULL, rough);
                 __syncwarp();
             }
-            if (__builtin_expect(rough, 0)) {
+            if (!Q8 && __builtin_expect(rough, 0)) {
 #pragma unroll 1
                 for (int r = 0; r < rows; ++r) add_values(r, at_use.s.len - at_use.s.n + (at_use.row0 + r) / p.G, Yes());
             } else {

@@ -569,6 +569,8 @@ gdn_status gdn_rotary(const gdn_rotary_args *args, gdn_stream_t stream);
  *   GDN_INT8      scale = max|x| / 127; q = x / scale rounded to nearest even
  * A row of zeros has scale 1; a row with an infinity or NaN has scale NaN, so
  * that it reads back as NaN.
+ * Rows written by others follow the same rules: a zero scale is fine for zeros,
+ * and an e4m3 NaN goes with a NaN scale.
  */
 typedef struct gdn_kv_cache {
     int32_t num_pages;    /* num_pages * page_size < 2^31 */
@@ -654,8 +656,10 @@ gdn_status gdn_kv_cache_read(const gdn_kv_read_args *args, gdn_stream_t stream);
  *   cu_seqlens   device [B+1] int32, or NULL: one query token per sequence (T = B)
  *   output       device [T, num_q_heads, head_dim] io_dtype, contiguous
  *   lse          device [T, num_q_heads] FP32 or NULL: ln sum_t exp(scale q k_t)
- * What the cache holds in slots that no query may see (uninitialised memory,
- * NaN) does not reach the results.  io_dtype is the cache's type, or FP16 or
+ * What the cache holds in slots that a query may not see (uninitialised memory,
+ * infinities, NaN, also of later drafted tokens) does not reach its results; an
+ * infinity or NaN that it does see makes the channels it is in infinite or NaN.
+ * io_dtype is the cache's type, or FP16 or
  * BF16 over an 8-bit cache.
  * The work is split over sequences, heads and cache length by the lengths on
  * the device, so a captured graph stays balanced as they change; pieces of one
