@@ -74,3 +74,22 @@ def test_capturing_writes_nothing():
     torch.cuda.synchronize()
     assert torch.all(cache.k == 3) and torch.all(cache.v == 4) and torch.equal(step.slots, before)
     assert torch.all(step.kv_lens == 20) and int(step.status) == 0
+
+
+def test_readme_attention_example_runs():
+    """The README's second example as written: shapes, and the new token's attention against the oracle
+    over what reading the cache back gives."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    scope = {}
+    exec(compile(re.findall(r"```python\n(.*?)```", text, re.S)[1], "README.md", "exec"), scope)
+    torch.cuda.synchronize()
+    assert scope["k_all"].shape == (318, 2, 256) and scope["o1"].shape == (3, 16, 256)
+    cu = torch.tensor([0, 301, 319, 321], dtype=torch.int32, device=dev())
+    k, v = gdn.kv_cache_read(scope["cache"], scope["block_table"], cu, 321, dtype=torch.float32)
+    for b, (i, j) in enumerate(((0, 301), (301, 319), (319, 321))):
+        want, lse = oa.attend(f64(scope["q1"])[b:b + 1], f64(k)[i:j], f64(v)[i:j], 256 ** -0.5)
+        # single FP16 weights (2^-11) and the output's rounding, over values of at most 5
+        assert np.abs(f64(scope["o1"])[b] - want[0]).max() <= 4 * 2.0 ** -11 * np.abs(f64(v)[i:j]).max()
+        assert np.abs(f64(scope["lse"])[b] - lse[0]).max() <= 2.0 ** -16 * (1 + np.abs(lse).max())
