@@ -55,6 +55,8 @@ struct KvWriteParams {
 struct KvReadParams {
     PagedCache c;
     int B, T, pages_per_seq;
+    int tok;                 // tokens a warp, set by the launch
+    unsigned per_token_inv;  // 2^32 / pieces of a token
     long long bt_stride;
     const int32_t *block_table, *cu;
     void *k_out, *v_out;

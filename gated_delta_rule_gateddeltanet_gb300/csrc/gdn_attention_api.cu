@@ -21,7 +21,7 @@ long long stride_or(int64_t given, int64_t least) { return given == 0 ? least : 
 gdn_status check_cache_sizes(const gdn_kv_cache &c) {
     if (!valid_io(c.cache_dtype) && !eight_bit(c.cache_dtype)) return GDN_ERR_DTYPE;
     if (c.num_pages < 1 || c.page_size < 1 || (int64_t)c.num_pages * c.page_size > INT32_MAX) return GDN_ERR_SHAPE;
-    if (c.num_kv_heads < 1 || (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)) return GDN_ERR_SHAPE;
+    if (c.num_kv_heads < 1 || c.num_kv_heads > 65535 || (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
 
@@ -204,7 +204,7 @@ gdn_status gdn_kv_cache_write(const gdn_kv_write_args *a, gdn_stream_t stream) {
         (qn && (!aligned16(a->q) || !aligned16(a->q_out) || (p.q_stride * esz) % 16 || (p.qo_stride * esz) % 16)))
         return GDN_ERR_ALIGN;
     if (qn && a->q == a->q_out && p.q_stride != p.qo_stride) return GDN_ERR_ARG;
-    if ((int64_t)a->total_tokens * (2 * kn + qn) / 256 >= INT32_MAX) return GDN_ERR_SHAPE;
+    if ((int64_t)a->total_tokens * (2 * kn + qn) / 64 >= INT32_MAX) return GDN_ERR_SHAPE;
     p.T = a->total_tokens;
     p.Hq = a->num_q_heads;
     p.rot = a->table ? a->rotary_dim : 0;

@@ -3,14 +3,28 @@
 //
 // Both are HBM streams: a write reads a token's k, v (and q) once and writes
 // its cache rows once; a read back reads cache rows once and writes them in
-// the I/O type.  At decode sizes a write is a launch latency and three
-// dependent loads (slot, row, table), so it takes the query rotation along.
+// the I/O type.  At decode sizes a write is a launch and two dependent loads
+// (position, table), so it takes the query rotation along: 1.8 us for 64 tokens
+// of 8 + 8 heads of 128.
 //
 // Write: a row (one token's channels of one head) belongs to a group of
 // d * sizeof(T) / 32 lanes, each holding two 16-byte groups with whole channel
 // pairs.  The rotation needs no exchange and the largest magnitude is a few
 // shuffles inside the group; the quantised row leaves as one contiguous run.
+// 8 x 512 BF16 tokens of 8 + 8 heads of 128: 8.8 us to e4m3, 10.5 us to int8
+// (their traffic: 3.9 us), bound by instructions (conversion and rotation).
+//
+// Read back: a warp looks up its tokens' rows, a lane each, and then moves them
+// in pieces of 16 output bytes, READ_UNROLL in flight a lane (2: 45.5 us instead of
+// 41.7 us for int8; 8: the same, 16-bit rows 19% slower).  Keys first, then values: the two in turn ran 20%
+// slower at 16 bits.  39,000 tokens of 8 + 8 int8 heads of 128 to BF16: 41.7 us,
+// 5.9 TB/s (0.87 of a copy's rate); 16-bit rows 52 us, 6.1 TB/s; four contexts
+// of at most 60 tokens 2.4 us.
 #include "attn_internal.cuh"
+
+#include <string.h>
+
+#include <algorithm>
 
 namespace gdn {
 namespace {
@@ -32,7 +46,7 @@ struct Elem<GDN_INT8> { using type = int8_t; };
 
 // A row's scale for its largest magnitude (infinity marks a row with a
 // non-finite channel).  e4m3 takes a power of two: with top = m 2^e, m in
-// [1/2, 1), top <= 448 * 2^x = 0.875 * 2^(x+9) for x = e - 9 if m <= 0.875, else e - 8.
+// [1, 2), top <= 448 * 2^x = 1.75 * 2^(x+8) for x = e - 8 if m <= 1.75, else e - 7.
 template <int CacheDtype>
 __device__ __forceinline__ float row_scale(float top) {
     if (!(top <= 3.402823466e38f)) return __int_as_float(0x7fc00000);
@@ -40,27 +54,47 @@ __device__ __forceinline__ float row_scale(float top) {
     if constexpr (CacheDtype == GDN_INT8) {
         return __fdiv_rn(top, 127.f);
     } else {
-        int e;
-        const float m = frexpf(top, &e);
-        return __int_as_float((max(e - (m > 0.875f ? 8 : 9), -120) + 127) << 23);
+        const int bits = __float_as_int(top);
+        const int e = (bits >> 23) - 127 - ((bits & 0x7fffff) > 0x600000 ? 7 : 8);
+        return __int_as_float((max(e, -120) + 127) << 23);
     }
 }
 
-// N channels (a multiple of 4) as 8-bit values.
+// N channels (a multiple of 4) as 8-bit values.  int8 is the correctly rounded
+// quotient x / scale, rounded to the nearest integer, ties to even.  The
+// product y with the reciprocal is within 2^-15 of it (at most 127, three
+// roundings of 2^-24), which decides unless y is that close to the middle of
+// two integers: 0.5% of 16-bit inputs, whose scale is a short ratio.  h, the
+// multiple of 1/2 next to y, is then that middle, x - h scale is exact, and
+// z = h + (x - h scale) / scale, rounded once, lies on the quotient's side of h
+// or on h: the reciprocal's error moves the second term by less than 2^-25 ulp
+// of h where it reaches half an ulp, and a quotient of two floats is further
+// than that from the middle between two floats.
 template <int CacheDtype, int N>
 __device__ __forceinline__ void quantise(const float (&x)[N], float scale, uint32_t (&out)[N / 4]) {
+    if constexpr (CacheDtype == GDN_INT8) {
+        int q[N];
+        if (scale >= 0x1p-100f) {
+            const float inv = __frcp_rn(scale);
+            constexpr float HALVES = 6291456.f, WHOLES = 12582912.f;  // 1.5 * 2^22, 1.5 * 2^23: ulps of 1/2 and 1
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        if constexpr (CacheDtype == GDN_INT8) {
-            uint32_t w = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int q = min(127, max(-127, __float2int_rn(__fdiv_rn(x[i + j], scale))));
-                w |= (uint32_t)(q & 255) << (8 * j);
+            for (int i = 0; i < N; ++i) {
+                const float h = __fsub_rn(__fadd_rn(__fmul_rn(x[i], inv), HALVES), HALVES);
+                const float z = __fmaf_rn(__fmaf_rn(-h, scale, x[i]), inv, h);
+                q[i] = __float_as_int(__fadd_rn(z, WHOLES));  // its low byte is the integer
             }
-            out[i / 4] = w;
-        } else {
-            const float inv = __fdiv_rn(1.f, scale);  // a power of two: exact
+        } else {  // subnormal remainders, and NaN
+#pragma unroll
+            for (int i = 0; i < N; ++i) q[i] = min(127, max(-127, __float2int_rn(__fdiv_rn(x[i], scale))));
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            out[i / 4] = __byte_perm(__byte_perm(q[i], q[i + 1], 0x0040), __byte_perm(q[i + 2], q[i + 3], 0x0040), 0x5410);
+    } else {
+        // the reciprocal of a power of two is exact; a NaN stays one
+        const float inv = scale == scale ? __int_as_float((254 << 23) - __float_as_int(scale)) : scale;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
             uint16_t lo, hi;
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[i + 1] * inv), "f"(x[i] * inv));
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[i + 3] * inv), "f"(x[i + 2] * inv));
@@ -75,36 +109,22 @@ __global__ void __launch_bounds__(NT) kv_write_kernel(const KvWriteParams p) {
     using C = typename Elem<CacheDtype>::type;
     constexpr int N = Vec16<T>::N;
     constexpr bool Q8 = CacheDtype == GDN_FP8_E4M3 || CacheDtype == GDN_INT8;
-    const int lanes = p.c.d / (2 * N);  // 4 to 32 lanes a row
-    const int rows = 2 * p.c.H + p.Hq;  // rows a token: k heads, v heads, q heads
-    const long long row = ((long long)blockIdx.x * NT + threadIdx.x) / lanes;
-    const int item = threadIdx.x % lanes;
-    const long long t = row / rows;
-    const int which = (int)(row - t * rows);
+    const int lane_bits = 31 - __clz(p.c.d / (2 * N)), lanes = 1 << lane_bits;  // 4 to 32 lanes a row
+    const unsigned rows = 2 * p.c.H + p.Hq;  // rows a token: k heads, v heads, q heads
+    // T * rows fits 32 bits (checked on the host)
+    const unsigned row = blockIdx.x * (unsigned)(NT >> lane_bits) + (threadIdx.x >> lane_bits);
+    const int item = threadIdx.x & (lanes - 1);
+    const unsigned token = row / rows;
+    const int which = (int)(row - token * rows);
+    const long long t = token;
     bool active = t < p.T;
     const bool is_k = which < p.c.H, is_q = which >= 2 * p.c.H;
     const int h = is_q ? which - 2 * p.c.H : is_k ? which : which - p.c.H;
-
-    int slot = -1, pos = 0;
-    if (active) {
-        slot = p.slots[t];
-        if (slot < -1 || slot >= p.c.num_pages * p.c.page_size) {
-            if (which == 0 && item == 0) flag_error(p.status, GDN_DEVERR_CACHE_SLOT);
-            active = false;
-        }
-        if (p.table) {
-            pos = p.pos[t];
-            if (pos < 0 || pos >= p.P) {
-                if (which == 0 && item == 0) flag_error(p.status, GDN_DEVERR_POSITION);
-                active = false;
-            }
-        }
-        if (slot < 0 && !is_q) active = false;
-    }
-
-    const bool turned = active && p.table && (is_k || is_q) && item * 2 * N < p.rot;
     int c1, c2;
     item_channels<N>(item, p.table ? p.rot : 0, p.interleaved != 0, c1, c2);
+
+    // The row, its slot and its position are independent loads.
+    int slot = -1, pos = 0;
     float x1[N] = {}, x2[N] = {};
     if (active) {
         const T *src = is_k ? static_cast<const T *>(p.k) + t * p.k_stride
@@ -114,9 +134,22 @@ __global__ void __launch_bounds__(NT) kv_write_kernel(const KvWriteParams p) {
         Vec16<T> a, b;
         a.load(src + c1);
         b.load(src + c2);
+        slot = p.slots[t];
+        if (p.table) pos = p.pos[t];
         a.to(x1);
         b.to(x2);
+        if (slot < -1 || slot >= p.c.num_pages * p.c.page_size) {
+            if (which == 0 && item == 0) flag_error(p.status, GDN_DEVERR_CACHE_SLOT);
+            active = false;
+        }
+        if (p.table && (pos < 0 || pos >= p.P)) {
+            if (which == 0 && item == 0) flag_error(p.status, GDN_DEVERR_POSITION);
+            active = false;
+        }
+        if (slot < 0 && !is_q) active = false;
     }
+
+    const bool turned = active && p.table && (is_k || is_q) && item * 2 * N < p.rot;
     if (turned) {
         float c[N], s[N];
         const float *tab = p.table + (long long)pos * p.rot + item * N;
@@ -146,7 +179,7 @@ __global__ void __launch_bounds__(NT) kv_write_kernel(const KvWriteParams p) {
         b.store(dst + c2);
         return;
     }
-    const long long page = slot / p.c.page_size, off = slot % p.c.page_size;
+    const long long page = slot / p.c.page_size, off = slot - page * p.c.page_size;
     C *dst = static_cast<C *>(is_k ? p.c.k : p.c.v) + page * p.c.page_stride + off * p.c.token_stride +
              h * p.c.head_stride;
     if constexpr (Q8) {
@@ -174,106 +207,139 @@ __global__ void __launch_bounds__(NT) kv_write_kernel(const KvWriteParams p) {
 
 // ---------------------------------------------------------------- read back
 
-constexpr int READ_TOKENS = 16;  // output tokens a CTA
-constexpr int ITEM = 16;         // channels a thread moves at a time
+constexpr int READ_UNROLL = 4;  // pieces in flight a lane
 
-template <int CacheDtype>
-__device__ __forceinline__ void load_item(const typename Elem<CacheDtype>::type *src, float scale, float (&x)[ITEM]) {
-    if constexpr (CacheDtype == GDN_FP8_E4M3 || CacheDtype == GDN_INT8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(src);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// N channels of a cache row, as loaded.
+template <int CacheDtype, int N>
+struct Raw {
+    using C = typename Elem<CacheDtype>::type;
+    static constexpr int WORDS = N * (int)sizeof(C) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const C *src) {
+        if constexpr (WORDS % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (CacheDtype == GDN_INT8) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[4 * i + j] = (float)(int8_t)(w[i] >> (8 * j)) * scale;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t h2;
-                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w[i] >> (16 * j))));
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-                    x[4 * i + 2 * j] = f.x * scale;
-                    x[4 * i + 2 * j + 1] = f.y * scale;
-                }
+            for (int i = 0; i < WORDS; i += 4) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(src + i * 4 / sizeof(C));
+                w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
             }
-        }
-    } else {
-        using T = typename Elem<CacheDtype>::type;
-        constexpr int N = Vec16<T>::N;
-#pragma unroll
-        for (int i = 0; i < ITEM; i += N) {
-            Vec16<T> v;
-            v.load(src + i);
-#pragma unroll
-            for (int j = 0; j < N; ++j) x[i + j] = to_f32(v.e[j]);
+        } else if constexpr (WORDS == 2) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(src);
+            w[0] = u.x, w[1] = u.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(src);
         }
     }
-}
+    __device__ __forceinline__ void to(float scale, float (&x)[N]) const {
+        if constexpr (CacheDtype == GDN_FP8_E4M3 || CacheDtype == GDN_INT8) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const uint32_t pair = w[i / 4] >> (8 * (i % 4));
+                if constexpr (CacheDtype == GDN_INT8) {
+                    x[i] = (float)(int8_t)pair * scale;
+                    x[i + 1] = (float)(int8_t)(pair >> 8) * scale;
+                } else {
+                    uint32_t h2;
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)pair));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+                    x[i] = f.x * scale;
+                    x[i + 1] = f.y * scale;
+                }
+            }
+        } else {
+            C e[N];
+            memcpy(e, w, sizeof(w));
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = to_f32(e[i]);
+        }
+    }
+};
 
+// blockIdx.y: keys, values.  A warp takes p.tok tokens (at most 32): a lane looks up each token's
+// sequence, page and row, then all lanes move the rows' pieces of 16 output
+// bytes, U of them in flight.
 template <typename T, int CacheDtype>
 __global__ void __launch_bounds__(NT) kv_read_kernel(const KvReadParams p) {
     dependent_prologue();
     using C = typename Elem<CacheDtype>::type;
     constexpr bool Q8 = CacheDtype == GDN_FP8_E4M3 || CacheDtype == GDN_INT8;
-    __shared__ long long row_off[READ_TOKENS], scale_off[READ_TOKENS];  // -1: skipped, -2: zero row
-    const int t0 = blockIdx.x * READ_TOKENS;
-    if (threadIdx.x < READ_TOKENS) {
-        const int t = t0 + threadIdx.x;
-        long long off = -1, soff = 0;
-        // the last sequence that starts at or before t
-        int lo = 0, hi = p.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.cu[mid] <= t) lo = mid;
-            else hi = mid;
+    constexpr int N = Vec16<T>::N;
+    constexpr int U = READ_UNROLL;
+    const int lane = threadIdx.x % 32;
+    const long long t0 = ((long long)blockIdx.x * (NT / 32) + threadIdx.x / 32) * p.tok;
+    if (t0 >= p.T) return;
+    const int tokens = (int)min((long long)p.tok, p.T - t0);
+
+    // the last sequence that starts at or before t0, all lanes probing; then before the lane's own token
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned before = __ballot_sync(0xffffffffu, at < hi && p.cu[at] <= t0);
+        const int k = before ? 31 - __clz(before) : 0;
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    long long off = -1, soff = 0;  // -1: skipped, -2: a row of zeros
+    if (lane < tokens) {
+        const int t = (int)t0 + lane;
+        int begin = p.cu[lo], end = p.cu[lo + 1];
+        if (t >= end && lo + 1 < p.B) {
+            hi = p.B;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.cu[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            begin = p.cu[lo], end = p.cu[lo + 1];
         }
-        const int begin = p.cu[lo], end = p.cu[lo + 1];
-        if (t < p.T) {
-            if (begin < 0 || t < begin || t >= end || end > p.T ||
-                (long long)(t - begin) >= (long long)p.pages_per_seq * p.c.page_size) {
-                flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
+        const int pos = t - begin;
+        if (begin < 0 || pos < 0 || t >= end || end > p.T ||
+            (long long)pos >= (long long)p.pages_per_seq * p.c.page_size) {
+            flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
+        } else {
+            const int page = p.block_table[lo * p.bt_stride + pos / p.c.page_size];
+            const int in_page = pos % p.c.page_size;
+            if (page < 0 || page >= p.c.num_pages) {
+                flag_error(p.status, GDN_DEVERR_PAGE);
+                off = -2;
             } else {
-                const int pos = t - begin;
-                const int page = p.block_table[lo * p.bt_stride + pos / p.c.page_size];
-                const int in_page = pos % p.c.page_size;
-                if (page < 0 || page >= p.c.num_pages) {
-                    flag_error(p.status, GDN_DEVERR_PAGE);
-                    off = -2;
-                } else {
-                    off = page * p.c.page_stride + in_page * p.c.token_stride;
-                    soff = page * p.c.s_page_stride + in_page * p.c.s_token_stride;
-                }
+                off = page * p.c.page_stride + in_page * p.c.token_stride;
+                soff = page * p.c.s_page_stride + in_page * p.c.s_token_stride;
             }
         }
-        row_off[threadIdx.x] = off;
-        scale_off[threadIdx.x] = soff;
     }
-    __syncthreads();
-    const int per_head = p.c.d / ITEM, per_half = p.c.H * per_head;
-    const int n = READ_TOKENS * 2 * per_half;
-    for (int i = threadIdx.x; i < n; i += NT) {
-        const int r = i / (2 * per_half), j = i - r * 2 * per_half;
-        const bool is_v = j >= per_half;
-        const int k = is_v ? j - per_half : j;
-        const int h = k / per_head, ch = (k - h * per_head) * ITEM;
-        const long long off = row_off[r];
-        if (off == -1) continue;
-        float x[ITEM] = {};
-        if (off >= 0) {
-            float scale = 1.f;
-            if constexpr (Q8) scale = (is_v ? p.c.v_scale : p.c.k_scale)[scale_off[r] + h * p.c.s_head_stride];
-            load_item<CacheDtype>(static_cast<const C *>(is_v ? p.c.v : p.c.k) + off + h * p.c.head_stride + ch, scale,
-                                  x);
+
+    const int head_shift = 31 - __clz(p.c.d / N);  // a head has 8 to 64 pieces
+    const int per_token = p.c.H << head_shift, n = tokens * per_token;
+    const C *src = static_cast<const C *>(blockIdx.y ? p.c.v : p.c.k);
+    const float *scales = blockIdx.y ? p.c.v_scale : p.c.k_scale;
+    T *out = static_cast<T *>(blockIdx.y ? p.v_out : p.k_out) + t0 * p.c.H * p.c.d;
+    for (int base = 0; base < n; base += 32 * U) {
+        Raw<CacheDtype, N> raw[U];
+        float scale[U];
+        T *dst[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + 32 * u + lane;
+            const int r = p.tok == 1 ? 0 : __umulhi((unsigned)i, p.per_token_inv);
+            const int k = i - r * per_token;
+            const int h = k >> head_shift, ch = (k & ((1 << head_shift) - 1)) * N;
+            const long long o = __shfl_sync(0xffffffffu, off, r), so = __shfl_sync(0xffffffffu, soff, r);
+            dst[u] = i < n && o != -1 ? out + (long long)i * N : nullptr;
+            raw[u] = {};
+            scale[u] = 0.f;
+            if (i < n && o >= 0) {
+                raw[u].load(src + o + h * p.c.head_stride + ch);
+                if constexpr (Q8) scale[u] = scales[so + h * p.c.s_head_stride];
+            }
         }
-        T *dst = static_cast<T *>(is_v ? p.v_out : p.k_out) + ((long long)(t0 + r) * p.c.H + h) * p.c.d + ch;
-        constexpr int N = Vec16<T>::N;
 #pragma unroll
-        for (int e = 0; e < ITEM; e += N) {
+        for (int u = 0; u < U; ++u) {
+            if (!dst[u]) continue;
+            float x[N];
+            raw[u].to(scale[u], x);
             Vec16<T> v;
-#pragma unroll
-            for (int u = 0; u < N; ++u) v.e[u] = from_f32<T>(x[e + u]);
-            v.store(dst + e);
+            v.from(x);
+            v.store(dst[u]);
         }
     }
 }
@@ -295,7 +361,8 @@ cudaError_t write_io(const KvWriteParams &p, int io_dtype, int cache_dtype, cuda
 
 template <typename T>
 cudaError_t read_io(const KvReadParams &p, int cache_dtype, cudaStream_t stream) {
-    const dim3 grid((unsigned)((p.T + READ_TOKENS - 1) / READ_TOKENS));
+    const long long warps = (p.T + (long long)p.tok - 1) / p.tok;
+    const dim3 grid((unsigned)((warps + NT / 32 - 1) / (NT / 32)), 2);
     switch (cache_dtype) {
         case GDN_F16: return launch_dependent(kv_read_kernel<T, GDN_F16>, grid, dim3(NT), 0, stream, p);
         case GDN_BF16: return launch_dependent(kv_read_kernel<T, GDN_BF16>, grid, dim3(NT), 0, stream, p);
@@ -316,8 +383,14 @@ cudaError_t launch_kv_write(const KvWriteParams &p, int io_dtype, int cache_dtyp
     }
 }
 
-cudaError_t launch_kv_read(const KvReadParams &p, int io_dtype, int cache_dtype, cudaStream_t stream) {
-    if (p.T == 0 || p.B == 0) return cudaSuccess;
+cudaError_t launch_kv_read(const KvReadParams &given, int io_dtype, int cache_dtype, cudaStream_t stream) {
+    if (given.T == 0 || given.B == 0) return cudaSuccess;
+    KvReadParams p = given;
+    // two passes of a warp's pieces, fewer tokens if that leaves warps out
+    const long long per_token = (long long)p.c.H * p.c.d * (io_dtype == GDN_F32 ? 4 : 2) / 16;
+    const long long most = 2 * 32 * READ_UNROLL / per_token, share = p.T / (32LL * current_device_sms());
+    p.tok = (int)std::max(1LL, std::min(std::min(most, share), 32LL));
+    p.per_token_inv = (unsigned)((1ULL << 32) / per_token + 1);  // exact below 2^32 / per_token (1: not used)
     switch (io_dtype) {
         case GDN_F16: return read_io<__half>(p, cache_dtype, stream);
         case GDN_BF16: return read_io<__nv_bfloat16>(p, cache_dtype, stream);

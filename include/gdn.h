@@ -575,7 +575,7 @@ gdn_status gdn_rotary(const gdn_rotary_args *args, gdn_stream_t stream);
 typedef struct gdn_kv_cache {
     int32_t num_pages;    /* num_pages * page_size < 2^31 */
     int32_t page_size;    /* >= 1 */
-    int32_t num_kv_heads;
+    int32_t num_kv_heads; /* 1 to 65535 */
     int32_t head_dim;     /* 64, 128 or 256 */
     int32_t cache_dtype;  /* GDN_F32, GDN_F16, GDN_BF16, GDN_FP8_E4M3 or GDN_INT8 */
     int64_t page_stride, token_stride, head_stride;                    /* elements */

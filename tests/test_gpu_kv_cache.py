@@ -224,3 +224,62 @@ def test_no_tokens():
     cu = torch.zeros(3, dtype=torch.int32, device=dev())
     a, b = gdn.kv_cache_read(cache, torch.zeros(2, 1, dtype=torch.int32, device=dev()), cu, 0)
     assert a.shape == (0, 2, 64) and a.dtype == F16
+
+
+@pytest.mark.parametrize("size", [2.0 ** -140, 2.0 ** -90, 1.0, 2.0 ** 90])
+def test_int8_rows_near_the_middle_of_two_integers(size):
+    """FP32 rows of one channel 127 s and the others within three units in the last place of (n + 1/2) s:
+    the stored integer is the FP32 quotient x / scale rounded to even, at subnormal scales too."""
+    rng = np.random.default_rng(int(abs(np.log2(size))))
+    T, d, page = 96, 64, 16
+    top = (rng.random((T, 1)) + 0.5).astype(np.float64) * size
+    x = ((rng.integers(-126, 126, (T, d)) + 0.5) * top / 127).astype(np.float32)
+    x = (x.view(np.int32) + rng.integers(-3, 4, (T, d)).astype(np.int32)).view(np.float32)
+    x[:, 5] = top[:, 0]
+    cache = gdn.PagedKVCache.allocate(T // page, page, 1, d, dtype=I8, device=dev())
+    k = torch.from_numpy(x).to(dev()).view(T, 1, d)
+    gdn.kv_cache_write(k, k, cache, torch.arange(T, dtype=torch.int32, device=dev()))
+    largest = np.abs(x).max(-1, keepdims=True)
+    scale = largest / np.float32(127)
+    # (bit patterns stepped below the smallest subnormal are NaN: such rows have a NaN scale, their integers mean nothing)
+    finite = np.isfinite(x).all(-1)
+    want = np.clip(np.rint(x[finite] / scale[finite]), -127, 127).astype(np.int8)
+    got_scale = cache.k_scale.cpu().numpy().reshape(T, 1)
+    assert scale.dtype == np.float32 and np.array_equal(got_scale, scale, equal_nan=True)
+    assert np.array_equal(cache.k.cpu().numpy().reshape(T, d)[finite], want)
+
+
+def test_read_back_of_many_short_and_empty_sequences():
+    """Sequences of zero to three tokens, more of them than a warp probes at once, some empty at both ends."""
+    lens = [0, 0] + [(7 * i) % 4 for i in range(1500)] + [0]
+    T, page, B = sum(lens), 2, len(lens)
+    for heads, d in ((1, 64), (3, 256)):
+        pages = B * 2
+        cache = gdn.PagedKVCache.allocate(pages, page, heads, d, dtype=F16, device=dev())
+        cache.k.copy_(torch.randn(cache.k.shape, device=dev()))
+        cache.v.copy_(torch.randn(cache.v.shape, device=dev()))
+        table = torch.randperm(pages, device=dev()).view(B, 2).to(torch.int32)
+        cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(dev())
+        k, v = gdn.kv_cache_read(cache, table, cu, T)
+        seq = torch.repeat_interleave(torch.arange(B), torch.tensor(lens)).to(dev())
+        pos = torch.arange(T, device=dev()) - cu[seq].long()
+        at = (table[seq, pos // page].long(), pos % page)
+        assert torch.equal(k, cache.k[at]) and torch.equal(v, cache.v[at])
+
+
+@pytest.mark.parametrize("kind", [F16, I8])
+def test_read_back_of_long_contexts(kind):
+    """Enough tokens that a warp takes several (one narrow head), with a last warp that is not full."""
+    T, page, d = 40001, 16, 64
+    cache = gdn.PagedKVCache.allocate(T // page + 1, page, 1, d, dtype=kind, device=dev())
+    x = torch.randn(T, 1, d, device=dev()).half()
+    slots = torch.arange(T, dtype=torch.int32, device=dev())
+    gdn.kv_cache_write(x, x.neg(), cache, slots)
+    table = torch.arange(T // page + 1, dtype=torch.int32, device=dev())[None]
+    k, v = gdn.kv_cache_read(cache, table, torch.tensor([0, T], dtype=torch.int32, device=dev()), T)
+    if kind == F16:
+        assert torch.equal(k, x) and torch.equal(v, x.neg())
+    else:
+        step = x.float().abs().amax(-1, keepdim=True) / 127
+        assert torch.all((k.float() - x.float()).abs() <= step * 0.5001 + x.float().abs() * 2.0 ** -10)
+        assert torch.equal(v, k.neg())
