@@ -102,7 +102,8 @@ def test_rotary_refusals(lib, kw, code):
 
 CACHE_REFUSALS = [
     ({"cache.cache_dtype": 7}, DTYPE), ({"cache.head_dim": 96}, SHAPE), ({"cache.page_size": 0}, SHAPE),
-    ({"cache.num_pages": 1 << 28}, SHAPE), ({"cache.num_kv_heads": 0}, SHAPE), ({"cache.k": None}, NULL),
+    ({"cache.num_pages": 1 << 28}, SHAPE), ({"cache.num_kv_heads": 0}, SHAPE), ({"cache.num_kv_heads": 65536}, SHAPE),
+    ({"cache.k": None}, NULL),
     ({"cache.v": FAKE + 8}, ALIGN), ({"cache.page_stride": 4096, "cache.token_stride": 260, "cache.head_stride": 128}, ALIGN),
     ({"cache.page_stride": 4096, "cache.token_stride": 0, "cache.head_stride": 128}, SHAPE),
     ({"cache.page_stride": 1 << 40, "cache.token_stride": 256, "cache.head_stride": 128}, SHAPE),
