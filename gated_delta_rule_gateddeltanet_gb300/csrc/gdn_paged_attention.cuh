@@ -60,13 +60,18 @@ namespace attn {
 
 // ---------------------------------------------------------------- instructions
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int src_bytes) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(src_bytes)
-                     : "memory");
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, int src_bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// 4 bytes of a line that stays in L2 for its other readers.
+__device__ __forceinline__ void copy_async4_kept(uint32_t dst, const void *src, int src_bytes, uint64_t policy) {
+    asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 4, %2, %3;" ::"r"(dst), "l"(src), "r"(src_bytes), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t keep_policy() {
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
 }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     if (tid < W * S) ptx::mbar_init(full + tid, Q8 || BY_ROWS ? 33 : 1);  // tensor copies, and each lane's other copies
     if (tid < 2) {
-        ptx::mbar_init(q_full + tid, 32);
+        ptx::mbar_init(q_full + tid, 32 * C::NJ);
         ptx::mbar_init(q_empty + tid, W);
     }
     if (tid == 0) {
@@ -522,82 +527,79 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         const Parts<C> parts(p.partials, gridDim.x);
         int split_parts = 0;
         open_segment<C>(use, 0);
-        // The queries of a segment into shared memory, by the first joiner warp.  Scores are (K q + bias) scale:
+        // The queries of a segment into shared memory, ROWS / NJ rows a warp with all loads in flight at once (the
+        // consumers' copies queue up in front of a later one: it took 5 us).  Scores are (K q + bias) scale:
         // queries over 8-bit rows go as FP16, BF16 ones scaled by a power of two that brings the row's largest
         // magnitude to [1, 2), and int8 keys are multiplied as (128 + k) 2^-24 (see widen_keys).
         auto fetch = [&](const Walk &w, int segment) {
-            if (j >= 32 || w.left <= 0) return;
+            if (w.left <= 0) return;
             const int b = segment & 1, rows = min(ROWS, w.s.n * p.G - w.row0);
             constexpr int EB = F32 ? 4 : 2, LANE = D * EB / 32;  // bytes a lane takes of a row: 4 to 32
-            constexpr int WORDS = LANE / 4, BATCH = ROWS < 8 ? ROWS : 8;
-            const int group = lane < ROWS ? w.row0 + min(lane, rows - 1) : 0;  // lane r: where row r is
+            constexpr int WORDS = LANE / 4, BATCH = ROWS / C::NJ;
+            const int r0 = BATCH * (warp - W);
+            const int group = w.row0 + min(lane, rows - 1);  // lane r: where row r is
             const int token = w.s.n == 1 ? 0 : (int)((uint32_t)group / (uint32_t)p.G);
             const long long row = ((long long)(w.s.cu0 + token) * p.q_stride + (w.head * p.G + group - token * p.G) * D) * EB;
-            bool free = false;
-#pragma unroll 1
-            for (int r0 = 0; r0 < ROWS; r0 += BATCH) {
-                uint32_t x[BATCH][WORDS];
+            uint32_t x[BATCH][WORDS];
 #pragma unroll
-                for (int r = 0; r < BATCH; ++r) {
-                    const uint8_t *src = static_cast<const uint8_t *>(p.q) + __shfl_sync(FULL, row, r0 + r) + lane * LANE;
+            for (int r = 0; r < BATCH; ++r) {
+                const uint8_t *src = static_cast<const uint8_t *>(p.q) + __shfl_sync(FULL, row, r0 + r) + lane * LANE;
 #pragma unroll
-                    for (int i = 0; i < WORDS; ++i) x[r][i] = 0u;
-                    if (r0 + r < rows) {
-                        if constexpr (WORDS == 1) x[r][0] = *reinterpret_cast<const uint32_t *>(src);
-                        if constexpr (WORDS == 2) lds<2>(x[r], src);
-                        if constexpr (WORDS == 4) lds<4>(x[r], src);
-                        if constexpr (WORDS == 8) {
-                            lds<4>(reinterpret_cast<uint32_t(&)[4]>(x[r][0]), src);
-                            lds<4>(reinterpret_cast<uint32_t(&)[4]>(x[r][4]), src + 16);
-                        }
+                for (int i = 0; i < WORDS; ++i) x[r][i] = 0u;
+                if (r0 + r < rows) {
+                    if constexpr (WORDS == 1) x[r][0] = *reinterpret_cast<const uint32_t *>(src);
+                    if constexpr (WORDS == 2) lds<2>(x[r], src);
+                    if constexpr (WORDS == 4) lds<4>(x[r], src);
+                    if constexpr (WORDS == 8) {
+                        lds<4>(reinterpret_cast<uint32_t(&)[4]>(x[r][0]), src);
+                        lds<4>(reinterpret_cast<uint32_t(&)[4]>(x[r][4]), src + 16);
                     }
                 }
-                if (!free) ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead);
-                free = true;
+            }
+            ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead);
 #pragma unroll
-                for (int r = 0; r < BATCH; ++r) {
-                    float scale = p.scale_log2, sum = 0.f;
-                    if constexpr (Q8) {
-                        if (p.io_bf16) {
-                            float top = 0.f;
+            for (int r = 0; r < BATCH; ++r) {
+                float scale = p.scale_log2, sum = 0.f;
+                if constexpr (Q8) {
+                    if (p.io_bf16) {
+                        float top = 0.f;
 #pragma unroll
-                            for (int i = 0; i < WORDS; ++i) {
-                                const float2 f = unpack2<true>(x[r][i]);
-                                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                            }
-#pragma unroll
-                            for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-                            // the exponent of top, kept where both powers of two are normal
-                            int e = (int)(__float_as_uint(top) >> 23 & 255) - 127;
-                            e = top > 0.f && top <= 3.402823466e38f ? min(max(e, -100), 126) : 0;
-                            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                            scale *= __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                            for (int i = 0; i < WORDS; ++i) {
-                                const float2 f = unpack2<true>(x[r][i]);
-                                x[r][i] = pack2<false>(f.x * down, f.y * down);
-                            }
+                        for (int i = 0; i < WORDS; ++i) {
+                            const float2 f = unpack2<true>(x[r][i]);
+                            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                         }
-                        if constexpr (CT == GDN_INT8) {
 #pragma unroll
-                            for (int i = 0; i < WORDS; ++i) {
-                                const float2 f = unpack2<false>(x[r][i]);
-                                sum += f.x + f.y;
-                            }
-                            sum = warp_sum(sum);
-                            scale *= 16777216.f;
+                        for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+                        // the exponent of top, kept where both powers of two are normal
+                        int e = (int)(__float_as_uint(top) >> 23 & 255) - 127;
+                        e = top > 0.f && top <= 3.402823466e38f ? min(max(e, -100), 126) : 0;
+                        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                        scale *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                        for (int i = 0; i < WORDS; ++i) {
+                            const float2 f = unpack2<true>(x[r][i]);
+                            x[r][i] = pack2<false>(f.x * down, f.y * down);
                         }
                     }
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(queries + (b * ROWS + r0 + r) * C::QROW + lane * LANE);
-                    if constexpr (WORDS == 1) dst[0] = x[r][0];
-                    if constexpr (WORDS == 2) *reinterpret_cast<uint2 *>(dst) = make_uint2(x[r][0], x[r][1]);
-                    if constexpr (WORDS >= 4) {
+                    if constexpr (CT == GDN_INT8) {
 #pragma unroll
-                        for (int i = 0; i < WORDS; i += 4)
-                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(x[r][i], x[r][i + 1], x[r][i + 2], x[r][i + 3]);
+                        for (int i = 0; i < WORDS; ++i) {
+                            const float2 f = unpack2<false>(x[r][i]);
+                            sum += f.x + f.y;
+                        }
+                        sum = warp_sum(sum);
+                        scale *= 16777216.f;
                     }
-                    if (lane == 0) q_stat[b * ROWS + r0 + r] = make_float2(scale, -128.f / 16777216.f * sum);
                 }
+                uint32_t *dst = reinterpret_cast<uint32_t *>(queries + (b * ROWS + r0 + r) * C::QROW + lane * LANE);
+                if constexpr (WORDS == 1) dst[0] = x[r][0];
+                if constexpr (WORDS == 2) *reinterpret_cast<uint2 *>(dst) = make_uint2(x[r][0], x[r][1]);
+                if constexpr (WORDS >= 4) {
+#pragma unroll
+                    for (int i = 0; i < WORDS; i += 4)
+                        *reinterpret_cast<uint4 *>(dst + i) = make_uint4(x[r][i], x[r][i + 1], x[r][i + 2], x[r][i + 3]);
+                }
+                if (lane == 0) q_stat[b * ROWS + r0 + r] = make_float2(scale, -128.f / 16777216.f * sum);
             }
             ptx::mbar_arrive(q_full + b);
         };
@@ -753,8 +755,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                         const uint32_t at = to + (x / PER_SPAN) * TT * C::SPAN + token * C::SPAN +
                                             ((y ^ (C::SPAN == 64 ? token >> 1 & 3 : token & 7)) << 4);
                         const long long src = o < 0 ? 0 : o + x * 16;
-                        copy_async<16>(at, static_cast<const uint8_t *>(p.c.k) + src, o < 0 ? 0 : 16);
-                        copy_async<16>(at + C::HALF, static_cast<const uint8_t *>(p.c.v) + src, o < 0 ? 0 : 16);
+                        copy_async16(at, static_cast<const uint8_t *>(p.c.k) + src, o < 0 ? 0 : 16);
+                        copy_async16(at + C::HALF, static_cast<const uint8_t *>(p.c.v) + src, o < 0 ? 0 : 16);
                     }
                 } else {
                     constexpr int MOST = TT / 8;  // boxes of 8 tokens or more
@@ -797,8 +799,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                                                   (long long)head * p.s_head_stride32
                                             : 0;
                     const uint32_t to = ptx::smem_u32(dst + 2 * C::HALF + 4 * lane);
-                    copy_async<4>(to, (TS == 2 || lane < 16 ? p.c.k_scale : p.c.v_scale) + at, ok);
-                    if (TS == 2) copy_async<4>(to + 4 * TT, p.c.v_scale + at, ok);
+                    const uint64_t keep = keep_policy();
+                    copy_async4_kept(to, (TS == 2 || lane < 16 ? p.c.k_scale : p.c.v_scale) + at, ok, keep);
+                    if (TS == 2) copy_async4_kept(to + 4 * TT, p.c.v_scale + at, ok, keep);
                 }
                 if (Q8 || BY_ROWS) copy_arrive(bar);
                 ++taken;
