@@ -70,7 +70,7 @@ __device__ __forceinline__ void copy_async4_kept(uint32_t dst, const void *src, 
 }
 __device__ __forceinline__ uint64_t keep_policy() {
     uint64_t policy;
-    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
     return policy;
 }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -233,7 +233,7 @@ struct Walk {
     int chunk, seg_chunks;   // the segment's chunks
     int head, row0;          // the unit's key head and first query row
     int seg_work, left;      // the work of the segment, and of this CTA from there on
-    int tile, tile_end;  // the warp's next tile and the segment's end
+    int tile, tile_end;  // the segment's tiles
 };
 
 constexpr int SMEM_LIMIT = 232448;
@@ -264,18 +264,21 @@ struct Cfg {
     // Bytes a staged query row; the padding keeps the lanes' reads of 8 rows free of bank conflicts.
     static constexpr int QROW = D * (F32 ? 4 : 2) + (Q8 ? 16 : 64);
     static constexpr int QUERIES = 2 * ROWS * (QROW + 8);  // and each row's (scale, bias)
-    static constexpr int HEAD = 3072;                    // scan, flags, barriers and walks
-    // Warps: W consumers and NJ joiners; 12 have 168 registers a thread, 8 (where a consumer's outputs alone
-    // take more than 64, or the ring has no room for more) have 255.
+    static constexpr int HEAD = 2048;                    // scan, flags, barriers and segments
+    // Warps: W consumers, NP producers and NJ joiners.  16 warps have 128 registers a thread, which they divide by
+    // role (a consumer's outputs take HELD); where the outputs take more than 64, or the ring has no room for more, 8 have 255.
     static constexpr int HELD = NT * D / 4;
     static constexpr int FACTORS = 8 * ROWS * 4 + ROWS * 8;
     static constexpr int ROOM = (SMEM_LIMIT - 1024 - HEAD - QUERIES - FACTORS) / SLOT;  // slots that fit
-    static constexpr int W = HELD <= 64 && ROOM >= 16 ? 8 : ROOM >= 12 ? 6 : ROOM >= 8 ? 4 : 3;
-    static constexpr int NJ = W == 8 ? 4 : 2;
+    static constexpr int W = HELD <= 64 && ROOM >= 16 ? 8 : ROOM >= 8 ? 4 : 3;
+    static constexpr int NP = W == 8 ? 4 : W == 4 ? 2 : 1, NJ = W == 8 ? 4 : 2;
+    static constexpr int PER = W / NP;  // consumers a producer feeds
+    static constexpr int LAUNCH_REGS = 128, CONSUMER_REGS = 168, PRODUCER_REGS = 72, JOINER_REGS = 104;
+    static_assert(8 * CONSUMER_REGS + 4 * PRODUCER_REGS + 4 * JOINER_REGS <= 16 * LAUNCH_REGS, "registers of the block");
     // What a unit costs besides its chunks (fetching queries, joining), in chunks: with 0 the CTAs with many
     // short units are late (256 requests of up to 1024 tokens: 59 us against 55 us; a decode step of 64 x 128 to 2048: 65 against 57).
     static constexpr int UNIT_WORK = 2;
-    static constexpr int THREADS = 32 * (W + NJ);
+    static constexpr int THREADS = 32 * (W + NP + NJ);
     static constexpr int S = ROOM / W < 8 ? ROOM / W : 8;  // ring slots a consumer
     static constexpr int SMEM = 1024 + HEAD + QUERIES + FACTORS + W * S * SLOT;  // (1024: the ring's alignment)
     // Weights of 8-bit values are single FP16 numbers: next to values of 8 bits, 11 are plenty, and the
@@ -283,7 +286,8 @@ struct Cfg {
     static constexpr bool SPLIT_P = !Q8;
     static constexpr float BIAS = CT == GDN_F16 || Q8 ? 6.f : -8.f;  // weights are 2^(s - m + BIAS)
     static constexpr float HEADROOM = 8.f;  // a score may exceed the maximum by this: FP16 weights stay below 2^14
-    static_assert(S >= 2 && 512 + W * S * 8 + 64 <= 1280 && 1280 + 2 * W * (int)sizeof(Walk) <= HEAD && HALF % 1024 == 0, "ring and barriers");
+    static_assert(S >= 2 && W % NP == 0 && 512 + 2 * W * S * 8 + 64 <= 1600 && 1600 + 2 * (int)sizeof(Walk) <= HEAD && HALF % 1024 == 0,
+                  "ring and barriers");
 };
 
 template <class C>
@@ -309,19 +313,19 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams &p, int b, bool fl
 }
 
 template <class C>
-__device__ __forceinline__ void open_segment(Walk &w, int first) {
+__device__ __forceinline__ void open_segment(Walk &w) {
     w.head = w.s.row_groups == 1 ? w.unit : (int)((uint32_t)w.unit / (uint32_t)w.s.row_groups);
     w.row0 = (w.unit - w.head * w.s.row_groups) * C::ROWS;
     w.seg_work = min(w.s.chunks + C::UNIT_WORK - w.pos, w.left);
     w.chunk = max(0, w.pos - C::UNIT_WORK);
     w.seg_chunks = max(0, w.pos + w.seg_work - C::UNIT_WORK) - w.chunk;
     if (w.seg_chunks == 0) w.left = 0;  // only a unit's fixed work is left: the next CTA, which has its chunks, does it
-    w.tile = w.chunk * C::W + first;
+    w.tile = w.chunk * C::W;
     w.tile_end = min((w.chunk + w.seg_chunks) * C::W, w.s.tiles);
 }
 
 template <class C>
-__device__ __forceinline__ void next_segment(Walk &w, const PagedAttnParams &p, int first) {
+__device__ __forceinline__ void next_segment(Walk &w, const PagedAttnParams &p) {
     w.left -= w.seg_work;
     if (w.left <= 0) return;
     w.pos = 0;
@@ -336,7 +340,7 @@ __device__ __forceinline__ void next_segment(Walk &w, const PagedAttnParams &p, 
         } while (w.s.units == 0);
         w.unit = 0;
     }
-    open_segment<C>(w, first);
+    open_segment<C>(w);
 }
 
 __device__ __forceinline__ long long divide(long long a, long long b) {
@@ -353,17 +357,18 @@ struct Shares {
     }
 };
 
-// Waits for a ring barrier's phase.  A wait that runs out (WAIT_LIMIT cycles;
-// it never does while the other side runs) marks the CTA dead: no wait of it
-// blocks any more and it writes no results.
+// The warp waits for a barrier's phase.  A wait that runs out (WAIT_LIMIT cycles;
+// it never does while the other roles run) marks the CTA dead: all waits of it
+// return false, its warps leave, and it writes no results.
 constexpr long long WAIT_LIMIT = 4000000000LL;
-__device__ __forceinline__ void ring_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
-    if (ptx::mbar_try_wait(bar, parity)) return;
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     const long long t0 = clock64();
-    while (!ptx::mbar_try_wait_for(bar, parity, 20000)) {
-        if (*dead) return;
+    while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_for(bar, parity, 20000))) {
         if (clock64() - t0 > WAIT_LIMIT) *dead = 1;
+        if (__any_sync(0xffffffffu, *dead != 0)) return false;
     }
+    return true;
 }
 
 // The barrier receives this lane's arrival when all its copies so far have landed.
@@ -371,6 +376,16 @@ __device__ __forceinline__ void copy_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void named_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+// The same, and whether x is set in any of the threads.
+__device__ __forceinline__ bool named_any(int id, int threads, bool x) {
+    int any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(threads), "r"((int)x)
+        : "memory");
+    return any != 0;
+}
 
 // What a CTA leaves for the join: the unit whose head it holds but not its end.
 struct Split {
@@ -419,6 +434,12 @@ struct Parts {
 
 // ---------------------------------------------------------------- the kernel
 
+// The registers that a role's warps (whole groups of four) go on with.
+template <int N>
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // BY_ROWS: pages are not a multiple of 8 tokens, rows are copied one by one (see launch_sized).
 template <int CT, class C, bool BY_ROWS>
 __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __grid_constant__ PagedAttnParams p,
@@ -436,10 +457,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     Walk *first = reinterpret_cast<Walk *>(smem + 128);                  // where this CTA's share begins
     volatile int *dead = reinterpret_cast<volatile int *>(smem + 272);   // a wait ran out
     int *part_slot = reinterpret_cast<int *>(smem + 288);                // [W] where a consumer left its part
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + 512);           // [W][S] a slot's tile has landed
-    uint64_t *q_full = full + W * S, *q_empty = q_full + 2;              // [2] a segment's queries
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + 512);           // [W][S] a slot's tile has landed, or it is free for a part
+    uint64_t *empty = full + W * S;                                      // [W][S] its tile or part has been used
+    uint64_t *q_full = empty + W * S, *q_empty = q_full + 2;             // [2] a segment and its queries
     uint64_t *j_full = q_empty + 2, *j_empty = j_full + 1;               // the consumers' parts of a segment
-    Walk *walks = reinterpret_cast<Walk *>(smem + 1280);                 // [W][2] where a consumer's products and copies are
+    Walk *segments = reinterpret_cast<Walk *>(smem + 1600);              // [2] for the consumers; none left: the end
     uint8_t *queries = smem + C::HEAD;                                   // [2][ROWS][QROW]
     float2 *q_stat = reinterpret_cast<float2 *>(queries + 2 * ROWS * C::QROW);  // [2][ROWS] scores' (scale, bias)
     float2 *joined = reinterpret_cast<float2 *>(queries + C::QUERIES);   // [ROWS] maxima and sums
@@ -448,7 +470,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     ring += (1024 - (ptx::smem_u32(ring) & 1023)) & 1023;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    if (tid < W * S) ptx::mbar_init(full + tid, Q8 || BY_ROWS ? 33 : 1);  // tensor copies, and each lane's other copies
+    if (tid < W * S) {
+        ptx::mbar_init(full + tid, Q8 || BY_ROWS ? 33 : 1);  // tensor copies, and each lane's other copies
+        ptx::mbar_init(empty + tid, 1);
+    }
     if (tid < 2) {
         ptx::mbar_init(q_full + tid, 32 * C::NJ);
         ptx::mbar_init(q_empty + tid, W);
@@ -521,22 +546,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     Walk use = *first;  // what the warp is at
 
     // ---- joiners: fetch the queries of the segments and add the consumers' parts of them
-    if (warp >= W) {
+    if (warp >= W + C::NP) {
+        if constexpr (W == 8) give_registers<C::JOINER_REGS>();
         constexpr int THREADS = 32 * C::NJ;
-        const int j = tid - 32 * W;
+        const int j = tid - 32 * (W + C::NP);
         const Parts<C> parts(p.partials, gridDim.x);
         int split_parts = 0;
-        open_segment<C>(use, 0);
+        open_segment<C>(use);
         // The queries of a segment into shared memory, ROWS / NJ rows a warp with all loads in flight at once (the
         // consumers' copies queue up in front of a later one: it took 5 us).  Scores are (K q + bias) scale:
         // queries over 8-bit rows go as FP16, BF16 ones scaled by a power of two that brings the row's largest
         // magnitude to [1, 2), and int8 keys are multiplied as (128 + k) 2^-24 (see widen_keys).
         auto fetch = [&](const Walk &w, int segment) {
-            if (w.left <= 0) return;
-            const int b = segment & 1, rows = min(ROWS, w.s.n * p.G - w.row0);
+            const int b = segment & 1;
+            if (w.left <= 0) {  // the end
+                if (!ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead)) return;
+                if (j == 0) segments[b].left = 0;
+                ptx::mbar_arrive(q_full + b);
+                return;
+            }
+            const int rows = min(ROWS, w.s.n * p.G - w.row0);
             constexpr int EB = F32 ? 4 : 2, LANE = D * EB / 32;  // bytes a lane takes of a row: 4 to 32
             constexpr int WORDS = LANE / 4, BATCH = ROWS / C::NJ;
-            const int r0 = BATCH * (warp - W);
+            const int r0 = BATCH * (warp - W - C::NP);
             const int group = w.row0 + min(lane, rows - 1);  // lane r: where row r is
             const int token = w.s.n == 1 ? 0 : (int)((uint32_t)group / (uint32_t)p.G);
             const long long row = ((long long)(w.s.cu0 + token) * p.q_stride + (w.head * p.G + group - token * p.G) * D) * EB;
@@ -556,7 +588,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     }
                 }
             }
-            ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead);
+            if (!ring_wait(q_empty + b, ((segment >> 1) + 1) & 1, dead)) return;
+            if (j == 0) segments[b] = w;
 #pragma unroll
             for (int r = 0; r < BATCH; ++r) {
                 float scale = p.scale_log2, sum = 0.f;
@@ -606,15 +639,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         fetch(use, 0);
         for (int segment = 0; use.left > 0; ++segment) {
             Walk next = use;
-            next_segment<C>(next, p, 0);
+            next_segment<C>(next, p);
             fetch(next, segment + 1);
             const int head = use.head, row0 = use.row0, rows = min(ROWS, use.s.n * p.G - row0);
             const int pos0 = use.s.len - use.s.n;
             const bool whole = use.seg_chunks == use.s.chunks;
-            ring_wait(j_full, segment & 1, dead);
+            if (named_any(1, THREADS, !ring_wait(j_full, segment & 1, dead))) break;  // (all of them, or none)
             const float *part[W];  // [ROWS][OROW], then the rows' (maximum, sum)
+            int at[W];
 #pragma unroll
-            for (int w = 0; w < W; ++w) part[w] = reinterpret_cast<const float *>(ring + (w * S + part_slot[w]) * C::SLOT);
+            for (int w = 0; w < W; ++w) {
+                at[w] = w * S + part_slot[w];
+                part[w] = reinterpret_cast<const float *>(ring + at[w] * C::SLOT);
+            }
             for (int r = j; r < ROWS; r += THREADS) {
                 float2 st[W];
                 float mm = NONE, ll = 0.f;
@@ -642,7 +679,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     const float f = factor[w * ROWS + r];
                     sum.x += f * x.x, sum.y += f * x.y, sum.z += f * x.z, sum.w += f * x.w;
                 }
-                if (*dead) continue;
                 if (whole) {
                     store_row<CT, C>(p, row0 + r, head, use.s.cu0, pos0, ch, sum, joined[r]);
                 } else {
@@ -653,6 +689,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             ptx::fence_proxy_async_smem();  // tensor copies will overwrite what the consumers stored
             named_sync(1, THREADS);
             if (j == 0) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) ptx::mbar_arrive(empty + at[w]);
                 ptx::mbar_arrive(j_empty);
                 if (!whole && use.chunk == 0) {  // the head of a unit that goes on: this CTA's last segment
                     split_parts = shares.owner(shares.begin(blockIdx.x + 1) - use.left - use.pos + C::UNIT_WORK + use.s.chunks - 1) - (int)blockIdx.x + 1;
@@ -665,155 +703,141 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             if (split_parts == 0) parts.split[blockIdx.x].parts = 0;
             if (*dead) flag_error(p.status, GDN_DEVERR_TIMEOUT);
         }
+        return;
+    }
+
+    // ---- producers: warp W + i copies the tiles of consumers i PER, ... ahead of them
+    if (warp >= W) {
+        if constexpr (W == 8) give_registers<C::PRODUCER_REGS>();
+        constexpr int PER = C::PER;
+        const int base = (warp - W) * PER;  // the first consumer
+        // A tile's keys (values) are `subs` boxes of box_tokens tokens, each within a page.  Lane i looks up box
+        // i % subs of the i / subs-th next of the producer's tiles (n-th tile: of consumer n % PER).
+        const int box_tokens = 1 << box_shift, subs = TT >> box_shift, batch = 32 / subs;
+        uint32_t puts = 0;     // byte q: consumer q's slot that is filled next
+        uint32_t wrapped = 0;  // bit q: the parity of its rounds through the ring
+        auto step = [&](int q) {
+            puts += 1u << 8 * q;
+            if ((puts >> 8 * q & 255) == S) puts -= (uint32_t)S << 8 * q, wrapped ^= 1u << q;
+        };
+        auto tile_of = [&](int n) { return use.tile + n / PER * W + base + n % PER; };
+        const uint64_t keep = Q8 ? keep_policy() : 0;
+        auto feed = [&]() {  // returns early in a dead CTA
+            open_segment<C>(use);
+            while (use.left > 0) {
+                const int head = use.head;
+                const int count = use.seg_chunks * PER;
+                for (int n0 = 0; n0 < count; n0 += batch) {
+                    int page = 0, in_page = 0;  // where the lane's box is
+                    const int tile = tile_of(n0 + lane / subs);
+                    const int t = use.s.t0 + tile * TT + (lane % subs << box_shift);
+                    const bool wanted = tile < use.tile_end && t < use.s.len && t + box_tokens > use.s.first;
+                    if (wanted) {
+                        const int i = p.page_shift >= 0 ? t >> p.page_shift : (int)((uint32_t)t / (uint32_t)p.c.page_size);
+                        in_page = t - i * p.c.page_size;
+                        page = p.block_table[use.s.b * p.bt_stride + i];
+                        // (a page outside the pool reads as zeros)
+                        if ((uint32_t)page >= (uint32_t)p.c.num_pages) flag_error(p.status, GDN_DEVERR_PAGE);
+                    }
+                    const uint32_t boxes = __ballot_sync(FULL, wanted);  // the lanes with boxes that are read
+                    for (int n = n0; n < min(n0 + batch, count); ++n) {
+                        const int box0 = (n - n0) * subs, q = n % PER;
+                        if (tile_of(n) >= use.tile_end) continue;
+                        const int slot = (base + q) * S + (puts >> 8 * q & 255);
+                        uint8_t *dst = ring + slot * C::SLOT;
+                        uint64_t *bar = full + slot;
+                        if (!ring_wait(empty + slot, (wrapped >> q & 1) ^ 1, dead)) return;
+                        const uint32_t mine = boxes >> box0 & (FULL >> (32 - subs));
+                        if constexpr (BY_ROWS) {
+                            if (lane == 0) ptx::mbar_arrive(bar);
+                            // lane box0 + i looked up token i: its row's byte offset, -1 if it is not read
+                            long long row = -1;
+                            if ((boxes >> lane & 1) && (uint32_t)page < (uint32_t)p.c.num_pages)
+                                row = (page * p.c.page_stride + in_page * p.c.token_stride + head * p.c.head_stride) * C::ESZ;
+                            constexpr int PIECES = C::RB / 16, PER_SPAN = C::SPAN / 16;
+                            const uint32_t to = ptx::smem_u32(dst);
+#pragma unroll 4
+                            for (int k = lane; k < TT * PIECES; k += 32) {
+                                const int token = k / PIECES, x = k % PIECES, y = x % PER_SPAN;
+                                const long long o = __shfl_sync(FULL, row, box0 + token);
+                                const uint32_t at = to + (x / PER_SPAN) * TT * C::SPAN + token * C::SPAN +
+                                                    ((y ^ (C::SPAN == 64 ? token >> 1 & 3 : token & 7)) << 4);
+                                const long long src = o < 0 ? 0 : o + x * 16;
+                                copy_async16(at, static_cast<const uint8_t *>(p.c.k) + src, o < 0 ? 0 : 16);
+                                copy_async16(at + C::HALF, static_cast<const uint8_t *>(p.c.v) + src, o < 0 ? 0 : 16);
+                            }
+                        } else {
+                            constexpr int MOST = TT / 8;  // boxes of 8 tokens or more
+                            int pg[MOST], off[MOST];
+#pragma unroll
+                            for (int b = 0; b < MOST; ++b) {
+                                if (b > 0 && b >= subs) break;
+                                // (num_pages is outside the map, which reads as zeros)
+                                pg[b] = (int)min((uint32_t)__shfl_sync(FULL, page, box0 + b), (uint32_t)p.c.num_pages);
+                                off[b] = __shfl_sync(FULL, in_page, box0 + b);
+                            }
+                            if (ptx::elect_one()) {
+                                ptx::mbar_arrive_expect_tx(bar, __popc(mine) * (2 * C::RB) << box_shift);
+                                if (subs == 1) {  // all spans at once
+                                    ptx::tma_load_5d(dst, &k_map, 0, off[0], 0, head, pg[0], bar);
+                                    ptx::tma_load_5d(dst + C::HALF, &v_map, 0, off[0], 0, head, pg[0], bar);
+                                } else {
+#pragma unroll
+                                    for (int b = 0; b < MOST; ++b) {
+                                        if (!(mine >> b & 1)) continue;
+                                        uint8_t *to = dst + (b << box_shift) * C::SPAN;
+#pragma unroll 1
+                                        for (int x = 0; x < C::BOXES; ++x) {
+                                            ptx::tma_load_5d(to + x * TT * C::SPAN, &k_map, 0, off[b], x, head, pg[b], bar);
+                                            ptx::tma_load_5d(to + C::HALF + x * TT * C::SPAN, &v_map, 0, off[b], x, head, pg[b], bar);
+                                        }
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        if constexpr (Q8) {
+                            // TS == 2: a token a lane; 16 tokens: the upper lanes fetch the value scales.  (Those of tokens
+                            // past the end are of the same page, and masked like their scores.)
+                            const int token = lane & (TT - 1), sub = token >> box_shift;
+                            const int pg = __shfl_sync(FULL, page, box0 + sub);
+                            const int off = __shfl_sync(FULL, in_page, box0 + sub) + (token & (box_tokens - 1));
+                            const int ok = (mine >> sub & 1) && (uint32_t)pg < (uint32_t)p.c.num_pages ? 4 : 0;
+                            const long long at = ok ? (long long)pg * p.s_page_stride32 + (long long)off * p.s_token_stride32 +
+                                                          (long long)head * p.s_head_stride32
+                                                    : 0;
+                            const uint32_t to = ptx::smem_u32(dst + 2 * C::HALF + 4 * lane);
+                            copy_async4_kept(to, (TS == 2 || lane < 16 ? p.c.k_scale : p.c.v_scale) + at, ok, keep);
+                            if (TS == 2) copy_async4_kept(to + 4 * TT, p.c.v_scale + at, ok, keep);
+                        }
+                        if (Q8 || BY_ROWS) copy_arrive(bar);
+                        step(q);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {  // a slot for each consumer's part of the segment
+                    const int slot = (base + q) * S + (puts >> 8 * q & 255);
+                    if (!ring_wait(empty + slot, (wrapped >> q & 1) ^ 1, dead)) return;
+                    if (Q8 || BY_ROWS || lane == 0) ptx::mbar_arrive(full + slot);
+                    if ((Q8 || BY_ROWS) && lane == 0) ptx::mbar_arrive(full + slot);
+                    step(q);
+                }
+                next_segment<C>(use, p);
+            }
+        };
+        feed();
         copy_wait_all();
+        if (*dead)  // nobody waits for the tensor copies in flight: a millisecond for them to land
+            for (int i = 0; i < 1000; ++i) __nanosleep(1000);
         return;
     }
 
     // ---- consumers: warp w multiplies tiles w, w + W, ... of each segment
-    // Both walks are in shared memory, changed by lane 0; what every tile needs of them is in registers.
-    Walk &at_use = walks[2 * warp], &at_get = walks[2 * warp + 1];
-    open_segment<C>(use, warp);
-    if (lane == 0) at_use = at_get = use;
-    __syncwarp();
-    int use_left = use.left, use_tile = use.tile, use_end = use.tile_end, use_t0 = use.s.t0;
-    int get_left = use.left, get_tile = use.tile, get_end = use.tile_end, get_head = use.head;
+    if constexpr (W == 8) take_registers<C::CONSUMER_REGS>();
     uint8_t *slots = ring + warp * (S * C::SLOT);  // this warp's
-    uint64_t *landed = full + warp * S;
+    uint64_t *landed = full + warp * S, *used = empty + warp * S;
     int at = 0;          // the slot that is used next
     uint32_t phase = 0;  // bit i: the parity of slot i's next landing
-    // A tile's keys (values) are `subs` boxes of box_tokens tokens, each within a page.  Lane i looks up box
-    // i % subs of the warp's (i / subs)-th next tile of the segment that copies are at, as soon as the last
-    // tile before has been copied, so that the table's latency passes behind the products.
-    const int box_tokens = 1 << box_shift, subs = TT >> box_shift, batch = 32 / subs;
-    int page = 0, in_page = 0;   // where the lane's box is
-    uint32_t boxes = 0;          // the lanes with boxes that are
-    int taken = 0;               // tiles of the batch that have been copied
-    bool owed = false;           // the slot for the part of the segment before comes first
-    int put = 0, free_slots = S; // the slot that is filled next, and how many may be
-    auto look_up = [&]() {
-        // (a page outside the pool reads as zeros; flagged here, when the entries have long arrived)
-        if ((boxes >> lane & 1) && (uint32_t)page >= (uint32_t)p.c.num_pages) flag_error(p.status, GDN_DEVERR_PAGE);
-        taken = 0;
-        boxes = 0;
-        if (get_left <= 0) return;  // (also after the last segment: its pages have been checked above)
-        const int box = lane << box_shift;  // in tokens
-        const int tile = get_tile + box / TT * W;
-        const int t = at_get.s.t0 + tile * TT + box % TT;
-        const bool wanted = tile < get_end && t < at_get.s.len && t + box_tokens > at_get.s.first;
-        if (wanted) {
-            const int i = p.page_shift >= 0 ? t >> p.page_shift : (int)((uint32_t)t / (uint32_t)p.c.page_size);
-            in_page = t - i * p.c.page_size;
-            page = p.block_table[at_get.s.b * p.bt_stride + i];
-        }
-        boxes = __ballot_sync(FULL, wanted);
-    };
-    // To the next segment once the warp's tiles of the current one are copied.
-    auto advance = [&]() {
-        if (get_tile + taken * W < get_end) {
-            if (taken == batch) {
-                get_tile += batch * W;
-                look_up();
-            }
-            return;
-        }
-        owed = true;
-        __syncwarp();
-        if (lane == 0) next_segment<C>(at_get, p, warp);
-        __syncwarp();
-        get_left = at_get.left, get_tile = at_get.tile, get_end = at_get.tile_end, get_head = at_get.head;
-        look_up();
-    };
-    // Fills free slots in the order of use: the tiles of a segment, then one that is left for the warp's part of
-    // it.  A slot that holds a part is free once the joiners are done with that segment; `block` waits for them.
-    int part_at = -1, part_segment = 0;  // the last part's slot, until it is known to be free
-    auto pump = [&](bool block) {
-        while (free_slots > 0 && (owed || get_left > 0)) {
-            if (put == part_at) {
-                if (block) ring_wait(j_empty, part_segment & 1, dead);
-                else if (!__all_sync(FULL, ptx::mbar_test_wait(j_empty, part_segment & 1))) return;
-                part_at = -1;
-            }
-            const bool is_part = owed, is_tile = !owed && get_tile + taken * W < get_end;
-            owed = false;
-            if (is_tile) {
-                const int box0 = taken * subs, head = get_head;
-                const uint32_t mine = boxes >> box0 & (FULL >> (32 - subs));
-                uint8_t *dst = slots + put * C::SLOT;
-                uint64_t *bar = landed + put;
-                if constexpr (BY_ROWS) {
-                    if (lane == 0) ptx::mbar_arrive(bar);
-                    // lane box0 + i looked up token i: its row's byte offset, -1 if it is not read
-                    long long row = -1;
-                    if ((boxes >> lane & 1) && (uint32_t)page < (uint32_t)p.c.num_pages)
-                        row = (page * p.c.page_stride + in_page * p.c.token_stride + head * p.c.head_stride) * C::ESZ;
-                    constexpr int PIECES = C::RB / 16, PER_SPAN = C::SPAN / 16;
-                    const uint32_t to = ptx::smem_u32(dst);
-#pragma unroll 4
-                    for (int k = lane; k < TT * PIECES; k += 32) {
-                        const int token = k / PIECES, x = k % PIECES, y = x % PER_SPAN;
-                        const long long o = __shfl_sync(FULL, row, box0 + token);
-                        const uint32_t at = to + (x / PER_SPAN) * TT * C::SPAN + token * C::SPAN +
-                                            ((y ^ (C::SPAN == 64 ? token >> 1 & 3 : token & 7)) << 4);
-                        const long long src = o < 0 ? 0 : o + x * 16;
-                        copy_async16(at, static_cast<const uint8_t *>(p.c.k) + src, o < 0 ? 0 : 16);
-                        copy_async16(at + C::HALF, static_cast<const uint8_t *>(p.c.v) + src, o < 0 ? 0 : 16);
-                    }
-                } else {
-                    constexpr int MOST = TT / 8;  // boxes of 8 tokens or more
-                    int pg[MOST], off[MOST];
-#pragma unroll
-                    for (int b = 0; b < MOST; ++b) {
-                        if (b > 0 && b >= subs) break;
-                        // (num_pages is outside the map, which reads as zeros)
-                        pg[b] = (int)min((uint32_t)__shfl_sync(FULL, page, box0 + b), (uint32_t)p.c.num_pages);
-                        off[b] = __shfl_sync(FULL, in_page, box0 + b);
-                    }
-                    if (ptx::elect_one()) {
-                        ptx::mbar_arrive_expect_tx(bar, __popc(mine) * (2 * C::RB) << box_shift);
-                        if (subs == 1) {  // all spans at once
-                            ptx::tma_load_5d(dst, &k_map, 0, off[0], 0, head, pg[0], bar);
-                            ptx::tma_load_5d(dst + C::HALF, &v_map, 0, off[0], 0, head, pg[0], bar);
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < MOST; ++b) {
-                                if (!(mine >> b & 1)) continue;
-                                uint8_t *to = dst + (b << box_shift) * C::SPAN;
-#pragma unroll 1
-                                for (int x = 0; x < C::BOXES; ++x) {
-                                    ptx::tma_load_5d(to + x * TT * C::SPAN, &k_map, 0, off[b], x, head, pg[b], bar);
-                                    ptx::tma_load_5d(to + C::HALF + x * TT * C::SPAN, &v_map, 0, off[b], x, head, pg[b], bar);
-                                }
-                            }
-                        }
-                    }
-                    __syncwarp();
-                }
-                if constexpr (Q8) {
-                    // TS == 2: a token a lane; 16 tokens: the upper lanes fetch the value scales.  (Those of tokens
-                    // past the end are of the same page, and masked like their scores.)
-                    const int token = lane & (TT - 1), sub = token >> box_shift;
-                    const int pg = __shfl_sync(FULL, page, box0 + sub);
-                    const int off = __shfl_sync(FULL, in_page, box0 + sub) + (token & (box_tokens - 1));
-                    const int ok = (mine >> sub & 1) && (uint32_t)pg < (uint32_t)p.c.num_pages ? 4 : 0;
-                    const long long at = ok ? (long long)pg * p.s_page_stride32 + (long long)off * p.s_token_stride32 +
-                                                  (long long)head * p.s_head_stride32
-                                            : 0;
-                    const uint32_t to = ptx::smem_u32(dst + 2 * C::HALF + 4 * lane);
-                    const uint64_t keep = keep_policy();
-                    copy_async4_kept(to, (TS == 2 || lane < 16 ? p.c.k_scale : p.c.v_scale) + at, ok, keep);
-                    if (TS == 2) copy_async4_kept(to + 4 * TT, p.c.v_scale + at, ok, keep);
-                }
-                if (Q8 || BY_ROWS) copy_arrive(bar);
-                ++taken;
-            }
-            if (get_left > 0) advance();
-            if (is_tile || is_part) {
-                put = put + 1 == S ? 0 : put + 1;
-                --free_slots;
-            }
-        }
-    };
-    look_up();
 
     // Where the lane's pieces are in a slot: key row g (and g + 8), piece c (odd steps: + 4); value rows
     // 2 c, 2 c + 1 (and + 8), its piece g.  Swizzled as the tensor copies leave them.
@@ -828,11 +852,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     int at_pos[NT][2];           // the positions of the queries of the lane's two columns
     int all_lo = 0, all_hi = 0;  // positions that every query row of the unit sees: [all_lo, all_hi)
     auto sees = [&](int pos, int t) { return t <= pos && (p.window == 0 || t > pos - p.window); };
-    bool fresh = true;
-    for (int segment = 0; use_left > 0;) {
-        pump(free_slots == S);
-        if (fresh) {  // a new segment
-            fresh = false;
+    for (int segment = 0;; ++segment) {
+        const Walk &at_use = segments[segment & 1];
+        int use_tile, use_end, use_t0;
+        {
+            if (!ring_wait(q_full + (segment & 1), segment >> 1 & 1, dead) || at_use.left <= 0) return;
+            use_tile = at_use.tile + warp, use_end = at_use.tile_end, use_t0 = at_use.s.t0;
             rows = min(ROWS, at_use.s.n * p.G - at_use.row0);
             const int pos0 = at_use.s.len - at_use.s.n;  // the first query's position
             auto position = [&](int r) {           // of row r's query (rows past the last repeat it)
@@ -845,8 +870,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             }
             all_hi = position(0) + 1;
             all_lo = p.window > 0 ? max(0, position(rows - 1) - p.window + 1) : 0;
-            // queries: lane (g, c) holds, of row 8 nt + g, the channels that its key pieces have
-            ring_wait(q_full + (segment & 1), segment >> 1 & 1, dead);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 col[nt][0] = q_stat[(segment & 1) * ROWS + nt * 8 + 2 * c];
@@ -860,12 +883,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
             }
         }
-        if (use_tile < use_end) {
+        for (; use_tile < use_end; use_tile += W) {
             const int tile_t = use_t0 + use_tile * TT;
             const bool edge = tile_t < all_lo || tile_t + TT > all_hi;
 
             // ---- scores: S^T = K Q^T
-            ring_wait(landed + at, phase >> at & 1, dead);
+            if (!ring_wait(landed + at, phase >> at & 1, dead)) return;
             phase ^= 1u << at;
             float sc[TS][NT][4], sc2[TS][NT][4];
 #pragma unroll
@@ -1145,10 +1168,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 add_values(0, 0, No());
             }
             __syncwarp();  // all of its readers are behind
-            use_tile += W;
-        } else {
+            if (lane == 0) ptx::mbar_arrive(used + at);
+            at = at + 1 == S ? 0 : at + 1;
+        }
+        {
             // ---- this warp's part of the segment, for the joiners
-            if (segment > 0) ring_wait(j_empty, (segment - 1) & 1, dead);  // the joiners take one segment at a time
+            if (!ring_wait(landed + at, phase >> at & 1, dead)) return;
+            phase ^= 1u << at;
+            if (segment > 0 && !ring_wait(j_empty, (segment - 1) & 1, dead)) return;  // the joiners take one segment at a time
             float *part = reinterpret_cast<float *>(slots + at * C::SLOT);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -1175,15 +1202,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 ptx::mbar_arrive(j_full);
                 ptx::mbar_arrive(q_empty + (segment & 1));
             }
-            part_at = at;
-            part_segment = segment++;
-            if (lane == 0) next_segment<C>(at_use, p, warp);
-            __syncwarp();
-            use_left = at_use.left, use_tile = at_use.tile, use_end = at_use.tile_end, use_t0 = at_use.s.t0;
-            fresh = true;
+            at = at + 1 == S ? 0 : at + 1;
         }
-        at = at + 1 == S ? 0 : at + 1;
-        ++free_slots;
     }
 }
 
@@ -1264,6 +1284,16 @@ cudaError_t launch_sized(const PagedAttnParams &p, cudaStream_t stream) {
     while (p.c.page_size % box_tokens) box_tokens >>= 1, --box_shift;
     const bool by_rows = box_tokens < 8;
     if (by_rows) box_tokens = 1, box_shift = 0;
+    if constexpr (C::W == 8) {
+        // the roles divide what the block is launched with, which has to be all of it
+        static const bool whole = [] {
+            cudaFuncAttributes a{}, b{};
+            return cudaFuncGetAttributes(&a, paged_attention_kernel<CT, C, false>) == cudaSuccess &&
+                   cudaFuncGetAttributes(&b, paged_attention_kernel<CT, C, true>) == cudaSuccess &&
+                   a.numRegs == C::LAUNCH_REGS && b.numRegs == C::LAUNCH_REGS;
+        }();
+        if (!whole) return cudaErrorInvalidConfiguration;
+    }
     auto kernel = by_rows ? paged_attention_kernel<CT, C, true> : paged_attention_kernel<CT, C, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
