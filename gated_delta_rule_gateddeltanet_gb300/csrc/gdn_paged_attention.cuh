@@ -256,11 +256,17 @@ struct Cfg {
     static constexpr int HALF = TT * RB;                // a tile's keys; its values
     static constexpr int SPAN = RB < 128 ? RB : 128;    // row bytes a tensor copy takes
     static constexpr int BOXES = RB / SPAN;             // spans a row; each half is [BOXES][TT][SPAN]
-    // A ring slot holds a tile (keys, values, scales of 8-bit rows) or a
-    // consumer's part of a finished segment (rows and their statistics).
-    static constexpr int OROW = D + 4;                  // floats a row of a part
-    static constexpr int TILE = 2 * HALF + (Q8 ? TT * 8 : 0), PART = ROWS * (OROW + 2) * 4;
+    // A ring slot holds a tile's keys and values or a consumer's part of a finished segment ([ROWS][D] floats); an
+    // extra beside it the scales of 8-bit rows (keys, values), or the part's statistics.
+    static constexpr int TILE = 2 * HALF, PART = ROWS * D * 4;
     static constexpr int SLOT = ((TILE > PART ? TILE : PART) + 1023) / 1024 * 1024;
+    static constexpr int EXTRA = Q8 && TT > ROWS ? TT * 8 : ROWS * 8;
+    // Row r's 16-byte piece x of a part is at x ^ part_swizzle(r): the lanes that store together (rows 2 c, pieces
+    // CPL / 4 apart) then meet no bank twice.
+    static __device__ __forceinline__ int part_swizzle(int r) {
+        const int c = r >> 1 & 3;
+        return CPL == 4 ? 2 * c : CPL == 8 ? (c & 1) | (c & 2) << 1 : c;
+    }
     // Bytes a staged query row; the padding keeps the lanes' reads of 8 rows free of bank conflicts.
     static constexpr int QROW = D * (F32 ? 4 : 2) + (Q8 ? 16 : 64);
     static constexpr int QUERIES = 2 * ROWS * (QROW + 8);  // and each row's (scale, bias)
@@ -269,7 +275,7 @@ struct Cfg {
     // role (a consumer's outputs take HELD); where the outputs take more than 64, or the ring has no room for more, 8 have 255.
     static constexpr int HELD = NT * D / 4;
     static constexpr int FACTORS = 8 * ROWS * 4 + ROWS * 8;
-    static constexpr int ROOM = (SMEM_LIMIT - 1024 - HEAD - QUERIES - FACTORS) / SLOT;  // slots that fit
+    static constexpr int ROOM = (SMEM_LIMIT - 1024 - HEAD - QUERIES - FACTORS) / (SLOT + EXTRA);  // slots that fit
     static constexpr int W = HELD <= 64 && ROOM >= 16 ? 8 : ROOM >= 8 ? 4 : 3;
     static constexpr int NP = W == 8 ? 4 : W == 4 ? 2 : 1, NJ = W == 8 ? 4 : 2;
     static constexpr int PER = W / NP;  // consumers a producer feeds
@@ -280,11 +286,16 @@ struct Cfg {
     static constexpr int UNIT_WORK = 2;
     static constexpr int THREADS = 32 * (W + NP + NJ);
     static constexpr int S = ROOM / W < 8 ? ROOM / W : 8;  // ring slots a consumer
-    static constexpr int SMEM = 1024 + HEAD + QUERIES + FACTORS + W * S * SLOT;  // (1024: the ring's alignment)
+    static constexpr int SMEM = 1024 + HEAD + QUERIES + FACTORS + W * S * (SLOT + EXTRA);  // (1024: the ring's alignment)
     // Weights of 8-bit values are single FP16 numbers: next to values of 8 bits, 11 are plenty, and the
     // second product would cost what these kernels are bound by.
     static constexpr bool SPLIT_P = !Q8;
     static constexpr float BIAS = CT == GDN_F16 || Q8 ? 6.f : -8.f;  // weights are 2^(s - m + BIAS)
+    // A tile's scores before the output of the tile before: 82.5 us instead of 87.6 us for a context of 131071 tokens,
+    // 161 us instead of 170 us for 64 x 4096 (FP16, 8 heads of 128).  Where a consumer holds more (two groups of rows)
+    // or converts (8 and 32 bits) it runs longer instead: draft verification 52.2 us against 49.4 us, many int8
+    // requests 45.2 us against 42.1 us, FP32 50.6 us against 48.9 us.
+    static constexpr bool AHEAD = !Q8 && !F32 && NT == 1;
     static constexpr float HEADROOM = 8.f;  // a score may exceed the maximum by this: FP16 weights stay below 2^14
     static_assert(S >= 2 && W % NP == 0 && 512 + 2 * W * S * 8 + 64 <= 1600 && 1600 + 2 * (int)sizeof(Walk) <= HEAD && HALF % 1024 == 0,
                   "ring and barriers");
@@ -466,6 +477,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     float2 *q_stat = reinterpret_cast<float2 *>(queries + 2 * ROWS * C::QROW);  // [2][ROWS] scores' (scale, bias)
     float2 *joined = reinterpret_cast<float2 *>(queries + C::QUERIES);   // [ROWS] maxima and sums
     float *factor = reinterpret_cast<float *>(joined + ROWS);            // [W][ROWS]
+    uint8_t *extras = reinterpret_cast<uint8_t *>(factor + 8 * ROWS);    // [W][S][EXTRA]
     uint8_t *ring = smem + (C::SMEM - W * S * C::SLOT - 1024);           // [W][S][SLOT], on a 1024-byte boundary
     ring += (1024 - (ptx::smem_u32(ring) & 1023)) & 1023;
 
@@ -645,19 +657,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             const int pos0 = use.s.len - use.s.n;
             const bool whole = use.seg_chunks == use.s.chunks;
             if (named_any(1, THREADS, !ring_wait(j_full, segment & 1, dead))) break;  // (all of them, or none)
-            const float *part[W];  // [ROWS][OROW], then the rows' (maximum, sum)
+            const float4 *part[W];
+            const float2 *part_stat[W];  // (maximum, sum)
             int at[W];
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 at[w] = w * S + part_slot[w];
-                part[w] = reinterpret_cast<const float *>(ring + at[w] * C::SLOT);
+                part[w] = reinterpret_cast<const float4 *>(ring + at[w] * C::SLOT);
+                part_stat[w] = reinterpret_cast<const float2 *>(extras + at[w] * C::EXTRA);
             }
             for (int r = j; r < ROWS; r += THREADS) {
                 float2 st[W];
                 float mm = NONE, ll = 0.f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    st[w] = reinterpret_cast<const float2 *>(part[w] + ROWS * C::OROW)[r];
+                    st[w] = part_stat[w][r];
                     mm = fmaxf(mm, st[w].x);
                 }
 #pragma unroll
@@ -675,7 +689,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    const float4 x = *reinterpret_cast<const float4 *>(part[w] + r * C::OROW + ch);
+                    const float4 x = part[w][r * (D / 4) + (ch / 4 ^ C::part_swizzle(r))];
                     const float f = factor[w * ROWS + r];
                     sum.x += f * x.x, sum.y += f * x.y, sum.z += f * x.z, sum.w += f * x.w;
                 }
@@ -806,7 +820,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                             const long long at = ok ? (long long)pg * p.s_page_stride32 + (long long)off * p.s_token_stride32 +
                                                           (long long)head * p.s_head_stride32
                                                     : 0;
-                            const uint32_t to = ptx::smem_u32(dst + 2 * C::HALF + 4 * lane);
+                            const uint32_t to = ptx::smem_u32(extras + slot * C::EXTRA + 4 * lane);
                             copy_async4_kept(to, (TS == 2 || lane < 16 ? p.c.k_scale : p.c.v_scale) + at, ok, keep);
                             if (TS == 2) copy_async4_kept(to + 4 * TT, p.c.v_scale + at, ok, keep);
                         }
@@ -883,21 +897,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
             }
         }
-        for (; use_tile < use_end; use_tile += W) {
-            const int tile_t = use_t0 + use_tile * TT;
-            const bool edge = tile_t < all_lo || tile_t + TT > all_hi;
-
-            // ---- scores: S^T = K Q^T
-            if (!ring_wait(landed + at, phase >> at & 1, dead)) return;
-            phase ^= 1u << at;
-            float sc[TS][NT][4], sc2[TS][NT][4];
+        // ---- scores of the tile in a slot: S^T = K Q^T
+        float sc[TS][NT][4];
+        auto scores = [&](int slot) {
+            float sc2[TS][NT][4];
 #pragma unroll
             for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[ts][nt][e] = sc2[ts][nt][e] = 0.f;
-            const uint8_t *ks = slots + at * C::SLOT;
+            const uint8_t *ks = slots + slot * C::SLOT;
             // lane (g, c) holds, of query row 8 nt + g, the channels that its key pieces have
             const uint8_t *qs = queries + ((segment & 1) * ROWS + g) * C::QROW + c * (Q8 ? 32 : 16);
 #pragma unroll
@@ -949,12 +959,36 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     }
                 }
             }
+#pragma unroll
+            for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[ts][nt][e] += sc2[ts][nt][e];
+        };
+        auto arrived = [&](int slot) {
+            const bool ok = ring_wait(landed + slot, phase >> slot & 1, dead);
+            phase ^= 1u << slot;
+            return ok;
+        };
+        if (C::AHEAD && use_tile < use_end) {
+            if (!arrived(at)) return;
+            scores(at);
+        }
+        for (; use_tile < use_end; use_tile += W) {
+            const int tile_t = use_t0 + use_tile * TT;
+            const bool edge = tile_t < all_lo || tile_t + TT > all_hi;
+            if (!C::AHEAD) {
+                if (!arrived(at)) return;
+                scores(at);
+            }
+
             // the lane's tokens are rows g and g + 8 of each subtile
             float vs[TS][2], lv[TS][2];
             float top[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = NEG_INF;
-            const float *scales = reinterpret_cast<const float *>(slots + at * C::SLOT + 2 * C::HALF);
+            const float *scales = reinterpret_cast<const float *>(extras + (warp * S + at) * C::EXTRA);
 #pragma unroll
             for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
@@ -971,7 +1005,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float &x = sc[ts][nt][2 * h + e];
-                            x += sc2[ts][nt][2 * h + e];
                             if constexpr (CT == GDN_INT8) x += col[nt][e].y;
                             x *= Q8 ? col[nt][e].x * ksc : col[nt][e].x;
                         }
@@ -1161,6 +1194,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 if (!Q8) rough = __any_sync(FULL, rough);
                 __syncwarp();
             }
+            // The next tile's scores before this one's output, so that neither waits for the other.
+            const int next = at + 1 == S ? 0 : at + 1;
+            if (C::AHEAD && use_tile + W < use_end) {
+                if (!arrived(next)) return;
+                scores(next);
+            }
             if (!Q8 && __builtin_expect(rough, 0)) {
 #pragma unroll 1
                 for (int r = 0; r < rows; ++r) add_values(r, at_use.s.len - at_use.s.n + (at_use.row0 + r) / p.G, Yes());
@@ -1169,14 +1208,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             }
             __syncwarp();  // all of its readers are behind
             if (lane == 0) ptx::mbar_arrive(used + at);
-            at = at + 1 == S ? 0 : at + 1;
+            at = next;
         }
         {
             // ---- this warp's part of the segment, for the joiners
-            if (!ring_wait(landed + at, phase >> at & 1, dead)) return;
-            phase ^= 1u << at;
+            if (!arrived(at)) return;
             if (segment > 0 && !ring_wait(j_empty, (segment - 1) & 1, dead)) return;  // the joiners take one segment at a time
-            float *part = reinterpret_cast<float *>(slots + at * C::SLOT);
+            float4 *part = reinterpret_cast<float4 *>(slots + at * C::SLOT);
+            float2 *part_stat = reinterpret_cast<float2 *>(extras + (warp * S + at) * C::EXTRA);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1186,14 +1225,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                     x += __shfl_xor_sync(FULL, x, 8);
                     x += __shfl_xor_sync(FULL, x, 16);
                     const int r = nt * 8 + 2 * c + e;
-                    if (g == 0) reinterpret_cast<float2 *>(part + ROWS * C::OROW)[r] = make_float2(m[nt][e], x);
-                    float *dst = part + r * C::OROW + g * C::CPL;
+                    if (g == 0) part_stat[r] = make_float2(m[nt][e], x);
 #pragma unroll
                     for (int vb = 0; vb < VB; ++vb)
 #pragma unroll
                         for (int i = 0; i < MPV; i += 2) {
                             const float(&a)[4] = o[nt][vb * MPV + i], (&b)[4] = o[nt][vb * MPV + i + 1];
-                            *reinterpret_cast<float4 *>(dst + vb * 8 * C::CPL + 2 * i) = make_float4(a[e], a[e + 2], b[e], b[e + 2]);
+                            const int x = ((vb * 8 + g) * C::CPL + 2 * i) / 4;
+                            part[r * (D / 4) + (x ^ C::part_swizzle(r))] = make_float4(a[e], a[e + 2], b[e], b[e + 2]);
                         }
                 }
             if (lane == 0) part_slot[warp] = at;
