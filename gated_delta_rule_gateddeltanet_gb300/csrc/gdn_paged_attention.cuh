@@ -279,7 +279,7 @@ struct Cfg {
     static constexpr int W = HELD <= 64 && ROOM >= 16 ? 8 : ROOM >= 8 ? 4 : 3;
     static constexpr int NP = W == 8 ? 4 : W == 4 ? 2 : 1, NJ = W == 8 ? 4 : 2;
     static constexpr int PER = W / NP;  // consumers a producer feeds
-    static constexpr int LAUNCH_REGS = 128, CONSUMER_REGS = 168, PRODUCER_REGS = 72, JOINER_REGS = 104;
+    static constexpr int LAUNCH_REGS = 128, CONSUMER_REGS = 168, PRODUCER_REGS = 88, JOINER_REGS = 88;
     static_assert(8 * CONSUMER_REGS + 4 * PRODUCER_REGS + 4 * JOINER_REGS <= 16 * LAUNCH_REGS, "registers of the block");
     // What a unit costs besides its chunks (fetching queries, joining), in chunks: with 0 the CTAs with many
     // short units are late (256 requests of up to 1024 tokens: 59 us against 55 us; a decode step of 64 x 128 to 2048: 65 against 57).
@@ -725,49 +725,68 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
         if constexpr (W == 8) give_registers<C::PRODUCER_REGS>();
         constexpr int PER = C::PER;
         const int base = (warp - W) * PER;  // the first consumer
-        // A tile's keys (values) are `subs` boxes of box_tokens tokens, each within a page.  Lane i looks up box
-        // i % subs of the i / subs-th next of the producer's tiles (n-th tile: of consumer n % PER).
-        const int box_tokens = 1 << box_shift, subs = TT >> box_shift, batch = 32 / subs;
+        // A tile's keys (values) are `subs` boxes of box_tokens tokens, each within a page.  For each of its consumers'
+        // tiles, lane i looks up box i % subs of the i / subs-th next.
+        constexpr int TT_SHIFT = TS == 2 ? 5 : 4;
+        const int box_tokens = 1 << box_shift, sub_shift = TT_SHIFT - box_shift, subs = 1 << sub_shift, batch = 32 >> sub_shift;
+        // (The loop over the consumers is not unrolled: the roles' code together has to stay in the instruction cache.)
         uint32_t puts = 0;     // byte q: consumer q's slot that is filled next
         uint32_t wrapped = 0;  // bit q: the parity of its rounds through the ring
+        auto put = [&](int q) { return (int)(puts >> 8 * q & 255); };
         auto step = [&](int q) {
             puts += 1u << 8 * q;
-            if ((puts >> 8 * q & 255) == S) puts -= (uint32_t)S << 8 * q, wrapped ^= 1u << q;
+            if (put(q) == S) puts -= (uint32_t)S << 8 * q, wrapped ^= 1u << q;
         };
-        auto tile_of = [&](int n) { return use.tile + n / PER * W + base + n % PER; };
         const uint64_t keep = Q8 ? keep_policy() : 0;
         auto feed = [&]() {  // returns early in a dead CTA
             open_segment<C>(use);
             while (use.left > 0) {
                 const int head = use.head;
-                const int count = use.seg_chunks * PER;
-                for (int n0 = 0; n0 < count; n0 += batch) {
-                    int page = 0, in_page = 0;  // where the lane's box is
-                    const int tile = tile_of(n0 + lane / subs);
-                    const int t = use.s.t0 + tile * TT + (lane % subs << box_shift);
-                    const bool wanted = tile < use.tile_end && t < use.s.len && t + box_tokens > use.s.first;
-                    if (wanted) {
-                        const int i = p.page_shift >= 0 ? t >> p.page_shift : (int)((uint32_t)t / (uint32_t)p.c.page_size);
-                        in_page = t - i * p.c.page_size;
-                        page = p.block_table[use.s.b * p.bt_stride + i];
-                        // (a page outside the pool reads as zeros)
-                        if ((uint32_t)page >= (uint32_t)p.c.num_pages) flag_error(p.status, GDN_DEVERR_PAGE);
+                for (int k0 = 0; k0 < use.seg_chunks; k0 += batch) {
+                    const int tile = use.tile + k0 * W + base;
+                    int page[PER], in_page[PER];  // where the lane's boxes are
+                    uint32_t boxes[PER];          // the lanes with boxes that are read
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) {
+                        const int my_tile = tile + (lane >> sub_shift) * W + q;
+                        const int t = use.s.t0 + my_tile * TT + ((lane & (subs - 1)) << box_shift);
+                        const bool wanted = my_tile < use.tile_end && t < use.s.len && t + box_tokens > use.s.first;
+                        page[q] = in_page[q] = 0;
+                        if (wanted) {
+                            const int i = p.page_shift >= 0 ? t >> p.page_shift : (int)((uint32_t)t / (uint32_t)p.c.page_size);
+                            in_page[q] = t - i * p.c.page_size;
+                            page[q] = p.block_table[use.s.b * p.bt_stride + i];
+                        }
+                        boxes[q] = __ballot_sync(FULL, wanted);
                     }
-                    const uint32_t boxes = __ballot_sync(FULL, wanted);  // the lanes with boxes that are read
-                    for (int n = n0; n < min(n0 + batch, count); ++n) {
-                        const int box0 = (n - n0) * subs, q = n % PER;
-                        if (tile_of(n) >= use.tile_end) continue;
-                        const int slot = (base + q) * S + (puts >> 8 * q & 255);
+#pragma unroll
+                    for (int q = 0; q < PER; ++q)  // a page outside the pool reads as zeros, like num_pages
+                        if ((uint32_t)page[q] >= (uint32_t)p.c.num_pages) {
+                            flag_error(p.status, GDN_DEVERR_PAGE);
+                            page[q] = p.c.num_pages;
+                        }
+                    const int end = (min(k0 + batch, use.seg_chunks) - k0) * PER;
+#pragma unroll 1
+                    for (int n = 0; n < end; ++n) {
+                        const int q = n % PER, box0 = n / PER * subs;
+                        if (tile + n / PER * W + q >= use.tile_end) continue;
+                        int at_page = page[0], at_off = in_page[0];
+                        uint32_t mine = boxes[0];
+#pragma unroll
+                        for (int i = 1; i < PER; ++i)
+                            if (q == i) at_page = page[i], at_off = in_page[i], mine = boxes[i];
+                        const bool my_box = mine >> lane & 1;
+                        mine = mine >> box0 & (FULL >> (32 - subs));
+                        const int slot = (base + q) * S + put(q);
                         uint8_t *dst = ring + slot * C::SLOT;
                         uint64_t *bar = full + slot;
                         if (!ring_wait(empty + slot, (wrapped >> q & 1) ^ 1, dead)) return;
-                        const uint32_t mine = boxes >> box0 & (FULL >> (32 - subs));
                         if constexpr (BY_ROWS) {
                             if (lane == 0) ptx::mbar_arrive(bar);
                             // lane box0 + i looked up token i: its row's byte offset, -1 if it is not read
                             long long row = -1;
-                            if ((boxes >> lane & 1) && (uint32_t)page < (uint32_t)p.c.num_pages)
-                                row = (page * p.c.page_stride + in_page * p.c.token_stride + head * p.c.head_stride) * C::ESZ;
+                            if (my_box && at_page < p.c.num_pages)
+                                row = (at_page * p.c.page_stride + at_off * p.c.token_stride + head * p.c.head_stride) * C::ESZ;
                             constexpr int PIECES = C::RB / 16, PER_SPAN = C::SPAN / 16;
                             const uint32_t to = ptx::smem_u32(dst);
 #pragma unroll 4
@@ -786,9 +805,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
 #pragma unroll
                             for (int b = 0; b < MOST; ++b) {
                                 if (b > 0 && b >= subs) break;
-                                // (num_pages is outside the map, which reads as zeros)
-                                pg[b] = (int)min((uint32_t)__shfl_sync(FULL, page, box0 + b), (uint32_t)p.c.num_pages);
-                                off[b] = __shfl_sync(FULL, in_page, box0 + b);
+                                pg[b] = __shfl_sync(FULL, at_page, box0 + b);
+                                off[b] = __shfl_sync(FULL, at_off, box0 + b);
                             }
                             if (ptx::elect_one()) {
                                 ptx::mbar_arrive_expect_tx(bar, __popc(mine) * (2 * C::RB) << box_shift);
@@ -814,9 +832,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                             // TS == 2: a token a lane; 16 tokens: the upper lanes fetch the value scales.  (Those of tokens
                             // past the end are of the same page, and masked like their scores.)
                             const int token = lane & (TT - 1), sub = token >> box_shift;
-                            const int pg = __shfl_sync(FULL, page, box0 + sub);
-                            const int off = __shfl_sync(FULL, in_page, box0 + sub) + (token & (box_tokens - 1));
-                            const int ok = (mine >> sub & 1) && (uint32_t)pg < (uint32_t)p.c.num_pages ? 4 : 0;
+                            const int pg = __shfl_sync(FULL, at_page, box0 + sub);
+                            const int off = __shfl_sync(FULL, at_off, box0 + sub) + (token & (box_tokens - 1));
+                            const int ok = (mine >> sub & 1) && pg < p.c.num_pages ? 4 : 0;
                             const long long at = ok ? (long long)pg * p.s_page_stride32 + (long long)off * p.s_token_stride32 +
                                                           (long long)head * p.s_head_stride32
                                                     : 0;
@@ -830,7 +848,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 }
 #pragma unroll
                 for (int q = 0; q < PER; ++q) {  // a slot for each consumer's part of the segment
-                    const int slot = (base + q) * S + (puts >> 8 * q & 255);
+                    const int slot = (base + q) * S + put(q);
                     if (!ring_wait(empty + slot, (wrapped >> q & 1) ^ 1, dead)) return;
                     if (Q8 || BY_ROWS || lane == 0) ptx::mbar_arrive(full + slot);
                     if ((Q8 || BY_ROWS) && lane == 0) ptx::mbar_arrive(full + slot);
