@@ -21,17 +21,16 @@
 // of channels among the output rows is free as long as both operands agree, so
 // a lane's 16 consecutive bytes of a key row serve as its k-slots of two
 // (8-bit: four) instructions, and 16 consecutive bytes of a value row as its
-// rows of four (eight).  Each lane therefore consumes exactly the 16-byte
-// pieces that it copied itself: a warp's ring of cp.async slots is a private
-// FIFO per lane, with no barrier, no bank conflict and no swizzle, and each
-// of the CTA's warps streams on its own (tiles of 16 or 32 tokens).
+// rows of four (eight).  Tensor copies swizzle the rows so that these reads
+// meet no bank twice.
 //
-// Roles.  Each consumer warp feeds itself: it owns a ring of slots, its tensor
-// copies run a ring ahead of its products (also across the ends of sequences),
-// and it looks its next 32 tiles' pages up in one load.  Nothing is shared
-// between consumers while they stream.  Joiner warps fetch queries ahead and add
-// the consumers' parts of a finished piece while these go on with the next, so
-// that memory never idles for a table lookup, a softmax or a join.
+// Roles.  A CTA per SM: W consumer warps multiply tiles of 16 or 32 tokens,
+// each from its own ring of slots; producer warps keep the rings full, a slot
+// at a time and ahead across the ends of sequences; joiner warps fetch the next
+// segment's queries and add the consumers' parts of a finished one while these
+// go on.  Consumers share nothing while they stream.  (When the consumers copied
+// for themselves, each copy's ~700 cycles of issue stood between two tiles: draft
+// verification ran 58.7 us instead of 52.5 us, many int8 requests 49 us instead of 42 us.)
 //
 // Work split.  The lengths are on the device, so the split is made there: all
 // (sequence, key head, group of query rows) units are cut into chunks of W
@@ -39,17 +38,27 @@
 // spans several CTAs leaves unnormalised parts with their maxima and sums in
 // the workspace, and a second kernel, a row to a CTA, joins them in order.
 //
-// Numerics.  Scores, maxima, sums and outputs are FP32.  The weights P are
-// 32-bit numbers that go to the tensor cores as two 16-bit parts (hi + lo, about
-// 22 bits for FP16 values and 16 for BF16), which leaves the rounding of the
-// result as the only one that matters; the memory-bound stream hides the
-// second product.  FP32 caches use three TF32 products for each (hi hi, hi lo,
-// lo hi).  The running maximum is only raised when a score exceeds it by more
-// than 2^8 (the exponent headroom of the weights), so most tiles need no
-// reduction across lanes and no rescaling.  8-bit rows: key scales multiply
-// scores and value scales multiply weights, so the maximum is taken over
-// score + log2(value scale); query rows are scaled to [1, 2) by a power of
-// two, because 8-bit caches use FP16 products whatever the I/O type.
+// Numerics.  Scores, maxima, sums and outputs are FP32.  The weights P of 16-bit
+// values go to the tensor cores as two 16-bit parts (hi + lo, about 22 bits for
+// FP16 values and 16 for BF16), which leaves the rounding of the result as the
+// only one that matters; over 8-bit values they are single FP16 numbers.  FP32
+// caches use three TF32 products for each (hi hi, hi lo, lo hi).  The running
+// maximum is only raised when a score exceeds it by more than 2^8 (the exponent
+// headroom of the weights), so most tiles need no reduction across lanes and no
+// rescaling.  8-bit rows: key scales multiply scores and value scales multiply
+// weights, so the maximum is taken over score + log2(value scale); BF16 query
+// rows are scaled to [1, 2) by a power of two as they are fetched, because 8-bit
+// caches use FP16 products whatever the I/O type.
+//
+// Measured (one key head serves 4 query heads, heads of 128, FP16): 64 x 4096
+// tokens 158-163 us, 6.6-6.8 TB/s (0.97 to 1.0 of a copy's rate); one context of 131071
+// 82-84 us, 6.4-6.5 TB/s; a decode step of 64 x 128 to 2048, writes included, 54-55 us
+// (5.3 TB/s); 64 e4m3 contexts of up to 16384, two heads of 256, 91 us (6.0 TB/s).
+// Long streams are bound by HBM.  Short units are bound by the fixed work of a
+// segment (about 1 us a CTA: queries, statistics, parts) and of a call (2.6 us to
+// the first copy, 2.4 us for the join): 16 x 512 tokens 9.6 us.  16 query rows are
+// bound by the consumers' instructions: draft verification (16 x 4 tokens of 8
+// heads a key head, up to 8191) reads the cache twice and takes 45 us.
 #pragma once
 
 #include "attn_internal.cuh"
@@ -127,8 +136,8 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // x = hi + lo with hi rounded to TF32 (to nearest in magnitude, so that lo and
-// the dropped lo lo products have no sign in common; in integers: the convert
-// instruction ran 64 x 4096 x 128 FP32 at half the rate).  The tensor cores drop lo's bits
+// the dropped lo lo products have no sign in common; in integers: with
+// the convert instruction 8 x 4096 tokens of heads of 128 took 58.6 us instead of 49.1 us).  The tensor cores drop lo's bits
 // past TF32, which leaves 21 bits.  A non-finite x stays in hi alone.
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
     hi = (x + 0x1000u) & 0xffffe000u;
@@ -283,9 +292,10 @@ struct Cfg {
     static constexpr int PER = W / NP;  // consumers a producer feeds
     static constexpr int LAUNCH_REGS = 128, CONSUMER_REGS = 168, PRODUCER_REGS = 88, JOINER_REGS = 88;
     static_assert(8 * CONSUMER_REGS + 4 * PRODUCER_REGS + 4 * JOINER_REGS <= 16 * LAUNCH_REGS, "registers of the block");
-    // What a unit costs besides its chunks (fetching queries, joining), in chunks: with 0 the CTAs with many
-    // short units are late (256 requests of up to 1024 tokens: 59 us against 55 us; a decode step of 64 x 128 to 2048: 65 against 57).
-    static constexpr int UNIT_WORK = 2;
+    // What a unit costs besides its chunks (fetching queries, statistics, joining), in chunks; those of FP32 take
+    // longer.  With 0 the CTAs with many short units are late: draft verification 49.1 us against 45.0 us, many int8
+    // requests 44.7 us against 41.4 us; with 1 46.1 and 41.4 us; FP32 heads 22.8 us with 1 and 24.6 us with 2.
+    static constexpr int UNIT_WORK = F32 ? 1 : 2;
     static constexpr int THREADS = 32 * (W + NP + NJ);
     static constexpr int S = ROOM / W < 8 ? ROOM / W : 8;  // ring slots a consumer
     static constexpr int SMEM = 1024 + HEAD + QUERIES + FACTORS + W * S * (SLOT + EXTRA);  // (1024: the ring's alignment)
@@ -1346,7 +1356,7 @@ cudaError_t launch_sized(const PagedAttnParams &p, cudaStream_t stream) {
     using C = Cfg<CT, D, NT>;
     // Tensor copies of the largest power of two of tokens, up to a tile, that never crosses a page; below 8
     // tokens they are so many (a lane issues them one by one) that 16-byte copies of single rows by all lanes
-    // are faster: pages of 7 tokens, 8 x 4099 x 8 heads of 64, FP32, 28 us against 56 us.
+    // are faster: pages of 7 tokens, 8 x 4099 x 8 heads of 64, FP32, took half the time (28 us then, 23 us now).
     int box_tokens = C::TT, box_shift = C::TS == 2 ? 5 : 4;
     while (p.c.page_size % box_tokens) box_tokens >>= 1, --box_shift;
     const bool by_rows = box_tokens < 8;
