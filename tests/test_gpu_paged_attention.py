@@ -109,6 +109,21 @@ def test_many_sequences():
     run(Paged(rng.integers(0, 60, 500).tolist(), 2, 64, 16, F16, seed=6), 4, F16)
 
 
+@pytest.mark.parametrize("kind,d", [(F16, 64), (BF16, 128), (F16, 256), (FP8, 64), (FP8, 256), (I8, 128), (F32, 64), (F32, 256)])
+@pytest.mark.parametrize("group,page", [(4, 16), (16, 5)])
+def test_ragged_batches_through_the_rings(kind, d, group, page):
+    """Segments of no, one and several tiles a warp in a row, in rings of every depth (8 and 16 query rows,
+    8 to 32 bits), launched again before the first launch has ended: the same bits."""
+    rng = np.random.default_rng(d + group)
+    lens = np.where(rng.random(180) < 0.3, rng.integers(0, 3, 180), rng.integers(0, 700, 180)).tolist()
+    p = Paged(lens, 1, d, page, kind, seed=d)
+    io = BF16 if kind in (FP8, I8) else kind
+    q = queries(180, group, d, io)
+    outs = [gdn.paged_attention(q, p.cache, p.table, p.kv_lens) for _ in range(4)]
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    run(p, group, io)
+
+
 def test_masked_places_may_hold_anything():
     """Infinities and NaN in keys and values of drafted tokens stay out of the queries before them."""
     for kind in (F16, BF16, F32):
