@@ -15,11 +15,11 @@
 // (their traffic: 3.9 us), bound by instructions (conversion and rotation).
 //
 // Read back: a warp looks up its tokens' rows, a lane each, and then moves them
-// in pieces of 16 output bytes, READ_UNROLL in flight a lane (2: 45.5 us instead of
-// 41.7 us for int8; 8: the same, 16-bit rows 19% slower).  Keys first, then values: the two in turn ran 20%
-// slower at 16 bits.  39,000 tokens of 8 + 8 int8 heads of 128 to BF16: 41.7 us,
-// 5.9 TB/s (0.87 of a copy's rate); 16-bit rows 52 us, 6.1 TB/s; four contexts
-// of at most 60 tokens 2.4 us.
+// in pieces of 16 output bytes, READ_UNROLL in flight a lane (with 2 45.5 us
+// where 4 took 41.7 us for int8; 8: the same, 16-bit rows 19% slower).  Keys
+// first, then values: the two in turn ran 20% slower at 16 bits.  39,000 tokens
+// of 8 + 8 int8 heads of 128 to BF16: 40.1 us, 6.1 TB/s (0.90 of a copy's rate);
+// 16-bit rows 51 us, 6.2 TB/s; four contexts of at most 77 tokens 2.1 us.
 #include "attn_internal.cuh"
 
 #include <string.h>
@@ -259,7 +259,8 @@ struct Raw {
 // blockIdx.y: keys, values.  A warp takes p.tok tokens (at most 32): a lane looks up each token's
 // sequence, page and row, then all lanes move the rows' pieces of 16 output
 // bytes, U of them in flight.
-template <typename T, int CacheDtype>
+// SINGLE: it takes one.
+template <typename T, int CacheDtype, bool SINGLE>
 __global__ void __launch_bounds__(NT) kv_read_kernel(const KvReadParams p) {
     dependent_prologue();
     using C = typename Elem<CacheDtype>::type;
@@ -267,9 +268,9 @@ __global__ void __launch_bounds__(NT) kv_read_kernel(const KvReadParams p) {
     constexpr int N = Vec16<T>::N;
     constexpr int U = READ_UNROLL;
     const int lane = threadIdx.x % 32;
-    const long long t0 = ((long long)blockIdx.x * (NT / 32) + threadIdx.x / 32) * p.tok;
+    const long long t0 = ((long long)blockIdx.x * (NT / 32) + threadIdx.x / 32) * (SINGLE ? 1 : p.tok);
     if (t0 >= p.T) return;
-    const int tokens = (int)min((long long)p.tok, p.T - t0);
+    const int tokens = SINGLE ? 1 : (int)min((long long)p.tok, p.T - t0);
 
     // the last sequence that starts at or before t0, all lanes probing; then before the lane's own token
     int lo = 0, hi = p.B;
@@ -315,6 +316,11 @@ __global__ void __launch_bounds__(NT) kv_read_kernel(const KvReadParams p) {
     const C *src = static_cast<const C *>(blockIdx.y ? p.c.v : p.c.k);
     const float *scales = blockIdx.y ? p.c.v_scale : p.c.k_scale;
     T *out = static_cast<T *>(blockIdx.y ? p.v_out : p.k_out) + t0 * p.c.H * p.c.d;
+    if constexpr (SINGLE) {
+        off = __shfl_sync(0xffffffffu, off, 0);
+        soff = __shfl_sync(0xffffffffu, soff, 0);
+        if (off == -1) return;
+    }
     for (int base = 0; base < n; base += 32 * U) {
         Raw<CacheDtype, N> raw[U];
         float scale[U];
@@ -322,10 +328,15 @@ __global__ void __launch_bounds__(NT) kv_read_kernel(const KvReadParams p) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = base + 32 * u + lane;
-            const int r = p.tok == 1 ? 0 : __umulhi((unsigned)i, p.per_token_inv);
-            const int k = i - r * per_token;
+            int k = i;
+            long long o = off, so = soff;
+            if constexpr (!SINGLE) {
+                const int r = __umulhi((unsigned)i, p.per_token_inv);
+                k = i - r * per_token;
+                o = __shfl_sync(0xffffffffu, off, r);
+                so = __shfl_sync(0xffffffffu, soff, r);
+            }
             const int h = k >> head_shift, ch = (k & ((1 << head_shift) - 1)) * N;
-            const long long o = __shfl_sync(0xffffffffu, off, r), so = __shfl_sync(0xffffffffu, soff, r);
             dst[u] = i < n && o != -1 ? out + (long long)i * N : nullptr;
             raw[u] = {};
             scale[u] = 0.f;
@@ -361,16 +372,16 @@ cudaError_t write_io(const KvWriteParams &p, int io_dtype, int cache_dtype, cuda
     return write_typed<T, same>(p, stream);
 }
 
-template <typename T>
+template <typename T, bool SINGLE>
 cudaError_t read_io(const KvReadParams &p, int cache_dtype, cudaStream_t stream) {
     const long long warps = (p.T + (long long)p.tok - 1) / p.tok;
     const dim3 grid((unsigned)((warps + NT / 32 - 1) / (NT / 32)), 2);
     switch (cache_dtype) {
-        case GDN_F16: return launch_dependent(kv_read_kernel<T, GDN_F16>, grid, dim3(NT), 0, stream, p);
-        case GDN_BF16: return launch_dependent(kv_read_kernel<T, GDN_BF16>, grid, dim3(NT), 0, stream, p);
-        case GDN_FP8_E4M3: return launch_dependent(kv_read_kernel<T, GDN_FP8_E4M3>, grid, dim3(NT), 0, stream, p);
-        case GDN_INT8: return launch_dependent(kv_read_kernel<T, GDN_INT8>, grid, dim3(NT), 0, stream, p);
-        default: return launch_dependent(kv_read_kernel<T, GDN_F32>, grid, dim3(NT), 0, stream, p);
+        case GDN_F16: return launch_dependent(kv_read_kernel<T, GDN_F16, SINGLE>, grid, dim3(NT), 0, stream, p);
+        case GDN_BF16: return launch_dependent(kv_read_kernel<T, GDN_BF16, SINGLE>, grid, dim3(NT), 0, stream, p);
+        case GDN_FP8_E4M3: return launch_dependent(kv_read_kernel<T, GDN_FP8_E4M3, SINGLE>, grid, dim3(NT), 0, stream, p);
+        case GDN_INT8: return launch_dependent(kv_read_kernel<T, GDN_INT8, SINGLE>, grid, dim3(NT), 0, stream, p);
+        default: return launch_dependent(kv_read_kernel<T, GDN_F32, SINGLE>, grid, dim3(NT), 0, stream, p);
     }
 }
 
@@ -388,15 +399,21 @@ cudaError_t launch_kv_write(const KvWriteParams &p, int io_dtype, int cache_dtyp
 cudaError_t launch_kv_read(const KvReadParams &given, int io_dtype, int cache_dtype, cudaStream_t stream) {
     if (given.T == 0 || given.B == 0) return cudaSuccess;
     KvReadParams p = given;
-    // two passes of a warp's pieces, fewer tokens if that leaves warps out
+    // A token a warp where that fills a pass of its lanes (or would leave warps out otherwise), else as many as
+    // two passes hold.  (39,000 tokens of 8 int8 heads of 128: 40.1 us with one, 41.6 us with two.)
     const long long per_token = (long long)p.c.H * p.c.d * (io_dtype == GDN_F32 ? 4 : 2) / 16;
     const long long most = 2 * 32 * READ_UNROLL / per_token, share = p.T / (32LL * current_device_sms());
-    p.tok = (int)std::max(1LL, std::min(std::min(most, share), 32LL));
-    p.per_token_inv = (unsigned)((1ULL << 32) / per_token + 1);  // exact below 2^32 / per_token (1: not used)
+    p.tok = per_token >= 32 * READ_UNROLL ? 1 : (int)std::max(1LL, std::min(std::min(most, share), 32LL));
+    p.per_token_inv = (unsigned)((1ULL << 32) / per_token + 1);  // exact below 2^32 / per_token (one token: not used)
+    const bool single = p.tok == 1;
+    auto launch = [&](auto t) {
+        using T = decltype(t);
+        return single ? read_io<T, true>(p, cache_dtype, stream) : read_io<T, false>(p, cache_dtype, stream);
+    };
     switch (io_dtype) {
-        case GDN_F16: return read_io<__half>(p, cache_dtype, stream);
-        case GDN_BF16: return read_io<__nv_bfloat16>(p, cache_dtype, stream);
-        default: return read_io<float>(p, cache_dtype, stream);
+        case GDN_F16: return launch(__half());
+        case GDN_BF16: return launch(__nv_bfloat16());
+        default: return launch(0.f);
     }
 }
 
