@@ -1363,13 +1363,16 @@ cudaError_t launch_sized(const PagedAttnParams &p, cudaStream_t stream) {
     if (by_rows) box_tokens = 1, box_shift = 0;
     if constexpr (C::W == 8) {
         // the roles divide what the block is launched with, which has to be all of it
-        static const bool whole = [] {
-            cudaFuncAttributes a{}, b{};
-            return cudaFuncGetAttributes(&a, paged_attention_kernel<CT, C, false>) == cudaSuccess &&
-                   cudaFuncGetAttributes(&b, paged_attention_kernel<CT, C, true>) == cudaSuccess &&
-                   a.numRegs == C::LAUNCH_REGS && b.numRegs == C::LAUNCH_REGS;
-        }();
-        if (!whole) return cudaErrorInvalidConfiguration;
+        static int whole = 0;  // 1: it is, -1: not
+        if (__atomic_load_n(&whole, __ATOMIC_RELAXED) == 0) {
+            cudaFuncAttributes tensor{}, rows{};
+            cudaError_t e = cudaFuncGetAttributes(&tensor, paged_attention_kernel<CT, C, false>);
+            if (e == cudaSuccess) e = cudaFuncGetAttributes(&rows, paged_attention_kernel<CT, C, true>);
+            if (e != cudaSuccess) return e;
+            const bool ok = tensor.numRegs == C::LAUNCH_REGS && rows.numRegs == C::LAUNCH_REGS;
+            __atomic_store_n(&whole, ok ? 1 : -1, __ATOMIC_RELAXED);
+        }
+        if (__atomic_load_n(&whole, __ATOMIC_RELAXED) < 0) return cudaErrorInvalidConfiguration;
     }
     auto kernel = by_rows ? paged_attention_kernel<CT, C, true> : paged_attention_kernel<CT, C, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
