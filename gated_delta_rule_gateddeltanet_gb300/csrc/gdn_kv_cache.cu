@@ -4,14 +4,14 @@
 // Both are HBM streams: a write reads a token's k, v (and q) once and writes
 // its cache rows once; a read back reads cache rows once and writes them in
 // the I/O type.  At decode sizes a write is a launch and two dependent loads
-// (position, table), so it takes the query rotation along: 1.8 us for 64 tokens
+// (position, table), so it takes the query rotation along: 1.7 us for 64 tokens
 // of 8 + 8 heads of 128.
 //
 // Write: a row (one token's channels of one head) belongs to a group of
 // d * sizeof(T) / 32 lanes, each holding two 16-byte groups with whole channel
 // pairs.  The rotation needs no exchange and the largest magnitude is a few
 // shuffles inside the group; the quantised row leaves as one contiguous run.
-// 8 x 512 BF16 tokens of 8 + 8 heads of 128: 8.8 us to e4m3, 9.6 us to int8
+// 8 x 512 BF16 tokens of 8 + 8 heads of 128: 8.3 us to e4m3, 9.4 us to int8
 // (their traffic: 3.9 us), bound by instructions (conversion and rotation).
 //
 // Read back: a warp looks up its tokens' rows, a lane each, and then moves them
@@ -19,7 +19,7 @@
 // where 4 took 41.7 us for int8; 8: the same, 16-bit rows 19% slower).  Keys
 // first, then values: the two in turn ran 20% slower at 16 bits.  39,000 tokens
 // of 8 + 8 int8 heads of 128 to BF16: 40.1 us, 6.1 TB/s (0.90 of a copy's rate);
-// 16-bit rows 51 us, 6.2 TB/s; four contexts of at most 77 tokens 2.1 us.
+// 16-bit rows 51 us, 6.2 TB/s; four contexts of at most 77 tokens 2.0 us.
 #include "attn_internal.cuh"
 
 #include <string.h>
@@ -29,7 +29,9 @@
 namespace gdn {
 namespace {
 
-constexpr int NT = 256;
+// (256: a write of 4096 int8 tokens 9.7 us instead of 9.4 us, four short ones with their read
+// back 4.1 us instead of 4.0 us; 512: 10.3 and 4.8 us)
+constexpr int NT = 128;
 
 template <int CacheDtype>
 struct Elem;

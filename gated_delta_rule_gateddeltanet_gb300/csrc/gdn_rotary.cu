@@ -9,14 +9,16 @@
 // loads the item's cosines and sines once and applies them to HEADS heads, so
 // the table costs one read per HEADS heads and HEADS independent pairs of
 // loads are in flight per thread.  8192 BF16 tokens of 18 heads of 256, a quarter
-// rotated: 24.8 us, 6.2 TB/s (0.91 of a copy's rate); 4111 FP32 tokens of 16 heads
-// of 64, interleaved, inverse: 6.1 us, 5.6 TB/s; 64 tokens of 40 heads: 1.8 us, a launch.
+// rotated: 24.4 us, 6.3 TB/s (0.93 of a copy's rate); 4111 FP32 tokens of 16 heads
+// of 64, interleaved, inverse: 6.1 us, 5.7 TB/s; 64 tokens of 40 heads: 1.7 us, a launch.
 #include "attn_internal.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int NT = 256;
+// (256: 24.8 us instead of 24.4 us for the prompt above, 6.3 us instead of 6.1 us for the gradient; 512: 30.7 and
+// 6.8 us; 64: 24.4 and 6.5 us.  Two heads a thread instead of four 25.3 us, six 26.9 us.)
+constexpr int NT = 128;
 
 // Table: a thread owns pair i and walks ROWS positions; its frequency is
 // evaluated once, in 64 bits like the angles (an FP32 product of position and
