@@ -138,11 +138,14 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 // x = hi + lo with hi rounded to TF32 (to nearest in magnitude, so that lo and
 // the dropped lo lo products have no sign in common; in integers: with
 // the convert instruction 8 x 4096 tokens of heads of 128 took 58.6 us instead of 49.1 us).  The tensor cores drop lo's bits
-// past TF32, which leaves 21 bits.  A non-finite x stays in hi alone.
+// past TF32, which leaves 21 bits.  From 0x7f7ff000 on (the largest numbers, infinities, NaN) hi is
+// cut instead, since rounding would carry into the exponent or the sign; lo is then NaN for an x
+// that is not finite, whatever the cut leaves of its bits.  (An infinity kept in hi alone would cost a compare and a
+// select more, 60.6 us, and meet the other operand's lo, whose sign is any, in its product.)
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
-    hi = (x + 0x1000u) & 0xffffe000u;
-    const float l = __uint_as_float(x) - __uint_as_float(hi);
-    lo = l == l ? __float_as_uint(l) : 0u;
+    const float f = __uint_as_float(x);
+    hi = (fabsf(f) < __uint_as_float(0x7f7ff000u) ? x + 0x1000u : x) & 0xffffe000u;
+    lo = __float_as_uint(f - __uint_as_float(hi));
 }
 // D += A B for FP32 operands.  The tensor cores cut what they add off at the bits of the largest
 // addend, always towards zero, so a D should hold a few products only and be added to

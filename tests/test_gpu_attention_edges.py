@@ -1,0 +1,135 @@
+"""Paged attention at the edges of its inputs' ranges: NaN of every bit pattern,
+infinities and values next to FP32's largest."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_gateddeltanet_gb300 as gdn
+from attention_common import Paged, check_attention, f64, rounding
+from gpu_common import dev
+from test_gpu_paged_attention import queries
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32, FP8, I8 = torch.float16, torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int8
+
+
+def bits(pattern):
+    """The FP32 number with this bit pattern."""
+    return torch.tensor([pattern - (1 << 32 if pattern >> 31 else 0)], dtype=torch.int32, device=dev()).view(F32)[0]
+
+
+def slot(p, b, t):
+    return int(p.table[b, t // p.page]), t % p.page
+
+
+def cu_of(spans):
+    return torch.tensor(np.concatenate([[0], np.cumsum(spans)]), dtype=torch.int32, device=dev())
+
+
+NANS = [0x7fffffff, 0xffffffff, 0x7fc00000, 0xffc00000, 0x7f800001, 0xff801fff, 0x7ffff000]
+INFS = [0x7f800000, 0xff800000]
+
+
+@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("pattern", NANS + INFS)
+def test_fp32_not_finite_where_it_is_seen(pattern, d, n):
+    """In a query, a seen key and a seen value, alone in its head's rows or channel; one token and a span."""
+    p = Paged([40, 21], 2, d, 16, F32, seed=d)
+    q = queries(2 * n, 4, d, F32)
+    cu = cu_of([n, n])
+    call = lambda q: gdn.paged_attention(q, p.cache, p.table, p.kv_lens, cu_seqlens=cu)  # noqa: E731
+    good = call(q)
+    assert torch.isfinite(good).all()
+    bad_q = q.clone()
+    bad_q[n - 1, 2, 5] = bits(pattern)
+    out = call(bad_q)  # one row of sequence 0
+    # (an infinite query has scores of both signs, and the largest is infinite)
+    assert torch.isnan(out[n - 1, 2]).all()
+    out[n - 1, 2] = good[n - 1, 2]
+    assert torch.equal(out, good)
+
+    page, off = slot(p, 1, 9)
+    keep = p.cache.k[page, off].clone()
+    p.cache.k[page, off, 1, 7] = bits(pattern)
+    out = call(q)  # key head 1, so query heads 2 and 3 of sequence 1
+    for i in range(n, 2 * n):
+        for h in (2, 3):
+            if pattern in NANS or (float(q[i, h, 7]) > 0) == (pattern == 0x7f800000):
+                assert torch.isnan(out[i, h]).all()
+    out[n:, 2:] = good[n:, 2:]
+    assert torch.equal(out, good)
+    p.cache.k[page, off] = keep
+
+    p.cache.v[page, off, 0, 3] = bits(pattern)
+    out = call(q)
+    seen = out[n:, :2, 3]
+    assert torch.isnan(seen).all() if pattern in NANS else not torch.isfinite(seen).any()
+    out[n:, :2, 3] = good[n:, :2, 3]
+    assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (256, 16), (64, 7)])
+@pytest.mark.parametrize("pattern", NANS + INFS)
+def test_fp32_not_finite_where_it_is_masked(pattern, d, page):
+    """In the last drafted token's key and value: the queries before it do not see it, the last does."""
+    p = Paged([40, 21], 2, d, page, F32, seed=d)
+    q = queries(8, 4, d, F32)
+    call = lambda: gdn.paged_attention(q, p.cache, p.table, p.kv_lens, cu_seqlens=cu_of([4, 4]))  # noqa: E731
+    good = call()
+    for b, length in enumerate(p.lens):
+        at = slot(p, b, length - 1)
+        p.cache.k[at][:, 2] = bits(pattern)
+        p.cache.v[at][:, ::3] = bits(pattern)
+    out = call()
+    for b in (0, 4):
+        # (a tile with such a value is added row by row, each row's values that it does not see as zeros)
+        assert (out[b:b + 3] - good[b:b + 3]).abs().max() <= 2.0 ** -20 * good.abs().max()
+        assert not torch.isfinite(out[b + 3, :, ::3]).any()
+
+
+def test_fp32_a_nan_key_that_the_write_rotated():
+    """What arithmetic on the GPU makes of a NaN is another pattern than the host's."""
+    table = gdn.rotary_table(64, 64, device=dev())
+    cache = gdn.PagedKVCache.allocate(4, 16, 1, 64, dtype=F32, device=dev())
+    k, v = (torch.randn(20, 1, 64, device=dev()) for _ in range(2))
+    k[3, 0, 5] = float("nan")
+    pos = torch.arange(20, dtype=torch.int32, device=dev())
+    gdn.kv_cache_write(k, v, cache, pos, positions=pos, table=table)
+    out, lse = gdn.paged_attention(queries(1, 4, 64, F32), cache, torch.arange(4, dtype=torch.int32, device=dev())[None],
+                                   torch.tensor([20], dtype=torch.int32, device=dev()), return_lse=True)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("pattern", [0x7f7fefff, 0x7f7ff000, 0x7f7ff800, 0xff7ff000, 0xff7ff800])
+def test_fp32_values_next_to_the_largest(pattern):
+    """Finite numbers that rounding to fewer bits would take to infinity.  A lone value comes back with the error of two
+    TF32 parts (2^-21) and of the weight's and the quotient's roundings; the patterns stay clear of the largest by more."""
+    p = Paged([1, 1], 1, 64, 16, F32)
+    x = bits(pattern)
+    p.cache.v[slot(p, 0, 0)][:, 5] = x
+    out = gdn.paged_attention(queries(2, 4, 64, F32), p.cache, p.table, p.kv_lens)
+    assert torch.isfinite(out).all()
+    assert np.all(np.abs(f64(out[0, :, 5]) / f64(x) - 1) <= 2.0 ** -19)
+
+
+@pytest.mark.parametrize("which", ["key", "query"])
+@pytest.mark.parametrize("pattern", [0x7f7ff000, 0x7f7fffff, 0xff7ff800])
+def test_fp32_products_with_numbers_next_to_the_largest(pattern, which):
+    """One channel of a key (or query) next to 2^128 against small whole multiples of 2^-126: scores of a few units."""
+    p = Paged([30], 1, 64, 16, F32, seed=2)
+    rows = torch.arange(30, device=dev())
+    at = (p.table[0].long()[rows // 16], rows % 16)
+    p.cache.k[at] = 0
+    big, small = bits(pattern), torch.tensor(2.0 ** -126, device=dev())
+    q = torch.zeros(1, 4, 64, device=dev())
+    steps = torch.arange(30, device=dev()) % 7 - 3
+    if which == "key":
+        p.cache.k[at[0][4], at[1][4], 0, 9] = big
+        q[0, :, 9] = small * torch.tensor([1.0, -2.0, 3.0, 0.0], device=dev())
+    else:
+        q[0, 1, 9] = big
+        p.cache.k[at[0], at[1], 0, 9] = small * steps
+    out, lse = gdn.paged_attention(q, p.cache, p.table, p.kv_lens, scale=0.25, return_lse=True)
+    check_attention(out, lse, q, p, [1], 0.25)
