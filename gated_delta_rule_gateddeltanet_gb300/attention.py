@@ -134,6 +134,8 @@ def _block_table(t, seqs, device):
         raise ValueError(f"block_table must be [{seqs}, pages], got {tuple(t.shape)}")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("block_table: a row's entries must be contiguous")
+    if seqs > 1 and t.shape[1] > 0 and t.stride(0) == 0:  # (0 is the C ABI's word for no gap)
+        raise ValueError("block_table: rows must not share memory (an expanded view)")
     return t.shape[1], t.stride(0) if seqs > 1 and t.shape[1] > 0 else t.shape[1]
 
 
