@@ -165,7 +165,16 @@ def _token_stride(t, name, inner):
         return inner
     if t.stride(2) != 1 or t.stride(1) != t.shape[2]:
         raise ValueError(f"{name}: heads and channels must be contiguous inside a token")
-    return t.stride(0) if t.shape[0] > 1 else inner
+    return _row_stride(t, name, inner)
+
+
+def _row_stride(t, name, inner):
+    """Elements between consecutive rows (tokens) of ``t``, ``inner`` where there is only one."""
+    if t.shape[0] <= 1:
+        return inner
+    if t.stride(0) == 0 and t.numel() > 0:  # (0 is the C ABI's word for no gap)
+        raise ValueError(f"{name}: tokens must not share memory (an expanded view)")
+    return t.stride(0)
 
 
 def build_forward_args(q, k, v, a, b, cu_seqlens, *, A_log=None, dt_bias=None, gate_mode="raw",
@@ -463,7 +472,7 @@ def build_conv_args(x, weight, cu_seqlens, *, bias=None, initial_state=None, fin
     a.num_state_slots, a.io_dtype = int(num_state_slots), DTYPE[x.dtype]
     a.activation, a.state_update_capacity = ACTIVATION[activation], int(capacity)
     a.max_seqlen = int(max_seqlen or 0)
-    a.x_stride = x.stride(0) if T > 1 else C
+    a.x_stride = _row_stride(x, "x", C)
     a.x, a.weight, a.bias = _ptr(x), _ptr(weight), _ptr(bias)
     a.cu_seqlens, a.state_slots, a.capture_count = _ptr(cu_seqlens), _ptr(state_slots), _ptr(capture_count)
     a.initial_state, a.final_state, a.output = _ptr(initial_state), _ptr(final_state), _ptr(output)

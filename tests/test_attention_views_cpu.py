@@ -23,3 +23,40 @@ def test_an_expanded_block_table_is_refused():
     # one sequence's stride is free
     one = dict(kw, q=z(1, 8, 64), kv_lens=ints(1))
     assert gdn.PagedAttentionCall(block_table=ints(2).expand(1, 2), **one).args.block_table_stride == 2
+
+
+@pytest.mark.parametrize("name", ["q", "k", "q_out", "k_out"])
+def test_expanded_tokens_are_refused_in_a_rotation(name):
+    kw = dict(q=z(3, 4, 64), k=z(3, 2, 64), positions=ints(3), table=torch.zeros(9, 64), q_out=z(3, 4, 64), k_out=z(3, 2, 64))
+    gdn.RotaryCall(**kw)
+    with pytest.raises(ValueError, match=name):
+        gdn.RotaryCall(**{**kw, name: kw[name][:1].expand_as(kw[name])})
+
+
+@pytest.mark.parametrize("name", ["k", "v", "q", "q_out"])
+def test_expanded_tokens_are_refused_in_a_write(name):
+    kw = dict(k=z(3, 2, 64), v=z(3, 2, 64), cache=_kv(), slots=ints(3), positions=ints(3), table=torch.zeros(9, 64),
+              q=z(3, 4, 64), q_out=z(3, 4, 64))
+    gdn.KVCacheWriteCall(**kw)
+    with pytest.raises(ValueError, match=name):
+        gdn.KVCacheWriteCall(**{**kw, name: kw[name][:1].expand_as(kw[name])})
+
+
+def test_expanded_queries_are_refused():
+    kw = dict(cache=_kv(), block_table=ints(3, 2), kv_lens=ints(3), workspace=torch.zeros(16, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="q"):
+        gdn.PagedAttentionCall(q=z(1, 8, 64).expand(3, 8, 64), **kw)
+
+
+def test_expanded_tokens_are_refused_by_the_recurrence_and_the_convolution():
+    t, h, d = 6, 2, 32
+    f = lambda *s: torch.zeros(s)  # noqa: E731
+    cu = torch.tensor([0, 6], dtype=torch.int32)
+    kw = dict(q=z(t, h, d), k=z(t, h, d), v=z(t, h, d), a=f(t, h), b=f(t, h), cu_seqlens=cu)
+    gdn.build_forward_args(**kw, A_log=f(h), dt_bias=f(h))
+    for name in "qkv":
+        with pytest.raises(ValueError, match=name):
+            gdn.build_forward_args(**{**kw, name: z(1, h, d).expand(t, h, d)}, A_log=f(h), dt_bias=f(h))
+    gdn.build_conv_args(z(t, 16), f(16, 4), cu)
+    with pytest.raises(ValueError, match="x"):
+        gdn.build_conv_args(z(1, 16).expand(t, 16), f(16, 4), cu)
