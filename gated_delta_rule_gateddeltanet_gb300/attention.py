@@ -262,6 +262,8 @@ class PagedKVCache:
         of = lambda t: tuple(t.stride(i) if t.shape[i] > 1 else dense[i] for i in range(3))  # noqa: E731
         if of(x) != of(y):
             raise ValueError(f"{names} must have the same strides")
+        if x.numel() and of(x) == (0, 0, 0):  # (the C ABI's word for no gaps)
+            raise ValueError(f"{names}: one row for all pages, tokens and heads (an expanded view)")
         return of(x)
 
     @classmethod

@@ -60,3 +60,17 @@ def test_expanded_tokens_are_refused_by_the_recurrence_and_the_convolution():
     gdn.build_conv_args(z(t, 16), f(16, 4), cu)
     with pytest.raises(ValueError, match="x"):
         gdn.build_conv_args(z(1, 16).expand(t, 16), f(16, 4), cu)
+
+
+def test_a_cache_of_one_expanded_row_or_scale_is_refused():
+    rows = z(1, 1, 1, 64).expand(6, 16, 2, 64)
+    with pytest.raises(ValueError, match="k and v"):
+        gdn.PagedKVCache(rows, rows.clone().as_strided(rows.shape, rows.stride()))
+    i8 = z(6, 16, 2, 64, dtype=torch.int8)
+    unit = torch.ones(1, 1, 1).expand(6, 16, 2)
+    with pytest.raises(ValueError, match="k_scale and v_scale"):
+        gdn.PagedKVCache(i8, i8.clone(), unit, unit)
+    # a scale for each head, whatever the page and token
+    heads = torch.ones(2).expand(6, 16, 2)
+    c = gdn.PagedKVCache(i8, i8.clone(), heads, heads).args
+    assert (c.scale_page_stride, c.scale_token_stride, c.scale_head_stride) == (0, 0, 1)
