@@ -197,6 +197,10 @@ gdn_status gdn_kv_cache_write(const gdn_kv_write_args *a, gdn_stream_t stream) {
     if (p.k_stride < 0 || p.v_stride < 0 || p.q_stride < 0 || p.qo_stride < 0) return GDN_ERR_SHAPE;
     const gdn_status st = resolve_cache(a->cache, &p.c);
     if (st != GDN_OK) return st;
+    if (eight_bit(a->cache.cache_dtype) &&  // rows that share a scale can be read, not written
+        ((p.c.num_pages > 1 && p.c.s_page_stride == 0) || (p.c.page_size > 1 && p.c.s_token_stride == 0) ||
+         (p.c.H > 1 && p.c.s_head_stride == 0)))
+        return GDN_ERR_SHAPE;
     if (a->total_tokens == 0) return GDN_OK;
     if (!a->k || !a->v || !a->slots || (a->table && !a->positions) || (qn && (!a->q || !a->q_out))) return GDN_ERR_NULL;
     const size_t esz = io_bytes(a->io_dtype);

@@ -560,7 +560,8 @@ gdn_status gdn_rotary(const gdn_rotary_args *args, gdn_stream_t stream);
  *                     16-byte aligned, strides whole multiples of 16 bytes.
  *   k_scale, v_scale  device FP32, one per (page, offset, head), by the three
  *                     scale strides (0, 0, 0: [num_pages, page_size, num_kv_heads]).
- *                     8-bit caches only; NULL otherwise.
+ *                     A stride of 0 beside others (rows that share a scale) can be
+ *                     read and attended to, not written.  8-bit caches only; NULL otherwise.
  * An 8-bit row holds channels x as q * scale:
  *   GDN_FP8_E4M3  scale = the smallest power of two (at least 2^-120) with
  *                 max|x| <= 448 scale; q = x / scale rounded to e4m3.  A power

@@ -1,6 +1,8 @@
 """The binding refuses views whose strides the C ABI would take for something
 else: a stride of 0 (an expanded view) is its word for rows without a gap, which
 would read or write past the view's memory.  CPU tensors: nothing is launched."""
+import ctypes
+
 import pytest
 import torch
 
@@ -74,3 +76,18 @@ def test_a_cache_of_one_expanded_row_or_scale_is_refused():
     heads = torch.ones(2).expand(6, 16, 2)
     c = gdn.PagedKVCache(i8, i8.clone(), heads, heads).args
     assert (c.scale_page_stride, c.scale_token_stride, c.scale_head_stride) == (0, 0, 1)
+
+
+@pytest.mark.parametrize("scales", [torch.ones(2).expand(6, 16, 2), torch.ones(16, 2).expand(6, 16, 2),
+                                    torch.ones(6, 16, 1).expand(6, 16, 2)])
+def test_rows_that_share_a_scale_are_not_written(scales):
+    """Every row's scale is written: rows that share one would overwrite each other's."""
+    from gated_delta_rule_gateddeltanet_gb300 import build
+    build.build()
+    i8 = z(6, 16, 2, 64, dtype=torch.int8)
+    call = gdn.KVCacheWriteCall(z(0, 2, 64), z(0, 2, 64), gdn.PagedKVCache(i8, i8.clone(), scales, scales), ints(0))
+    fn = gdn.load_library().gdn_kv_cache_write
+    assert fn(ctypes.byref(call.args), None) == 3  # GDN_ERR_SHAPE, before any launch
+    own = [torch.ones(6, 2, 16).transpose(1, 2) for _ in range(2)]
+    call = gdn.KVCacheWriteCall(z(0, 2, 64), z(0, 2, 64), gdn.PagedKVCache(i8, i8.clone(), *own), ints(0))
+    assert fn(ctypes.byref(call.args), None) == 0
