@@ -36,6 +36,8 @@ class AttentionStep:
 
     def __init__(self, cache, table, *, seqs, num_q_heads, pages_per_seq, tokens=1, dtype=torch.float16,
                  interleaved=False, scale=0.0, window=0):
+        if pages_per_seq < 1:
+            raise ValueError("pages_per_seq must be at least 1")
         dev, (_, page, heads, d) = cache.device, cache.k.shape
         self.cache, self.seqs, self.tokens, self.page = cache, seqs, tokens, page
         T = seqs * tokens
@@ -55,11 +57,14 @@ class AttentionStep:
         self.graph = None
 
     def place(self):
-        """Positions and slots of the new tokens, from ``kv_lens`` and ``block_table`` (device operations only)."""
+        """Positions and slots of the new tokens, from ``kv_lens`` and ``block_table`` (device operations only).  A token
+        past the table's last page gets a slot outside the pool, so that it is flagged and not written."""
         at = self.kv_lens[:, None] - self.tokens + torch.arange(self.tokens, dtype=torch.int32, device=self.kv_lens.device)
-        page = self.block_table.gather(1, (at // self.page).clamp(min=0).long())
+        index, pages = at // self.page, self.block_table.shape[1]
+        page = self.block_table.gather(1, index.clamp(0, pages - 1).long())
+        slot = torch.where(index < pages, page * self.page + at % self.page, self.cache.args.num_pages * self.page)
         self.positions.copy_(at.flatten())
-        self.slots.copy_((page * self.page + at % self.page).flatten())
+        self.slots.copy_(slot.flatten())
 
     def launch(self, stream=None):
         """The step's two calls on ``stream`` (default: the current one)."""
