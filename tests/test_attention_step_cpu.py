@@ -1,5 +1,5 @@
 """Where ``AttentionStep.place`` puts new tokens, on the CPU (it is torch
-operations on the step's buffers): sequences past the block table's end."""
+operations on the step's buffers): sequences past the block table's end, idle ones."""
 import pytest
 import torch
 
@@ -39,6 +39,14 @@ def test_tokens_past_the_table_get_a_slot_outside_the_pool():
     out = PAGES * PAGE
     assert slots == [[95, out], [out, out], [out, out], [3, 4]]
     assert pos[0] == [31, 32] and pos[3] == [3, 4]
+
+
+def test_idle_rows_are_not_stored():
+    pos, slots = step_of([0, 1, 0], [[3, 5], [1, 2], [0, 0]])
+    assert pos == [[0], [0], [0]] and slots == [[-1], [16], [-1]]
+    pos, slots = step_of([0, 2, 4], [[3, 5], [1, 2], [0, 0]], tokens=4)
+    assert pos == [[0, 0, 0, 0], [0, 0, 0, 1], [0, 1, 2, 3]]
+    assert slots == [[-1] * 4, [-1, -1, 16, 17], [0, 1, 2, 3]]
 
 
 def test_a_step_needs_a_page_a_sequence():
