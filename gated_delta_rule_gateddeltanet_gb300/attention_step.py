@@ -59,11 +59,14 @@ class AttentionStep:
     def place(self):
         """Positions and slots of the new tokens, from ``kv_lens`` and ``block_table`` (device operations only).  A token
         before a sequence's first position (an idle row: ``kv_lens`` 0, or fewer than the new tokens) is not stored: slot -1.
-        One past the table's last page gets a slot outside the pool, so that it is flagged and not written."""
+        One past the table's last page, or in a page that the pool does not have, gets a slot outside the pool, so that
+        it is flagged and not written."""
         at = self.kv_lens[:, None] - self.tokens + torch.arange(self.tokens, dtype=torch.int32, device=self.kv_lens.device)
         index, pages = at // self.page, self.block_table.shape[1]
         page = self.block_table.gather(1, index.clamp(0, pages - 1).long())
-        slot = torch.where(index < pages, page * self.page + at % self.page, self.cache.args.num_pages * self.page)
+        pool = self.cache.args.num_pages
+        inside = (index < pages) & (page >= 0) & (page < pool)
+        slot = torch.where(inside, page.clamp(0, pool - 1) * self.page + at % self.page, pool * self.page)
         self.positions.copy_(at.clamp(min=0).flatten())
         self.slots.copy_(torch.where(at < 0, -1, slot).flatten())
 

@@ -1,5 +1,6 @@
 """Where ``AttentionStep.place`` puts new tokens, on the CPU (it is torch
-operations on the step's buffers): sequences past the block table's end, idle ones."""
+operations on the step's buffers): sequences past the
+block table's end, idle ones, pages that the pool does not have."""
 import pytest
 import torch
 
@@ -47,6 +48,13 @@ def test_idle_rows_are_not_stored():
     pos, slots = step_of([0, 2, 4], [[3, 5], [1, 2], [0, 0]], tokens=4)
     assert pos == [[0, 0, 0, 0], [0, 0, 0, 1], [0, 1, 2, 3]]
     assert slots == [[-1] * 4, [-1, -1, 16, 17], [0, 1, 2, 3]]
+
+
+@pytest.mark.parametrize("entry", [-1, -2, PAGES, 2 ** 27 + 1, 2 ** 31 - 1, -2 ** 31])
+def test_entries_outside_the_pool_give_a_slot_outside_it(entry):
+    """Whatever the offset: -1 is no token's slot (it would mean not stored), a product does not wrap into the pool."""
+    for length in (1, 9, 16):
+        assert step_of([length, 16], [[entry, 5], [1, 2]]) == ([[length - 1], [15]], [[PAGES * PAGE], [31]])
 
 
 def test_a_step_needs_a_page_a_sequence():

@@ -50,3 +50,27 @@ def test_fewer_cached_tokens_than_new_ones():
     assert int(step.status) == 0
     assert torch.all(step.out[4:6] == 0) and torch.all(step.out[6:8] != 0)
     assert changed(step, before) == [16, 17, 18, 19, 48, 49, 6 * 16 + 26, 6 * 16 + 27, 6 * 16 + 28, 6 * 16 + 29]
+
+
+@pytest.mark.parametrize("tokens", [1, 4])
+def test_rows_past_their_table_and_pages_outside_the_pool_are_flagged(tokens):
+    good, _ = run([20, 20, 30], tokens, torch.float16)
+    t = tokens
+    for length in (3 * 16 + 1, 3 * 16 + t, 1000, 2 ** 31 - 1):
+        step, before = run([20, length, 30], t, torch.float16)
+        assert int(step.status) & gdn.DEVERR["kv_len"] and int(step.status) & gdn.DEVERR["cache_slot"]
+        assert torch.equal(step.out[:t], good.out[:t]) and torch.equal(step.out[2 * t:], good.out[2 * t:])
+        stored = [3 * 16 + i for i in range(length - t, 3 * 16)]
+        assert changed(step, before) == [20 - t + i for i in range(t)] + stored + [6 * 16 + 30 - t + i for i in range(t)]
+    for entry in (-1, 9, 2 ** 31 - 1):
+        step = good
+        step.status.zero_()
+        step.kv_lens[1] = 32
+        step.block_table[1, 1] = entry
+        before = step.cache.k.clone().view(torch.uint8)
+        step.k.add_(1)
+        step.place()
+        step.replay()
+        torch.cuda.synchronize()
+        assert int(step.status) == gdn.DEVERR["cache_slot"] | gdn.DEVERR["page"]
+        assert changed(step, before) == [20 - t + i for i in range(t)] + [6 * 16 + 30 - t + i for i in range(t)]
