@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
             const int r0 = BATCH * (warp - W - C::NP);
             const int group = w.row0 + min(lane, rows - 1);  // lane r: where row r is
             const int token = w.s.n == 1 ? 0 : (int)((uint32_t)group / (uint32_t)p.G);
-            const long long row = ((long long)(w.s.cu0 + token) * p.q_stride + (w.head * p.G + group - token * p.G) * D) * EB;
+            const long long head = (long long)w.head * p.G + group - token * p.G;
+            const long long row = ((long long)(w.s.cu0 + token) * p.q_stride + head * D) * EB;
             uint32_t x[BATCH][WORDS];
 #pragma unroll
             for (int r = 0; r < BATCH; ++r) {
