@@ -329,7 +329,8 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams &p, int b, bool fl
     if (flag && bad_cu) flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
     if (flag && bad_len) flag_error(p.status, GDN_DEVERR_KV_LEN);
     if (bad_cu || bad_len) s.n = 0;
-    s.first = p.window > 0 ? max(0, s.len - s.n - p.window + 1) : 0;
+    const int upto = s.len - s.n + 1;  // (compared, not subtracted: a window may be as large as an int)
+    s.first = p.window > 0 && upto > p.window ? upto - p.window : 0;
     s.t0 = s.first / C::TT * C::TT;
     s.tiles = s.len > s.t0 ? (s.len - s.t0 - 1) / C::TT + 1 : 0;
     s.chunks = s.tiles > 0 ? (s.tiles - 1) / C::W + 1 : 1;
@@ -899,7 +900,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     int rows = 0;                // query rows of the unit
     int at_pos[NT][2];           // the positions of the queries of the lane's two columns
     int all_lo = 0, all_hi = 0;  // positions that every query row of the unit sees: [all_lo, all_hi)
-    auto sees = [&](int pos, int t) { return t <= pos && (p.window == 0 || t > pos - p.window); };
+    auto sees = [&](int pos, int t) { return t <= pos && (p.window == 0 || pos - t < p.window); };
     for (int segment = 0;; ++segment) {
         const Walk &at_use = segments[segment & 1];
         int use_tile, use_end, use_t0;
@@ -917,7 +918,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
                 at_pos[nt][1] = position(nt * 8 + 2 * c + 1);
             }
             all_hi = position(0) + 1;
-            all_lo = p.window > 0 ? max(0, position(rows - 1) - p.window + 1) : 0;
+            const int upto = position(rows - 1) + 1;
+            all_lo = p.window > 0 && upto > p.window ? upto - p.window : 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 col[nt][0] = q_stat[(segment & 1) * ROWS + nt * 8 + 2 * c];

@@ -1,5 +1,6 @@
 """Paged attention at the edges of its inputs' ranges: NaN of every bit pattern,
-infinities and values next to FP32's largest."""
+infinities and values next to FP32's largest, windows past every
+length."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,7 @@ import torch
 import gated_delta_rule_gateddeltanet_gb300 as gdn
 from attention_common import Paged, check_attention, f64, rounding
 from gpu_common import dev
-from test_gpu_paged_attention import queries
+from test_gpu_paged_attention import queries, run
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +134,10 @@ def test_fp32_products_with_numbers_next_to_the_largest(pattern, which):
         p.cache.k[at[0], at[1], 0, 9] = small * steps
     out, lse = gdn.paged_attention(q, p.cache, p.table, p.kv_lens, scale=0.25, return_lse=True)
     check_attention(out, lse, q, p, [1], 0.25)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 40, 1 << 20])
+@pytest.mark.parametrize("kind,io", [(F16, F16), (I8, BF16), (F32, F32)])
+def test_windows_past_every_length(window, kind, io):
+    """Spans longer than what is cached, so that queries stand at positions far below zero less the window."""
+    run(Paged([3, 1, 40, 0], 2, 64, 16, kind, seed=5), 4, io, spans=[8, 45, 60, 7], window=window)
