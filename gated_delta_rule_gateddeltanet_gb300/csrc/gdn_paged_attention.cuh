@@ -421,6 +421,9 @@ struct Split {
     int pad[2];  // 32 bytes, so that what follows the records is aligned
 };
 
+// The maximum before any score: as low as a finite number can be, so that any score raises it and 2^(-inf - NONE) is 0.
+constexpr float NONE = -3.402823466e38f;
+
 // What a part's sums count for when its maximum is `part` and that of all parts `all`.
 __device__ __forceinline__ float part_factor(float part, float all) { return exp2_fast(part - all); }
 
@@ -477,7 +480,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_attention_kernel(const __
     constexpr bool Q8 = C::Q8, F32 = C::F32, BF16 = C::BF16;
     constexpr uint32_t FULL = 0xffffffffu;
     const float NEG_INF = __int_as_float(0xff800000);
-    constexpr float NONE = -1e30f;  // the maximum before any score: finite, so that 2^(-inf - NONE) is 0
 
     extern __shared__ __align__(1024) uint8_t smem[];
     long long *scan = reinterpret_cast<long long *>(smem);               // [warps] sums
@@ -1302,7 +1304,6 @@ __global__ void __launch_bounds__(JOIN_GROUPS * C::D / 4) join_kernel(const __gr
     __shared__ float2 stats[JOIN_GROUPS];
     const int groups = blockDim.x / LANES;
     dependent_prologue();
-    constexpr float NONE = -1e30f;
     const Parts<C> parts(p.partials, gridDim.x);
     const int i = blockIdx.x, r = blockIdx.y;
     const Split s = parts.split[i];

@@ -1,6 +1,6 @@
 """Paged attention at the edges of its inputs' ranges: NaN of every bit pattern,
 infinities and values next to FP32's largest, windows past every
-length."""
+length, scores far below zero."""
 import numpy as np
 import pytest
 import torch
@@ -141,3 +141,27 @@ def test_fp32_products_with_numbers_next_to_the_largest(pattern, which):
 def test_windows_past_every_length(window, kind, io):
     """Spans longer than what is cached, so that queries stand at positions far below zero less the window."""
     run(Paged([3, 1, 40, 0], 2, 64, 16, kind, seed=5), 4, io, spans=[8, 45, 60, 7], window=window)
+
+
+@pytest.mark.parametrize("kind,io", [(F32, F32), (BF16, BF16), (I8, BF16), (FP8, BF16)])
+@pytest.mark.parametrize("length", [1, 20, 6000])
+def test_scores_far_below_zero(kind, io, length):
+    """Every score the same large negative number: the mean of the values, and that number as log-sum-exp."""
+    p = Paged([length], 1, 128, 16, kind, seed=3)
+    page = torch.arange(p.cache.k.shape[0], device=dev())
+    p.cache.k.view(torch.uint8)[:] = 0
+    if kind in (I8, FP8):  # one channel of -64 times 2^100
+        p.cache.k[..., 7] = torch.full(p.cache.k.shape[:3], -64.0, device=dev()).to(kind)
+        p.cache.k_scale[p.cache.k_scale == p.cache.k_scale] = 2.0 ** 100
+    else:
+        p.cache.k[..., 7] = -2.0 ** 60
+    q = torch.zeros(1, 4, 128, dtype=io, device=dev())
+    q[..., 7] = 2.0 ** 47 if kind not in (I8, FP8) else 2.0
+    scale = 1.0
+    out, lse = gdn.paged_attention(q, p.cache, p.table, p.kv_lens, scale=scale, return_lse=True)
+    v = p.rows(0)[1]
+    want = v.mean(0)[0]
+    # the weights are equal: 2^-22 and their own rounding each (2^-11 for the 8-bit types, 2^-16 for BF16), and the output's
+    bound = 2 * (2.0 ** -22 + (2.0 ** -11 if kind in (I8, FP8) else 2.0 ** -16)) * np.abs(v).max() + rounding(want, io)
+    assert len(page) and np.all(np.abs(f64(out)[0] - want) <= bound)
+    assert np.all(np.abs(f64(lse) / -2.0 ** 107 - 1) <= 2.0 ** -20)
