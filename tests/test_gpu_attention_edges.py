@@ -1,6 +1,6 @@
 """Paged attention at the edges of its inputs' ranges: NaN of every bit pattern,
 infinities and values next to FP32's largest, windows past every
-length, scores far below zero."""
+length, scores far below zero, pages outside the pool."""
 import numpy as np
 import pytest
 import torch
@@ -165,3 +165,26 @@ def test_scores_far_below_zero(kind, io, length):
     bound = 2 * (2.0 ** -22 + (2.0 ** -11 if kind in (I8, FP8) else 2.0 ** -16)) * np.abs(v).max() + rounding(want, io)
     assert len(page) and np.all(np.abs(f64(out)[0] - want) <= bound)
     assert np.all(np.abs(f64(lse) / -2.0 ** 107 - 1) <= 2.0 ** -20)
+
+
+@pytest.mark.parametrize("kind,page", [(F16, 16), (F16, 7), (BF16, 32), (F32, 16), (F32, 5), (FP8, 16), (FP8, 5), (I8, 16),
+                                       (I8, 7), (I8, 64)])
+@pytest.mark.parametrize("entry", [-1, 10 ** 6, -2 ** 31])
+@pytest.mark.parametrize("spans", [[1, 1], [3, 2]])
+def test_pages_outside_the_pool_are_rows_of_zeros(kind, page, entry, spans):
+    """By value: the same as over a page of the pool that holds zeros."""
+    p = Paged([40, 3 * page + 3], 2, 64, page, kind, seed=14)
+    io = F16 if kind in (FP8, I8) else kind
+    q = queries(sum(spans), 8, 64, io)
+    table = p.table.clone()
+    table[1, 1] = entry
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    out, lse = gdn.paged_attention(q, p.cache, table, p.kv_lens, cu_seqlens=cu_of(spans), status=status, return_lse=True)
+    assert int(status) == gdn.DEVERR["page"]
+    zeros = next(i for i in range(p.cache.k.shape[0]) if i not in p.table.cpu().flatten().tolist())
+    for x, s in ((p.cache.k, p.cache.k_scale), (p.cache.v, p.cache.v_scale)):
+        x.view(torch.uint8)[zeros] = 0
+        if s is not None:
+            s[zeros] = 1
+    p.table[1, 1] = zeros
+    check_attention(out, lse, q, p, spans, 64 ** -0.5)
