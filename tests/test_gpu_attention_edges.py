@@ -1,6 +1,6 @@
 """Paged attention at the edges of its inputs' ranges: NaN of every bit pattern,
 infinities and values next to FP32's largest, windows past every
-length, scores far below zero, pages outside the pool."""
+length, scores far below zero, pages outside the pool, rows of zeros among small 8-bit values."""
 import numpy as np
 import pytest
 import torch
@@ -188,3 +188,21 @@ def test_pages_outside_the_pool_are_rows_of_zeros(kind, page, entry, spans):
             s[zeros] = 1
     p.table[1, 1] = zeros
     check_attention(out, lse, q, p, spans, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("kind", [FP8, I8])
+@pytest.mark.parametrize("d,length,spans", [(64, 64, [1]), (128, 300, [4]), (256, 64, [1]), (128, 6000, [1]), (64, 40, [12])])
+@pytest.mark.parametrize("rows", ["first", "last", "odd", "block", "all"])
+def test_zero_rows_among_small_8_bit_values(kind, d, length, spans, rows):
+    """A value row of zeros has scale 1, however small the scales of the others are: it must not cost them bits."""
+    p = Paged([length], 2, d, 16, kind, seed=d, std=2.0 ** -28)
+    p.cache.k_scale *= 2.0 ** 28
+    t = torch.arange(length, device=dev())
+    pick = {"first": t < 1, "last": t >= length - 1, "odd": t % 2 == 1, "block": (t >= 16) & (t < 40), "all": t >= 0}[rows]
+    t = t[pick]
+    at = (p.table[0].long()[t // 16], t % 16)
+    p.cache.v.view(torch.uint8)[at] = 0
+    p.cache.v_scale[at] = 1
+    if kind == FP8:
+        p.cache.v.view(torch.uint8)[at[0][::2], at[1][::2], :, 5] = 0x80  # minus zero
+    run(p, 4, BF16, spans=spans)
