@@ -109,6 +109,14 @@ class _Call:
         return self.outputs
 
 
+def _int32(x, name):
+    """``x`` as the int32 of a C struct, which would take a larger number modulo 2^32."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 def _io(t, name):
     if t.dtype not in DTYPE:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
@@ -175,7 +183,8 @@ def rotary_table(max_positions, rotary_dim, *, base=10000.0, scaling="none", fac
         table = torch.empty((max_positions, rotary_dim), dtype=torch.float32, device=device)
     _check(table, "table", dtype=torch.float32)
     _shape(table, "table", (max_positions, rotary_dim))
-    a = RotaryTableArgs(int(max_positions), int(rotary_dim), ROPE_SCALING[scaling], int(original_positions),
+    a = RotaryTableArgs(int(max_positions), int(rotary_dim), ROPE_SCALING[scaling],
+                        _int32(original_positions, "original_positions"),
                         float(base), float(factor), float(beta_fast), float(beta_slow), float(attention_factor),
                         _ptr(table))
     call = _Call()
@@ -349,7 +358,7 @@ class KVCacheReadCall(_Call):
         B = _cu_seqlens(cu_seqlens, dev)
         a.pages_per_seq, a.block_table_stride = _block_table(block_table, B, dev)
         _status(status, dev)
-        T = int(total_tokens)
+        T = _int32(total_tokens, "total_tokens")
         outs = []
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is None:
@@ -404,7 +413,8 @@ class PagedAttentionCall(_Call):
         _check(lse, "lse", dtype=torch.float32, device=dev)
         _shape(lse, "lse", (T, Hq), leading_at_least=True)
         a.num_seqs, a.total_tokens, a.num_q_heads = B, T, Hq
-        a.window, a.max_seqlen, a.scale = int(window), int(max_seqlen or 0), float(scale or 0.0)
+        a.window, a.max_seqlen = _int32(window, "window"), _int32(max_seqlen or 0, "max_seqlen")
+        a.scale = float(scale or 0.0)
         a.q_stride = _token_stride(q, "q", Hq * d)
         a.q, a.block_table, a.kv_lens, a.cu_seqlens = _ptr(q), _ptr(block_table), _ptr(kv_lens), _ptr(cu_seqlens)
         a.output, a.lse, a.status = _ptr(output), _ptr(lse), _ptr(status)
@@ -431,7 +441,8 @@ def paged_attention_workspace(cache, num_q_heads, *, dtype=torch.float16, max_se
     a = PagedAttentionArgs()
     a.cache = cache.args
     a.num_seqs = a.total_tokens = 1
-    a.num_q_heads, a.max_seqlen, a.io_dtype = int(num_q_heads), int(max_seqlen), DTYPE[dtype]
+    a.num_q_heads, a.max_seqlen = _int32(num_q_heads, "num_q_heads"), _int32(max_seqlen, "max_seqlen")
+    a.io_dtype = DTYPE[dtype]
     return torch.empty(_workspace_size(a), dtype=torch.uint8, device=cache.device)
 
 

@@ -1,6 +1,6 @@
-"""The binding refuses views whose strides the C ABI would take for something
-else: a stride of 0 (an expanded view) is its word for rows without a gap, which
-would read or write past the view's memory.  CPU tensors: nothing is launched."""
+"""The binding refuses what the C ABI would take for something else: views with
+a stride of 0 (expanded), its word for rows without a gap, which would read or
+write past the view's memory, and numbers past 32 bits.  CPU tensors: nothing is launched."""
 import ctypes
 
 import pytest
@@ -91,3 +91,19 @@ def test_rows_that_share_a_scale_are_not_written(scales):
     own = [torch.ones(6, 2, 16).transpose(1, 2) for _ in range(2)]
     call = gdn.KVCacheWriteCall(z(0, 2, 64), z(0, 2, 64), gdn.PagedKVCache(i8, i8.clone(), *own), ints(0))
     assert fn(ctypes.byref(call.args), None) == 0
+
+
+def test_numbers_past_32_bits_are_refused():
+    """A C struct's int32 would take them modulo 2^32: a window of 2^32 + 1 as 1."""
+    kw = dict(q=z(3, 8, 64), cache=_kv(), block_table=ints(3, 2), kv_lens=ints(3), workspace=torch.zeros(16, dtype=torch.uint8))
+    assert gdn.PagedAttentionCall(window=2 ** 31 - 1, **kw).args.window == 2 ** 31 - 1
+    for name in ("window", "max_seqlen"):
+        for n in (2 ** 31, 2 ** 32 + 1):
+            with pytest.raises(ValueError, match=name):
+                gdn.PagedAttentionCall(**kw, **{name: n})
+    with pytest.raises(ValueError, match="max_seqlen"):
+        gdn.paged_attention_workspace(_kv(), 8, max_seqlen=2 ** 32 + 1)
+    with pytest.raises(ValueError, match="total_tokens"):
+        gdn.KVCacheReadCall(_kv(), ints(1, 2), ints(2), 2 ** 32 + 1, k_out=z(3, 2, 64), v_out=z(3, 2, 64))
+    with pytest.raises(ValueError, match="original_positions"):
+        gdn.rotary_table(4, 32, scaling="yarn", factor=2.0, original_positions=2 ** 32 + 1, device="cpu")
