@@ -101,6 +101,8 @@ class _Call:
     def launch(self, stream=None):
         """Runs the call on ``stream`` (a torch.cuda.Stream; default: the current stream); returns ``outputs``."""
         if self._fn is None:
+            if self._device.type != "cuda":
+                raise ValueError(f"{self._name}: tensors must be on a GPU, got {self._device}")
             self._fn = getattr(load_library(), self._name)
         # (the raw handle of the current stream: building a Stream object takes 2 of a launch's 5 us)
         rc = self._fn(self._ref, torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream)

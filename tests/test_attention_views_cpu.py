@@ -1,7 +1,9 @@
 """The binding refuses what the C ABI would take for something else: views with
 a stride of 0 (expanded), its word for rows without a gap, which would read or
-write past the view's memory, and numbers past 32 bits.  CPU tensors: nothing is launched."""
+write past the view's memory, numbers past 32 bits,
+and the host's memory.  CPU tensors: nothing is launched."""
 import ctypes
+import types
 
 import pytest
 import torch
@@ -107,3 +109,14 @@ def test_numbers_past_32_bits_are_refused():
         gdn.KVCacheReadCall(_kv(), ints(1, 2), ints(2), 2 ** 32 + 1, k_out=z(3, 2, 64), v_out=z(3, 2, 64))
     with pytest.raises(ValueError, match="original_positions"):
         gdn.rotary_table(4, 32, scaling="yarn", factor=2.0, original_positions=2 ** 32 + 1, device="cpu")
+
+
+@pytest.mark.parametrize("stream", [None, types.SimpleNamespace(cuda_stream=0)])
+def test_tensors_of_the_host_are_not_launched_on(stream):
+    calls = [gdn.RotaryCall(z(3, 4, 64), z(3, 2, 64), ints(3), torch.zeros(9, 64)),
+             gdn.KVCacheWriteCall(z(3, 2, 64), z(3, 2, 64), _kv(), ints(3)),
+             gdn.KVCacheReadCall(_kv(), ints(2, 2), ints(3), 10),
+             gdn.PagedAttentionCall(z(3, 8, 64), _kv(), ints(3, 2), ints(3), workspace=torch.zeros(16, dtype=torch.uint8))]
+    for call in calls:
+        with pytest.raises(ValueError, match="GPU"):
+            call.launch(stream)
