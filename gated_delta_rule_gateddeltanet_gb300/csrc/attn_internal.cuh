@@ -21,6 +21,8 @@ struct RotaryTableParams {
     float *table;
 };
 
+constexpr int ROTARY_THREADS = 128;  // of a CTA; a thread rotates at least one pair
+
 struct RotaryParams {
     int T, Hq, Hk, d, rot, P, interleaved;
     float sign;  // -1: the inverse rotation

@@ -158,7 +158,7 @@ gdn_status gdn_rotary(const gdn_rotary_args *a, gdn_stream_t stream) {
     if ((qn && a->q == a->q_out && p.q_stride != p.qo_stride) || (kn && a->k == a->k_out && p.k_stride != p.ko_stride))
         return GDN_ERR_ARG;
     const int64_t pairs = (int64_t)a->total_tokens * ((a->num_q_heads + a->num_k_heads) * (int64_t)a->head_dim / 2);
-    if (pairs / 256 >= INT32_MAX || a->num_q_heads + (int64_t)a->num_k_heads > 65535) return GDN_ERR_SHAPE;
+    if (pairs / gdn::ROTARY_THREADS >= INT32_MAX || a->num_q_heads + (int64_t)a->num_k_heads > 65535) return GDN_ERR_SHAPE;
     p.T = a->total_tokens;
     p.Hq = a->num_q_heads;
     p.Hk = a->num_k_heads;

@@ -18,7 +18,7 @@ namespace {
 
 // (256: 24.8 us instead of 24.4 us for the prompt above, 6.3 us instead of 6.1 us for the gradient; 512: 30.7 and
 // 6.8 us; 64: 24.4 and 6.5 us.  Two heads a thread instead of four 25.3 us, six 26.9 us.)
-constexpr int NT = 128;
+constexpr int NT = ROTARY_THREADS;
 
 // Table: a thread owns pair i and walks ROWS positions; its frequency is
 // evaluated once, in 64 bits like the angles (an FP32 product of position and

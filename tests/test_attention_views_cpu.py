@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import gated_delta_rule_gateddeltanet_gb300 as gdn
+from gated_delta_rule_gateddeltanet_gb300 import attention as at
 from test_attention_abi_cpu import _kv, z
 
 
@@ -120,3 +121,13 @@ def test_tensors_of_the_host_are_not_launched_on(stream):
     for call in calls:
         with pytest.raises(ValueError, match="GPU"):
             call.launch(stream)
+
+
+def test_rotations_of_more_pairs_than_a_grid_holds_are_refused():
+    """CTAs of 128 pairs, at most 2^31 - 1 of them.  (No call reaches a kernel here: there is no memory of that size.)"""
+    from gated_delta_rule_gateddeltanet_gb300 import build
+    build.build()
+    a = at.RotaryArgs()
+    a.total_tokens, a.num_q_heads, a.head_dim, a.rotary_dim, a.max_positions, a.io_dtype = 2 ** 31 - 1, 2, 128, 64, 99, 1
+    a.q = a.q_out = a.positions = a.table = 0x1000
+    assert gdn.load_library().gdn_rotary(ctypes.byref(a), None) == 3  # GDN_ERR_SHAPE
