@@ -326,7 +326,8 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams &p, int b, bool fl
     s.n = cu1 - s.cu0;
     const bool bad_cu = s.cu0 < 0 || s.n < 0 || cu1 > p.T || (b == 0 && s.cu0 != 0);
     const bool bad_len = s.len < 0 || (long long)s.len > (long long)p.pages_per_seq * p.c.page_size;
-    if (flag && bad_cu) flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
+    // (tokens past the last sequence's are an error of the packing, not of that sequence)
+    if (flag && (bad_cu || (b == p.B - 1 && cu1 != p.T))) flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
     if (flag && bad_len) flag_error(p.status, GDN_DEVERR_KV_LEN);
     if (bad_cu || bad_len) s.n = 0;
     const int upto = s.len - s.n + 1;  // (compared, not subtracted: a window may be as large as an int)

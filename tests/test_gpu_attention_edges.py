@@ -1,6 +1,6 @@
 """Paged attention at the edges of its inputs' ranges: NaN of every bit pattern,
 infinities and values next to FP32's largest, windows past every
-length, scores far below zero, pages outside the pool, rows of zeros among small 8-bit values."""
+length, scores far below zero, pages outside the pool, rows of zeros among small 8-bit values, tokens in no sequence."""
 import numpy as np
 import pytest
 import torch
@@ -206,3 +206,16 @@ def test_zero_rows_among_small_8_bit_values(kind, d, length, spans, rows):
     if kind == FP8:
         p.cache.v.view(torch.uint8)[at[0][::2], at[1][::2], :, 5] = 0x80  # minus zero
     run(p, 4, BF16, spans=spans)
+
+
+def test_tokens_past_the_last_sequence_are_flagged():
+    """As by the library's other packed operators; the sequences are computed."""
+    p = Paged([40, 50], 2, 64, 16, F16, seed=13)
+    q = queries(5, 8, 64, F16)
+    good = gdn.paged_attention(q, p.cache, p.table, p.kv_lens, cu_seqlens=cu_of([2, 3]))
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    out = torch.full((7, 8, 64), 7.0, dtype=F16, device=dev())
+    more = torch.cat([q, q[:2]])
+    gdn.paged_attention(more, p.cache, p.table, p.kv_lens, cu_seqlens=cu_of([2, 3]), output=out, status=status)
+    assert int(status) == gdn.DEVERR["cu_seqlens"]
+    assert torch.equal(out[:5], good) and torch.all(out[5:] == 7)
