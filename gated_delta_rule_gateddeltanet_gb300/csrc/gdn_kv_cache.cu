@@ -269,6 +269,11 @@ __global__ void __launch_bounds__(NT) kv_read_kernel(const KvReadParams p) {
     constexpr bool Q8 = CacheDtype == GDN_FP8_E4M3 || CacheDtype == GDN_INT8;
     constexpr int N = Vec16<T>::N;
     constexpr int U = READ_UNROLL;
+    // The look-ups below assume ascending entries; the value CTAs check them, some each.
+    if (blockIdx.y == 1)
+        for (long long b = (long long)blockIdx.x * NT + threadIdx.x; b < p.B; b += (long long)gridDim.x * NT)
+            if (p.cu[b + 1] < p.cu[b] || (b == 0 && p.cu[0] != 0) || (b == p.B - 1 && p.cu[p.B] != p.T))
+                flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
     const int lane = threadIdx.x % 32;
     const long long t0 = ((long long)blockIdx.x * (NT / 32) + threadIdx.x / 32) * (SINGLE ? 1 : p.tok);
     if (t0 >= p.T) return;
