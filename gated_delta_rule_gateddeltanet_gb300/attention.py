@@ -239,7 +239,8 @@ class PagedKVCache:
     with contiguous channels and the same strides (any order of pages, tokens
     and heads in memory), in fp16, bf16, fp32, float8_e4m3fn or int8; the 8-bit
     types come with ``k_scale`` and ``v_scale`` [pages, page_size, heads] fp32
-    (one scale a row, any strides, the same for both)."""
+    (one scale a row, any strides, the same for both; a cache whose rows share
+    scales, a stride of 0, can be read but not written)."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4:

@@ -11,8 +11,10 @@
 // d * sizeof(T) / 32 lanes, each holding two 16-byte groups with whole channel
 // pairs.  The rotation needs no exchange and the largest magnitude is a few
 // shuffles inside the group; the quantised row leaves as one contiguous run.
-// 8 x 512 BF16 tokens of 8 + 8 heads of 128: 8.3 us to e4m3, 9.4 us to int8
-// (their traffic: 3.9 us), bound by instructions (conversion and rotation).
+// 8 x 512 BF16 tokens of 8 + 8 heads of 128: 7.4 us as they are (traffic: 5.3 us), 8.2
+// us to e4m3, 9.3 us to int8 (4.1 us).  No one resource is full: over the int8 write's 2.7
+// waves of CTAs the issue slots are 68% busy while the SMs are active (a launch's start and
+// end are a quarter of the time), its ALU 51%, and warps wait for the row, then the table.
 //
 // Read back: a warp looks up its tokens' rows, a lane each, and then moves them
 // in pieces of 16 output bytes, READ_UNROLL in flight a lane (with 2 45.5 us

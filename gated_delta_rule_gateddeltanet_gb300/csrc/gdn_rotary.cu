@@ -22,7 +22,8 @@ constexpr int NT = ROTARY_THREADS;
 
 // Table: a thread owns pair i and walks ROWS positions; its frequency is
 // evaluated once, in 64 bits like the angles (an FP32 product of position and
-// frequency would be off by 0.03 rad at position 10^6).
+// frequency would be off by 0.03 rad at position 10^6).  Bound by the sine and cosine
+// in 64 bits: 262,144 positions x 64 take 572 us (writing them: 10 us), once a program.
 constexpr int TABLE_ROWS = 16;
 
 __global__ void __launch_bounds__(NT) table_kernel(const RotaryTableParams p) {

@@ -464,8 +464,9 @@ gdn_status causal_conv_replay_prefix(void *conv_states, int32_t num_slots, int32
  * (kept as they are or quantised to 8 bits as they are written) and attention
  * of new tokens over that cache.  Argument and data errors, streams and
  * launches follow the rules at the top of this file; unlike the operators
- * above, these accept FP32, FP16 and BF16.  Arithmetic is FP32 throughout and
- * each result is rounded once, when it is stored.
+ * above, these accept FP32, FP16 and BF16.  Rotations and cache entries are
+ * computed in FP32 and rounded once, when they are stored; the attention's
+ * arithmetic is described with it.
  * ------------------------------------------------------------------------ */
 
 /* How the angles of a rotary table are scaled for contexts longer than the
@@ -570,8 +571,9 @@ gdn_status gdn_rotary(const gdn_rotary_args *args, gdn_stream_t stream);
  *   GDN_INT8      scale = max|x| / 127; q = x / scale rounded to nearest even
  * A row of zeros has scale 1; a row with an infinity or NaN has scale NaN, so
  * that it reads back as NaN.
- * Rows written by others follow the same rules: a zero scale is fine for zeros,
- * and an e4m3 NaN goes with a NaN scale.
+ * Rows written by others follow the same rules: a zero scale is fine for zeros
+ * (another scale than 0 or 1 counts as that of values of its size, beside which
+ * much smaller values lose bits in the attention), and an e4m3 NaN goes with a NaN scale.
  */
 typedef struct gdn_kv_cache {
     int32_t num_pages;    /* num_pages * page_size < 2^31 */
@@ -658,10 +660,27 @@ gdn_status gdn_kv_cache_read(const gdn_kv_read_args *args, gdn_stream_t stream);
  *   output       device [T, num_q_heads, head_dim] io_dtype, contiguous
  *   lse          device [T, num_q_heads] FP32 or NULL: ln sum_t exp(scale q k_t)
  * What the cache holds in slots that a query may not see (uninitialised memory,
- * infinities, NaN, also of later drafted tokens) does not reach its results; an
- * infinity or NaN that it does see makes the channels it is in infinite or NaN.
- * io_dtype is the cache's type, or FP16 or
- * BF16 over an 8-bit cache.
+ * infinities, NaN, also of later drafted tokens) does not reach its results.  An
+ * infinity or NaN that it does see makes the channels it is in, of a value,
+ * infinite or NaN, and the whole row NaN, of a key or of the query itself; a
+ * score of -inf (from an infinite key or query of 16 bits) has weight 0.
+ * io_dtype is the cache's type, or FP16 or BF16 over an 8-bit cache.
+ * Arithmetic.  Scores, their maxima, the sums and the outputs are FP32; what
+ * the tensor cores multiply has fewer bits where said:
+ *   scores    16-bit queries and keys are exact.  FP32 ones are two TF32 parts
+ *             without the product of the lower parts (21 bits).  8-bit keys are
+ *             exact, their scale multiplies the score; BF16 queries over them
+ *             become FP16, the row scaled by a power of two to a largest magnitude
+ *             of 1 to 2 (channels below 2^-17 of it lose bits).
+ *   weights   softmax numerators (base 2, relative error 2^-22 or less) are
+ *             multiplied with the values as two BF16 parts over BF16 (16 bits), two
+ *             TF32 parts over FP32 (21), two FP16 parts over FP16 (22) and one FP16
+ *             number over 8-bit values (11).  The FP16 ones have an absolute floor:
+ *             an error of up to 2^-31 of the row's largest weight (8 bits: of its
+ *             largest weight times scale).  Their sum, the denominator, is of the
+ *             FP32 numbers.
+ * An output's error is thus at most 2 max|v| times the sum of the weights' and the
+ * scores' errors, and its own rounding.
  * The work is split over sequences, heads and cache length by the lengths on
  * the device, so a captured graph stays balanced as they change; pieces of one
  * sequence are joined in a fixed order (the same call gives the same bits).

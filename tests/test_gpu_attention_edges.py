@@ -1,6 +1,7 @@
 """Paged attention at the edges of its inputs' ranges: NaN of every bit pattern,
 infinities and values next to FP32's largest, windows past every
-length, scores far below zero, pages outside the pool, rows of zeros among small 8-bit values, tokens in no sequence."""
+length, scores far below zero, pages outside the pool, rows of zeros among small 8-bit values, tokens in no sequence, weights far below
+the largest."""
 import numpy as np
 import pytest
 import torch
@@ -219,3 +220,31 @@ def test_tokens_past_the_last_sequence_are_flagged():
     gdn.paged_attention(more, p.cache, p.table, p.kv_lens, cu_seqlens=cu_of([2, 3]), output=out, status=status)
     assert int(status) == gdn.DEVERR["cu_seqlens"]
     assert torch.equal(out[:5], good) and torch.all(out[5:] == 7)
+
+
+@pytest.mark.parametrize("kind,io", [(F16, F16), (BF16, BF16), (F32, F32), (I8, F16), (FP8, BF16)])
+@pytest.mark.parametrize("above", [10.0, 15.0, 17.0, 20.0, 24.0])
+def test_one_score_far_above_many_equal_ones(kind, io, above):
+    """A first token whose value is zero takes nearly all of the weight of 100,000 others, whose values are one: what
+    is left for them is their weights' sum, with the error that each may have (relative, and 2^-31 of the largest
+    weight as an FP16 number)."""
+    n = 100000
+    p = Paged([n], 1, 64, 64, kind, seed=1)
+    p.cache.k.view(torch.uint8)[:] = 0
+    p.cache.v.copy_(torch.ones(p.cache.v.shape, device=dev()).to(kind))
+    if p.cache.k_scale is not None:
+        p.cache.k_scale.fill_(0.5), p.cache.v_scale.fill_(1.0)
+    at = slot(p, 0, 0)
+    p.cache.v.view(torch.uint8)[at] = 0
+    p.cache.k[at[0], at[1], 0, 3] = torch.tensor(16.0, device=dev()).to(kind)
+    q = torch.zeros(1, 4, 64, dtype=io, device=dev())
+    q[..., 3] = above / 8 if p.cache.k_scale is not None else above / 16
+    out, lse = gdn.paged_attention(q, p.cache, p.table, p.kv_lens, scale=1.0, return_lse=True)
+    share = (n - 1) * np.exp(-above)
+    want = share / (1 + share)
+    relative = {F16: 2.0 ** -21, BF16: 2.0 ** -16, F32: 2.0 ** -20, I8: 2.0 ** -11, FP8: 2.0 ** -11}[kind]
+    floor = 0.0 if kind in (BF16, F32) else (n - 1) * 2.0 ** -31
+    # 2^-20: 2^-22 of each numerator and of their FP32 sum's parts, in the numerator and the denominator
+    bound = want * (relative + 2.0 ** -20) + floor + rounding(want, io)
+    assert np.all(np.abs(f64(out) - want) <= bound)
+    assert np.all(np.abs(f64(lse) - (above + np.log1p(share))) <= 2.0 ** -18)
