@@ -47,6 +47,7 @@ class AttentionStep:
         self.block_table, self.kv_lens = idx(seqs, pages_per_seq), idx(seqs)
         self.positions, self.slots = idx(T), idx(T) - 1
         self.status = idx(1)
+        self._offsets = torch.arange(-tokens, 0, device=dev)  # of the new tokens' positions from the lengths
         cu = torch.arange(0, T + 1, tokens, dtype=torch.int32, device=dev) if tokens > 1 else None
         self._write = KVCacheWriteCall(self.k, self.v, cache, self.slots, positions=self.positions, table=table,
                                        interleaved=interleaved, q=self.q, status=self.status)
@@ -61,14 +62,16 @@ class AttentionStep:
         before a sequence's first position (an idle row: ``kv_lens`` 0, or fewer than the new tokens) is not stored: slot -1.
         One past the table's last page, or in a page that the pool does not have, gets a slot outside the pool, so that
         it is flagged and not written."""
-        at = self.kv_lens[:, None] - self.tokens + torch.arange(self.tokens, dtype=torch.int32, device=self.kv_lens.device)
-        index, pages = at // self.page, self.block_table.shape[1]
-        page = self.block_table.gather(1, index.clamp(0, pages - 1).long())
-        pool = self.cache.args.num_pages
-        inside = (index < pages) & (page >= 0) & (page < pool)
-        slot = torch.where(inside, page.clamp(0, pool - 1) * self.page + at % self.page, pool * self.page)
-        self.positions.copy_(at.clamp(min=0).flatten())
-        self.slots.copy_(torch.where(at < 0, -1, slot).flatten())
+        capacity, pool = self.block_table.shape[1] * self.page, self.cache.args.num_pages * self.page
+        at = self.kv_lens[:, None] + self._offsets  # (64 bits, for the sums below)
+        self.positions.view_as(at).copy_(at.clamp(min=0))
+        inside = at.clamp(0, capacity - 1)
+        page = self.block_table.gather(1, inside // self.page)
+        slot = (inside % self.page).add_(page, alpha=self.page)
+        slot.masked_fill_(slot < 0, pool).clamp_(max=pool)
+        # at - inside is 0 for a token inside the table, negative before it and positive past it
+        slot.add_(at.sub_(inside), alpha=1 << 31)
+        self.slots.view_as(slot).copy_(slot.clamp_(-1, pool))
 
     def launch(self, stream=None):
         """The step's two calls on ``stream`` (default: the current one)."""

@@ -57,6 +57,12 @@ def test_entries_outside_the_pool_give_a_slot_outside_it(entry):
         assert step_of([length, 16], [[entry, 5], [1, 2]]) == ([[length - 1], [15]], [[PAGES * PAGE], [31]])
 
 
+@pytest.mark.parametrize("entry", [-1, PAGES, 2 ** 31 - 1, -2 ** 31])
+def test_idle_rows_may_have_any_entries(entry):
+    assert step_of([0, 16], [[entry, entry], [1, 2]]) == ([[0], [15]], [[-1], [31]])
+    assert step_of([2, 0], [[1, 2], [entry] * 2], tokens=3)[1] == [[-1, 16, 17], [-1, -1, -1]]
+
+
 def test_a_step_needs_a_page_a_sequence():
     cache = gdn.PagedKVCache.allocate(PAGES, PAGE, 2, 64, device="cpu")
     with pytest.raises(ValueError, match="pages_per_seq"):
