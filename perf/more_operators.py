@@ -275,8 +275,7 @@ def _plain_recurrence_training(st):
     before[first] = st["initial_state"][slots]
     carry = torch.cat([g[1:], g[:1]])
     carry[last] = 0
-    arrives = st["dy"].float()
-    arrives[last] += st["dfinal"][slots]
+    arrives = st["dy"].float().index_add(0, last, st["dfinal"][slots])
     l = _scan(carry.flip(0), arrives.flip(0), st["longest"]).flip(0)  # noqa: E741
     x = st["x"].float()
     dw = l * x
