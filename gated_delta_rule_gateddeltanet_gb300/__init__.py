@@ -12,7 +12,8 @@ Entry points (same names as the C ABI):
     gdn_replay_prefix(...)  -> state_banks (updated in place)
 
 The softmax-attention operators (rotary positions, paged key-value cache,
-attention over it) are in ``attention.py`` and exported from here.
+attention over it) are in ``attention.py``, the gated linear recurrence in
+``recurrence.py`` and the root-mean-square norm in ``norm.py``, exported from here.
 """
 from __future__ import annotations
 
@@ -27,7 +28,8 @@ __all__ = ["gdn_forward", "ForwardCall", "gdn_forward_dense", "state_transpose",
            "causal_conv_replay_prefix", "GdnError", "load_library", "capsule_width",
            "STATUS", "DEVERR", "PLAN", "rotary_table", "rotary", "RotaryCall", "PagedKVCache", "kv_cache_write",
            "KVCacheWriteCall", "kv_cache_read", "KVCacheReadCall", "paged_attention", "PagedAttentionCall",
-           "paged_attention_workspace"]
+           "paged_attention_workspace", "linear_recurrence", "LinearRecurrenceCall", "linear_recurrence_backward",
+           "LinearRecurrenceBackwardCall", "rms_norm", "RMSNormCall", "rms_norm_backward", "RMSNormBackwardCall"]
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_DTYPE", 3: "GDN_ERR_SHAPE", 4: "GDN_ERR_ALIGN",
           5: "GDN_ERR_WORKSPACE", 6: "GDN_ERR_CUDA", 7: "GDN_ERR_UNSUPPORTED", 8: "GDN_ERR_ARG"}
@@ -109,7 +111,8 @@ def load_library(path: str | None = None):
     lib.gdn_state_transpose.argtypes = [P, P, ctypes.c_int64, i32, i32, P]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_status_string.argtypes = [i32]
-    attention.declare(lib)
+    for module in (attention, recurrence, norm):
+        module.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -524,7 +527,10 @@ def causal_conv_replay_prefix(conv_states, src_slots, dst_slots, state_update, a
     return conv_states
 
 
-from . import attention  # noqa: E402  (it uses this module's checks)
+from . import attention, norm, recurrence  # noqa: E402  (they use this module's checks)
 from .attention import (KVCacheReadCall, KVCacheWriteCall, PagedAttentionCall, PagedKVCache, RotaryCall,  # noqa: E402
                         kv_cache_read, kv_cache_write, paged_attention, paged_attention_workspace, rotary,
                         rotary_table)
+from .norm import RMSNormBackwardCall, RMSNormCall, rms_norm, rms_norm_backward  # noqa: E402
+from .recurrence import (LinearRecurrenceBackwardCall, LinearRecurrenceCall, linear_recurrence,  # noqa: E402
+                         linear_recurrence_backward)

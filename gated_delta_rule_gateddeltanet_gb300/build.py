@@ -27,7 +27,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libgdn_debug.so")
-DEBUG_SOURCES = ("gdn_api.cu", "gdn_debug.cu")  # the units whose code GDN_DEBUG_CHECKS changes
+DEBUG_SOURCES = ("gdn_api.cu", "gdn_layer_api.cu", "gdn_debug.cu")  # the units whose code GDN_DEBUG_CHECKS changes
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

@@ -712,6 +712,188 @@ gdn_status gdn_paged_attention_workspace_size(const gdn_paged_attention_args *ar
 
 gdn_status gdn_paged_attention(const gdn_paged_attention_args *args, gdn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Layers with a diagonal state, and the norms around recurrent and attention layers.
+ *
+ * The gated linear recurrence is the gated delta rule's sibling with one number
+ * of state a channel: the same packed batches, state slots and gate arithmetic,
+ * with a backward pass.  The root-mean-square norm is what stands before such
+ * layers' projections (with the residual's addition), on their outputs (with a
+ * gate, a head at a time) and on queries and keys before gdn_rotary; it can
+ * leave rows in 8 bits with scales for an 8-bit product.  FP32, FP16 and BF16;
+ * sums, statistics and states are FP32, and every stored value is rounded once.
+ * ------------------------------------------------------------------------ */
+
+/* Tokens between the states that gdn_linear_recurrence leaves for its backward pass. */
+#define GDN_RECURRENCE_CHECKPOINT 64
+
+/*
+ * Arguments of gdn_linear_recurrence.  Per channel c, over the tokens t of each
+ * sequence in order, with h the sequence's FP32 state:
+ *   h_t = g_t h_(t-1) + w_t x_t,   y_t = h_t
+ *   GDN_GATES_RAW          g = exp(-exp(A_log) softplus(a + dt_bias)), w = sigmoid(b) (1 if b is NULL);
+ *                          with unit_input, w is that times sqrt(1 - g^2), which keeps
+ *                          the state's variance at the input's
+ *   GDN_GATES_PRECOMPUTED  g = a, w = b (1 if b is NULL); any finite values
+ *   x             device [T, C] io_dtype; token stride x_stride elements (0 = C)
+ *   a, b          device [T, C], strides a_stride, b_stride (0 = C): io_dtype if RAW, FP32
+ *                 if PRECOMPUTED (16 bits cannot hold a decay next to 1)
+ *   A_log, dt_bias device [C] FP32 (RAW only)
+ *   cu_seqlens    device [B+1] int32, or NULL: B sequences of T / B tokens each
+ *   state_slots   device [B] int32, or NULL for slot b = b
+ *   initial_state device [num_state_slots, C] FP32, or NULL for zeros
+ *   final_state   device, same shape, or NULL (not written); may equal initial_state.  Only
+ *                 the batch's slots are written; that of a sequence without tokens gets its initial state.
+ *   output        device [T, C] io_dtype, contiguous
+ *   checkpoints   device [ceil(T / GDN_RECURRENCE_CHECKPOINT), C] FP32 or NULL: the state
+ *                 before every GDN_RECURRENCE_CHECKPOINT-th packed token (0 where that token begins
+ *                 a sequence or belongs to none), for gdn_linear_recurrence_backward
+ * Sequences in one call must use distinct state slots (checked by the debug
+ * build).  A sequence whose slot is out of range is skipped; tokens past cu[B]
+ * are flagged and left as they were; of a cu_seqlens that is out of order, which is
+ * flagged, any sequences may be skipped or computed.
+ * Long sequences are split over time: a call gives the same bits every time, and
+ * those of another batching or max_seqlen up to FP32 rounding.
+ *   workspace     device scratch of gdn_linear_recurrence_workspace_size bytes, 16-byte aligned;
+ *                 its contents need not be kept or set.  Not shared by calls that overlap.
+ */
+typedef struct gdn_linear_recurrence_args {
+    int32_t num_seqs;        /* B, at most 65535 */
+    int32_t total_tokens;    /* T */
+    int32_t channels;        /* C >= 1 */
+    int32_t num_state_slots;
+    int32_t io_dtype;        /* GDN_F32, GDN_F16 or GDN_BF16 */
+    int32_t gate_mode;       /* GDN_GATES_* */
+    int32_t unit_input;      /* 0 or 1 (RAW only) */
+    int32_t max_seqlen;      /* upper bound on the longest sequence, 0 = unknown; a hint: up to 16
+                                a thread carries its channels through a sequence's tokens */
+    int64_t x_stride, a_stride, b_stride;
+    const void *x, *a, *b;
+    const float *A_log, *dt_bias;
+    const int32_t *cu_seqlens, *state_slots;
+    const float *initial_state;
+    float *final_state;
+    void *output;
+    float *checkpoints;
+    int32_t *status;
+    void *workspace;
+    size_t workspace_bytes;
+} gdn_linear_recurrence_args;
+
+/* Bytes of workspace for these sizes (pointers are not read). */
+gdn_status gdn_linear_recurrence_workspace_size(const gdn_linear_recurrence_args *args, size_t *bytes);
+
+gdn_status gdn_linear_recurrence(const gdn_linear_recurrence_args *args, gdn_stream_t stream);
+
+/*
+ * Arguments of gdn_linear_recurrence_backward: the gradients of a loss with
+ * respect to the forward call's inputs, from those of its outputs.  With
+ * l_t = dy_t + g_(t+1) l_(t+1) (d_final_state is added at a sequence's last token):
+ *   dx = w l,  dg = l h_(t-1),  dw = l x,  d_initial_state = g_0 l_0,
+ * and a, b, A_log, dt_bias through the gates' formulas.
+ *   x, a, b, A_log, dt_bias, cu_seqlens, state_slots, initial_state  as in the forward call, and
+ *                 unchanged since (a forward call in place has overwritten its initial states)
+ *   checkpoints   as the forward call wrote them
+ *   dy            device [T, C] io_dtype, token stride dy_stride elements (0 = C)
+ *   d_final_state device [num_state_slots, C] FP32, or NULL for zeros
+ *   dx            device [T, C] io_dtype;  da, db  device [T, C] in a's and b's type (db goes
+ *                 with b); all contiguous
+ *   dA_log, ddt_bias device [C] FP32 or NULL (RAW only): summed over all tokens
+ *   d_initial_state device [num_state_slots, C] FP32 or NULL; only the batch's slots are
+ *                 written; may equal d_final_state
+ * Outputs must not overlap inputs otherwise.  Where unit_input meets a decay that rounds to 1
+ * (its factor is 0), that factor's part of da is 0, its limit.
+ */
+typedef struct gdn_linear_recurrence_backward_args {
+    int32_t num_seqs, total_tokens, channels, num_state_slots;
+    int32_t io_dtype, gate_mode, unit_input;
+    int64_t x_stride, a_stride, b_stride, dy_stride;
+    const void *x, *a, *b, *dy;
+    const float *A_log, *dt_bias;
+    const int32_t *cu_seqlens, *state_slots;
+    const float *initial_state, *checkpoints, *d_final_state;
+    void *dx, *da, *db;
+    float *dA_log, *ddt_bias, *d_initial_state;
+    int32_t *status;
+    void *workspace;
+    size_t workspace_bytes;
+} gdn_linear_recurrence_backward_args;
+
+gdn_status gdn_linear_recurrence_backward_workspace_size(const gdn_linear_recurrence_backward_args *args,
+                                                         size_t *bytes);
+
+gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_args *args, gdn_stream_t stream);
+
+/*
+ * Arguments of gdn_rms_norm.  Every head of every token is a row of head_dim
+ * channels that is normalised by itself (num_heads = 1: the whole token):
+ *   s = x (+ residual, rounded to io_dtype as it is stored)
+ *   y = s / sqrt(mean(s^2) + eps) * (weight + weight_offset) * silu(gate)
+ * without the factors whose pointer is NULL.
+ *   x, residual, gate  device [T, num_heads, head_dim] io_dtype, heads and channels contiguous
+ *                 inside a token; x_stride, residual_stride, gate_stride elements between tokens
+ *                 (0 = num_heads * head_dim)
+ *   weight        device [head_dim] FP32 or NULL
+ *   residual_out  device [T, num_heads, head_dim] io_dtype, contiguous: s; with residual only.
+ *                 May equal x or residual (then without gaps).
+ *   output        device [T, num_heads, head_dim], contiguous, out_dtype; of io_dtype it may
+ *                 equal x (without gaps; not with a residual_out that is x) or gate
+ *   scale         device FP32 (8-bit outputs only): [T], one for all channels of a token, for
+ *                 scale_group = 0; else [T, num_heads * head_dim / scale_group], one for every
+ *                 scale_group channels.  scale = max|y| / 448 (e4m3) or / 127 (int8) of its
+ *                 channels, 1 if they are all 0, NaN if one is infinite or NaN;
+ *                 output = y / scale rounded to nearest even (the quotient up to FP32 rounding).
+ * Other overlaps of outputs with inputs or with each other are not allowed.
+ */
+typedef struct gdn_rms_norm_args {
+    int32_t total_tokens; /* T */
+    int32_t num_heads;    /* >= 1 */
+    int32_t head_dim;     /* >= 1 */
+    int32_t io_dtype;     /* GDN_F32, GDN_F16 or GDN_BF16 */
+    int32_t out_dtype;    /* io_dtype, GDN_FP8_E4M3 or GDN_INT8 */
+    int32_t scale_group;  /* 0, or 32, 64 or 128 that divides head_dim */
+    float eps;            /* > 0 */
+    float weight_offset;  /* 1 for weights kept as differences from 1 */
+    int64_t x_stride, residual_stride, gate_stride;
+    const void *x, *residual, *gate;
+    const float *weight;
+    void *residual_out, *output;
+    float *scale;
+} gdn_rms_norm_args;
+
+gdn_status gdn_rms_norm(const gdn_rms_norm_args *args, gdn_stream_t stream);
+
+/*
+ * Arguments of gdn_rms_norm_backward (of calls whose output is not in 8 bits).
+ * With n = s / sqrt(mean(s^2) + eps), w = weight + weight_offset, e = dy w silu(gate):
+ *   dx = (e - n mean(e n)) / sqrt(mean(s^2) + eps) + d_residual
+ *   dweight = sum over rows of dy n silu(gate),  dgate = dy n w silu'(gate)
+ * dx is the gradient of x and of residual alike.
+ *   x             what was normalised: the forward call's x, or its residual_out
+ *   dy, gate, d_residual  [T, num_heads, head_dim] io_dtype with token strides; d_residual is the
+ *                 gradient that reaches residual_out from elsewhere, or NULL
+ *   dx, dgate     [T, num_heads, head_dim] io_dtype, contiguous; dgate goes with gate
+ *   dweight       [head_dim] FP32 or NULL; needs weight
+ *   workspace     device scratch of gdn_rms_norm_backward_workspace_size bytes, 16-byte aligned;
+ *                 its contents need not be kept or set.  Not shared by calls that overlap.
+ * Outputs must not overlap inputs.  The same call gives the same bits every time.
+ */
+typedef struct gdn_rms_norm_backward_args {
+    int32_t total_tokens, num_heads, head_dim, io_dtype;
+    float eps, weight_offset;
+    int64_t x_stride, dy_stride, gate_stride, d_residual_stride;
+    const void *x, *dy, *gate, *d_residual;
+    const float *weight;
+    void *dx, *dgate;
+    float *dweight;
+    void *workspace;
+    size_t workspace_bytes;
+} gdn_rms_norm_backward_args;
+
+gdn_status gdn_rms_norm_backward_workspace_size(const gdn_rms_norm_backward_args *args, size_t *bytes);
+
+gdn_status gdn_rms_norm_backward(const gdn_rms_norm_backward_args *args, gdn_stream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char *gdn_status_string(gdn_status status);
 
