@@ -24,7 +24,9 @@ gdn_status check_recurrence_sizes(const Args *a) {
     if (!valid_io(a->io_dtype)) return GDN_ERR_DTYPE;
     if (a->gate_mode != GDN_GATES_RAW && a->gate_mode != GDN_GATES_PRECOMPUTED) return GDN_ERR_ARG;
     if ((a->unit_input != 0 && a->unit_input != 1) || (a->unit_input && a->gate_mode != GDN_GATES_RAW)) return GDN_ERR_ARG;
-    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->total_tokens < 0 || a->channels < 1) return GDN_ERR_SHAPE;
+    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->total_tokens < 0 || a->channels < 1 || a->channels > (1 << 30)) return GDN_ERR_SHAPE;
+    // tiles of 64 tokens and 64 channels are counted in 32 bits
+    if (((int64_t)a->total_tokens + 63) / 64 * (((int64_t)a->channels + 63) / 64) > (1 << 30)) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
 
@@ -82,7 +84,7 @@ int longest(const gdn_linear_recurrence_args *a) {
 }
 
 size_t forward_bytes(const gdn_linear_recurrence_args *a) {
-    return gdn::recurrence_workspace_bytes(a->num_seqs, a->total_tokens, a->channels, longest(a));
+    return gdn::recurrence_workspace_bytes(a->total_tokens, a->channels, longest(a));
 }
 
 gdn_status check_norm_sizes(int T, int H, int d, int io, float eps, float offset) {

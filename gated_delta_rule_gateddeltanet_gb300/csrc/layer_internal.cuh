@@ -2,6 +2,8 @@
 // norm; not part of the C ABI.
 #pragma once
 
+#include <algorithm>
+
 #include "attn_internal.cuh"
 
 namespace gdn {
@@ -31,7 +33,7 @@ struct RecurrenceParams {
     void *workspace;
 };
 
-size_t recurrence_workspace_bytes(int B, int T, int C, int longest);
+size_t recurrence_workspace_bytes(int T, int C, int longest);
 size_t recurrence_backward_workspace_bytes(int B, int T, int C);
 // longest: an upper bound on the longest sequence (a hint)
 cudaError_t launch_recurrence(const RecurrenceParams &p, int io_dtype, int mode, int longest, cudaStream_t stream);

@@ -746,8 +746,8 @@ gdn_status gdn_paged_attention(const gdn_paged_attention_args *args, gdn_stream_
  *                 the batch's slots are written; that of a sequence without tokens gets its initial state.
  *   output        device [T, C] io_dtype, contiguous
  *   checkpoints   device [ceil(T / GDN_RECURRENCE_CHECKPOINT), C] FP32 or NULL: the state
- *                 before every GDN_RECURRENCE_CHECKPOINT-th packed token (0 where that token begins
- *                 a sequence or belongs to none), for gdn_linear_recurrence_backward
+ *                 before every GDN_RECURRENCE_CHECKPOINT-th packed token (unspecified where that token
+ *                 begins a sequence or belongs to none), for gdn_linear_recurrence_backward
  * Sequences in one call must use distinct state slots (checked by the debug
  * build).  A sequence whose slot is out of range is skipped; tokens past cu[B]
  * are flagged and left as they were; of a cu_seqlens that is out of order, which is
