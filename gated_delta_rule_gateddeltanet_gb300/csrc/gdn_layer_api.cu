@@ -24,9 +24,7 @@ gdn_status check_recurrence_sizes(const Args *a) {
     if (!valid_io(a->io_dtype)) return GDN_ERR_DTYPE;
     if (a->gate_mode != GDN_GATES_RAW && a->gate_mode != GDN_GATES_PRECOMPUTED) return GDN_ERR_ARG;
     if ((a->unit_input != 0 && a->unit_input != 1) || (a->unit_input && a->gate_mode != GDN_GATES_RAW)) return GDN_ERR_ARG;
-    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->total_tokens < 0 || a->channels < 1 || a->channels > (1 << 30)) return GDN_ERR_SHAPE;
-    // tiles of 64 tokens and 64 channels are counted in 32 bits
-    if (((int64_t)a->total_tokens + 63) / 64 * (((int64_t)a->channels + 63) / 64) > (1 << 30)) return GDN_ERR_SHAPE;
+    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->total_tokens < 0 || a->channels < 1 || a->channels > (1 << 24)) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
 
@@ -83,10 +81,6 @@ int longest(const gdn_linear_recurrence_args *a) {
     return n;
 }
 
-size_t forward_bytes(const gdn_linear_recurrence_args *a) {
-    return gdn::recurrence_workspace_bytes(a->total_tokens, a->channels, longest(a));
-}
-
 gdn_status check_norm_sizes(int T, int H, int d, int io, float eps, float offset) {
     if (!valid_io(io)) return GDN_ERR_DTYPE;
     if (T < 0 || H < 1 || d < 1 || (int64_t)H * d > INT32_MAX) return GDN_ERR_SHAPE;
@@ -98,14 +92,6 @@ gdn_status check_norm_sizes(int T, int H, int d, int io, float eps, float offset
 
 extern "C" {
 
-gdn_status gdn_linear_recurrence_workspace_size(const gdn_linear_recurrence_args *a, size_t *bytes) {
-    if (!bytes) return GDN_ERR_NULL;
-    const gdn_status st = check_forward_sizes(a);
-    if (st != GDN_OK) return st;
-    *bytes = forward_bytes(a);
-    return GDN_OK;
-}
-
 gdn_status gdn_linear_recurrence(const gdn_linear_recurrence_args *a, gdn_stream_t stream) {
     gdn_status st = check_forward_sizes(a);
     if (st != GDN_OK) return st;
@@ -116,11 +102,9 @@ gdn_status gdn_linear_recurrence(const gdn_linear_recurrence_args *a, gdn_stream
     if (a->total_tokens > 0 && !a->output) return GDN_ERR_NULL;
     if (!aligned(a->output, io_bytes(a->io_dtype)) || !aligned(a->final_state, 4) || !aligned(a->checkpoints, 4))
         return GDN_ERR_ALIGN;
-    if ((st = check_workspace(a->workspace, a->workspace_bytes, forward_bytes(a))) != GDN_OK) return st;
     p.y = a->output;
     p.final_state = a->final_state;
     p.checkpoints = a->checkpoints;
-    p.workspace = a->workspace;
     cudaStream_t s = cuda_stream(stream);
 #ifdef GDN_DEBUG_CHECKS
     if (p.final_state && gdn::debug_check_distinct_slots(p.slots, nullptr, p.B, p.num_slots, p.status, s) != cudaSuccess)

@@ -2,232 +2,198 @@
 #include "recurrence_tiles.cuh"
 
 namespace gdn {
-namespace recur {
-
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const RecurrenceParams p, const Work k) {
-    dependent_prologue();
-    const int i = blockIdx.x * PLAN_THREADS + threadIdx.x;
-    if (i == 0) {
-        *k.counter = 0;
-        if (p.cu && (p.cu[0] != 0 || p.cu[p.B] != p.T)) flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
-    }
-    if (i < k.tiles) k.flags[i] = NOT_YET;
-    if (!p.cu) return;
-    if (i <= k.time_tiles) k.first[i] = last_start(p.cu, 0, p.B - 1, min(i * (long long)TILE, (long long)p.T - 1));
-    if (i < p.B && p.cu[i] > p.cu[i + 1]) flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
-}
-
-}  // namespace recur
-
 namespace {
 
 using namespace recur;
 
 // ---------------------------------------------------------------- long sequences
 
-constexpr int TT = 8, W = TILE / TT, NT = 32 * W;
+constexpr int TT = 8, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA
 
-enum { VEC_X = 1, VEC_A = 2, VEC_B = 4, VEC_Y = 8, VEC_STATE = 16 };
+// What the host found to be aligned.
+struct Access {
+    int x, a, b;   // bytes of a copy
+    bool y, state;  // VC elements at once
+};
 
 template <typename T, int MODE>
 struct Shape {
     using G = typename GateType<T, MODE>::type;
-    static constexpr int VC = sizeof(G) == 4 ? 2 : 4, SLAB = 32 * VC;
+    static constexpr int VC = sizeof(G) == 4 ? 2 : 4, SLAB = LANES * VC;
     struct Shared {
-        T x[TILE * SLAB];
-        G a[TILE * SLAB], b[TILE * SLAB];
-        float A_log[SLAB], dt_bias[SLAB];
-        float A[W][SLAB], B[W][SLAB];  // the warps' maps, then those of what stands in front of each in the tile
+        alignas(16) T x[TILE * SLAB];
+        alignas(16) G a[TILE * SLAB], b[TILE * SLAB];
+        float A[SUBS][SLAB], B[SUBS][SLAB];  // the half-warps' maps, then those of what stands in front of each in the tile
+        float2 map[2][MAX_CLUSTER][SLAB];    // the cluster's tiles' maps, of this round and the one before
+        int closed[2][MAX_CLUSTER];          // whether a tile holds a reset
         float carry[SLAB];
         int what[2][TILE], slot[2][TILE];
-        int resets[W + 1];  // whether a warp's tokens hold a reset; whether one stands before a warp's in the tile
-        int next;
+        unsigned resets[2][TILE / 32];  // a bit a token
     };
 };
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(NT, 2) recurrence_tile_kernel(const RecurrenceParams p, const Work k, int vec) {
+__global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParams p, const Access access, int cluster) {
     dependent_prologue();
     using S = Shape<T, MODE>;
     using G = typename S::G;
     constexpr int VC = S::VC, SLAB = S::SLAB;
     extern __shared__ __align__(16) unsigned char raw[];
     typename S::Shared &sm = *reinterpret_cast<typename S::Shared *>(raw);
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const bool chained = k.time_tiles > 1, has_b = p.b != nullptr;
+    const int tid = threadIdx.x, lane = tid % LANES, sub = tid / LANES;
+    const int rank = cluster > 1 ? cluster_rank() : 0, slab = blockIdx.x / cluster;
+    const int s0 = slab * SLAB, c0 = s0 + lane * VC, inside = p.C - c0;
+    const bool has_b = p.b != nullptr;
 
-    auto fetch = [&](int tile, int buf, int tid, int threads) {
-        const int j = tile / k.slabs, c0 = (tile - j * k.slabs) * SLAB, t0 = j * TILE;
-        load_tile<T, SLAB>(sm.x, p.x, p.x_stride, t0, p.T, c0, p.C, vec & VEC_X, tid, threads);
-        load_tile<G, SLAB>(sm.a, p.a, p.a_stride, t0, p.T, c0, p.C, vec & VEC_A, tid, threads);
-        if (has_b) load_tile<G, SLAB>(sm.b, p.b, p.b_stride, t0, p.T, c0, p.C, vec & VEC_B, tid, threads);
-        if (MODE != RECUR_PRECOMPUTED) {
-            load_row<SLAB>(sm.A_log, p.A_log, c0, p.C, tid, threads);
-            load_row<SLAB>(sm.dt_bias, p.dt_bias, c0, p.C, tid, threads);
-        }
+    float rate[VC], dt[VC];
+#pragma unroll
+    for (int v = 0; v < VC; ++v) {
+        rate[v] = MODE && v < inside ? expf(p.A_log[c0 + v]) : 0.f;
+        dt[v] = MODE && v < inside ? p.dt_bias[c0 + v] : 0.f;
+    }
+    auto fetch = [&](int t0) {
+        load_tile<T, SLAB, TILE>(sm.x, p.x, p.x_stride, t0, p.T, s0, p.C, access.x);
+        load_tile<G, SLAB, TILE>(sm.a, p.a, p.a_stride, t0, p.T, s0, p.C, access.a);
+        if (has_b) load_tile<G, SLAB, TILE>(sm.b, p.b, p.b_stride, t0, p.T, s0, p.C, access.b);
     };
-    auto tokens = [&](int tile, int buf) {
-        if (threadIdx.x >= TILE) return;
-        int what, slot;
-        token_of(p, k, tile / k.slabs, tile % k.slabs == 0, what, slot);
-        sm.what[buf][threadIdx.x] = what;
-        sm.slot[buf][threadIdx.x] = slot;
+    auto tokens = [&](int t0, int buf) {
+        if (tid >= TILE) return;  // (whole warps)
+        int slot;
+        const int what = token_of(p, t0 + tid, slab == 0, slot);
+        sm.what[buf][tid] = what;
+        sm.slot[buf][tid] = slot;
+        const unsigned resets = __ballot_sync(0xffffffffu, what & RESET);
+        if (tid % 32 == 0) sm.resets[buf][tid / 32] = resets;
     };
 
-    int cur = blockIdx.x, nxt = k.tiles;
-    if (chained) {
-        if (threadIdx.x == 0) {
-            cur = atomicAdd(k.counter, 1);
-            nxt = atomicAdd(k.counter, 1);
-            sm.resets[0] = cur;
-            sm.next = nxt;
-        }
-        __syncthreads();
-        cur = sm.resets[0];
-        nxt = sm.next;
-        __syncthreads();
-    }
-    if (cur < k.tiles) {
-        fetch(cur, 0, threadIdx.x, NT);
-        tokens(cur, 0);
-    }
-    for (int buf = 0; cur < k.tiles; buf ^= 1) {
-        const int j = cur / k.slabs, slab = cur - j * k.slabs, c0 = slab * SLAB + lane * VC, inside = p.C - c0;
+    const int step = cluster * TILE, rounds = (p.T + step - 1) / step;
+    fetch(rank * TILE);
+    tokens(rank * TILE, 0);
+    if (blockIdx.x == 0) check_packing(p);
+    if (cluster > 1) cluster_sync();  // every CTA has begun before another writes to its shared memory
+    float run = 0.f;  // the state in front of the cluster's tiles, channel tid of the slab
+    for (int n = 0, buf = 0; n < rounds; ++n, buf ^= 1) {
+        const int t0 = n * step + rank * TILE;
         copies_done();
         __syncthreads();
 
-        // every token's state and decay with nothing in front of the warp's tokens
+        // every token's state and decay with nothing in front of the half-warp's tokens
         float h[TT][VC], P[TT][VC];
-        unsigned after = 0;  // tokens at or behind a reset among the warp's
-        {
-            float rate[VC], dt[VC];
+        unsigned after = 0;  // tokens at or behind a reset among them
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            const int r = sub * TT + i, what = sm.what[buf][r];
+            float x[VC], a[VC], b[VC] = {};
+            read<T, VC>(sm.x + r * SLAB + lane * VC, x);
+            read<G, VC>(sm.a + r * SLAB + lane * VC, a);
+            if (has_b) read<G, VC>(sm.b + r * SLAB + lane * VC, b);
+            float g[VC], u[VC];
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
-                rate[v] = MODE ? expf(sm.A_log[lane * VC + v]) : 0.f;
-                dt[v] = MODE ? sm.dt_bias[lane * VC + v] : 0.f;
+                const Gate q = gate_of<MODE>(a[v], b[v], rate[v], dt[v], has_b);
+                g[v] = q.g;
+                u[v] = q.w * x[v];
             }
-            bool reset = false;
-#pragma unroll
-            for (int i = 0; i < TT; ++i) {
-                const int r = warp * TT + i, what = sm.what[buf][r];
-                float x[VC], a[VC], b[VC] = {};
-                read<T, VC>(sm.x + r * SLAB + lane * VC, x);
-                read<G, VC>(sm.a + r * SLAB + lane * VC, a);
-                if (has_b) read<G, VC>(sm.b + r * SLAB + lane * VC, b);
-                float g[VC], u[VC];
+            if (what & RESET) {
+                float h0[VC] = {};
+                if ((what & LOAD) && p.init)
+                    load<VC>(p.init + (long long)sm.slot[buf][r] * p.C + c0, h0, inside, access.state);
 #pragma unroll
                 for (int v = 0; v < VC; ++v) {
-                    const Gate q = gate_of<MODE>(a[v], b[v], rate[v], dt[v], has_b);
-                    g[v] = q.g;
-                    u[v] = q.w * x[v];
+                    h[i][v] = what & VALID ? fmaf(g[v], h0[v], u[v]) : 0.f;
+                    P[i][v] = 0.f;
                 }
-                if (what & RESET) {
-                    float h0[VC] = {};
-                    if ((what & LOAD) && p.init)
-                        load<VC>(p.init + (long long)sm.slot[buf][r] * p.C + c0, h0, inside, vec & VEC_STATE);
-                    reset = true;
+                after |= ~0u << i;
+            } else {
 #pragma unroll
-                    for (int v = 0; v < VC; ++v) {
-                        h[i][v] = what & VALID ? fmaf(g[v], h0[v], u[v]) : 0.f;
-                        P[i][v] = 0.f;
-                    }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < VC; ++v) {
-                        h[i][v] = i ? fmaf(g[v], h[i - 1][v], u[v]) : u[v];
-                        P[i][v] = i ? g[v] * P[i - 1][v] : g[v];
-                    }
+                for (int v = 0; v < VC; ++v) {
+                    h[i][v] = i ? fmaf(g[v], h[i - 1][v], u[v]) : u[v];
+                    P[i][v] = i ? g[v] * P[i - 1][v] : g[v];
                 }
-                if (reset) after |= 1u << i;
             }
+        }
 #pragma unroll
-            for (int v = 0; v < VC; ++v) {
-                sm.A[warp][lane * VC + v] = P[TT - 1][v];
-                sm.B[warp][lane * VC + v] = h[TT - 1][v];
-            }
-            if (lane == 0) sm.resets[warp] = after != 0;
+        for (int v = 0; v < VC; ++v) {
+            sm.A[sub][lane * VC + v] = P[TT - 1][v];
+            sm.B[sub][lane * VC + v] = h[TT - 1][v];
         }
         __syncthreads();
 
-        if (warp == 0) {
-            // the map of the tile, and on the way that of what stands in front of each warp's tokens
-            float A[VC], B[VC], carry[VC];
+        const bool more = n + 1 < rounds;
+        if (more) fetch(t0 + step);
+        unsigned closed = 0;  // half-warps whose tokens hold a reset
 #pragma unroll
-            for (int v = 0; v < VC; ++v) A[v] = 1.f, B[v] = 0.f;
-            bool closed = false;
-            int front = 0;
+        for (int s = 0; s < SUBS; ++s) closed |= (unsigned)((sm.resets[buf][s * TT / 32] >> (s * TT % 32) & ((1u << TT) - 1)) != 0) << s;
+        if (tid < SLAB) {
+            // the map of the tile, and on the way that of what stands in front of each half-warp's tokens
+            float a[SUBS], b[SUBS];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const bool r = sm.resets[w];
-                front |= (int)closed << w;
+            for (int s = 0; s < SUBS; ++s) a[s] = sm.A[s][tid], b[s] = sm.B[s][tid];
+            float A = 1.f, B = 0.f;
 #pragma unroll
-                for (int v = 0; v < VC; ++v) {
-                    const float a = sm.A[w][lane * VC + v], b = sm.B[w][lane * VC + v];
-                    sm.A[w][lane * VC + v] = A[v];
-                    sm.B[w][lane * VC + v] = B[v];
-                    B[v] = r ? b : fmaf(a, B[v], b);
-                    A[v] = r ? 0.f : a * A[v];
-                }
-                closed |= r;
+            for (int s = 0; s < SUBS; ++s) {
+                sm.A[s][tid] = A;
+                sm.B[s][tid] = B;
+                const bool cut = closed >> s & 1;
+                B = cut ? b[s] : fmaf(a[s], B, b[s]);
+                A = cut ? 0.f : a[s] * A;
             }
-            const bool open = chained && j > 0 && !(sm.what[buf][0] & RESET);
-            chain<VC>(k, j, slab, A, B, closed, open, j + 1 < k.time_tiles, p.status, carry);
-#pragma unroll
-            for (int v = 0; v < VC; ++v) sm.carry[lane * VC + v] = carry[v];
-            if (lane == 0) sm.resets[W] = front;
-            if (p.checkpoints) store<float, VC>(p.checkpoints + (long long)j * p.C + c0, carry, inside, vec & VEC_STATE);
-        } else {
-            // meanwhile the other warps ask for the next tile
-            if (threadIdx.x == 32) sm.next = chained ? atomicAdd(k.counter, 1) : k.tiles;
-            if (nxt < k.tiles) fetch(nxt, buf ^ 1, threadIdx.x - 32, NT - 32);
+            if (cluster > 1) {
+                for (int r = 0; r < cluster; ++r) store_cluster(in_cta(&sm.map[buf][rank][tid], r), A, B);
+                if (tid < cluster) store_cluster(in_cta(&sm.closed[buf][rank], tid), closed != 0);
+            } else {
+                sm.carry[tid] = run;
+                run = closed ? B : fmaf(A, run, B);
+            }
         }
-        if (nxt < k.tiles) tokens(nxt, buf ^ 1);
+        if (more) tokens(t0 + step, buf ^ 1);
+        if (cluster > 1) {
+            cluster_sync();
+            if (tid < SLAB) {
+                for (int r = 0; r < cluster; ++r) {
+                    const float2 m = sm.map[buf][r][tid];
+                    if (r == rank) sm.carry[tid] = run;
+                    run = sm.closed[buf][r] ? m.y : fmaf(m.x, run, m.y);
+                }
+            }
+        }
         __syncthreads();
 
         float front[VC];
-        const bool cut = sm.resets[W] >> warp & 1;
+        const bool cut = closed & ((1u << sub) - 1);
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
-            const float a = sm.A[warp][lane * VC + v], b = sm.B[warp][lane * VC + v];
+            const float a = sm.A[sub][lane * VC + v], b = sm.B[sub][lane * VC + v];
             front[v] = cut ? b : fmaf(a, sm.carry[lane * VC + v], b);
         }
+        const int first = t0 + sub * TT;
+        if (p.checkpoints && first % CHECK == 0 && first < p.T)
+            store<float, VC>(p.checkpoints + (long long)(first / CHECK) * p.C + c0, front, inside, access.state);
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-            const int r = warp * TT + i, what = sm.what[buf][r];
+            const int r = sub * TT + i, what = sm.what[buf][r];
             if (!(what & VALID)) continue;
             if (!(after >> i & 1))
 #pragma unroll
                 for (int v = 0; v < VC; ++v) h[i][v] = fmaf(P[i][v], front[v], h[i][v]);
-            store<T, VC>(static_cast<T *>(p.y) + (long long)(j * TILE + r) * p.C + c0, h[i], inside, vec & VEC_Y);
+            store<T, VC>(static_cast<T *>(p.y) + (long long)(t0 + r) * p.C + c0, h[i], inside, access.y);
             if ((what & LAST) && p.final_state)
-                store<float, VC>(p.final_state + (long long)sm.slot[buf][r] * p.C + c0, h[i], inside, vec & VEC_STATE);
+                store<float, VC>(p.final_state + (long long)sm.slot[buf][r] * p.C + c0, h[i], inside, access.state);
         }
-        if (j == 0) {
-            // sequences without tokens keep their state; checks that the plan makes where there is one
-            if (slab == 0 && !chained && p.cu) {
-                if (threadIdx.x == 0 && (p.cu[0] != 0 || p.cu[p.B] != p.T)) flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
-                for (int b = threadIdx.x; b < p.B; b += NT)
-                    if (p.cu[b] > p.cu[b + 1]) flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
-            }
-            if (p.cu && p.final_state) {
-                for (int b0 = warp * 32; b0 < p.B; b0 += NT) {
-                    const int mine = b0 + lane;
-                    unsigned empty = __ballot_sync(0xffffffffu, mine < p.B && p.cu[mine] == p.cu[mine + 1]);
-                    for (; empty; empty &= empty - 1) {
-                        const int b = b0 + __ffs(empty) - 1, slot = p.slots ? p.slots[b] : b;
-                        if (slot < 0 || slot >= p.num_slots) {
-                            if (lane == 0 && slab == 0) flag_error(p.status, GDN_DEVERR_STATE_SLOT);
-                            continue;
-                        }
-                        float h0[VC] = {};
-                        if (p.init) load<VC>(p.init + (long long)slot * p.C + c0, h0, inside, vec & VEC_STATE);
-                        store<float, VC>(p.final_state + (long long)slot * p.C + c0, h0, inside, vec & VEC_STATE);
-                    }
-                }
-            }
+    }
+
+    // sequences without tokens keep their state
+    if (rank != 0 || !p.cu || !p.final_state) return;
+    for (int b = sub; b < p.B; b += SUBS) {
+        if (p.cu[b] != p.cu[b + 1]) continue;
+        const int slot = p.slots ? p.slots[b] : b;
+        if (slot < 0 || slot >= p.num_slots) {
+            if (lane == 0 && slab == 0) flag_error(p.status, GDN_DEVERR_STATE_SLOT);
+            continue;
         }
-        cur = nxt;
-        nxt = sm.next;
+        float h0[VC] = {};
+        if (p.init) load<VC>(p.init + (long long)slot * p.C + c0, h0, inside, access.state);
+        store<float, VC>(p.final_state + (long long)slot * p.C + c0, h0, inside, access.state);
     }
 }
 
@@ -259,7 +225,7 @@ __global__ void __launch_bounds__(SHORT_NT) recurrence_short_kernel(const Recurr
         if (c == 0) flag_error(p.status, GDN_DEVERR_STATE_SLOT);
         return;
     }
-    if (p.init) load<VC>(p.init + (long long)slot * p.C + c, h, VC, VC > 1);
+    if (p.init) load<VC>(p.init + (long long)slot * p.C + c, h, VC, true);
     for (int t0 = begin; t0 < end; t0 += AHEAD) {
         float x[AHEAD][VC] = {}, a[AHEAD][VC] = {}, bv[AHEAD][VC] = {};
 #pragma unroll
@@ -274,63 +240,55 @@ __global__ void __launch_bounds__(SHORT_NT) recurrence_short_kernel(const Recurr
         for (int i = 0; i < AHEAD; ++i) {
             const long long t = t0 + i;
             if (t >= end) break;
-            if (p.checkpoints && t % TILE == 0) {
-                float s[VC];
-#pragma unroll
-                for (int v = 0; v < VC; ++v) s[v] = t == begin ? 0.f : h[v];
-                store<float, VC>(p.checkpoints + t / TILE * p.C + c, s, VC, VC > 1);
-            }
+            if (p.checkpoints && t % CHECK == 0) store<float, VC>(p.checkpoints + t / CHECK * p.C + c, h, VC, true);
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
                 const Gate q = gate_of<MODE>(a[i][v], bv[i][v], rate[v], dt[v], p.b != nullptr);
                 h[v] = fmaf(q.g, h[v], q.w * x[i][v]);
             }
-            store<T, VC>(static_cast<T *>(p.y) + t * p.C + c, h, VC, VC > 1);
+            store<T, VC>(static_cast<T *>(p.y) + t * p.C + c, h, VC, true);
         }
     }
-    if (p.final_state) store<float, VC>(p.final_state + (long long)slot * p.C + c, h, VC, VC > 1);
+    if (p.final_state) store<float, VC>(p.final_state + (long long)slot * p.C + c, h, VC, true);
 }
 
 // ---------------------------------------------------------------- launches
 
-bool whole(const void *ptr, long long stride, int C, size_t elem, size_t bytes) {
-    return reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && stride * elem % bytes == 0 && C * elem % bytes == 0;
+template <typename T, int MODE>
+cudaError_t launch_short(const RecurrenceParams &p, cudaStream_t stream) {
+    using G = typename GateType<T, MODE>::type;
+    constexpr int VC = 4;
+    auto whole = [&](const void *ptr, long long stride, size_t elem) {
+        return (reinterpret_cast<uintptr_t>(ptr) | (unsigned long long)stride * elem) % (VC * elem) == 0;
+    };
+    const bool vec = p.C % VC == 0 && whole(p.x, p.x_stride, sizeof(T)) && whole(p.a, p.a_stride, sizeof(G)) &&
+                     whole(p.b, p.b_stride, sizeof(G)) && whole(p.y, p.C, sizeof(T)) && whole(p.init, p.C, 4) &&
+                     whole(p.final_state, p.C, 4) && whole(p.checkpoints, p.C, 4);
+    const int step = SHORT_NT * (vec ? VC : 1);
+    const dim3 grid((unsigned)((p.C + step - 1) / step), (unsigned)p.B);
+    if (vec) return launch_dependent(recurrence_short_kernel<T, MODE, VC>, grid, dim3(SHORT_NT), 0, stream, p);
+    return launch_dependent(recurrence_short_kernel<T, MODE, 1>, grid, dim3(SHORT_NT), 0, stream, p);
 }
 
 template <typename T, int MODE>
 cudaError_t launch_typed(const RecurrenceParams &p, int longest, cudaStream_t stream) {
+    if (longest <= SHORT_LEN) return launch_short<T, MODE>(p, stream);
     using S = Shape<T, MODE>;
     using G = typename S::G;
-    if (longest <= SHORT_LEN) {
-        constexpr int VC = 4;
-        const bool vec = whole(p.x, p.x_stride, p.C, sizeof(T), VC * sizeof(T)) && whole(p.a, p.a_stride, p.C, sizeof(G), VC * sizeof(G)) &&
-                         whole(p.b, p.b_stride, p.C, sizeof(G), VC * sizeof(G)) && whole(p.y, p.C, p.C, sizeof(T), VC * sizeof(T)) &&
-                         whole(p.init, p.C, p.C, 4, 16) && whole(p.final_state, p.C, p.C, 4, 16) && whole(p.checkpoints, p.C, p.C, 4, 16);
-        const int step = SHORT_NT * (vec ? VC : 1);
-        const dim3 grid((unsigned)((p.C + step - 1) / step), (unsigned)p.B);
-        if (vec) return launch_dependent(recurrence_short_kernel<T, MODE, VC>, grid, dim3(SHORT_NT), 0, stream, p);
-        return launch_dependent(recurrence_short_kernel<T, MODE, 1>, grid, dim3(SHORT_NT), 0, stream, p);
-    }
-    const Layout l = layout(p.T, p.C, S::SLAB, false);
-    const Work k = work_of(p.workspace, l);
-    constexpr int VC = S::VC;
-    const int vec = (whole(p.x, p.x_stride, p.C, sizeof(T), 16) ? VEC_X : 0) | (whole(p.a, p.a_stride, p.C, sizeof(G), 16) ? VEC_A : 0) |
-                    (whole(p.b, p.b_stride, p.C, sizeof(G), 16) ? VEC_B : 0) |
-                    (whole(p.y, p.C, p.C, sizeof(T), VC * sizeof(T)) ? VEC_Y : 0) |
-                    (whole(p.init, p.C, p.C, 4, VC * 4) && whole(p.final_state, p.C, p.C, 4, VC * 4) &&
-                             whole(p.checkpoints, p.C, p.C, 4, VC * 4) ? VEC_STATE : 0);
+    Access access;
+    access.x = whole_bytes(p.x, p.x_stride, p.C, sizeof(T));
+    access.a = whole_bytes(p.a, p.a_stride, p.C, sizeof(G));
+    access.b = whole_bytes(p.b, p.b_stride, p.C, sizeof(G));
+    access.y = whole_rows(p.y, p.C, sizeof(T), S::VC * sizeof(T));
+    access.state = whole_rows(p.init, p.C, 4, S::VC * 4) && whole_rows(p.final_state, p.C, 4, S::VC * 4) &&
+                   whole_rows(p.checkpoints, p.C, 4, S::VC * 4);
     constexpr int smem = (int)sizeof(typename S::Shared);
-    auto kernel = recurrence_tile_kernel<T, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto kernel = recurrence_kernel<T, MODE>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    long long ctas = l.tiles;
-    if (l.time_tiles > 1) {
-        const long long items = std::max<long long>(l.tiles, p.B), most = 3LL * current_device_sms();
-        e = launch_dependent(plan_kernel, dim3((unsigned)((items + PLAN_THREADS) / PLAN_THREADS)), dim3(PLAN_THREADS), 0, stream, p, k);
-        if (e != cudaSuccess) return e;
-        ctas = std::min(ctas, most);
-    }
-    return launch_dependent(kernel, dim3((unsigned)ctas), dim3(NT), smem, stream, p, k, vec);
+    const long long slabs = ((long long)p.C + S::SLAB - 1) / S::SLAB, tiles = ((long long)p.T + TILE - 1) / TILE;
+    const int size = cluster_size(slabs, tiles);
+    return launch_clusters(kernel, (unsigned)slabs, (unsigned)size, smem, stream, p, access, size);
 }
 
 template <typename T>
@@ -343,12 +301,6 @@ cudaError_t launch_mode(const RecurrenceParams &p, int mode, int longest, cudaSt
 }
 
 }  // namespace
-
-// (a slab of 64 channels takes no less than one of 128)
-size_t recurrence_workspace_bytes(int T, int C, int longest) {
-    if (longest <= SHORT_LEN || T <= TILE) return 0;
-    return std::max(layout(T, C, 64, false).bytes, layout(T, C, 128, false).bytes);
-}
 
 cudaError_t launch_recurrence(const RecurrenceParams &p, int io_dtype, int mode, int longest, cudaStream_t stream) {
     switch (io_dtype) {

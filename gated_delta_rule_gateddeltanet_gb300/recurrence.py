@@ -27,8 +27,7 @@ class LinearRecurrenceArgs(ctypes.Structure):
                 ("io_dtype", _i32), ("gate_mode", _i32), ("unit_input", _i32), ("max_seqlen", _i32),
                 ("x_stride", _i64), ("a_stride", _i64), ("b_stride", _i64), ("x", _p), ("a", _p), ("b", _p),
                 ("A_log", _p), ("dt_bias", _p), ("cu_seqlens", _p), ("state_slots", _p), ("initial_state", _p),
-                ("final_state", _p), ("output", _p), ("checkpoints", _p), ("status", _p), ("workspace", _p),
-                ("workspace_bytes", ctypes.c_size_t)]
+                ("final_state", _p), ("output", _p), ("checkpoints", _p), ("status", _p)]
 
 
 class LinearRecurrenceBackwardArgs(ctypes.Structure):
@@ -51,8 +50,8 @@ def declare(lib):
     for name, args in ENTRY_POINTS.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = _i32, [ctypes.POINTER(args), _p]
-        f = getattr(lib, name + "_workspace_size")
-        f.restype, f.argtypes = _i32, [ctypes.POINTER(args), ctypes.POINTER(ctypes.c_size_t)]
+    f = lib.gdn_linear_recurrence_backward_workspace_size
+    f.restype, f.argtypes = _i32, [ctypes.POINTER(LinearRecurrenceBackwardArgs), ctypes.POINTER(ctypes.c_size_t)]
 
 
 def _tokens(t, name, shape, dtype, device):
@@ -155,7 +154,7 @@ class LinearRecurrenceCall(_Call):
     def __init__(self, x, a, b=None, cu_seqlens=None, *, A_log=None, dt_bias=None, gate_mode="raw", unit_input=False,
                  initial_state=None, final_state=None, state_slots=None, num_seqs=None, num_state_slots=None,
                  output=None, checkpoints=None, return_checkpoints=False, max_seqlen=0, write_final_state=True,
-                 workspace=None, status=None):
+                 status=None):
         args, dev = LinearRecurrenceArgs(), x.device
         T, C, B, slots, _ = _inputs(args, x, a, b, cu_seqlens, A_log, dt_bias, gate_mode, unit_input, initial_state,
                                     state_slots, num_seqs, num_state_slots, status, (initial_state, final_state))
@@ -171,10 +170,9 @@ class LinearRecurrenceCall(_Call):
         if checkpoints is not None or return_checkpoints:
             checkpoints = _output(checkpoints, "checkpoints", _checkpoint_shape(T, C), torch.float32, dev)
         args.output, args.final_state, args.checkpoints = _ptr(output), _ptr(final_state), _ptr(checkpoints)
-        workspace = _workspace(args, workspace, "gdn_linear_recurrence", dev)
         self._resolve("gdn_linear_recurrence", args,
                       (output, final_state) if checkpoints is None else (output, final_state, checkpoints),
-                      (x, a, b, cu_seqlens, A_log, dt_bias, initial_state, state_slots, workspace, status), dev)
+                      (x, a, b, cu_seqlens, A_log, dt_bias, initial_state, state_slots, status), dev)
 
 
 def linear_recurrence(x, a, b=None, cu_seqlens=None, **kw):

@@ -754,13 +754,11 @@ gdn_status gdn_paged_attention(const gdn_paged_attention_args *args, gdn_stream_
  * flagged, any sequences may be skipped or computed.
  * Long sequences are split over time: a call gives the same bits every time, and
  * those of another batching or max_seqlen up to FP32 rounding.
- *   workspace     device scratch of gdn_linear_recurrence_workspace_size bytes, 16-byte aligned;
- *                 its contents need not be kept or set.  Not shared by calls that overlap.
  */
 typedef struct gdn_linear_recurrence_args {
     int32_t num_seqs;        /* B, at most 65535 */
     int32_t total_tokens;    /* T */
-    int32_t channels;        /* C >= 1 */
+    int32_t channels;        /* C, 1 to 2^24 */
     int32_t num_state_slots;
     int32_t io_dtype;        /* GDN_F32, GDN_F16 or GDN_BF16 */
     int32_t gate_mode;       /* GDN_GATES_* */
@@ -776,12 +774,7 @@ typedef struct gdn_linear_recurrence_args {
     void *output;
     float *checkpoints;
     int32_t *status;
-    void *workspace;
-    size_t workspace_bytes;
 } gdn_linear_recurrence_args;
-
-/* Bytes of workspace for these sizes (pointers are not read). */
-gdn_status gdn_linear_recurrence_workspace_size(const gdn_linear_recurrence_args *args, size_t *bytes);
 
 gdn_status gdn_linear_recurrence(const gdn_linear_recurrence_args *args, gdn_stream_t stream);
 
@@ -819,6 +812,7 @@ typedef struct gdn_linear_recurrence_backward_args {
     size_t workspace_bytes;
 } gdn_linear_recurrence_backward_args;
 
+/* Bytes of workspace for these sizes (pointers are not read). */
 gdn_status gdn_linear_recurrence_backward_workspace_size(const gdn_linear_recurrence_backward_args *args,
                                                          size_t *bytes);
 

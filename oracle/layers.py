@@ -5,10 +5,11 @@ Written token by token and row by row from the operators' formulas; shares no co
 with the library.  Inputs are the values that the library was given, in 64 bits.
 
 The bounds follow the error of each formula to first order, with u = 2^-24 (half a unit in
-the last place of FP32, relative).  A decay's exponent lg = -rate softplus(v) has a
-relative error of at most (|v| + 8) u (v is rounded, softplus and rate are good to a few
-u each, two products), g = e^lg one of |lg| (|v| + 8) u + 4 u, a sigmoid of b one of
-(|b| + 8) u, sqrt(1 - g^2) that of lg plus 8 u.  A state's error obeys the state's own
+the last place of FP32, relative).  e^-|v| has a relative error of at most (2 |v| + 4) u: v is a
+rounded sum, its product with log2(e) is rounded, each worth |v| u in the exponent, and the
+base-2 exponential is good to 4 u.  The exponent of a decay, lg = -rate softplus(v), thus has one
+of (2 |v| + 12) u (a polynomial of 2 u, two sums and products, rate to 4 u), g = e^lg one of |lg| times
+that plus 5 u, a sigmoid of b one of (|b| + 8) u, sqrt(1 - g^2) that of lg plus 8 u.  A state's error obeys the state's own
 recurrence: e_t = g e_(t-1) + (rel(g) + 4 u) g M_(t-1) + (rel(w) + 4 u) |w x|, with M the
 recurrence of the magnitudes.  The 4 u cover the roundings of a step however the scan is
 split: the product of decays, its use, and the sums of the parts.
@@ -46,8 +47,8 @@ class Gates:
         self.sig_b = np.ones_like(a) if b is None else sigmoid(b)
         self.factor = np.sqrt(-np.expm1(2 * self.lg)) if unit else np.ones_like(a)
         self.w = self.sig_b * self.factor
-        self.rel_lg = (np.abs(v) + 8) * U
-        self.rel_g = np.abs(self.lg) * self.rel_lg + 4 * U
+        self.rel_lg = (2 * np.abs(v) + 12) * U
+        self.rel_g = np.abs(self.lg) * (self.rel_lg + 2 * U) + 5 * U
         self.rel_f = self.rel_lg + 8 * U if unit else np.zeros_like(a)
         self.rel_b = 0.0 if b is None else (np.abs(b) + 8) * U
         self.rel_w = self.rel_f + self.rel_b + U
@@ -103,7 +104,7 @@ def linear_recurrence_backward(x, gates, spans, before, err_before, dy, d_final)
         dlg = dlg - dw * k
     slope = gates.rate * gates.sig_a
     da = -dlg * slope
-    da_err = dlg_err * slope + np.abs(da) * ((np.abs(gates.v) + 16) * U)
+    da_err = dlg_err * slope + np.abs(da) * ((2 * np.abs(gates.v) + 16) * U)
     out["da"] = (da, da_err)
     if gates.has_b:
         s = gates.sig_b * (1 - gates.sig_b)
