@@ -8,7 +8,8 @@ using namespace recur;
 
 // ---------------------------------------------------------------- long sequences
 
-constexpr int TT = 8, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA
+constexpr int NT = 512, SUBS = NT / LANES;
+constexpr int TT = 4, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA
 
 // What the host found to be aligned.
 struct Access {
@@ -23,12 +24,11 @@ struct Shape {
     struct Shared {
         alignas(16) T x[TILE * SLAB];
         alignas(16) G a[TILE * SLAB], b[TILE * SLAB];
-        float A[SUBS][SLAB], B[SUBS][SLAB];  // the half-warps' maps, then those of what stands in front of each in the tile
-        float2 map[2][MAX_CLUSTER][SLAB];    // the cluster's tiles' maps, of this round and the one before
-        int closed[2][MAX_CLUSTER];          // whether a tile holds a reset
-        float carry[SLAB];
-        int what[2][TILE], slot[2][TILE];
-        unsigned resets[2][TILE / 32];  // a bit a token
+        alignas(16) float A[SUBS][SLAB], B[SUBS][SLAB];  // the half-warps' maps, then those of what stands in front of each
+        float2 map[2][MAX_CLUSTER][SLAB];  // the cluster's tiles' maps, of this round and the one before
+        int closed[2][MAX_CLUSTER];        // whether a tile holds a reset
+        alignas(16) float carry[SLAB];
+        Tokens<TILE> tokens[2];
     };
 };
 
@@ -52,101 +52,89 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
         dt[v] = MODE && v < inside ? p.dt_bias[c0 + v] : 0.f;
     }
     auto fetch = [&](int t0) {
-        load_tile<T, SLAB, TILE>(sm.x, p.x, p.x_stride, t0, p.T, s0, p.C, access.x);
-        load_tile<G, SLAB, TILE>(sm.a, p.a, p.a_stride, t0, p.T, s0, p.C, access.a);
-        if (has_b) load_tile<G, SLAB, TILE>(sm.b, p.b, p.b_stride, t0, p.T, s0, p.C, access.b);
-    };
-    auto tokens = [&](int t0, int buf) {
-        if (tid >= TILE) return;  // (whole warps)
-        int slot;
-        const int what = token_of(p, t0 + tid, slab == 0, slot);
-        sm.what[buf][tid] = what;
-        sm.slot[buf][tid] = slot;
-        const unsigned resets = __ballot_sync(0xffffffffu, what & RESET);
-        if (tid % 32 == 0) sm.resets[buf][tid / 32] = resets;
+        load_tile<T, SLAB, TILE, NT>(sm.x, p.x, p.x_stride, t0, p.T, s0, p.C, access.x);
+        load_tile<G, SLAB, TILE, NT>(sm.a, p.a, p.a_stride, t0, p.T, s0, p.C, access.a);
+        if (has_b) load_tile<G, SLAB, TILE, NT>(sm.b, p.b, p.b_stride, t0, p.T, s0, p.C, access.b);
     };
 
     const int step = cluster * TILE, rounds = (p.T + step - 1) / step;
     fetch(rank * TILE);
-    tokens(rank * TILE, 0);
+    tokens_of(sm.tokens[0], p, rank * TILE, slab == 0);
     if (blockIdx.x == 0) check_packing(p);
     if (cluster > 1) cluster_sync();  // every CTA has begun before another writes to its shared memory
     float run = 0.f;  // the state in front of the cluster's tiles, channel tid of the slab
     for (int n = 0, buf = 0; n < rounds; ++n, buf ^= 1) {
         const int t0 = n * step + rank * TILE;
+        const Tokens<TILE> &tokens = sm.tokens[buf];
         copies_done();
         __syncthreads();
 
         // every token's state and decay with nothing in front of the half-warp's tokens
+        const unsigned reset = bits_of<TT>(tokens.reset, sub), loads = bits_of<TT>(tokens.load, sub);
         float h[TT][VC], P[TT][VC];
-        unsigned after = 0;  // tokens at or behind a reset among them
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-            const int r = sub * TT + i, what = sm.what[buf][r];
-            float x[VC], a[VC], b[VC] = {};
+            const int r = sub * TT + i;
+            float x[VC], a[VC], b[VC] = {}, front[VC];
             read<T, VC>(sm.x + r * SLAB + lane * VC, x);
             read<G, VC>(sm.a + r * SLAB + lane * VC, a);
             if (has_b) read<G, VC>(sm.b + r * SLAB + lane * VC, b);
-            float g[VC], u[VC];
+            const bool cut = reset >> i & 1;
+#pragma unroll
+            for (int v = 0; v < VC; ++v) front[v] = i == 0 || cut ? 0.f : h[i - 1][v];
+            if ((loads >> i & 1) && p.init) load<VC>(p.init + (long long)tokens.slot[r] * p.C + c0, front, inside, false);
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
                 const Gate q = gate_of<MODE>(a[v], b[v], rate[v], dt[v], has_b);
-                g[v] = q.g;
-                u[v] = q.w * x[v];
-            }
-            if (what & RESET) {
-                float h0[VC] = {};
-                if ((what & LOAD) && p.init)
-                    load<VC>(p.init + (long long)sm.slot[buf][r] * p.C + c0, h0, inside, access.state);
-#pragma unroll
-                for (int v = 0; v < VC; ++v) {
-                    h[i][v] = what & VALID ? fmaf(g[v], h0[v], u[v]) : 0.f;
-                    P[i][v] = 0.f;
-                }
-                after |= ~0u << i;
-            } else {
-#pragma unroll
-                for (int v = 0; v < VC; ++v) {
-                    h[i][v] = i ? fmaf(g[v], h[i - 1][v], u[v]) : u[v];
-                    P[i][v] = i ? g[v] * P[i - 1][v] : g[v];
-                }
+                h[i][v] = fmaf(q.g, front[v], q.w * x[v]);
+                P[i][v] = cut ? 0.f : i ? q.g * P[i - 1][v] : q.g;
             }
         }
+        {
+            Pack<float, VC> A, B;
 #pragma unroll
-        for (int v = 0; v < VC; ++v) {
-            sm.A[sub][lane * VC + v] = P[TT - 1][v];
-            sm.B[sub][lane * VC + v] = h[TT - 1][v];
+            for (int v = 0; v < VC; ++v) A.e[v] = P[TT - 1][v], B.e[v] = h[TT - 1][v];
+            if constexpr (VC == 4) {
+                *reinterpret_cast<uint4 *>(&sm.A[sub][lane * VC]) = A.u4;
+                *reinterpret_cast<uint4 *>(&sm.B[sub][lane * VC]) = B.u4;
+            } else {
+                *reinterpret_cast<uint2 *>(&sm.A[sub][lane * VC]) = A.u2;
+                *reinterpret_cast<uint2 *>(&sm.B[sub][lane * VC]) = B.u2;
+            }
         }
         __syncthreads();
 
         const bool more = n + 1 < rounds;
-        if (more) fetch(t0 + step);
-        unsigned closed = 0;  // half-warps whose tokens hold a reset
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s) closed |= (unsigned)((sm.resets[buf][s * TT / 32] >> (s * TT % 32) & ((1u << TT) - 1)) != 0) << s;
         if (tid < SLAB) {
             // the map of the tile, and on the way that of what stands in front of each half-warp's tokens
-            float a[SUBS], b[SUBS];
-#pragma unroll
-            for (int s = 0; s < SUBS; ++s) a[s] = sm.A[s][tid], b[s] = sm.B[s][tid];
             float A = 1.f, B = 0.f;
+            bool closed = false;
+            for (int s0 = 0; s0 < SUBS; s0 += 8) {
+                float a[8], b[8];
 #pragma unroll
-            for (int s = 0; s < SUBS; ++s) {
-                sm.A[s][tid] = A;
-                sm.B[s][tid] = B;
-                const bool cut = closed >> s & 1;
-                B = cut ? b[s] : fmaf(a[s], B, b[s]);
-                A = cut ? 0.f : a[s] * A;
+                for (int s = 0; s < 8; ++s) a[s] = sm.A[s0 + s][tid], b[s] = sm.B[s0 + s][tid];
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    sm.A[s0 + s][tid] = A;
+                    sm.B[s0 + s][tid] = B;
+                    const bool cut = bits_of<TT>(tokens.reset, s0 + s);
+                    B = cut ? b[s] : fmaf(a[s], B, b[s]);
+                    A = cut ? 0.f : a[s] * A;
+                    closed |= cut;
+                }
             }
             if (cluster > 1) {
                 for (int r = 0; r < cluster; ++r) store_cluster(in_cta(&sm.map[buf][rank][tid], r), A, B);
-                if (tid < cluster) store_cluster(in_cta(&sm.closed[buf][rank], tid), closed != 0);
+                if (tid < cluster) store_cluster(in_cta(&sm.closed[buf][rank], tid), closed);
             } else {
                 sm.carry[tid] = run;
                 run = closed ? B : fmaf(A, run, B);
             }
         }
-        if (more) tokens(t0 + step, buf ^ 1);
+        if (more) {
+            fetch(t0 + step);
+            tokens_of(sm.tokens[buf ^ 1], p, t0 + step, slab == 0);
+        }
         if (cluster > 1) {
             cluster_sync();
             if (tid < SLAB) {
@@ -159,26 +147,29 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
         }
         __syncthreads();
 
-        float front[VC];
-        const bool cut = closed & ((1u << sub) - 1);
+        // whether a reset stands before the half-warp's tokens in the tile
+        unsigned before = tokens.reset[sub * TT / 32] & ((1u << (sub * TT % 32)) - 1);
 #pragma unroll
-        for (int v = 0; v < VC; ++v) {
-            const float a = sm.A[sub][lane * VC + v], b = sm.B[sub][lane * VC + v];
-            front[v] = cut ? b : fmaf(a, sm.carry[lane * VC + v], b);
-        }
+        for (int w = 0; w < TILE / 32 - 1; ++w) before |= w < sub * TT / 32 ? tokens.reset[w] : 0;
+        float front[VC], A[VC], B[VC], carry[VC];
+        read<float, VC>(&sm.A[sub][lane * VC], A);
+        read<float, VC>(&sm.B[sub][lane * VC], B);
+        read<float, VC>(&sm.carry[lane * VC], carry);
+#pragma unroll
+        for (int v = 0; v < VC; ++v) front[v] = before ? B[v] : fmaf(A[v], carry[v], B[v]);
         const int first = t0 + sub * TT;
         if (p.checkpoints && first % CHECK == 0 && first < p.T)
             store<float, VC>(p.checkpoints + (long long)(first / CHECK) * p.C + c0, front, inside, access.state);
+        const unsigned valid = bits_of<TT>(tokens.valid, sub), lasts = bits_of<TT>(tokens.last, sub);
+        T *y = static_cast<T *>(p.y) + (long long)first * p.C + c0;
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            const int r = sub * TT + i, what = sm.what[buf][r];
-            if (!(what & VALID)) continue;
-            if (!(after >> i & 1))
+        for (int i = 0; i < TT; ++i, y += p.C) {
+            if (!(reset & ((2u << i) - 1)))
 #pragma unroll
                 for (int v = 0; v < VC; ++v) h[i][v] = fmaf(P[i][v], front[v], h[i][v]);
-            store<T, VC>(static_cast<T *>(p.y) + (long long)(t0 + r) * p.C + c0, h[i], inside, access.y);
-            if ((what & LAST) && p.final_state)
-                store<float, VC>(p.final_state + (long long)sm.slot[buf][r] * p.C + c0, h[i], inside, access.state);
+            if (valid >> i & 1) store<T, VC>(y, h[i], inside, access.y);
+            if ((lasts >> i & 1) && p.final_state)
+                store<float, VC>(p.final_state + (long long)tokens.slot[sub * TT + i] * p.C + c0, h[i], inside, false);
         }
     }
 
@@ -282,13 +273,14 @@ cudaError_t launch_typed(const RecurrenceParams &p, int longest, cudaStream_t st
     access.y = whole_rows(p.y, p.C, sizeof(T), S::VC * sizeof(T));
     access.state = whole_rows(p.init, p.C, 4, S::VC * 4) && whole_rows(p.final_state, p.C, 4, S::VC * 4) &&
                    whole_rows(p.checkpoints, p.C, 4, S::VC * 4);
-    constexpr int smem = (int)sizeof(typename S::Shared);
+    constexpr size_t smem = sizeof(typename S::Shared);
     auto kernel = recurrence_kernel<T, MODE>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const Resident *resident;
+    const cudaError_t e = prepare_clusters<T, MODE>(kernel, NT, smem, &resident);
     if (e != cudaSuccess) return e;
     const long long slabs = ((long long)p.C + S::SLAB - 1) / S::SLAB, tiles = ((long long)p.T + TILE - 1) / TILE;
-    const int size = cluster_size(slabs, tiles);
-    return launch_clusters(kernel, (unsigned)slabs, (unsigned)size, smem, stream, p, access, size);
+    const int size = cluster_size(*resident, slabs, tiles);
+    return launch_clusters(kernel, (unsigned)slabs, (unsigned)size, NT, smem, stream, p, access, size);
 }
 
 template <typename T>

@@ -15,6 +15,8 @@
 // infinities and NaN of one sequence do not reach the next.
 #pragma once
 
+#include <type_traits>
+
 #include "layer_internal.cuh"
 
 namespace gdn {
@@ -22,7 +24,6 @@ namespace recur {
 
 constexpr int CHECK = GDN_RECURRENCE_CHECKPOINT;
 constexpr int LANES = 16;  // lanes beside one another along the channels
-constexpr int NT = 256, SUBS = NT / LANES;
 constexpr int MAX_CLUSTER = 8;
 enum { RESET = 1, LOAD = 2, LAST = 4, VALID = 8 };  // LOAD: a sequence begins here; RESET: so, or no sequence's token
 
@@ -61,11 +62,42 @@ __device__ __forceinline__ int token_of(const RecurrenceParams &p, int t, bool f
     return VALID | (t == begin ? RESET | LOAD : 0) | (t == end - 1 ? LAST : 0);
 }
 
+// Which of a tile's tokens are what, a bit a token, and their slots.
+template <int TILE>
+struct Tokens {
+    unsigned reset[TILE / 32], load[TILE / 32], last[TILE / 32], valid[TILE / 32];
+    int slot[TILE];
+};
+
+// Fills them for the tile at t0 (whole warps of the first TILE threads).
+template <int TILE>
+__device__ __forceinline__ void tokens_of(Tokens<TILE> &k, const RecurrenceParams &p, int t0, bool flag) {
+    const int i = threadIdx.x;
+    if (i >= TILE) return;
+    int slot;
+    const int what = token_of(p, t0 + i, flag, slot);
+    k.slot[i] = slot;
+    const unsigned reset = __ballot_sync(0xffffffffu, what & RESET), load = __ballot_sync(0xffffffffu, what & LOAD);
+    const unsigned last = __ballot_sync(0xffffffffu, what & LAST), valid = __ballot_sync(0xffffffffu, what & VALID);
+    if (i % 32 == 0) {
+        k.reset[i / 32] = reset;
+        k.load[i / 32] = load;
+        k.last[i / 32] = last;
+        k.valid[i / 32] = valid;
+    }
+}
+
+// The bits of run `sub` of TT tokens.
+template <int TT>
+__device__ __forceinline__ unsigned bits_of(const unsigned *words, int sub) {
+    return words[sub * TT / 32] >> (sub * TT % 32) & ((1u << TT) - 1);
+}
+
 // The packing's own checks, by one CTA of a call.
 __device__ __forceinline__ void check_packing(const RecurrenceParams &p) {
     if (!p.cu) return;
     bool bad = threadIdx.x == 0 && (p.cu[0] != 0 || p.cu[p.B] != p.T);
-    for (int b = threadIdx.x; b < p.B; b += NT) bad |= p.cu[b] > p.cu[b + 1];
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) bad |= p.cu[b] > p.cu[b + 1];
     if (bad) flag_error(p.status, GDN_DEVERR_CU_SEQLENS);
 }
 
@@ -81,27 +113,36 @@ __device__ __forceinline__ void copy(void *dst, const void *src, bool in) {
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <typename E, int SLAB, int TILE, int BYTES>
+// A thread copies one column of its pieces, every ROWS-th row.
+template <typename E, int SLAB, int TILE, int NT, int BYTES>
 __device__ __forceinline__ void copy_tile(E *dst, const E *base, long long stride, int t0, int T, int c0, int C) {
-    constexpr int N = BYTES / (int)sizeof(E), ROW = SLAB / N;
-    const E *src = base + (long long)t0 * stride + c0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < TILE * ROW; i += NT) {
-        const int r = i / ROW, c = i % ROW * N;
-        const bool in = t0 + r < T && c0 + c < C;
-        copy<BYTES>(dst + r * SLAB + c, in ? src + r * stride + c : base, in);
+    constexpr int N = BYTES / (int)sizeof(E), ROW = SLAB / N, ROWS = NT / ROW;
+    static_assert(NT % ROW == 0 && TILE % ROWS == 0, "");
+    const int r = threadIdx.x / ROW, c = threadIdx.x % ROW * N;
+    const bool column = c0 + c < C;
+    int left = T - t0 - r;
+    const E *src = base + (long long)(t0 + r) * stride + (c0 + c);
+    dst += r * SLAB + c;
+    stride *= ROWS;
+#pragma unroll
+    for (int k = 0; k < TILE / ROWS; ++k) {
+        const bool in = column && left > 0;
+        copy<BYTES>(dst, in ? src : base, in);
+        src += stride;
+        dst += ROWS * SLAB;
+        left -= ROWS;
     }
 }
 
 // A tile of E's, [TILE][SLAB], from rows `stride` apart; zeros past T and C.  bytes: what base, stride and C are whole
 // multiples of (16, 4, or less).
-template <typename E, int SLAB, int TILE>
+template <typename E, int SLAB, int TILE, int NT>
 __device__ __forceinline__ void load_tile(E *dst, const void *base, long long stride, int t0, int T, int c0, int C, int bytes) {
     const E *src = static_cast<const E *>(base);
     if (bytes == 16) {
-        copy_tile<E, SLAB, TILE, 16>(dst, src, stride, t0, T, c0, C);
+        copy_tile<E, SLAB, TILE, NT, 16>(dst, src, stride, t0, T, c0, C);
     } else if (bytes == 4) {
-        copy_tile<E, SLAB, TILE, 4>(dst, src, stride, t0, T, c0, C);
+        copy_tile<E, SLAB, TILE, NT, 4>(dst, src, stride, t0, T, c0, C);
     } else {
         src += (long long)t0 * stride + c0;
 #pragma unroll 8
@@ -129,7 +170,7 @@ union Pack {
     E e[VC];
     uint4 u4;
     uint2 u2;
-    uint32_t u1;
+    uint32_t u1, words[4];
     __device__ __forceinline__ Pack() {}
 };
 
@@ -145,12 +186,27 @@ __device__ __forceinline__ void read(const E *src, float (&f)[VC]) {
     for (int i = 0; i < VC; ++i) f[i] = to_f32(v.e[i]);
 }
 
+template <typename E, int VC>
+__device__ __forceinline__ void pack(Pack<E, VC> &v, const float (&f)[VC]) {
+    if constexpr (sizeof(E) == 2 && VC % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < VC; i += 2) {
+            uint32_t two;
+            if constexpr (std::is_same<E, __half>::value) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(two) : "f"(f[i + 1]), "f"(f[i]));
+            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(two) : "f"(f[i + 1]), "f"(f[i]));
+            v.words[i / 2] = two;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VC; ++i) v.e[i] = from_f32<E>(f[i]);
+    }
+}
+
 // `inside` of them at most; vec: they are aligned, and all inside or none.
 template <typename E, int VC>
 __device__ __forceinline__ void store(E *dst, const float (&f)[VC], int inside, bool vec) {
     Pack<E, VC> v;
-#pragma unroll
-    for (int i = 0; i < VC; ++i) v.e[i] = from_f32<E>(f[i]);
+    pack(v, f);
     if (vec) {
         if (inside <= 0) return;
         if constexpr (sizeof(E) * VC == 16) *reinterpret_cast<uint4 *>(dst) = v.u4;
@@ -199,11 +255,11 @@ __device__ __forceinline__ void store_cluster(uint32_t a, int x) {
 
 // A cluster's launch as a programmatic dependent (launch_dependent with clusters).
 template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(Params...), unsigned clusters, unsigned size, size_t smem, cudaStream_t stream,
-                            Args &&...args) {
+cudaError_t launch_clusters(void (*kernel)(Params...), unsigned clusters, unsigned size, unsigned threads, size_t smem,
+                            cudaStream_t stream, Args &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * size);
-    cfg.blockDim = dim3(NT);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -217,10 +273,57 @@ cudaError_t launch_clusters(void (*kernel)(Params...), unsigned clusters, unsign
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
 }
 
-// CTAs a cluster: as many as keep all clusters resident at once (two CTAs an SM), and no more than there are tiles.
-inline int cluster_size(long long slabs, long long tiles) {
-    const long long room = 2LL * current_device_sms() / slabs;
-    return (int)std::max(1LL, std::min({(long long)MAX_CLUSTER, room, tiles}));
+// Clusters of each size (1 to MAX_CLUSTER) of a kernel that are resident at once on the current device.
+struct Resident {
+    int most[MAX_CLUSTER + 1];
+};
+template <typename Kernel>
+cudaError_t resident_clusters(Kernel kernel, unsigned threads, size_t smem, Resident &out) {
+    for (int size = 1; size <= MAX_CLUSTER; ++size) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = size;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&out.most[size], kernel, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// CTAs a cluster: the largest size at which all clusters are resident at once, and no more than there are tiles.
+inline int cluster_size(const Resident &r, long long slabs, long long tiles) {
+    int size = 1;
+    for (int s = 2; s <= MAX_CLUSTER && s <= tiles; ++s)
+        if (slabs <= r.most[s]) size = s;
+    return size;
+}
+
+// A kernel's shared memory set and its residency looked up, once a device (as current_device_sms); a template of
+// what tells the kernels apart, since they share a type.
+template <typename T, int MODE, typename Kernel>
+cudaError_t prepare_clusters(Kernel kernel, unsigned threads, size_t smem, const Resident **out) {
+    constexpr int kMaxDevices = 128;
+    static Resident known[kMaxDevices];
+    static int ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
+        Resident r;
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        if ((e = resident_clusters(kernel, threads, smem, r)) != cudaSuccess) return e;
+        known[dev] = r;  // (two threads that come here at once write the same)
+        __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
+    }
+    *out = &known[dev];
+    return cudaSuccess;
 }
 
 }  // namespace recur
