@@ -8,8 +8,8 @@ using namespace recur;
 
 // ---------------------------------------------------------------- long sequences
 
-constexpr int NT = 512, SUBS = NT / LANES;
-constexpr int TT = 4, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA
+constexpr int NT = 256, SUBS = NT / LANES;
+constexpr int TT = 8, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA
 
 // What the host found to be aligned.
 struct Access {
@@ -22,13 +22,13 @@ struct Shape {
     using G = typename GateType<T, MODE>::type;
     static constexpr int VC = sizeof(G) == 4 ? 2 : 4, SLAB = LANES * VC;
     struct Shared {
-        alignas(16) T x[TILE * SLAB];
-        alignas(16) G a[TILE * SLAB], b[TILE * SLAB];
+        alignas(128) T x[TILE * SLAB];
+        alignas(128) G a[TILE * SLAB], b[TILE * SLAB];
         alignas(16) float A[SUBS][SLAB], B[SUBS][SLAB];  // the half-warps' maps, then those of what stands in front of each
-        float2 map[2][MAX_CLUSTER][SLAB];  // the cluster's tiles' maps, of this round and the one before
-        int closed[2][MAX_CLUSTER];        // whether a tile holds a reset
+        alignas(16) float4 map[2][MAX_CLUSTER][SLAB];  // the cluster's tiles' maps (A, B, whether it holds a reset)
         alignas(16) float carry[SLAB];
         Tokens<TILE> tokens[2];
+        alignas(8) uint64_t full, maps[2];
     };
 };
 
@@ -37,114 +37,145 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
     dependent_prologue();
     using S = Shape<T, MODE>;
     using G = typename S::G;
-    constexpr int VC = S::VC, SLAB = S::SLAB;
-    extern __shared__ __align__(16) unsigned char raw[];
+    constexpr int VC = S::VC, SLAB = S::SLAB, PAIRS = VC / 2;
+    extern __shared__ __align__(128) unsigned char raw[];
     typename S::Shared &sm = *reinterpret_cast<typename S::Shared *>(raw);
     const int tid = threadIdx.x, lane = tid % LANES, sub = tid / LANES;
     const int rank = cluster > 1 ? cluster_rank() : 0, slab = blockIdx.x / cluster;
     const int s0 = slab * SLAB, c0 = s0 + lane * VC, inside = p.C - c0;
     const bool has_b = p.b != nullptr;
 
-    float rate[VC], dt[VC];
+    F2 rate[PAIRS], dt[PAIRS];
 #pragma unroll
-    for (int v = 0; v < VC; ++v) {
-        rate[v] = MODE && v < inside ? expf(p.A_log[c0 + v]) : 0.f;
-        dt[v] = MODE && v < inside ? p.dt_bias[c0 + v] : 0.f;
+    for (int v = 0; v < PAIRS; ++v) {
+        float r[2] = {}, d[2] = {};
+        if (MODE != RECUR_PRECOMPUTED)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (2 * v + k < inside) r[k] = -LOG2E * expf(p.A_log[c0 + 2 * v + k]), d[k] = p.dt_bias[c0 + 2 * v + k];
+        rate[v] = F2(r[0], r[1]);
+        dt[v] = F2(d[0], d[1]);
     }
+    if (tid == 0) {
+        ptx::mbar_init(&sm.full, 1);
+        ptx::mbar_init(&sm.maps[0], 1);
+        ptx::mbar_init(&sm.maps[1], 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+
+    const bool bulk = access.x == 16 || access.a == 16 || (has_b && access.b == 16);
     auto fetch = [&](int t0) {
-        load_tile<T, SLAB, TILE, NT>(sm.x, p.x, p.x_stride, t0, p.T, s0, p.C, access.x);
-        load_tile<G, SLAB, TILE, NT>(sm.a, p.a, p.a_stride, t0, p.T, s0, p.C, access.a);
-        if (has_b) load_tile<G, SLAB, TILE, NT>(sm.b, p.b, p.b_stride, t0, p.T, s0, p.C, access.b);
+        if (bulk && t0 < p.T) {
+            if (tid == 0) {
+                uint32_t bytes = access.x == 16 ? bulk_bytes<T, SLAB, TILE>(t0, p.T, s0, p.C) : 0;
+                if (access.a == 16) bytes += bulk_bytes<G, SLAB, TILE>(t0, p.T, s0, p.C);
+                if (has_b && access.b == 16) bytes += bulk_bytes<G, SLAB, TILE>(t0, p.T, s0, p.C);
+                ptx::mbar_arrive_expect_tx(&sm.full, bytes);
+            }
+            // the first half of the threads x, then b, the second a
+            if (tid < NT / 2) {
+                if (access.x == 16) bulk_tile<T, SLAB, TILE>(sm.x, p.x, p.x_stride, t0, p.T, s0, p.C, tid, NT / 2, &sm.full);
+                if (has_b && access.b == 16) bulk_tile<G, SLAB, TILE>(sm.b, p.b, p.b_stride, t0, p.T, s0, p.C, tid, NT / 2, &sm.full);
+            } else if (access.a == 16) {
+                bulk_tile<G, SLAB, TILE>(sm.a, p.a, p.a_stride, t0, p.T, s0, p.C, tid - NT / 2, NT / 2, &sm.full);
+            }
+        }
+        if (access.x != 16) load_tile<T, SLAB, TILE, NT>(sm.x, p.x, p.x_stride, t0, p.T, s0, p.C, access.x);
+        if (access.a != 16) load_tile<G, SLAB, TILE, NT>(sm.a, p.a, p.a_stride, t0, p.T, s0, p.C, access.a);
+        if (has_b && access.b != 16) load_tile<G, SLAB, TILE, NT>(sm.b, p.b, p.b_stride, t0, p.T, s0, p.C, access.b);
     };
 
     const int step = cluster * TILE, rounds = (p.T + step - 1) / step;
     fetch(rank * TILE);
     tokens_of(sm.tokens[0], p, rank * TILE, slab == 0);
     if (blockIdx.x == 0) check_packing(p);
-    if (cluster > 1) cluster_sync();  // every CTA has begun before another writes to its shared memory
+    if (cluster > 1) cluster_sync();  // every CTA has its barriers before another writes to its shared memory
     float run = 0.f;  // the state in front of the cluster's tiles, channel tid of the slab
     for (int n = 0, buf = 0; n < rounds; ++n, buf ^= 1) {
         const int t0 = n * step + rank * TILE;
         const Tokens<TILE> &tokens = sm.tokens[buf];
+        if (bulk && t0 < p.T) wait(&sm.full, n & 1, p.status);
         copies_done();
         __syncthreads();
 
         // every token's state and decay with nothing in front of the half-warp's tokens
         const unsigned reset = bits_of<TT>(tokens.reset, sub), loads = bits_of<TT>(tokens.load, sub);
-        float h[TT][VC], P[TT][VC];
+        F2 h[TT][PAIRS], P[TT][PAIRS];
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             const int r = sub * TT + i;
-            float x[VC], a[VC], b[VC] = {}, front[VC];
+            float x[VC], a[VC], b[VC] = {};
             read<T, VC>(sm.x + r * SLAB + lane * VC, x);
             read<G, VC>(sm.a + r * SLAB + lane * VC, a);
             if (has_b) read<G, VC>(sm.b + r * SLAB + lane * VC, b);
             const bool cut = reset >> i & 1;
+            F2 front[PAIRS];
 #pragma unroll
-            for (int v = 0; v < VC; ++v) front[v] = i == 0 || cut ? 0.f : h[i - 1][v];
-            if ((loads >> i & 1) && p.init) load<VC>(p.init + (long long)tokens.slot[r] * p.C + c0, front, inside, false);
+            for (int v = 0; v < PAIRS; ++v) {
+                front[v] = F2(0.f);
+                if (i > 0 && !cut) front[v] = h[i - 1][v];
+            }
+            if ((loads >> i & 1) && p.init) {
+                float h0[VC];
+                load<VC>(p.init + (long long)tokens.slot[r] * p.C + c0, h0, inside, false);
 #pragma unroll
-            for (int v = 0; v < VC; ++v) {
-                const Gate q = gate_of<MODE>(a[v], b[v], rate[v], dt[v], has_b);
-                h[i][v] = fmaf(q.g, front[v], q.w * x[v]);
-                P[i][v] = cut ? 0.f : i ? q.g * P[i - 1][v] : q.g;
+                for (int v = 0; v < PAIRS; ++v) front[v] = F2(h0[2 * v], h0[2 * v + 1]);
+            }
+#pragma unroll
+            for (int v = 0; v < PAIRS; ++v) {
+                F2 g, w;
+                gate_pair<MODE>(F2(a[2 * v], a[2 * v + 1]), F2(b[2 * v], b[2 * v + 1]), rate[v], dt[v], has_b, g, w);
+                h[i][v] = fma2(g, front[v], mul2(w, F2(x[2 * v], x[2 * v + 1])));
+                P[i][v] = i == 0 ? g : mul2(g, P[i - 1][v]);
             }
         }
         {
             Pack<float, VC> A, B;
 #pragma unroll
-            for (int v = 0; v < VC; ++v) A.e[v] = P[TT - 1][v], B.e[v] = h[TT - 1][v];
-            if constexpr (VC == 4) {
-                *reinterpret_cast<uint4 *>(&sm.A[sub][lane * VC]) = A.u4;
-                *reinterpret_cast<uint4 *>(&sm.B[sub][lane * VC]) = B.u4;
-            } else {
-                *reinterpret_cast<uint2 *>(&sm.A[sub][lane * VC]) = A.u2;
-                *reinterpret_cast<uint2 *>(&sm.B[sub][lane * VC]) = B.u2;
+            for (int v = 0; v < PAIRS; ++v) {
+                P[TT - 1][v].get(A.e[2 * v], A.e[2 * v + 1]);
+                h[TT - 1][v].get(B.e[2 * v], B.e[2 * v + 1]);
             }
+            put_pack(&sm.A[sub][lane * VC], A);
+            put_pack(&sm.B[sub][lane * VC], B);
         }
         __syncthreads();
 
         const bool more = n + 1 < rounds;
+        if (more) fetch(t0 + step);
         if (tid < SLAB) {
             // the map of the tile, and on the way that of what stands in front of each half-warp's tokens
-            float A = 1.f, B = 0.f;
+            float A = 1.f, B = 0.f, a[SUBS], b[SUBS];
             bool closed = false;
-            for (int s0 = 0; s0 < SUBS; s0 += 8) {
-                float a[8], b[8];
 #pragma unroll
-                for (int s = 0; s < 8; ++s) a[s] = sm.A[s0 + s][tid], b[s] = sm.B[s0 + s][tid];
+            for (int s = 0; s < SUBS; ++s) a[s] = sm.A[s][tid], b[s] = sm.B[s][tid];
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    sm.A[s0 + s][tid] = A;
-                    sm.B[s0 + s][tid] = B;
-                    const bool cut = bits_of<TT>(tokens.reset, s0 + s);
-                    B = cut ? b[s] : fmaf(a[s], B, b[s]);
-                    A = cut ? 0.f : a[s] * A;
-                    closed |= cut;
-                }
+            for (int s = 0; s < SUBS; ++s) {
+                sm.A[s][tid] = A;
+                sm.B[s][tid] = B;
+                const bool cut = bits_of<TT>(tokens.reset, s);
+                B = cut ? b[s] : fmaf(a[s], B, b[s]);
+                A = cut ? 0.f : a[s] * A;
+                closed |= cut;
             }
             if (cluster > 1) {
-                for (int r = 0; r < cluster; ++r) store_cluster(in_cta(&sm.map[buf][rank][tid], r), A, B);
-                if (tid < cluster) store_cluster(in_cta(&sm.closed[buf][rank], tid), closed);
+                uint64_t *bar = &sm.maps[buf];
+                if (tid == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)cluster * SLAB * 16);
+                for (int r = 0; r < cluster; ++r)
+                    store_async(in_cta(&sm.map[buf][rank][tid], r), in_cta(bar, r), A, B, closed ? 1.f : 0.f);
+                wait_cluster(bar, n >> 1 & 1, p.status);
+                for (int r = 0; r < cluster; ++r) {
+                    const float4 m = sm.map[buf][r][tid];
+                    if (r == rank) sm.carry[tid] = run;
+                    run = m.z != 0.f ? m.y : fmaf(m.x, run, m.y);
+                }
             } else {
                 sm.carry[tid] = run;
                 run = closed ? B : fmaf(A, run, B);
             }
         }
-        if (more) {
-            fetch(t0 + step);
-            tokens_of(sm.tokens[buf ^ 1], p, t0 + step, slab == 0);
-        }
-        if (cluster > 1) {
-            cluster_sync();
-            if (tid < SLAB) {
-                for (int r = 0; r < cluster; ++r) {
-                    const float2 m = sm.map[buf][r][tid];
-                    if (r == rank) sm.carry[tid] = run;
-                    run = sm.closed[buf][r] ? m.y : fmaf(m.x, run, m.y);
-                }
-            }
-        }
+        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 + step, slab == 0);
         __syncthreads();
 
         // whether a reset stands before the half-warp's tokens in the tile
@@ -160,16 +191,23 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
         const int first = t0 + sub * TT;
         if (p.checkpoints && first % CHECK == 0 && first < p.T)
             store<float, VC>(p.checkpoints + (long long)(first / CHECK) * p.C + c0, front, inside, access.state);
+        F2 front2[PAIRS];
+#pragma unroll
+        for (int v = 0; v < PAIRS; ++v) front2[v] = F2(front[2 * v], front[2 * v + 1]);
         const unsigned valid = bits_of<TT>(tokens.valid, sub), lasts = bits_of<TT>(tokens.last, sub);
         T *y = static_cast<T *>(p.y) + (long long)first * p.C + c0;
 #pragma unroll
         for (int i = 0; i < TT; ++i, y += p.C) {
-            if (!(reset & ((2u << i) - 1)))
+            float out[VC];
+            const bool open = !(reset & ((2u << i) - 1));
 #pragma unroll
-                for (int v = 0; v < VC; ++v) h[i][v] = fmaf(P[i][v], front[v], h[i][v]);
-            if (valid >> i & 1) store<T, VC>(y, h[i], inside, access.y);
+            for (int v = 0; v < PAIRS; ++v) {
+                if (open) h[i][v] = fma2(P[i][v], front2[v], h[i][v]);
+                h[i][v].get(out[2 * v], out[2 * v + 1]);
+            }
+            if (valid >> i & 1) store<T, VC>(y, out, inside, access.y);
             if ((lasts >> i & 1) && p.final_state)
-                store<float, VC>(p.final_state + (long long)tokens.slot[sub * TT + i] * p.C + c0, h[i], inside, false);
+                store<float, VC>(p.final_state + (long long)tokens.slot[sub * TT + i] * p.C + c0, out, inside, false);
         }
     }
 

@@ -142,6 +142,78 @@ __device__ __forceinline__ Gate gate_of(float a, float b, float rate, float dt_b
     return r;
 }
 
+// ---------------------------------------------------------------- two channels at once
+
+// Two FP32 numbers in one register pair, for the instructions that take two at a time.
+struct F2 {
+    unsigned long long u;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ explicit F2(float x) : F2(x, x) {}
+    __device__ __forceinline__ void get(float &x, float &y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(u)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
+    return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
+    return d;
+}
+
+// gate_of's decays and input weights of two channels, with the same results; minus_rate: -log2(e) exp(A_log).
+template <int MODE>
+__device__ __forceinline__ void gate_pair(F2 a, F2 b, F2 minus_rate, F2 dt_bias, bool has_b, F2 &g, F2 &w) {
+    if constexpr (MODE == RECUR_PRECOMPUTED) {
+        g = a;
+        w = has_b ? b : F2(1.f);
+    } else {
+        float x, y;
+        add2(a, dt_bias).get(x, y);
+        const F2 e(exp2_approx(-LOG2E * fabsf(x)), exp2_approx(-LOG2E * fabsf(y)));
+        F2 q = fma2(e, F2(-0.00324376044f), F2(0.019850269f));
+        q = fma2(q, e, F2(-0.0569572933f));
+        q = fma2(q, e, F2(0.106034279f));
+        q = fma2(q, e, F2(-0.15305458f));
+        q = fma2(q, e, F2(0.196758926f));
+        q = fma2(q, e, F2(-0.249541253f));
+        q = fma2(q, e, F2(0.333299607f));
+        q = fma2(q, e, F2(-0.499999017f));
+        q = fma2(q, e, F2(1.f));
+        const F2 exponent = mul2(minus_rate, fma2(q, e, F2(fmaxf(x, 0.f), fmaxf(y, 0.f))));
+        exponent.get(x, y);
+        g = F2(exp2_approx(x), exp2_approx(y));
+        w = F2(1.f);
+        if (has_b) {
+            mul2(b, F2(-LOG2E)).get(x, y);
+            add2(F2(exp2_approx(x), exp2_approx(y)), F2(1.f)).get(x, y);
+            w = F2(rcp_approx(x), rcp_approx(y));
+        }
+        if constexpr (MODE == RECUR_RAW_UNIT) {
+            // 1 - g^2, as one_minus_square
+            const F2 t = mul2(exponent, F2(-0.69314718056f)), t2 = mul2(t, t);
+            F2 s = fma2(t2, F2(1.f / 362880.f), F2(1.f / 5040.f));
+            s = fma2(s, t2, F2(1.f / 120.f));
+            s = fma2(s, t2, F2(1.f / 6.f));
+            s = mul2(fma2(s, t2, F2(1.f)), mul2(t, add2(g, g)));
+            float g1, g2, t1, t2s, s1, s2;
+            g.get(g1, g2);
+            t.get(t1, t2s);
+            s.get(s1, s2);
+            s1 = t1 < 0.9f ? s1 : fmaf(-g1, g1, 1.f);
+            s2 = t2s < 0.9f ? s2 : fmaf(-g2, g2, 1.f);
+            w = mul2(w, F2(sqrt_approx(s1), sqrt_approx(s2)));
+        }
+    }
+}
+
 // The gradients of a and b (and their parameters) from those of g and w.
 struct GateGrad {
     float da, db, dA;  // dA: that of A_log; dt_bias has a's

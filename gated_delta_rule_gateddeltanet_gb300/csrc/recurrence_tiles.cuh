@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "layer_internal.cuh"
+#include "ptx.cuh"
 
 namespace gdn {
 namespace recur {
@@ -117,7 +118,7 @@ __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;
 template <typename E, int SLAB, int TILE, int NT, int BYTES>
 __device__ __forceinline__ void copy_tile(E *dst, const E *base, long long stride, int t0, int T, int c0, int C) {
     constexpr int N = BYTES / (int)sizeof(E), ROW = SLAB / N, ROWS = NT / ROW;
-    static_assert(NT % ROW == 0 && TILE % ROWS == 0, "");
+    static_assert(NT % ROW == 0 && TILE % ROWS == 0, "whole rows, the same number for every thread");
     const int r = threadIdx.x / ROW, c = threadIdx.x % ROW * N;
     const bool column = c0 + c < C;
     int left = T - t0 - r;
@@ -153,6 +154,21 @@ __device__ __forceinline__ void load_tile(E *dst, const void *base, long long st
     }
 }
 
+// The rows of such a tile as bulk copies that complete on `bar` (16-byte pieces only), rows tid, tid + threads ..; what
+// lies past T or C is left as it was.
+template <typename E, int SLAB, int TILE>
+__device__ __forceinline__ void bulk_tile(E *dst, const void *base, long long stride, int t0, int T, int c0, int C, int tid, int threads,
+                                          uint64_t *bar) {
+    const uint32_t bytes = (uint32_t)min(SLAB, C - c0) * (uint32_t)sizeof(E);
+    const E *src = static_cast<const E *>(base) + (long long)t0 * stride + c0;
+    const int rows = min(TILE, T - t0);
+    for (int r = tid; r < rows; r += threads) ptx::bulk_g2s(dst + r * SLAB, src + r * stride, bytes, bar);
+}
+template <typename E, int SLAB, int TILE>
+__device__ __forceinline__ uint32_t bulk_bytes(int t0, int T, int c0, int C) {
+    return (uint32_t)min(TILE, T - t0) * (uint32_t)min(SLAB, C - c0) * (uint32_t)sizeof(E);
+}
+
 // 16 or 4 if address and rows are whole multiples of it, else 2; for rows of C elements `stride` apart.
 inline int whole_bytes(const void *ptr, long long stride, long long C, size_t elem) {
     const unsigned long long all = reinterpret_cast<uintptr_t>(ptr) | (unsigned long long)stride * elem | (unsigned long long)C * elem;
@@ -184,6 +200,12 @@ __device__ __forceinline__ void read(const E *src, float (&f)[VC]) {
     else v.e[0] = *src;
 #pragma unroll
     for (int i = 0; i < VC; ++i) f[i] = to_f32(v.e[i]);
+}
+
+template <int VC>
+__device__ __forceinline__ void put_pack(float *dst, const Pack<float, VC> &v) {
+    if constexpr (VC == 4) *reinterpret_cast<uint4 *>(dst) = v.u4;
+    else *reinterpret_cast<uint2 *>(dst) = v.u2;
 }
 
 template <typename E, int VC>
@@ -246,11 +268,34 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, int rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ void store_cluster(uint32_t a, float x, float y) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+// 16 bytes to another CTA's shared memory, counted by the barrier there.
+__device__ __forceinline__ void store_async(uint32_t a, uint32_t bar, float x, float y, float z) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a), "f"(x), "f"(y),
+                 "f"(z), "f"(0.f), "r"(bar)
+                 : "memory");
 }
-__device__ __forceinline__ void store_cluster(uint32_t a, int x) {
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+
+// Waits for a phase of `bar`; after about a second without it the caller goes on and the status word says so.
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, int32_t *status) {
+    if (!ptx::mbar_wait_bounded(bar, parity, 2000000000ll)) flag_error(status, GDN_DEVERR_TIMEOUT);
+}
+
+// The same for a barrier that other CTAs' stores complete.
+__device__ __forceinline__ void wait_cluster(uint64_t *bar, uint32_t parity, int32_t *status) {
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(ptx::smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return;
+        if (clock64() - t0 > 2000000000ll) break;
+    }
+    flag_error(status, GDN_DEVERR_TIMEOUT);
 }
 
 // A cluster's launch as a programmatic dependent (launch_dependent with clusters).
