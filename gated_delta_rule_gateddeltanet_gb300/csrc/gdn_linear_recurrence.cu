@@ -16,6 +16,9 @@ struct Access {
     int x, a, b;   // bytes of a copy
     bool y, state;  // VC elements at once
 };
+struct Maps {
+    CUtensorMap x, a, b;  // of what is copied 16 bytes at a time
+};
 
 template <typename T, int MODE>
 struct Shape {
@@ -33,7 +36,8 @@ struct Shape {
 };
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParams p, const Access access, int cluster) {
+__global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParams p, const Access access,
+                                                           const __grid_constant__ Maps maps, int cluster) {
     dependent_prologue();
     using S = Shape<T, MODE>;
     using G = typename S::G;
@@ -66,20 +70,13 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
 
     const bool bulk = access.x == 16 || access.a == 16 || (has_b && access.b == 16);
     auto fetch = [&](int t0) {
-        if (bulk && t0 < p.T) {
-            if (tid == 0) {
-                uint32_t bytes = access.x == 16 ? bulk_bytes<T, SLAB, TILE>(t0, p.T, s0, p.C) : 0;
-                if (access.a == 16) bytes += bulk_bytes<G, SLAB, TILE>(t0, p.T, s0, p.C);
-                if (has_b && access.b == 16) bytes += bulk_bytes<G, SLAB, TILE>(t0, p.T, s0, p.C);
-                ptx::mbar_arrive_expect_tx(&sm.full, bytes);
-            }
-            // the first half of the threads x, then b, the second a
-            if (tid < NT / 2) {
-                if (access.x == 16) bulk_tile<T, SLAB, TILE>(sm.x, p.x, p.x_stride, t0, p.T, s0, p.C, tid, NT / 2, &sm.full);
-                if (has_b && access.b == 16) bulk_tile<G, SLAB, TILE>(sm.b, p.b, p.b_stride, t0, p.T, s0, p.C, tid, NT / 2, &sm.full);
-            } else if (access.a == 16) {
-                bulk_tile<G, SLAB, TILE>(sm.a, p.a, p.a_stride, t0, p.T, s0, p.C, tid - NT / 2, NT / 2, &sm.full);
-            }
+        if (bulk && tid == 0 && t0 < p.T) {
+            constexpr uint32_t XB = sizeof(T) * TILE * SLAB, GB = sizeof(G) * TILE * SLAB;
+            ptx::mbar_arrive_expect_tx(&sm.full, (access.x == 16 ? XB : 0) + (access.a == 16 ? GB : 0) +
+                                                     (has_b && access.b == 16 ? GB : 0));
+            if (access.x == 16) ptx::tma_load_2d(sm.x, &maps.x, s0, t0, &sm.full);
+            if (access.a == 16) ptx::tma_load_2d(sm.a, &maps.a, s0, t0, &sm.full);
+            if (has_b && access.b == 16) ptx::tma_load_2d(sm.b, &maps.b, s0, t0, &sm.full);
         }
         if (access.x != 16) load_tile<T, SLAB, TILE, NT>(sm.x, p.x, p.x_stride, t0, p.T, s0, p.C, access.x);
         if (access.a != 16) load_tile<G, SLAB, TILE, NT>(sm.a, p.a, p.a_stride, t0, p.T, s0, p.C, access.a);
@@ -88,7 +85,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
 
     const int step = cluster * TILE, rounds = (p.T + step - 1) / step;
     fetch(rank * TILE);
-    tokens_of(sm.tokens[0], p, rank * TILE, slab == 0);
+    tokens_of(sm.tokens[0], p, rank * TILE, slab == 0, tid - (NT - TILE));
     if (blockIdx.x == 0) check_packing(p);
     if (cluster > 1) cluster_sync();  // every CTA has its barriers before another writes to its shared memory
     float run = 0.f;  // the state in front of the cluster's tiles, channel tid of the slab
@@ -175,7 +172,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
                 run = closed ? B : fmaf(A, run, B);
             }
         }
-        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 + step, slab == 0);
+        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 + step, slab == 0, tid - (NT - TILE));  // (not by the threads above)
         __syncthreads();
 
         // whether a reset stands before the half-warp's tokens in the tile
@@ -308,6 +305,10 @@ cudaError_t launch_typed(const RecurrenceParams &p, int longest, cudaStream_t st
     access.x = whole_bytes(p.x, p.x_stride, p.C, sizeof(T));
     access.a = whole_bytes(p.a, p.a_stride, p.C, sizeof(G));
     access.b = whole_bytes(p.b, p.b_stride, p.C, sizeof(G));
+    Maps maps{};
+    if (access.x == 16 && !tile_map<T, S::SLAB, TILE>(&maps.x, p.x, p.x_stride, p.T, p.C)) access.x = 4;
+    if (access.a == 16 && !tile_map<G, S::SLAB, TILE>(&maps.a, p.a, p.a_stride, p.T, p.C)) access.a = 4;
+    if (p.b && access.b == 16 && !tile_map<G, S::SLAB, TILE>(&maps.b, p.b, p.b_stride, p.T, p.C)) access.b = 4;
     access.y = whole_rows(p.y, p.C, sizeof(T), S::VC * sizeof(T));
     access.state = whole_rows(p.init, p.C, 4, S::VC * 4) && whole_rows(p.final_state, p.C, 4, S::VC * 4) &&
                    whole_rows(p.checkpoints, p.C, 4, S::VC * 4);
@@ -318,7 +319,7 @@ cudaError_t launch_typed(const RecurrenceParams &p, int longest, cudaStream_t st
     if (e != cudaSuccess) return e;
     const long long slabs = ((long long)p.C + S::SLAB - 1) / S::SLAB, tiles = ((long long)p.T + TILE - 1) / TILE;
     const int size = cluster_size(*resident, slabs, tiles);
-    return launch_clusters(kernel, (unsigned)slabs, (unsigned)size, NT, smem, stream, p, access, size);
+    return launch_clusters(kernel, (unsigned)slabs, (unsigned)size, NT, smem, stream, p, access, maps, size);
 }
 
 template <typename T>

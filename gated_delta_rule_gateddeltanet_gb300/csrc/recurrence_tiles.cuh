@@ -70,11 +70,10 @@ struct Tokens {
     int slot[TILE];
 };
 
-// Fills them for the tile at t0 (whole warps of the first TILE threads).
+// Fills them for the tile at t0 (whole warps of TILE threads i).
 template <int TILE>
-__device__ __forceinline__ void tokens_of(Tokens<TILE> &k, const RecurrenceParams &p, int t0, bool flag) {
-    const int i = threadIdx.x;
-    if (i >= TILE) return;
+__device__ __forceinline__ void tokens_of(Tokens<TILE> &k, const RecurrenceParams &p, int t0, bool flag, int i) {
+    if (i < 0 || i >= TILE) return;
     int slot;
     const int what = token_of(p, t0 + i, flag, slot);
     k.slot[i] = slot;
@@ -154,19 +153,11 @@ __device__ __forceinline__ void load_tile(E *dst, const void *base, long long st
     }
 }
 
-// The rows of such a tile as bulk copies that complete on `bar` (16-byte pieces only), rows tid, tid + threads ..; what
-// lies past T or C is left as it was.
+// Tensor map of such rows for boxes of a tile; false if the driver does not take it.
 template <typename E, int SLAB, int TILE>
-__device__ __forceinline__ void bulk_tile(E *dst, const void *base, long long stride, int t0, int T, int c0, int C, int tid, int threads,
-                                          uint64_t *bar) {
-    const uint32_t bytes = (uint32_t)min(SLAB, C - c0) * (uint32_t)sizeof(E);
-    const E *src = static_cast<const E *>(base) + (long long)t0 * stride + c0;
-    const int rows = min(TILE, T - t0);
-    for (int r = tid; r < rows; r += threads) ptx::bulk_g2s(dst + r * SLAB, src + r * stride, bytes, bar);
-}
-template <typename E, int SLAB, int TILE>
-__device__ __forceinline__ uint32_t bulk_bytes(int t0, int T, int c0, int C) {
-    return (uint32_t)min(TILE, T - t0) * (uint32_t)min(SLAB, C - c0) * (uint32_t)sizeof(E);
+bool tile_map(CUtensorMap *map, const void *base, long long stride, int T, long long C) {
+    if constexpr (sizeof(E) == 2) return encode_rows_f16(map, base, C, stride, T, SLAB, TILE, false);
+    else return encode_rows_f32_strided(map, static_cast<const float *>(base), C, stride, T, SLAB, TILE);
 }
 
 // 16 or 4 if address and rows are whole multiples of it, else 2; for rows of C elements `stride` apart.
