@@ -113,14 +113,6 @@ gdn_status gdn_linear_recurrence(const gdn_linear_recurrence_args *a, gdn_stream
     return of(gdn::launch_recurrence(p, a->io_dtype, mode, longest(a), s));
 }
 
-gdn_status gdn_linear_recurrence_backward_workspace_size(const gdn_linear_recurrence_backward_args *a, size_t *bytes) {
-    if (!bytes) return GDN_ERR_NULL;
-    const gdn_status st = check_recurrence_sizes(a);
-    if (st != GDN_OK) return st;
-    *bytes = gdn::recurrence_backward_workspace_bytes(a->num_seqs, a->total_tokens, a->channels);
-    return GDN_OK;
-}
-
 gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_args *a, gdn_stream_t stream) {
     gdn_status st = check_recurrence_sizes(a);
     if (st != GDN_OK) return st;
@@ -138,8 +130,7 @@ gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_a
         !aligned(a->checkpoints, 4) || !aligned(a->d_final_state, 4) || !aligned(a->d_initial_state, 4) ||
         !aligned(a->dA_log, 4) || !aligned(a->ddt_bias, 4))
         return GDN_ERR_ALIGN;
-    const size_t needs = gdn::recurrence_backward_workspace_bytes(a->num_seqs, a->total_tokens, a->channels);
-    if ((st = check_workspace(a->workspace, a->workspace_bytes, needs)) != GDN_OK) return st;
+    if (a->d_initial_state && a->d_initial_state == a->d_final_state) return GDN_ERR_ARG;
     p.dy = a->dy;
     p.states = a->checkpoints;
     p.dfinal = a->d_final_state;
@@ -149,7 +140,6 @@ gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_a
     p.dA_log = a->dA_log;
     p.ddt_bias = a->ddt_bias;
     p.dinit = a->d_initial_state;
-    p.workspace = a->workspace;
     cudaStream_t s = cuda_stream(stream);
 #ifdef GDN_DEBUG_CHECKS
     if (p.dinit && gdn::debug_check_distinct_slots(p.slots, nullptr, p.B, p.num_slots, p.status, s) != cudaSuccess)

@@ -30,10 +30,8 @@ struct RecurrenceParams {
     const float *dfinal;
     void *dx, *da, *db;
     float *dA_log, *ddt_bias, *dinit;
-    void *workspace;
 };
 
-size_t recurrence_backward_workspace_bytes(int B, int T, int C);
 // longest: an upper bound on the longest sequence (a hint)
 cudaError_t launch_recurrence(const RecurrenceParams &p, int io_dtype, int mode, int longest, cudaStream_t stream);
 cudaError_t launch_recurrence_backward(const RecurrenceParams &p, int io_dtype, int mode, cudaStream_t stream);

@@ -42,7 +42,7 @@ __device__ __forceinline__ int last_start(const int32_t *cu, int hi, int t) {
 // What token t is, and its sequence's slot.
 __device__ __forceinline__ int token_of(const RecurrenceParams &p, int t, bool flag, int &slot) {
     slot = 0;
-    if (t >= p.T) return RESET;
+    if (t >= p.T || p.B == 0) return RESET;
     int b, begin, end;
     if (p.cu) {
         b = last_start(p.cu, p.B - 1, t);
@@ -258,6 +258,9 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, int rank) {
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
     return a;
+}
+__device__ __forceinline__ void store_cluster(uint32_t a, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
 }
 // 16 bytes to another CTA's shared memory, counted by the barrier there.
 __device__ __forceinline__ void store_async(uint32_t a, uint32_t bar, float x, float y, float z) {

@@ -9,9 +9,8 @@ import ctypes
 
 import torch
 
-from . import _check, _ptr, _shape, _token_stride
+from . import GdnError, _check, _ptr, _shape, _token_stride, load_library
 from .attention import _Call, _heads_out, _io
-from .recurrence import _workspace
 
 OUT_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3, torch.int8: 4}
 
@@ -69,6 +68,14 @@ def _geometry(args, x, weight, eps, weight_offset):
     _shape(weight, "weight", (x.shape[2],))
     args.weight = _ptr(weight)
     args.x_stride, args.x = _like(x, "x", x), _ptr(x)
+
+
+def _workspace_size(args):
+    n = ctypes.c_size_t(0)
+    rc = load_library().gdn_rms_norm_backward_workspace_size(ctypes.byref(args), ctypes.byref(n))
+    if rc != 0:
+        raise GdnError(rc, "gdn_rms_norm_backward_workspace_size")
+    return int(n.value)
 
 
 class RMSNormCall(_Call):
@@ -163,7 +170,10 @@ class RMSNormBackwardCall(_Call):
             _check(dweight, "dweight", dtype=torch.float32, device=dev)
             _shape(dweight, "dweight", weight.shape)
             a.dweight = _ptr(dweight)
-            workspace = _workspace(a, workspace, "gdn_rms_norm_backward", dev)
+            if workspace is None:
+                workspace = torch.empty(_workspace_size(a), dtype=torch.uint8, device=dev)
+            _check(workspace, "workspace", device=dev)
+            a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
         elif dweight is not None:
             raise ValueError("dweight without weight")
         a.dx, a.dgate = _ptr(dx), _ptr(dgate)

@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from . import GATE_MODE, GdnError, _check, _ptr, _row_stride, _shape, load_library
+from . import GATE_MODE, _check, _ptr, _row_stride, _shape
 from .attention import _Call, _cu_seqlens, _int32, _io, _status
 
 CHECKPOINT = 64  # GDN_RECURRENCE_CHECKPOINT
@@ -37,8 +37,7 @@ class LinearRecurrenceBackwardArgs(ctypes.Structure):
                 ("x_stride", _i64), ("a_stride", _i64), ("b_stride", _i64), ("dy_stride", _i64),
                 ("x", _p), ("a", _p), ("b", _p), ("dy", _p), ("A_log", _p), ("dt_bias", _p), ("cu_seqlens", _p),
                 ("state_slots", _p), ("initial_state", _p), ("checkpoints", _p), ("d_final_state", _p), ("dx", _p),
-                ("da", _p), ("db", _p), ("dA_log", _p), ("ddt_bias", _p), ("d_initial_state", _p), ("status", _p),
-                ("workspace", _p), ("workspace_bytes", ctypes.c_size_t)]
+                ("da", _p), ("db", _p), ("dA_log", _p), ("ddt_bias", _p), ("d_initial_state", _p), ("status", _p)]
 
 
 ENTRY_POINTS = {"gdn_linear_recurrence": LinearRecurrenceArgs,
@@ -50,8 +49,6 @@ def declare(lib):
     for name, args in ENTRY_POINTS.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = _i32, [ctypes.POINTER(args), _p]
-    f = lib.gdn_linear_recurrence_backward_workspace_size
-    f.restype, f.argtypes = _i32, [ctypes.POINTER(LinearRecurrenceBackwardArgs), ctypes.POINTER(ctypes.c_size_t)]
 
 
 def _tokens(t, name, shape, dtype, device):
@@ -119,21 +116,6 @@ def _inputs(args, x, a, b, cu_seqlens, A_log, dt_bias, gate_mode, unit_input, in
     return T, C, B, slots, gate_dtype
 
 
-def _workspace(args, workspace, name, device):
-    """The call's workspace: the one given, or one of the size that the library asks for."""
-    if workspace is None:
-        n = ctypes.c_size_t(0)
-        rc = getattr(load_library(), name + "_workspace_size")(ctypes.byref(args), ctypes.byref(n))
-        if rc != 0:
-            raise GdnError(rc, name + "_workspace_size")
-        if n.value:
-            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=device)
-    if workspace is not None:
-        _check(workspace, "workspace", device=device)
-        args.workspace, args.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    return workspace
-
-
 def _checkpoint_shape(T, C):
     return (T + CHECKPOINT - 1) // CHECKPOINT, C
 
@@ -191,7 +173,7 @@ class LinearRecurrenceBackwardCall(_Call):
     def __init__(self, dy, x, a, b, checkpoints, cu_seqlens=None, *, A_log=None, dt_bias=None, gate_mode="raw",
                  unit_input=False, initial_state=None, state_slots=None, num_seqs=None, num_state_slots=None,
                  d_final_state=None, dx=None, da=None, db=None, d_initial_state=None, dA_log=None, ddt_bias=None,
-                 max_seqlen=0, workspace=None, status=None):
+                 max_seqlen=0, status=None):
         args, dev = LinearRecurrenceBackwardArgs(), x.device
         T, C, B, slots, gate_dtype = _inputs(args, x, a, b, cu_seqlens, A_log, dt_bias, gate_mode, unit_input,
                                              initial_state, state_slots, num_seqs, num_state_slots, status,
@@ -218,10 +200,9 @@ class LinearRecurrenceBackwardCall(_Call):
         args.dy, args.checkpoints, args.d_final_state = _ptr(dy), _ptr(checkpoints), _ptr(d_final_state)
         args.dx, args.da, args.db, args.d_initial_state = _ptr(dx), _ptr(da), _ptr(db), _ptr(d_initial_state)
         args.dA_log, args.ddt_bias = _ptr(dA_log), _ptr(ddt_bias)
-        workspace = _workspace(args, workspace, "gdn_linear_recurrence_backward", dev)
         self._resolve("gdn_linear_recurrence_backward", args, outputs,
                       (dy, x, a, b, checkpoints, cu_seqlens, A_log, dt_bias, initial_state, state_slots, d_final_state,
-                       workspace, status), dev)
+                       status), dev)
 
 
 def linear_recurrence_backward(dy, x, a, b, checkpoints, cu_seqlens=None, **kw):

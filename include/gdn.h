@@ -792,9 +792,8 @@ gdn_status gdn_linear_recurrence(const gdn_linear_recurrence_args *args, gdn_str
  *   dx            device [T, C] io_dtype;  da, db  device [T, C] in a's and b's type (db goes
  *                 with b); all contiguous
  *   dA_log, ddt_bias device [C] FP32 or NULL (RAW only): summed over all tokens
- *   d_initial_state device [num_state_slots, C] FP32 or NULL; only the batch's slots are
- *                 written; may equal d_final_state
- * Outputs must not overlap inputs otherwise.  Where unit_input meets a decay that rounds to 1
+ *   d_initial_state device [num_state_slots, C] FP32 or NULL; only the batch's slots are written
+ * Outputs must not overlap inputs (also d_initial_state not d_final_state).  Where unit_input meets a decay that rounds to 1
  * (its factor is 0), that factor's part of da is 0, its limit.
  */
 typedef struct gdn_linear_recurrence_backward_args {
@@ -808,13 +807,7 @@ typedef struct gdn_linear_recurrence_backward_args {
     void *dx, *da, *db;
     float *dA_log, *ddt_bias, *d_initial_state;
     int32_t *status;
-    void *workspace;
-    size_t workspace_bytes;
 } gdn_linear_recurrence_backward_args;
-
-/* Bytes of workspace for these sizes (pointers are not read). */
-gdn_status gdn_linear_recurrence_backward_workspace_size(const gdn_linear_recurrence_backward_args *args,
-                                                         size_t *bytes);
 
 gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_args *args, gdn_stream_t stream);
 
@@ -884,6 +877,7 @@ typedef struct gdn_rms_norm_backward_args {
     size_t workspace_bytes;
 } gdn_rms_norm_backward_args;
 
+/* Bytes of workspace for these sizes (pointers are not read). */
 gdn_status gdn_rms_norm_backward_workspace_size(const gdn_rms_norm_backward_args *args, size_t *bytes);
 
 gdn_status gdn_rms_norm_backward(const gdn_rms_norm_backward_args *args, gdn_stream_t stream);

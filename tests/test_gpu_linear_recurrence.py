@@ -106,12 +106,11 @@ def test_states_in_place(lens, hint):
     idle = torch.ones(r.num_slots, dtype=torch.bool)
     idle[r.slots.cpu().long()] = False
     assert torch.equal(pool[idle.to(dev())], r.initial[idle.to(dev())])
-    outs = r.backward(chk)
-    grads = r.d_final.clone()
-    r2 = r.backward(chk, d_final_state=grads, d_initial_state=grads)
-    rows = r.slots.long()
-    assert torch.equal(outs[3][rows], grads[rows]) and torch.equal(outs[1], r2[1])
-    assert torch.equal(grads[idle.to(dev())], r.d_final[idle.to(dev())])
+    mark = torch.full_like(r.initial, 7.0)
+    r.backward(chk, d_initial_state=mark)
+    assert torch.all(mark[idle.to(dev())] == 7) and not torch.any(mark[r.slots.long()] == 7)
+    with pytest.raises(gdn.GdnError):  # (its rows are read while others are written)
+        r.backward(chk, d_final_state=mark, d_initial_state=mark)
 
 
 @pytest.mark.parametrize("decay", [0.0, 1.0, -0.5, 2.0 ** -140])
