@@ -10,6 +10,7 @@ using namespace recur;
 
 constexpr int NT = 256, SUBS = NT / LANES;
 constexpr int TT = 8, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA
+constexpr int COPIER = 96;  // a thread that has nothing else to do between the two halves of a round
 
 // What the host found to be aligned.
 struct Access {
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
 
     const bool bulk = access.x == 16 || access.a == 16 || (has_b && access.b == 16);
     auto fetch = [&](int t0) {
-        if (bulk && tid == 0 && t0 < p.T) {
+        if (bulk && tid == COPIER && t0 < p.T) {
             constexpr uint32_t XB = sizeof(T) * TILE * SLAB, GB = sizeof(G) * TILE * SLAB;
             ptx::mbar_arrive_expect_tx(&sm.full, (access.x == 16 ? XB : 0) + (access.a == 16 ? GB : 0) +
                                                      (has_b && access.b == 16 ? GB : 0));
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(SHORT_NT) recurrence_short_kernel(const Recurr
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
                 const Gate q = gate_of<MODE>(a[i][v], bv[i][v], rate[v], dt[v], p.b != nullptr);
-                h[v] = fmaf(q.g, h[v], q.w * x[i][v]);
+                h[v] = fmaf(q.g, h[v], q.w() * x[i][v]);
             }
             store<T, VC>(static_cast<T *>(p.y) + t * p.C + c, h, VC, true);
         }

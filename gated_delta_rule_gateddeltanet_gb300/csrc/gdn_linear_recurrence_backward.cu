@@ -9,6 +9,7 @@ using namespace recur;
 
 constexpr int NT = 256, SUBS = NT / LANES;
 constexpr int TT = 4, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA
+constexpr int COPIER = 160;  // a thread that has nothing else to do between the two halves of a round
 static_assert(TILE == CHECK, "a tile begins at a checkpoint");
 
 struct Access {
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
     const bool bulk = access.x == 16 || access.dy == 16 || access.a == 16 || (has_b && access.b == 16);
     auto fetch = [&](int t0, int buf) {
         typename S::Tile &tile = sm.tile[buf];
-        if (bulk && tid == 0 && t0 < p.T) {
+        if (bulk && tid == COPIER && t0 < p.T) {
             constexpr uint32_t XB = sizeof(T) * TILE * SLAB, GB = sizeof(G) * TILE * SLAB;
             uint64_t *bar = &sm.full[buf];
             ptx::mbar_arrive_expect_tx(bar, (access.x == 16 ? XB : 0) + (access.dy == 16 ? XB : 0) + (access.a == 16 ? GB : 0) +
@@ -111,42 +112,34 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         copies_done();
         __syncthreads();
         const bool more = n + 1 < rounds;
-        if (more) fetch(t0 - step, buf ^ 1);
-
         const unsigned reset = bits_of<TT>(tokens.reset, sub), loads = bits_of<TT>(tokens.load, sub);
         const unsigned valid = bits_of<TT>(tokens.valid, sub), lasts = bits_of<TT>(tokens.last, sub);
         // Backwards a sequence's last token cuts off what stands behind it, and so does one of no sequence.
         const unsigned cuts = lasts | (~valid & ((1u << TT) - 1));
-        auto gate = [&](int i, float (&x)[VC], Gate (&q)[VC]) {
-            const int at = (sub * TT + i) * SLAB + lane * VC;
-            float a[VC], b[VC] = {};
-            read<T, VC>(tile.x + at, x);
-            read<G, VC>(tile.a + at, a);
-            if (has_b) read<G, VC>(tile.b + at, b);
-#pragma unroll
-            for (int v = 0; v < VC; ++v) q[v] = gate_of<MODE>(a[v], b[v], rate[v], dt[v], has_b);
-        };
+        const int place = sub * TT * SLAB + lane * VC;
         auto row = [&](int i) { return (long long)tokens.slot[sub * TT + i] * p.C + c0; };
 
-        float g[TT][VC], u[TT][VC];
+        Gate q[TT][VC];
         {
             Pack<float, VC> A, B;  // forwards
 #pragma unroll
             for (int v = 0; v < VC; ++v) A.e[v] = 1.f, B.e[v] = 0.f;
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
-                float x[VC], front[VC];
-                Gate q[VC];
-                gate(i, x, q);
+                float x[VC], a[VC], b[VC] = {}, front[VC];
+                read<T, VC>(tile.x + place + i * SLAB, x);
+                read<G, VC>(tile.a + place + i * SLAB, a);
+                if (has_b) read<G, VC>(tile.b + place + i * SLAB, b);
 #pragma unroll
-                for (int v = 0; v < VC; ++v) front[v] = reset >> i & 1 ? 0.f : B.e[v];
+                for (int v = 0; v < VC; ++v) {
+                    q[i][v] = gate_of<MODE>(a[v], b[v], rate[v], dt[v], has_b);
+                    front[v] = reset >> i & 1 ? 0.f : B.e[v];
+                }
                 if ((loads >> i & 1) && p.init) load<VC>(p.init + row(i), front, inside, false);
 #pragma unroll
                 for (int v = 0; v < VC; ++v) {
-                    g[i][v] = q[v].g;
-                    u[i][v] = q[v].w * x[v];
-                    B.e[v] = fmaf(g[i][v], front[v], u[i][v]);
-                    A.e[v] *= g[i][v];
+                    B.e[v] = fmaf(q[i][v].g, front[v], q[i][v].w() * x[v]);
+                    A.e[v] *= q[i][v].g;
                 }
             }
             put_pack(&sm.FA[sub][lane * VC], A);
@@ -156,7 +149,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
 #pragma unroll
             for (int i = TT - 1; i >= 0; --i) {
                 float dy[VC];
-                read<T, VC>(tile.dy + (sub * TT + i) * SLAB + lane * VC, dy);
+                read<T, VC>(tile.dy + place + i * SLAB, dy);
                 if (cuts >> i & 1) {
 #pragma unroll
                     for (int v = 0; v < VC; ++v) B.e[v] = 0.f;
@@ -168,13 +161,14 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
                     }
                 }
 #pragma unroll
-                for (int v = 0; v < VC; ++v) B.e[v] = valid >> i & 1 ? g[i][v] * (dy[v] + B.e[v]) : 0.f;
+                for (int v = 0; v < VC; ++v) B.e[v] = valid >> i & 1 ? q[i][v].g * (dy[v] + B.e[v]) : 0.f;
             }
             put_pack(&sm.RA[sub][lane * VC], A);
             put_pack(&sm.RB[sub][lane * VC], B);
         }
         __syncthreads();
 
+        if (more) fetch(t0 - step, buf ^ 1);
         if (tid < SLAB) {
             // the map backwards of the tile, and on the way that of what stands behind each half-warp's tokens
             float A = 1.f, B = 0.f, a[SUBS], b[SUBS];
@@ -226,6 +220,8 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
             read<float, VC>(&sm.FB[sub][lane * VC], h);
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
+                float x[VC];
+                read<T, VC>(tile.x + place + i * SLAB, x);
                 if (reset >> i & 1) {
 #pragma unroll
                     for (int v = 0; v < VC; ++v) h[v] = 0.f;
@@ -234,7 +230,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
 #pragma unroll
                 for (int v = 0; v < VC; ++v) {
                     before[i][v] = h[v];
-                    h[v] = fmaf(g[i][v], h[v], u[i][v]);
+                    h[v] = fmaf(q[i][v].g, h[v], q[i][v].w() * x[v]);
                 }
             }
         }
@@ -258,10 +254,10 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         long long at = (long long)(t0 + sub * TT + TT - 1) * p.C + c0;
 #pragma unroll
         for (int i = TT - 1; i >= 0; --i, at -= p.C) {
-            float x[VC], dy[VC], dx[VC], da[VC], db[VC];
-            Gate q[VC];
-            gate(i, x, q);
-            read<T, VC>(tile.dy + (sub * TT + i) * SLAB + lane * VC, dy);
+            float x[VC], a[VC], dy[VC], dx[VC], da[VC], db[VC];
+            read<T, VC>(tile.x + place + i * SLAB, x);
+            read<G, VC>(tile.a + place + i * SLAB, a);
+            read<T, VC>(tile.dy + place + i * SLAB, dy);
             if (cuts >> i & 1) {
 #pragma unroll
                 for (int v = 0; v < VC; ++v) m[v] = 0.f;
@@ -271,13 +267,13 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
                 const float l = m[v] + dy[v];
-                const GateGrad d = gate_grad<MODE>(q[v], l * before[i][v], l * x[v], rate[v]);
-                dx[v] = l * q[v].w;
+                const GateGrad d = gate_grad<MODE>(q[i][v], a[v], l * before[i][v], l * x[v], rate[v], dt[v]);
+                dx[v] = l * q[i][v].w();
                 da[v] = d.da;
                 db[v] = d.db;
                 sum_A[v] += d.dA;
                 sum_dt[v] += d.da;
-                m[v] = q[v].g * l;
+                m[v] = q[i][v].g * l;
             }
             store<T, VC>(static_cast<T *>(p.dx) + at, dx, inside, access.dx);
             store<G, VC>(static_cast<G *>(p.da) + at, da, inside, access.da);

@@ -69,9 +69,9 @@ struct GateType<T, RECUR_PRECOMPUTED> {
 
 // What the gates of one (token, channel) come to.
 struct Gate {
-    float g, w;           // decay, input weight
-    float lg, sig_a;      // log g; sigmoid(a + dt_bias)
+    float g, lg;          // decay and its logarithm
     float sig_b, factor;  // sigmoid(b); sqrt(1 - g^2) (1 without unit_input)
+    __device__ __forceinline__ float w() const { return sig_b * factor; }  // the input's weight
 };
 
 // The gates' arithmetic is that of FP32 to a few units in the last place, in the fewest instructions: the
@@ -124,18 +124,17 @@ __device__ __forceinline__ Gate gate_of(float a, float b, float rate, float dt_b
     Gate r;
     if constexpr (MODE == RECUR_PRECOMPUTED) {
         r.g = a;
-        r.w = has_b ? b : 1.f;
-        r.lg = r.sig_a = r.sig_b = r.factor = 0.f;
+        r.sig_b = has_b ? b : 1.f;
+        r.lg = 0.f;
+        r.factor = 1.f;
     } else {
         const float v = a + dt_bias;
         const float e = exp2_approx(-LOG2E * fabsf(v));
         const float t = rate * fmaf(log1p_over(e), e, fmaxf(v, 0.f));
         r.lg = -t;
         r.g = exp2_approx(-LOG2E * t);
-        r.sig_a = (v >= 0.f ? 1.f : e) * rcp_approx(1.f + e);
         r.sig_b = has_b ? rcp_approx(1.f + exp2_approx(-LOG2E * b)) : 1.f;
         r.factor = MODE == RECUR_RAW_UNIT ? sqrt_approx(one_minus_square(r.g, t)) : 1.f;
-        r.w = r.sig_b * r.factor;
     }
     return r;
 }
@@ -218,18 +217,24 @@ struct GateGrad {
 };
 
 template <int MODE>
-__device__ __forceinline__ GateGrad gate_grad(const Gate &r, float dg, float dw, float rate) {
+__device__ __forceinline__ GateGrad gate_grad(const Gate &r, float a, float dg, float dw, float rate, float dt_bias) {
     GateGrad o;
     if constexpr (MODE == RECUR_PRECOMPUTED) {
         o.da = dg;
         o.db = dw;
         o.dA = 0.f;
     } else {
+        const float v = a + dt_bias, e = exp2_approx(-LOG2E * fabsf(v));
+        const float sig_a = (v >= 0.f ? 1.f : e) * rcp_approx(1.f + e);
         float dlg = dg * r.g;
-        if (MODE == RECUR_RAW_UNIT && r.factor > 0.f) dlg -= dw * r.sig_b * (r.g * r.g / r.factor);
-        o.da = -dlg * rate * r.sig_a;
+        const float di = dw * r.sig_b;
+        if constexpr (MODE == RECUR_RAW_UNIT) {
+            const float k = r.g * r.g * rcp_approx(r.factor);
+            dlg -= r.factor > 0.f ? di * k : 0.f;
+        }
+        o.da = -dlg * (rate * sig_a);
         o.dA = dlg * r.lg;
-        o.db = dw * r.factor * (r.sig_b * (1.f - r.sig_b));
+        o.db = di * r.factor * (1.f - r.sig_b);
     }
     return o;
 }
