@@ -1,11 +1,17 @@
 // Root-mean-square norm of rows, with the residual's addition before it, a gate after
 // it and an output in 8 bits; forward and backward.
+//
+//   s = x (+ r),  y = s / sqrt(mean s^2 + eps) * (w + offset) * silu(z)
+//
+// Both directions are HBM streams: a row is read once into registers, 8 channels a
+// thread and piece, and everything about it is worked out there.  What a row needs of
+// other threads is one sum (two backwards) and, for 8 bits, a maximum.  A CTA takes
+// a token at a time (whole-token norms and scales), or tokens are cut into runs of
+// pieces of heads whose sums are shuffles inside a warp.
 #include "layer_internal.cuh"
 
 namespace gdn {
 namespace {
-
-constexpr int NT = 128;
 
 __device__ __forceinline__ float max_or_nan(float a, float b) {
     float y;
@@ -13,49 +19,295 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     return y;
 }
 
-__device__ __forceinline__ float cta_sum(float v, float *buf) {
-    v = warp_sum(v);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) s += buf[i];
-    return s;
-}
-
-__device__ __forceinline__ float cta_max(float v, float *buf) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = max_or_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) s = max_or_nan(s, buf[i]);
-    return s;
-}
-
-__device__ __forceinline__ float silu(float z) { return z / (1.f + expf(-z)); }
-
 // The scale of 8-bit values whose largest magnitude is top.
 __device__ __forceinline__ float scale_of(float top, float most) {
     if (!(top <= 3.402823466e38f)) return __int_as_float(0x7fc00000);
     return top == 0.f ? 1.f : __fdiv_rn(top, most);
 }
 
-__device__ __forceinline__ uint8_t to_e4m3(float q) {
-    uint16_t v;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(0.f), "f"(q));
-    return (uint8_t)v;
-}
-__device__ __forceinline__ int8_t to_int8(float q) { return (int8_t)min(127, max(-127, __float2int_rn(q))); }
+// z sigmoid(z), and its derivative
+__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + exp2_approx(-LOG2E * z)); }
+__device__ __forceinline__ float silu(float z) { return z > -80.f ? z * sigmoid(z) : z * expf(z); }
 
-// A CTA a token; any sizes, alignment and types.  Rows are read again for every step.
+constexpr int V = 8;  // channels of a piece
+
+// A piece as it is loaded, so that all of a thread's loads can be on their way before the first is used.
 template <typename T>
-__global__ void __launch_bounds__(NT) norm_any_kernel(const RmsNormParams p, int out_dtype) {
+struct Piece {
+    static constexpr int N = Vec16<T>::N;
+    Vec16<T> v[V / N];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int k = 0; k < V / N; ++k) v[k].load(p + k * N);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int k = 0; k < V / N; ++k) v[k].u = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void to(float (&f)[V]) const {
+#pragma unroll
+        for (int k = 0; k < V / N; ++k) {
+            float g[N];
+            v[k].to(g);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[k * N + i] = g[i];
+        }
+    }
+};
+template <typename T>
+__device__ __forceinline__ void read8(const T *p, float (&f)[V]) {
+    Piece<T> v;
+    v.load(p);
+    v.to(f);
+}
+template <typename T>
+__device__ __forceinline__ void write8(T *p, const float (&f)[V]) {
+    constexpr int N = Vec16<T>::N;
+#pragma unroll
+    for (int k = 0; k < V / N; ++k) {
+        Vec16<T> v;
+        float g[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = f[k * N + i];
+        v.from(g);
+        v.store(p + k * N);
+    }
+}
+
+// 8-bit values of y / scale.  The quotient is a product with the reciprocal where that is exact to a rounding, which it
+// is for all but scales below 2^-100.
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+    uint16_t v;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+__device__ __forceinline__ int int8_of(float q) { return min(127, max(-127, __float2int_rn(q))); }
+template <int OUT>
+__device__ __forceinline__ void quantise8(uint8_t *p, const float (&f)[V], float scale) {
+    float q[V];
+    const float inv = __frcp_rn(scale);
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = scale >= 0x1p-100f ? f[i] * inv : __fdiv_rn(f[i], scale);
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float *r = q + 4 * k;
+        if constexpr (OUT == GDN_INT8) {
+            w[k] = __byte_perm(__byte_perm(int8_of(r[0]), int8_of(r[1]), 0x0040), __byte_perm(int8_of(r[2]), int8_of(r[3]), 0x0040), 0x5410);
+        } else {
+            w[k] = (uint32_t)e4m3x2(r[0], r[1]) | (uint32_t)e4m3x2(r[2], r[3]) << 16;
+        }
+    }
+    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ uint8_t quantise1(float y, float scale, int out) {
+    const float q = __fdiv_rn(y, scale);
+    return out == GDN_INT8 ? (uint8_t)int8_of(q) : (uint8_t)e4m3x2(q, 0.f);
+}
+
+// The sum (or maximum) over `lanes` neighbouring lanes, a power of two.
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+    for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float lanes_max(float v, int lanes) {
+    for (int o = 1; o < lanes; o <<= 1) v = max_or_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+// Over the CTA; buf: 32 floats that no one else uses until the next barrier but one.
+__device__ __forceinline__ float cta_sum(float v, float *buf) {
+    v = lanes_sum(v, 32);
+    if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
+    __syncthreads();
+    const int warps = (blockDim.x + 31) / 32, lane = threadIdx.x % 32;
+    return lanes_sum(lane < warps ? buf[lane] : 0.f, 32);
+}
+__device__ __forceinline__ float cta_max(float v, float *buf) {
+    v = lanes_max(v, 32);
+    if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
+    __syncthreads();
+    const int warps = (blockDim.x + 31) / 32, lane = threadIdx.x % 32;
+    return lanes_max(lane < warps ? buf[lane] : 0.f, 32);
+}
+
+// OUT: GDN_F32 stands for the I/O type.
+constexpr int SAME = GDN_F32;
+
+// ---------------------------------------------------------------- forward
+
+// What a row's sum is taken over: `lanes` neighbouring threads (heads of at most 256 channels), or the CTA.
+// A CTA takes one token: thread i holds pieces i, i + threads, .. of it (U at most).
+template <typename T, int OUT, int U>
+__global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p, int lanes) {
     dependent_prologue();
-    __shared__ float buf[NT / 32];
+    __shared__ float buf[3][32];
+    const int n = p.H * p.d, pieces = n / V, threads = blockDim.x;
+    const long long t = blockIdx.x;
+    Piece<T> x[U], r[U], z[U];
+    float s[U][V], w[U][V];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int i = threadIdx.x + k * threads;
+        x[k].zero();
+        if (i >= pieces) continue;
+        x[k].load(static_cast<const T *>(p.x) + t * p.x_stride + i * V);
+        if (p.r) r[k].load(static_cast<const T *>(p.r) + t * p.r_stride + i * V);
+        if (p.z) z[k].load(static_cast<const T *>(p.z) + t * p.z_stride + i * V);
+        if (p.w) read8(p.w + i * V % p.d, w[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int i = threadIdx.x + k * threads;
+        x[k].to(s[k]);
+        if (p.r && i < pieces) {
+            float add[V];
+            r[k].to(add);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[k][v] = to_f32(from_f32<T>(s[k][v] + add[v]));
+            write8(static_cast<T *>(p.s_out) + t * n + i * V, s[k]);
+        }
+    }
+    float sum[U], all = 0.f;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        sum[k] = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum[k] = fmaf(s[k][v], s[k][v], sum[k]);
+        all += sum[k];
+    }
+    if (lanes) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) sum[k] = lanes_sum(sum[k], lanes);
+    } else {
+        all = cta_sum(all, buf[0]);
+#pragma unroll
+        for (int k = 0; k < U; ++k) sum[k] = all;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int i = threadIdx.x + k * threads;
+        const float rstd = rsqrtf(sum[k] / (float)p.d + p.eps);
+        if (i >= pieces) continue;
+        if (p.w) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[k][v] *= rstd * (w[k][v] + p.offset);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[k][v] *= rstd;
+        }
+        if (p.z) {
+            float gate[V];
+            z[k].to(gate);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[k][v] *= silu(gate[v]);
+        }
+        if constexpr (OUT == SAME) {
+            write8(static_cast<T *>(p.y) + t * n + i * V, s[k]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) top = max_or_nan(top, fabsf(s[k][v]));
+        }
+    }
+    if constexpr (OUT != SAME) {
+        constexpr float MOST = OUT == GDN_INT8 ? 127.f : 448.f;
+        float scale = 0.f;
+        if (p.group == 0) {
+            scale = scale_of(cta_max(top, buf[1]), MOST);
+            if (threadIdx.x == 0) p.scale[t] = scale;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = threadIdx.x + k * threads;
+            if (p.group) {  // (whole groups of lanes are past the end together)
+                float m = 0.f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) m = max_or_nan(m, fabsf(s[k][v]));
+                scale = scale_of(lanes_max(m, p.group / V), MOST);
+                if (i < pieces && i % (p.group / V) == 0) p.scale[(t * n + i * V) / p.group] = scale;
+            }
+            if (i < pieces) quantise8<OUT>(static_cast<uint8_t *>(p.y) + t * n + i * V, s[k], scale);
+        }
+    }
+}
+
+// Heads of 32 to 256 channels (a power of two), no scale over whole tokens: pieces of all tokens in a row, U a thread.
+constexpr int HEAD_NT = 256, HEAD_U = 2;
+
+template <typename T, int OUT>
+__global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams p, int lanes) {
+    dependent_prologue();
+    constexpr int U = HEAD_U;
+    const int n = p.H * p.d, pieces = n / V;
+    const long long total = (long long)p.T * pieces, first = (long long)blockIdx.x * (HEAD_NT * U) + threadIdx.x;
+    Piece<T> x[U], r[U], z[U];
+    float s[U][V];
+    long long at[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const long long i = first + k * HEAD_NT, t = i / pieces, c = (i - t * pieces) * V;
+        at[k] = i < total ? t * n + c : -1;
+        x[k].zero();
+        z[k].zero();
+        if (i >= total) continue;
+        x[k].load(static_cast<const T *>(p.x) + t * p.x_stride + c);
+        if (p.z) z[k].load(static_cast<const T *>(p.z) + t * p.z_stride + c);
+        if (p.r) r[k].load(static_cast<const T *>(p.r) + t * p.r_stride + c);
+    }
+    float w[V];  // (a thread's pieces lie at the same place of their heads: HEAD_NT is a multiple of the lanes)
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = 1.f;
+    if (p.w) {
+        read8(p.w + threadIdx.x % lanes * V, w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[v] += p.offset;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        x[k].to(s[k]);
+        if (p.r && at[k] >= 0) {
+            float add[V];
+            r[k].to(add);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[k][v] = to_f32(from_f32<T>(s[k][v] + add[v]));
+            write8(static_cast<T *>(p.s_out) + at[k], s[k]);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum = fmaf(s[k][v], s[k][v], sum);
+        const float rstd = rsqrtf(lanes_sum(sum, lanes) / (float)p.d + p.eps);
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[k][v] *= rstd * w[v];
+        if (p.z) {
+            float gate[V];
+            z[k].to(gate);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[k][v] *= silu(gate[v]);
+        }
+        if constexpr (OUT == SAME) {
+            if (at[k] >= 0) write8(static_cast<T *>(p.y) + at[k], s[k]);
+        } else {
+            constexpr float MOST = OUT == GDN_INT8 ? 127.f : 448.f;
+            const int group = p.group / V;
+            float m = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) m = max_or_nan(m, fabsf(s[k][v]));
+            const float scale = scale_of(lanes_max(m, group), MOST);
+            if (at[k] >= 0) {
+                if (threadIdx.x % group == 0) p.scale[at[k] / p.group] = scale;
+                quantise8<OUT>(static_cast<uint8_t *>(p.y) + at[k], s[k], scale);
+            }
+        }
+    }
+}
+
+// Any sizes, alignment and types: a CTA a token, whose rows are read again for every step.
+constexpr int ANY_NT = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(ANY_NT) norm_any_kernel(const RmsNormParams p, int out_dtype) {
+    dependent_prologue();
+    __shared__ float buf[2][32];
     const long long t = blockIdx.x, n = (long long)p.H * p.d;
     const T *x = static_cast<const T *>(p.x) + t * p.x_stride;
     const T *r = p.r ? static_cast<const T *>(p.r) + t * p.r_stride : nullptr;
@@ -65,64 +317,184 @@ __global__ void __launch_bounds__(NT) norm_any_kernel(const RmsNormParams p, int
     const float most = out_dtype == GDN_INT8 ? 127.f : 448.f;
     const T *s = r ? s_out : x;
     float top = 0.f;
+    int turn = 0;
     // pass 0: 16 or 32 bits are written, or a token's largest magnitude found; pass 1: 8 bits
     for (int pass = 0; pass < (eight ? 2 : 1); ++pass) {
-        const float token_scale = pass ? scale_of(cta_max(top, buf), most) : 0.f;
-        if (pass && p.group == 0 && threadIdx.x == 0) p.scale[t] = token_scale;
+        float token_scale = 0.f;
+        if (pass && p.group == 0) {
+            token_scale = scale_of(cta_max(top, buf[turn ^= 1]), most);
+            if (threadIdx.x == 0) p.scale[t] = token_scale;
+        }
         for (int h = 0; h < p.H; ++h) {
             const long long at = (long long)h * p.d;
             float sum = 0.f;
-            for (int i = threadIdx.x; i < p.d; i += NT) {
+            for (int i = threadIdx.x; i < p.d; i += ANY_NT) {
                 if (r && pass == 0) s_out[at + i] = from_f32<T>(to_f32(x[at + i]) + to_f32(r[at + i]));
                 const float v = to_f32(s[at + i]);
                 sum += v * v;
             }
-            const float rstd = rsqrtf(cta_sum(sum, buf) / (float)p.d + p.eps);
+            const float rstd = rsqrtf(cta_sum(sum, buf[turn ^= 1]) / (float)p.d + p.eps);
             auto value = [&](int i) {
-                float v = to_f32(s[at + i]) * rstd;
-                if (p.w) v *= p.w[i] + p.offset;
+                float v = to_f32(s[at + i]);
+                v *= p.w ? rstd * (p.w[i] + p.offset) : rstd;
                 if (z) v *= silu(to_f32(z[at + i]));
                 return v;
             };
             if (!eight) {
-                for (int i = threadIdx.x; i < p.d; i += NT) static_cast<T *>(p.y)[t * n + at + i] = from_f32<T>(value(i));
+                for (int i = threadIdx.x; i < p.d; i += ANY_NT) static_cast<T *>(p.y)[t * n + at + i] = from_f32<T>(value(i));
             } else if (pass == 0) {
                 if (p.group == 0)
-                    for (int i = threadIdx.x; i < p.d; i += NT) top = max_or_nan(top, fabsf(value(i)));
+                    for (int i = threadIdx.x; i < p.d; i += ANY_NT) top = max_or_nan(top, fabsf(value(i)));
             } else {
-                // a warp takes whole groups; without groups a thread takes channels as before
-                const int step = p.group ? p.group : 32;
-                for (int g0 = threadIdx.x / 32 * step; g0 < p.d; g0 += NT / 32 * step) {
-                    float scale = token_scale;
-                    if (p.group) {
+                // (a thread's channels of s are its own: what it added, it reads)
+                uint8_t *y = static_cast<uint8_t *>(p.y) + t * n + at;
+                if (p.group == 0) {
+                    for (int i = threadIdx.x; i < p.d; i += ANY_NT) y[i] = quantise1(value(i), token_scale, out_dtype);
+                } else {
+                    for (int g0 = threadIdx.x / 32 * 32; g0 < p.d; g0 += ANY_NT) {
+                        // a warp's 32 channels; groups of 64 and 128 look at those of the other warps as well
+                        const int start = g0 / p.group * p.group;
                         float m = 0.f;
-                        for (int i = g0 + threadIdx.x % 32; i < g0 + step; i += 32) m = max_or_nan(m, fabsf(value(i)));
-                        for (int o = 16; o; o >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        scale = scale_of(m, most);
-                        if (threadIdx.x % 32 == 0) p.scale[(t * n + at + g0) / p.group] = scale;
-                    }
-                    for (int i = g0 + threadIdx.x % 32; i < min(g0 + step, p.d); i += 32) {
-                        const float q = __fdiv_rn(value(i), scale);
-                        uint8_t *dst = static_cast<uint8_t *>(p.y) + t * n + at + i;
-                        *dst = out_dtype == GDN_INT8 ? (uint8_t)to_int8(q) : to_e4m3(q);
+                        for (int i = start + threadIdx.x % 32; i < start + p.group; i += 32) m = max_or_nan(m, fabsf(value(i)));
+                        const float scale = scale_of(lanes_max(m, 32), most);
+                        if (g0 == start && threadIdx.x % 32 == 0) p.scale[(t * n + at + start) / p.group] = scale;
+                        y[g0 + threadIdx.x % 32] = quantise1(value(g0 + threadIdx.x % 32), scale, out_dtype);
                     }
                 }
             }
         }
+        __syncthreads();  // pass 1 reads sums that other threads stored
     }
 }
 
-// Backward, a CTA for every PART_TOKENS-th token; its rows' part of dweight.
-constexpr int PART_CTAS = 592;
+// ---------------------------------------------------------------- backward
+
+// With e = dy silu(z): dx = rstd (e w - n mean(e w n)) + dr, dw = sum e n, dz = dy n w silu'(z), n = s rstd.
+// CTAs walk over tokens, so that a thread's channels and their part of dw stay the same; the parts are summed by a
+// second kernel in the order of the CTAs.
+
+// One piece of the gradient; e, n: as above.
+template <typename T>
+__device__ __forceinline__ void finish8(const RmsNormParams &p, long long at, const Piece<T> &r, const Piece<T> &z,
+                                        const float (&x)[V], const float (&dy)[V], const float (&w)[V], float rstd, float dot,
+                                        float (&part)[V]) {
+    float dx[V], dz[V], zv[V], rv[V];
+    if (p.z) z.to(zv);
+    if (p.r) r.to(rv);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float n = x[v] * rstd;
+        float e = dy[v];
+        if (p.z) {
+            const float sig = sigmoid(zv[v]);
+            e = dy[v] * silu(zv[v]);
+            dz[v] = dy[v] * n * w[v] * (sig * fmaf(zv[v], 1.f - sig, 1.f));
+        }
+        part[v] = fmaf(e, n, part[v]);
+        dx[v] = rstd * fmaf(-n, dot, e * w[v]);
+        if (p.r) dx[v] += rv[v];
+    }
+    write8(static_cast<T *>(p.dx) + at, dx);
+    if (p.z) write8(static_cast<T *>(p.dz) + at, dz);
+}
+
+// A CTA takes every gridDim-th token: thread i holds pieces i, i + threads, .. of it (U at most).
+template <typename T, int U>
+__global__ void __launch_bounds__(512) norm_token_backward_kernel(const RmsNormParams p, int lanes) {
+    dependent_prologue();
+    __shared__ float2 buf[2][16];
+    const int n = p.H * p.d, pieces = n / V, threads = blockDim.x;
+    float part[U][V] = {}, w[U][V];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int i = threadIdx.x + k * threads;
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[k][v] = 1.f;
+        if (p.w && i < pieces) {
+            read8(p.w + i * V % p.d, w[k]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) w[k][v] += p.offset;
+        }
+    }
+    int turn = 0;
+    for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
+        Piece<T> px[U], pdy[U], z[U], r[U];
+        float x[U][V], dy[U][V];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = threadIdx.x + k * threads;
+            px[k].zero();
+            pdy[k].zero();
+            z[k].zero();
+            if (i >= pieces) continue;
+            px[k].load(static_cast<const T *>(p.x) + t * p.x_stride + i * V);
+            pdy[k].load(static_cast<const T *>(p.dy) + t * p.dy_stride + i * V);
+            if (p.z) z[k].load(static_cast<const T *>(p.z) + t * p.z_stride + i * V);
+            if (p.r) r[k].load(static_cast<const T *>(p.r) + t * p.r_stride + i * V);
+        }
+        // the sums of s^2 and of e w s together: mean(e w n) = rstd mean(e w s)
+        float2 sum[U], all = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            float zv[V];
+            px[k].to(x[k]);
+            pdy[k].to(dy[k]);
+            z[k].to(zv);
+            sum[k] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float e = dy[k][v];
+                if (p.z) e *= silu(zv[v]);
+                sum[k].x = fmaf(x[k][v], x[k][v], sum[k].x);
+                sum[k].y = fmaf(e * w[k][v], x[k][v], sum[k].y);
+            }
+            all.x += sum[k].x;
+            all.y += sum[k].y;
+        }
+        if (lanes) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) sum[k] = make_float2(lanes_sum(sum[k].x, lanes), lanes_sum(sum[k].y, lanes));
+        } else {
+            all = make_float2(lanes_sum(all.x, 32), lanes_sum(all.y, 32));
+            turn ^= 1;
+            const int lane = threadIdx.x % 32, warps = (threads + 31) / 32;
+            if (lane == 0) buf[turn][threadIdx.x / 32] = all;
+            __syncthreads();
+            all = lane < warps ? buf[turn][lane] : make_float2(0.f, 0.f);
+            all = make_float2(lanes_sum(all.x, 16), lanes_sum(all.y, 16));
+            all.x = __shfl_sync(0xffffffffu, all.x, 0);
+            all.y = __shfl_sync(0xffffffffu, all.y, 0);
+#pragma unroll
+            for (int k = 0; k < U; ++k) sum[k] = all;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = threadIdx.x + k * threads;
+            if (i >= pieces) continue;
+            const float rstd = rsqrtf(sum[k].x / (float)p.d + p.eps), dot = sum[k].y * rstd / (float)p.d;
+            finish8<T>(p, t * n + i * V, r[k], z[k], x[k], dy[k], w[k], rstd, dot, part[k]);
+        }
+    }
+    if (p.dw) {
+        float *out = p.partials + (long long)blockIdx.x * n;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = threadIdx.x + k * threads;
+            if (i < pieces) write8(out + i * V, part[k]);
+        }
+    }
+}
 
 template <typename T>
-__global__ void __launch_bounds__(NT) norm_any_backward_kernel(const RmsNormParams p) {
+__global__ void __launch_bounds__(ANY_NT) norm_any_backward_kernel(const RmsNormParams p) {
     dependent_prologue();
-    __shared__ float buf[NT / 32];
+    __shared__ float buf[2][32];
     const long long n = (long long)p.H * p.d;
-    float *part = p.dw ? p.partials + (long long)blockIdx.x * p.d : nullptr;
+    float *part = p.dw ? p.partials + (long long)blockIdx.x * n : nullptr;
     if (part)
-        for (int i = threadIdx.x; i < p.d; i += NT) part[i] = 0.f;
+        for (int i = threadIdx.x; i < p.d; i += ANY_NT)
+            for (int h = 0; h < p.H; ++h) part[(long long)h * p.d + i] = 0.f;
+    int turn = 0;
     for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
         for (int h = 0; h < p.H; ++h) {
             const long long at = (long long)h * p.d;
@@ -132,56 +504,128 @@ __global__ void __launch_bounds__(NT) norm_any_backward_kernel(const RmsNormPara
             const T *z = p.z ? static_cast<const T *>(p.z) + t * p.z_stride + at : nullptr;
             auto weight = [&](int i) { return p.w ? p.w[i] + p.offset : 1.f; };
             auto gated = [&](int i) { return to_f32(dy[i]) * (z ? silu(to_f32(z[i])) : 1.f); };
-            float sum = 0.f;
-            for (int i = threadIdx.x; i < p.d; i += NT) sum += to_f32(x[i]) * to_f32(x[i]);
-            const float rstd = rsqrtf(cta_sum(sum, buf) / (float)p.d + p.eps);
-            float dot = 0.f;
-            for (int i = threadIdx.x; i < p.d; i += NT) dot += gated(i) * weight(i) * (to_f32(x[i]) * rstd);
-            dot = cta_sum(dot, buf) / (float)p.d;
-            for (int i = threadIdx.x; i < p.d; i += NT) {
+            float sum = 0.f, dot = 0.f;
+            for (int i = threadIdx.x; i < p.d; i += ANY_NT) {
+                const float v = to_f32(x[i]);
+                sum = fmaf(v, v, sum);
+                dot = fmaf(gated(i) * weight(i), v, dot);
+            }
+            const float rstd = rsqrtf(cta_sum(sum, buf[turn ^= 1]) / (float)p.d + p.eps);
+            dot = cta_sum(dot, buf[turn ^= 1]) * rstd / (float)p.d;
+            for (int i = threadIdx.x; i < p.d; i += ANY_NT) {
                 const float nx = to_f32(x[i]) * rstd, e = gated(i);
-                float dx = rstd * (e * weight(i) - nx * dot);
+                float dx = rstd * fmaf(-nx, dot, e * weight(i));
                 if (r) dx += to_f32(r[i]);
                 static_cast<T *>(p.dx)[t * n + at + i] = from_f32<T>(dx);
-                if (part) part[i] += e * nx;
+                if (part) part[at + i] += e * nx;
                 if (z) {
-                    const float zv = to_f32(z[i]), sig = 1.f / (1.f + expf(-zv));
-                    static_cast<T *>(p.dz)[t * n + at + i] =
-                        from_f32<T>(to_f32(dy[i]) * nx * weight(i) * (sig * (1.f + zv * (1.f - sig))));
+                    const float zv = to_f32(z[i]), sig = sigmoid(zv);
+                    static_cast<T *>(p.dz)[t * n + at + i] = from_f32<T>(to_f32(dy[i]) * nx * weight(i) * (sig * fmaf(zv, 1.f - sig, 1.f)));
                 }
             }
         }
     }
 }
 
-__global__ void __launch_bounds__(NT) norm_sums_kernel(const RmsNormParams p, int parts) {
+// dw of 32 channels a CTA: warps take rows of the parts in turn, their sums are joined in order.
+constexpr int SUM_WARPS = 16;
+__global__ void __launch_bounds__(32 * SUM_WARPS) norm_sums_kernel(const RmsNormParams p, int parts) {
     dependent_prologue();
-    const int i = blockIdx.x * NT + threadIdx.x;
-    if (i >= p.d) return;
+    __shared__ float buf[SUM_WARPS][32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    const long long rows = (long long)parts * p.H;
     float sum = 0.f;
-    for (int k = 0; k < parts; ++k) sum += p.partials[(long long)k * p.d + i];
-    p.dw[i] = sum;
+    if (c < p.d) {
+#pragma unroll 8
+        for (long long k = warp; k < rows; k += SUM_WARPS) sum += p.partials[k * p.d + c];
+    }
+    buf[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && c < p.d) {
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < SUM_WARPS; ++k) sum += buf[k][lane];
+        p.dw[c] = sum;
+    }
 }
 
-int parts_of(int T) { return T < PART_CTAS ? T : PART_CTAS; }
+// ---------------------------------------------------------------- launches
+
+bool whole(const void *ptr, long long stride, size_t elem) {
+    return ((reinterpret_cast<uintptr_t>(ptr) | (unsigned long long)stride * elem) & 15u) == 0;
+}
+bool power_of_two(int n) { return (n & (n - 1)) == 0; }
+
+// Lanes that a head's sum is taken over if it is a few lanes', else 0.
+int head_lanes(int d) { return d % V == 0 && d / V <= 32 && power_of_two(d / V) ? d / V : 0; }
+
+// Threads of a CTA that takes a token of `pieces`, U each: whole warps, as even as can be.
+int token_threads(int pieces, int U) { return ((pieces + U - 1) / U + 31) / 32 * 32; }
+
+// CTAs that walk over the tokens backwards: what is resident at once, or one a token.
+int backward_ctas(int T) { return (int)std::min<long long>(T, 4LL * current_device_sms()); }
+
+template <typename T, int OUT>
+cudaError_t forward_typed(const RmsNormParams &p, int out_dtype, cudaStream_t stream) {
+    const long long n = (long long)p.H * p.d;
+    const int lanes = head_lanes(p.d);
+    const bool vec = n % V == 0 && p.d % V == 0 && whole(p.x, p.x_stride, sizeof(T)) && whole(p.r, p.r_stride, sizeof(T)) &&
+                     whole(p.z, p.z_stride, sizeof(T)) && whole(p.w, 0, 4) && whole(p.s_out, n, sizeof(T)) &&
+                     (OUT == SAME ? whole(p.y, n, sizeof(T)) : reinterpret_cast<uintptr_t>(p.y) % 8 == 0);
+    const long long pieces = n / V;
+    if (vec && lanes && (OUT == SAME || p.group)) {
+        const long long ctas = ((long long)p.T * pieces + HEAD_NT * HEAD_U - 1) / (HEAD_NT * HEAD_U);
+        if (ctas <= INT32_MAX)
+            return launch_dependent(norm_head_kernel<T, OUT>, dim3((unsigned)ctas), dim3(HEAD_NT), 0, stream, p, lanes);
+    }
+    if (vec && (p.H == 1 || lanes) && pieces <= 4096) {
+        const dim3 grid((unsigned)p.T);
+        if (pieces <= 512) return launch_dependent(norm_token_kernel<T, OUT, 1>, grid, dim3(token_threads((int)pieces, 1)), 0, stream, p, p.H > 1 ? lanes : 0);
+        if (pieces <= 1024) return launch_dependent(norm_token_kernel<T, OUT, 2>, grid, dim3(token_threads((int)pieces, 2)), 0, stream, p, p.H > 1 ? lanes : 0);
+        return launch_dependent(norm_token_kernel<T, OUT, 4>, grid, dim3(token_threads((int)pieces, 4)), 0, stream, p, p.H > 1 ? lanes : 0);
+    }
+    return launch_dependent(norm_any_kernel<T>, dim3((unsigned)p.T), dim3(ANY_NT), 0, stream, p, out_dtype);
+}
+
+template <typename T>
+cudaError_t forward_out(const RmsNormParams &p, int out_dtype, cudaStream_t stream) {
+    switch (out_dtype) {
+        case GDN_FP8_E4M3: return forward_typed<T, GDN_FP8_E4M3>(p, out_dtype, stream);
+        case GDN_INT8: return forward_typed<T, GDN_INT8>(p, out_dtype, stream);
+        default: return forward_typed<T, SAME>(p, out_dtype, stream);
+    }
+}
 
 template <typename T>
 cudaError_t backward_typed(const RmsNormParams &p, cudaStream_t stream) {
-    cudaError_t e = p.T == 0 ? cudaSuccess : launch_dependent(norm_any_backward_kernel<T>, dim3((unsigned)parts_of(p.T)), dim3(NT), 0, stream, p);
+    const long long n = (long long)p.H * p.d, pieces = n / V;
+    const int lanes = head_lanes(p.d), ctas = backward_ctas(p.T);
+    cudaError_t e = cudaSuccess;
+    if (p.T > 0) {
+        const bool vec = n % V == 0 && p.d % V == 0 && whole(p.x, p.x_stride, sizeof(T)) && whole(p.dy, p.dy_stride, sizeof(T)) &&
+                         whole(p.r, p.r_stride, sizeof(T)) && whole(p.z, p.z_stride, sizeof(T)) && whole(p.w, 0, 4) &&
+                         whole(p.dx, n, sizeof(T)) && whole(p.dz, n, sizeof(T));
+        const dim3 grid((unsigned)ctas);
+        if (vec && (p.H == 1 || lanes) && pieces <= 512)
+            e = launch_dependent(norm_token_backward_kernel<T, 1>, grid, dim3(token_threads((int)pieces, 1)), 0, stream, p, p.H > 1 ? lanes : 0);
+        else if (vec && (p.H == 1 || lanes) && pieces <= 1024)
+            e = launch_dependent(norm_token_backward_kernel<T, 2>, grid, dim3(token_threads((int)pieces, 2)), 0, stream, p, p.H > 1 ? lanes : 0);
+        else
+            e = launch_dependent(norm_any_backward_kernel<T>, grid, dim3(ANY_NT), 0, stream, p);
+    }
     if (e != cudaSuccess || !p.dw) return e;
-    return launch_dependent(norm_sums_kernel, dim3((unsigned)((p.d + NT - 1) / NT)), dim3(NT), 0, stream, p, parts_of(p.T));
+    return launch_dependent(norm_sums_kernel, dim3((unsigned)((p.d + 31) / 32)), dim3(32 * SUM_WARPS), 0, stream, p, ctas);
 }
 
 }  // namespace
 
-size_t rms_norm_backward_workspace_bytes(int T, int, int d) { return 4 * (size_t)parts_of(T) * d; }
+size_t rms_norm_backward_workspace_bytes(int T, int H, int d) { return 4 * (size_t)backward_ctas(T) * H * d; }
 
 cudaError_t launch_rms_norm(const RmsNormParams &p, int io_dtype, int out_dtype, cudaStream_t stream) {
-    const dim3 grid((unsigned)p.T), block(NT);
     switch (io_dtype) {
-        case GDN_F16: return launch_dependent(norm_any_kernel<__half>, grid, block, 0, stream, p, out_dtype);
-        case GDN_BF16: return launch_dependent(norm_any_kernel<__nv_bfloat16>, grid, block, 0, stream, p, out_dtype);
-        default: return launch_dependent(norm_any_kernel<float>, grid, block, 0, stream, p, out_dtype);
+        case GDN_F16: return forward_out<__half>(p, out_dtype, stream);
+        case GDN_BF16: return forward_out<__nv_bfloat16>(p, out_dtype, stream);
+        default: return forward_out<float>(p, out_dtype, stream);
     }
 }
 
