@@ -19,15 +19,15 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     return y;
 }
 
-// The scale of 8-bit values whose largest magnitude is top.
+// The scale of 8-bit values whose largest magnitude is top (its reciprocal is a normal number).
 __device__ __forceinline__ float scale_of(float top, float most) {
     if (!(top <= 3.402823466e38f)) return __int_as_float(0x7fc00000);
-    return top == 0.f ? 1.f : __fdiv_rn(top, most);
+    return top == 0.f ? 1.f : fmaxf(__fdiv_rn(top, most), 0x1p-120f);
 }
 
-// z sigmoid(z), and its derivative
+// (0 for z below -88, where e^-z is infinite)
 __device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + exp2_approx(-LOG2E * z)); }
-__device__ __forceinline__ float silu(float z) { return z > -80.f ? z * sigmoid(z) : z * expf(z); }
+__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 
 constexpr int V = 8;  // channels of a piece
 
@@ -43,6 +43,19 @@ struct Piece {
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int k = 0; k < V / N; ++k) v[k].u = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+        for (int k = 0; k < V / N; ++k) v[k].store(p + k * N);
+    }
+    __device__ __forceinline__ void from(const float (&f)[V]) {
+#pragma unroll
+        for (int k = 0; k < V / N; ++k) {
+            float g[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] = f[k * N + i];
+            v[k].from(g);
+        }
     }
     __device__ __forceinline__ void to(float (&f)[V]) const {
 #pragma unroll
@@ -62,20 +75,12 @@ __device__ __forceinline__ void read8(const T *p, float (&f)[V]) {
 }
 template <typename T>
 __device__ __forceinline__ void write8(T *p, const float (&f)[V]) {
-    constexpr int N = Vec16<T>::N;
-#pragma unroll
-    for (int k = 0; k < V / N; ++k) {
-        Vec16<T> v;
-        float g[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = f[k * N + i];
-        v.from(g);
-        v.store(p + k * N);
-    }
+    Piece<T> v;
+    v.from(f);
+    v.store(p);
 }
 
-// 8-bit values of y / scale.  The quotient is a product with the reciprocal where that is exact to a rounding, which it
-// is for all but scales below 2^-100.
+// 8-bit values of y / scale, as products with the scale's reciprocal (two roundings in FP32 instead of one).
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
     uint16_t v;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
@@ -87,7 +92,7 @@ __device__ __forceinline__ void quantise8(uint8_t *p, const float (&f)[V], float
     float q[V];
     const float inv = __frcp_rn(scale);
 #pragma unroll
-    for (int i = 0; i < V; ++i) q[i] = scale >= 0x1p-100f ? f[i] * inv : __fdiv_rn(f[i], scale);
+    for (int i = 0; i < V; ++i) q[i] = f[i] * inv;
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -101,7 +106,7 @@ __device__ __forceinline__ void quantise8(uint8_t *p, const float (&f)[V], float
     *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 __device__ __forceinline__ uint8_t quantise1(float y, float scale, int out) {
-    const float q = __fdiv_rn(y, scale);
+    const float q = y * __frcp_rn(scale);
     return out == GDN_INT8 ? (uint8_t)int8_of(q) : (uint8_t)e4m3x2(q, 0.f);
 }
 
@@ -144,7 +149,6 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
     const int n = p.H * p.d, pieces = n / V, threads = blockDim.x;
     const long long t = blockIdx.x;
     Piece<T> x[U], r[U], z[U];
-    float s[U][V], w[U][V];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int i = threadIdx.x + k * threads;
@@ -153,26 +157,25 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
         x[k].load(static_cast<const T *>(p.x) + t * p.x_stride + i * V);
         if (p.r) r[k].load(static_cast<const T *>(p.r) + t * p.r_stride + i * V);
         if (p.z) z[k].load(static_cast<const T *>(p.z) + t * p.z_stride + i * V);
-        if (p.w) read8(p.w + i * V % p.d, w[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int i = threadIdx.x + k * threads;
-        x[k].to(s[k]);
-        if (p.r && i < pieces) {
-            float add[V];
-            r[k].to(add);
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[k][v] = to_f32(from_f32<T>(s[k][v] + add[v]));
-            write8(static_cast<T *>(p.s_out) + t * n + i * V, s[k]);
-        }
     }
     float sum[U], all = 0.f;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
+        const int i = threadIdx.x + k * threads;
+        float s[V];
+        x[k].to(s);
+        if (p.r && i < pieces) {
+            float add[V];
+            r[k].to(add);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] += add[v];
+            x[k].from(s);
+            x[k].to(s);  // what is normalised is the sum as it is stored
+            x[k].store(static_cast<T *>(p.s_out) + t * n + i * V);
+        }
         sum[k] = 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum[k] = fmaf(s[k][v], s[k][v], sum[k]);
+        for (int v = 0; v < V; ++v) sum[k] = fmaf(s[v], s[v], sum[k]);
         all += sum[k];
     }
     if (lanes) {
@@ -183,15 +186,19 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
 #pragma unroll
         for (int k = 0; k < U; ++k) sum[k] = all;
     }
-    float top = 0.f;
+    float top = 0.f, s[U][V];
+    const float mean = 1.f / (float)p.d;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int i = threadIdx.x + k * threads;
-        const float rstd = rsqrtf(sum[k] / (float)p.d + p.eps);
+        const float rstd = rsqrtf(sum[k] * mean + p.eps);
+        x[k].to(s[k]);
         if (i >= pieces) continue;
         if (p.w) {
+            float w[V];
+            read8(p.w + i * V % p.d, w);
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[k][v] *= rstd * (w[k][v] + p.offset);
+            for (int v = 0; v < V; ++v) s[k][v] *= rstd * (w[v] + p.offset);
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) s[k][v] *= rstd;
@@ -234,18 +241,19 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
 // Heads of 32 to 256 channels (a power of two), no scale over whole tokens: pieces of all tokens in a row, U a thread.
 constexpr int HEAD_NT = 256, HEAD_U = 2;
 
-template <typename T, int OUT>
-__global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams p, int lanes) {
+template <typename T, int OUT, int LANES>
+__global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams p) {
     dependent_prologue();
     constexpr int U = HEAD_U;
-    const int n = p.H * p.d, pieces = n / V;
-    const long long total = (long long)p.T * pieces, first = (long long)blockIdx.x * (HEAD_NT * U) + threadIdx.x;
+    const unsigned n = p.H * p.d, pieces = n / V;
+    const unsigned total = p.T * pieces, first = blockIdx.x * (HEAD_NT * U) + threadIdx.x;  // (below 2^31: checked on the host)
     Piece<T> x[U], r[U], z[U];
     float s[U][V];
     long long at[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        const long long i = first + k * HEAD_NT, t = i / pieces, c = (i - t * pieces) * V;
+        const unsigned i = first + k * HEAD_NT;
+        const long long t = i / pieces, c = (i - (unsigned)t * pieces) * V;
         at[k] = i < total ? t * n + c : -1;
         x[k].zero();
         z[k].zero();
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams 
 #pragma unroll
     for (int v = 0; v < V; ++v) w[v] = 1.f;
     if (p.w) {
-        read8(p.w + threadIdx.x % lanes * V, w);
+        read8(p.w + threadIdx.x % LANES * V, w);
 #pragma unroll
         for (int v = 0; v < V; ++v) w[v] += p.offset;
     }
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams 
         float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) sum = fmaf(s[k][v], s[k][v], sum);
-        const float rstd = rsqrtf(lanes_sum(sum, lanes) / (float)p.d + p.eps);
+        const float rstd = rsqrtf(lanes_sum(sum, LANES) * (1.f / (LANES * V)) + p.eps);
 #pragma unroll
         for (int v = 0; v < V; ++v) s[k][v] *= rstd * w[v];
         if (p.z) {
@@ -573,16 +581,23 @@ cudaError_t forward_typed(const RmsNormParams &p, int out_dtype, cudaStream_t st
                      whole(p.z, p.z_stride, sizeof(T)) && whole(p.w, 0, 4) && whole(p.s_out, n, sizeof(T)) &&
                      (OUT == SAME ? whole(p.y, n, sizeof(T)) : reinterpret_cast<uintptr_t>(p.y) % 8 == 0);
     const long long pieces = n / V;
-    if (vec && lanes && (OUT == SAME || p.group)) {
-        const long long ctas = ((long long)p.T * pieces + HEAD_NT * HEAD_U - 1) / (HEAD_NT * HEAD_U);
-        if (ctas <= INT32_MAX)
-            return launch_dependent(norm_head_kernel<T, OUT>, dim3((unsigned)ctas), dim3(HEAD_NT), 0, stream, p, lanes);
+    if (vec && lanes >= 4 && (OUT == SAME || p.group) && p.T * pieces <= INT32_MAX) {
+        const dim3 grid((unsigned)((p.T * pieces + HEAD_NT * HEAD_U - 1) / (HEAD_NT * HEAD_U))), block(HEAD_NT);
+        switch (lanes) {
+            case 4: return launch_dependent(norm_head_kernel<T, OUT, 4>, grid, block, 0, stream, p);
+            case 8: return launch_dependent(norm_head_kernel<T, OUT, 8>, grid, block, 0, stream, p);
+            case 16: return launch_dependent(norm_head_kernel<T, OUT, 16>, grid, block, 0, stream, p);
+            default: return launch_dependent(norm_head_kernel<T, OUT, 32>, grid, block, 0, stream, p);
+        }
     }
     if (vec && (p.H == 1 || lanes) && pieces <= 4096) {
+        // Few tokens: as many threads as there are pieces, for latency.  Many: four pieces a thread, whose loads are all
+        // on their way at once, and fewer threads to wait for one another.
         const dim3 grid((unsigned)p.T);
-        if (pieces <= 512) return launch_dependent(norm_token_kernel<T, OUT, 1>, grid, dim3(token_threads((int)pieces, 1)), 0, stream, p, p.H > 1 ? lanes : 0);
-        if (pieces <= 1024) return launch_dependent(norm_token_kernel<T, OUT, 2>, grid, dim3(token_threads((int)pieces, 2)), 0, stream, p, p.H > 1 ? lanes : 0);
-        return launch_dependent(norm_token_kernel<T, OUT, 4>, grid, dim3(token_threads((int)pieces, 4)), 0, stream, p, p.H > 1 ? lanes : 0);
+        const int few = p.H > 1 ? lanes : 0;
+        if (pieces <= 512 && p.T < 8 * current_device_sms())
+            return launch_dependent(norm_token_kernel<T, OUT, 1>, grid, dim3(token_threads((int)pieces, 1)), 0, stream, p, few);
+        return launch_dependent(norm_token_kernel<T, OUT, 4>, grid, dim3(token_threads((int)pieces, 4)), 0, stream, p, few);
     }
     return launch_dependent(norm_any_kernel<T>, dim3((unsigned)p.T), dim3(ANY_NT), 0, stream, p, out_dtype);
 }

@@ -828,7 +828,7 @@ gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_a
  *   scale         device FP32 (8-bit outputs only): [T], one for all channels of a token, for
  *                 scale_group = 0; else [T, num_heads * head_dim / scale_group], one for every
  *                 scale_group channels.  scale = max|y| / 448 (e4m3) or / 127 (int8) of its
- *                 channels, 1 if they are all 0, NaN if one is infinite or NaN;
+ *                 channels, 2^-120 at least, 1 if they are all 0, NaN if one is infinite or NaN;
  *                 output = y / scale rounded to nearest even (the quotient up to FP32 rounding).
  * Other overlaps of outputs with inputs or with each other are not allowed.
  */
