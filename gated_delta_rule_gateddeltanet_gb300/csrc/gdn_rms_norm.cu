@@ -8,6 +8,8 @@
 // other threads is one sum (two backwards) and, for 8 bits, a maximum.  A CTA takes
 // a token at a time (whole-token norms and scales), or tokens are cut into runs of
 // pieces of heads whose sums are shuffles inside a warp.
+#include <type_traits>
+
 #include "layer_internal.cuh"
 
 namespace gdn {
@@ -19,15 +21,28 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     return y;
 }
 
-// The scale of 8-bit values whose largest magnitude is top (its reciprocal is a normal number).
-__device__ __forceinline__ float scale_of(float top, float most) {
+// The larger of two or three numbers, NaN if one is.
+__device__ __forceinline__ float max_or_nan(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// The scale of 8-bit values whose largest magnitude is top (its reciprocal is a normal number); one_most: 1 / 448 or 1 / 127.
+__device__ __forceinline__ float scale_of(float top, float one_most) {
     if (!(top <= 3.402823466e38f)) return __int_as_float(0x7fc00000);
-    return top == 0.f ? 1.f : fmaxf(__fdiv_rn(top, most), 0x1p-120f);
+    return top == 0.f ? 1.f : fmaxf(top * one_most, 0x1p-120f);
 }
 
 // (0 for z below -88, where e^-z is infinite)
 __device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + exp2_approx(-LOG2E * z)); }
 __device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
+__device__ __forceinline__ F2 silu(F2 z) {
+    float a, b;
+    mul2(z, F2(-LOG2E)).get(a, b);
+    add2(F2(exp2_approx(a), exp2_approx(b)), F2(1.f)).get(a, b);
+    return mul2(z, F2(rcp_approx(a), rcp_approx(b)));
+}
 
 constexpr int V = 8;  // channels of a piece
 
@@ -57,6 +72,26 @@ struct Piece {
             v[k].from(g);
         }
     }
+    __device__ __forceinline__ void to(F2 (&f)[V / 2]) const {
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) f[k] = F2(to_f32(v[2 * k / N].e[2 * k % N]), to_f32(v[2 * k / N].e[2 * k % N + 1]));
+    }
+    __device__ __forceinline__ void from(const F2 (&f)[V / 2]) {
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
+            float a, b;
+            f[k].get(a, b);
+            if constexpr (N == 8) {
+                uint32_t two;
+                if constexpr (std::is_same<T, __half>::value) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(two) : "f"(b), "f"(a));
+                else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(two) : "f"(b), "f"(a));
+                (k == 0 ? v[0].u.x : k == 1 ? v[0].u.y : k == 2 ? v[0].u.z : v[0].u.w) = two;
+            } else {
+                v[2 * k / N].e[2 * k % N] = from_f32<T>(a);
+                v[2 * k / N].e[2 * k % N + 1] = from_f32<T>(b);
+            }
+        }
+    }
     __device__ __forceinline__ void to(float (&f)[V]) const {
 #pragma unroll
         for (int k = 0; k < V / N; ++k) {
@@ -73,8 +108,8 @@ __device__ __forceinline__ void read8(const T *p, float (&f)[V]) {
     v.load(p);
     v.to(f);
 }
-template <typename T>
-__device__ __forceinline__ void write8(T *p, const float (&f)[V]) {
+template <typename T, typename F, int M>
+__device__ __forceinline__ void write8(T *p, const F (&f)[M]) {
     Piece<T> v;
     v.from(f);
     v.store(p);
@@ -88,11 +123,11 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
 }
 __device__ __forceinline__ int int8_of(float q) { return min(127, max(-127, __float2int_rn(q))); }
 template <int OUT>
-__device__ __forceinline__ void quantise8(uint8_t *p, const float (&f)[V], float scale) {
+__device__ __forceinline__ void quantise8(uint8_t *p, const F2 (&f)[V / 2], float scale) {
     float q[V];
-    const float inv = __frcp_rn(scale);
+    const F2 inv(rcp_approx(scale));
 #pragma unroll
-    for (int i = 0; i < V; ++i) q[i] = f[i] * inv;
+    for (int i = 0; i < V / 2; ++i) mul2(f[i], inv).get(q[2 * i], q[2 * i + 1]);
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -106,8 +141,27 @@ __device__ __forceinline__ void quantise8(uint8_t *p, const float (&f)[V], float
     *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 __device__ __forceinline__ uint8_t quantise1(float y, float scale, int out) {
-    const float q = y * __frcp_rn(scale);
+    const float q = y * rcp_approx(scale);
     return out == GDN_INT8 ? (uint8_t)int8_of(q) : (uint8_t)e4m3x2(q, 0.f);
+}
+
+// The sum of the squares, and the largest magnitude.
+__device__ __forceinline__ float squares(const F2 (&f)[V / 2]) {
+    F2 sum = mul2(f[0], f[0]);
+#pragma unroll
+    for (int i = 1; i < V / 2; ++i) sum = fma2(f[i], f[i], sum);
+    float a, b;
+    sum.get(a, b);
+    return a + b;
+}
+__device__ __forceinline__ float largest(const F2 (&f)[V / 2], float top) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        float a, b;
+        f[i].get(a, b);
+        top = max_or_nan(top, fabsf(a), fabsf(b));
+    }
+    return top;
 }
 
 // The sum (or maximum) over `lanes` neighbouring lanes, a power of two.
@@ -162,20 +216,18 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int i = threadIdx.x + k * threads;
-        float s[V];
+        F2 s[V / 2];
         x[k].to(s);
         if (p.r && i < pieces) {
-            float add[V];
+            F2 add[V / 2];
             r[k].to(add);
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[v] += add[v];
+            for (int v = 0; v < V / 2; ++v) s[v] = add2(s[v], add[v]);
             x[k].from(s);
             x[k].to(s);  // what is normalised is the sum as it is stored
             x[k].store(static_cast<T *>(p.s_out) + t * n + i * V);
         }
-        sum[k] = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) sum[k] = fmaf(s[v], s[v], sum[k]);
+        sum[k] = squares(s);
         all += sum[k];
     }
     if (lanes) {
@@ -186,51 +238,47 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
 #pragma unroll
         for (int k = 0; k < U; ++k) sum[k] = all;
     }
-    float top = 0.f, s[U][V];
+    float top = 0.f;
+    F2 s[U][V / 2];
     const float mean = 1.f / (float)p.d;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int i = threadIdx.x + k * threads;
-        const float rstd = rsqrtf(sum[k] * mean + p.eps);
+        const F2 rstd(rsqrtf(sum[k] * mean + p.eps)), offset(p.offset);
         x[k].to(s[k]);
         if (i >= pieces) continue;
         if (p.w) {
-            float w[V];
-            read8(p.w + i * V % p.d, w);
+            F2 w[V / 2];
+            Piece<float> pw;
+            pw.load(p.w + i * V % p.d);
+            pw.to(w);
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[k][v] *= rstd * (w[v] + p.offset);
+            for (int v = 0; v < V / 2; ++v) s[k][v] = mul2(s[k][v], mul2(rstd, add2(w[v], offset)));
         } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[k][v] *= rstd;
+            for (int v = 0; v < V / 2; ++v) s[k][v] = mul2(s[k][v], rstd);
         }
         if (p.z) {
-            float gate[V];
+            F2 gate[V / 2];
             z[k].to(gate);
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[k][v] *= silu(gate[v]);
+            for (int v = 0; v < V / 2; ++v) s[k][v] = mul2(s[k][v], silu(gate[v]));
         }
-        if constexpr (OUT == SAME) {
-            write8(static_cast<T *>(p.y) + t * n + i * V, s[k]);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) top = max_or_nan(top, fabsf(s[k][v]));
-        }
+        if constexpr (OUT == SAME) write8(static_cast<T *>(p.y) + t * n + i * V, s[k]);
+        else top = largest(s[k], top);
     }
     if constexpr (OUT != SAME) {
-        constexpr float MOST = OUT == GDN_INT8 ? 127.f : 448.f;
+        constexpr float ONE_MOST = OUT == GDN_INT8 ? 1.f / 127.f : 1.f / 448.f;
         float scale = 0.f;
         if (p.group == 0) {
-            scale = scale_of(cta_max(top, buf[1]), MOST);
+            scale = scale_of(cta_max(top, buf[1]), ONE_MOST);
             if (threadIdx.x == 0) p.scale[t] = scale;
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int i = threadIdx.x + k * threads;
             if (p.group) {  // (whole groups of lanes are past the end together)
-                float m = 0.f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) m = max_or_nan(m, fabsf(s[k][v]));
-                scale = scale_of(lanes_max(m, p.group / V), MOST);
+                scale = scale_of(lanes_max(largest(s[k], 0.f), p.group / V), ONE_MOST);
                 if (i < pieces && i % (p.group / V) == 0) p.scale[(t * n + i * V) / p.group] = scale;
             }
             if (i < pieces) quantise8<OUT>(static_cast<uint8_t *>(p.y) + t * n + i * V, s[k], scale);
@@ -238,72 +286,72 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
     }
 }
 
-// Heads of 32 to 256 channels (a power of two), no scale over whole tokens: pieces of all tokens in a row, U a thread.
-constexpr int HEAD_NT = 256, HEAD_U = 2;
+// Heads of 32 to 256 channels (a power of two), no scale over whole tokens.  A CTA's threads lie side by side over the
+// pieces of `rows` tokens (blockIdx.x: over the parts of a long token); each takes its piece of U tokens, `rows` apart.
+constexpr int HEAD_NT = 256, HEAD_U = 4;
 
 template <typename T, int OUT, int LANES>
-__global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams p) {
+__global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams p, int rows) {
     dependent_prologue();
     constexpr int U = HEAD_U;
-    const unsigned n = p.H * p.d, pieces = n / V;
-    const unsigned total = p.T * pieces, first = blockIdx.x * (HEAD_NT * U) + threadIdx.x;  // (below 2^31: checked on the host)
-    Piece<T> x[U], r[U], z[U];
-    float s[U][V];
-    long long at[U];
+    const int n = p.H * p.d, pieces = n / V;
+    const int j = blockIdx.x * blockDim.x + threadIdx.x, row = j / pieces, c = (j - row * pieces) * V;
+    const long long t0 = (long long)blockIdx.y * (rows * U) + row;
+    const bool column = row < rows;
+    auto in = [&](int k) { return column && t0 + k * rows < p.T; };
+    Piece<T> x[U], z[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        const unsigned i = first + k * HEAD_NT;
-        const long long t = i / pieces, c = (i - (unsigned)t * pieces) * V;
-        at[k] = i < total ? t * n + c : -1;
         x[k].zero();
         z[k].zero();
-        if (i >= total) continue;
-        x[k].load(static_cast<const T *>(p.x) + t * p.x_stride + c);
-        if (p.z) z[k].load(static_cast<const T *>(p.z) + t * p.z_stride + c);
-        if (p.r) r[k].load(static_cast<const T *>(p.r) + t * p.r_stride + c);
+        if (!in(k)) continue;
+        x[k].load(static_cast<const T *>(p.x) + (t0 + k * rows) * p.x_stride + c);
+        if (p.z) z[k].load(static_cast<const T *>(p.z) + (t0 + k * rows) * p.z_stride + c);
     }
-    float w[V];  // (a thread's pieces lie at the same place of their heads: HEAD_NT is a multiple of the lanes)
+    F2 w[V / 2];
 #pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = 1.f;
-    if (p.w) {
-        read8(p.w + threadIdx.x % LANES * V, w);
+    for (int v = 0; v < V / 2; ++v) w[v] = F2(1.f);
+    if (p.w) {  // (a multiple of the lanes stands before each CTA's threads)
+        Piece<float> pw;
+        pw.load(p.w + j % LANES * V);
+        pw.to(w);
 #pragma unroll
-        for (int v = 0; v < V; ++v) w[v] += p.offset;
+        for (int v = 0; v < V / 2; ++v) w[v] = add2(w[v], F2(p.offset));
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        x[k].to(s[k]);
-        if (p.r && at[k] >= 0) {
-            float add[V];
-            r[k].to(add);
+        const long long at = (t0 + k * rows) * n + c;
+        F2 s[V / 2];
+        x[k].to(s);
+        if (p.r && in(k)) {
+            Piece<T> r;
+            F2 add[V / 2];
+            r.load(static_cast<const T *>(p.r) + (t0 + k * rows) * p.r_stride + c);
+            r.to(add);
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[k][v] = to_f32(from_f32<T>(s[k][v] + add[v]));
-            write8(static_cast<T *>(p.s_out) + at[k], s[k]);
+            for (int v = 0; v < V / 2; ++v) s[v] = add2(s[v], add[v]);
+            x[k].from(s);
+            x[k].to(s);
+            x[k].store(static_cast<T *>(p.s_out) + at);
         }
-        float sum = 0.f;
+        const F2 rstd(rsqrtf(lanes_sum(squares(s), LANES) * (1.f / (LANES * V)) + p.eps));
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum = fmaf(s[k][v], s[k][v], sum);
-        const float rstd = rsqrtf(lanes_sum(sum, LANES) * (1.f / (LANES * V)) + p.eps);
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[k][v] *= rstd * w[v];
+        for (int v = 0; v < V / 2; ++v) s[v] = mul2(s[v], mul2(rstd, w[v]));
         if (p.z) {
-            float gate[V];
+            F2 gate[V / 2];
             z[k].to(gate);
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[k][v] *= silu(gate[v]);
+            for (int v = 0; v < V / 2; ++v) s[v] = mul2(s[v], silu(gate[v]));
         }
         if constexpr (OUT == SAME) {
-            if (at[k] >= 0) write8(static_cast<T *>(p.y) + at[k], s[k]);
+            if (in(k)) write8(static_cast<T *>(p.y) + at, s);
         } else {
-            constexpr float MOST = OUT == GDN_INT8 ? 127.f : 448.f;
+            constexpr float ONE_MOST = OUT == GDN_INT8 ? 1.f / 127.f : 1.f / 448.f;
             const int group = p.group / V;
-            float m = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) m = max_or_nan(m, fabsf(s[k][v]));
-            const float scale = scale_of(lanes_max(m, group), MOST);
-            if (at[k] >= 0) {
-                if (threadIdx.x % group == 0) p.scale[at[k] / p.group] = scale;
-                quantise8<OUT>(static_cast<uint8_t *>(p.y) + at[k], s[k], scale);
+            const float scale = scale_of(lanes_max(largest(s, 0.f), group), ONE_MOST);
+            if (in(k)) {
+                if (j % group == 0) p.scale[at / p.group] = scale;
+                quantise8<OUT>(static_cast<uint8_t *>(p.y) + at, s, scale);
             }
         }
     }
@@ -322,7 +370,7 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_kernel(const RmsNormParams p,
     const T *z = p.z ? static_cast<const T *>(p.z) + t * p.z_stride : nullptr;
     T *s_out = r ? static_cast<T *>(p.s_out) + t * n : nullptr;
     const bool eight = out_dtype == GDN_FP8_E4M3 || out_dtype == GDN_INT8;
-    const float most = out_dtype == GDN_INT8 ? 127.f : 448.f;
+    const float most = out_dtype == GDN_INT8 ? 1.f / 127.f : 1.f / 448.f;
     const T *s = r ? s_out : x;
     float top = 0.f;
     int turn = 0;
@@ -581,13 +629,18 @@ cudaError_t forward_typed(const RmsNormParams &p, int out_dtype, cudaStream_t st
                      whole(p.z, p.z_stride, sizeof(T)) && whole(p.w, 0, 4) && whole(p.s_out, n, sizeof(T)) &&
                      (OUT == SAME ? whole(p.y, n, sizeof(T)) : reinterpret_cast<uintptr_t>(p.y) % 8 == 0);
     const long long pieces = n / V;
-    if (vec && lanes >= 4 && (OUT == SAME || p.group) && p.T * pieces <= INT32_MAX) {
-        const dim3 grid((unsigned)((p.T * pieces + HEAD_NT * HEAD_U - 1) / (HEAD_NT * HEAD_U))), block(HEAD_NT);
-        switch (lanes) {
-            case 4: return launch_dependent(norm_head_kernel<T, OUT, 4>, grid, block, 0, stream, p);
-            case 8: return launch_dependent(norm_head_kernel<T, OUT, 8>, grid, block, 0, stream, p);
-            case 16: return launch_dependent(norm_head_kernel<T, OUT, 16>, grid, block, 0, stream, p);
-            default: return launch_dependent(norm_head_kernel<T, OUT, 32>, grid, block, 0, stream, p);
+    if (vec && lanes >= 4 && (OUT == SAME || p.group)) {
+        const int rows = (int)std::max<long long>(1, HEAD_NT / pieces), parts = (int)((pieces * rows + HEAD_NT - 1) / HEAD_NT);
+        const int threads = (int)((pieces * rows + parts * 32 - 1) / (parts * 32)) * 32;
+        const long long runs = ((long long)p.T + rows * HEAD_U - 1) / (rows * HEAD_U);
+        if (runs <= 65535) {
+            const dim3 grid((unsigned)parts, (unsigned)runs), block((unsigned)threads);
+            switch (lanes) {
+                case 4: return launch_dependent(norm_head_kernel<T, OUT, 4>, grid, block, 0, stream, p, rows);
+                case 8: return launch_dependent(norm_head_kernel<T, OUT, 8>, grid, block, 0, stream, p, rows);
+                case 16: return launch_dependent(norm_head_kernel<T, OUT, 16>, grid, block, 0, stream, p, rows);
+                default: return launch_dependent(norm_head_kernel<T, OUT, 32>, grid, block, 0, stream, p, rows);
+            }
         }
     }
     if (vec && (p.H == 1 || lanes) && pieces <= 4096) {
