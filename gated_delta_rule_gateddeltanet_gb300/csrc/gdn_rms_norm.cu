@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "layer_internal.cuh"
+#include "ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
             const int i = threadIdx.x + k * threads;
             if (p.group) {  // (whole groups of lanes are past the end together)
                 scale = scale_of(lanes_max(largest(s[k], 0.f), p.group / V), ONE_MOST);
-                if (i < pieces && i % (p.group / V) == 0) p.scale[(t * n + i * V) / p.group] = scale;
+                if (i < pieces && (i & (p.group / V - 1)) == 0) p.scale[(t * n + i * V) >> (31 - __clz(p.group))] = scale;
             }
             if (i < pieces) quantise8<OUT>(static_cast<uint8_t *>(p.y) + t * n + i * V, s[k], scale);
         }
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
 
 // Heads of 32 to 256 channels (a power of two), no scale over whole tokens.  A CTA's threads lie side by side over the
 // pieces of `rows` tokens (blockIdx.x: over the parts of a long token); each takes its piece of U tokens, `rows` apart.
-constexpr int HEAD_NT = 256, HEAD_U = 4;
+constexpr int HEAD_NT = 128, HEAD_U = 4;
 
 template <typename T, int OUT, int LANES>
 __global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams p, int rows) {
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams 
         x[k].load(static_cast<const T *>(p.x) + (t0 + k * rows) * p.x_stride + c);
         if (p.z) z[k].load(static_cast<const T *>(p.z) + (t0 + k * rows) * p.z_stride + c);
     }
+    const int group = p.group / V, shift = 31 - __clz(p.group);  // (a power of two)
     F2 w[V / 2];
 #pragma unroll
     for (int v = 0; v < V / 2; ++v) w[v] = F2(1.f);
@@ -347,10 +349,9 @@ __global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams 
             if (in(k)) write8(static_cast<T *>(p.y) + at, s);
         } else {
             constexpr float ONE_MOST = OUT == GDN_INT8 ? 1.f / 127.f : 1.f / 448.f;
-            const int group = p.group / V;
             const float scale = scale_of(lanes_max(largest(s, 0.f), group), ONE_MOST);
             if (in(k)) {
-                if (j % group == 0) p.scale[at / p.group] = scale;
+                if ((j & (group - 1)) == 0) p.scale[at >> shift] = scale;
                 quantise8<OUT>(static_cast<uint8_t *>(p.y) + at, s, scale);
             }
         }
@@ -429,80 +430,84 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_kernel(const RmsNormParams p,
 // CTAs walk over tokens, so that a thread's channels and their part of dw stay the same; the parts are summed by a
 // second kernel in the order of the CTAs.
 
-// One piece of the gradient; e, n: as above.
-template <typename T>
-__device__ __forceinline__ void finish8(const RmsNormParams &p, long long at, const Piece<T> &r, const Piece<T> &z,
-                                        const float (&x)[V], const float (&dy)[V], const float (&w)[V], float rstd, float dot,
-                                        float (&part)[V]) {
-    float dx[V], dz[V], zv[V], rv[V];
-    if (p.z) z.to(zv);
-    if (p.r) r.to(rv);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const float n = x[v] * rstd;
-        float e = dy[v];
-        if (p.z) {
-            const float sig = sigmoid(zv[v]);
-            e = dy[v] * silu(zv[v]);
-            dz[v] = dy[v] * n * w[v] * (sig * fmaf(zv[v], 1.f - sig, 1.f));
-        }
-        part[v] = fmaf(e, n, part[v]);
-        dx[v] = rstd * fmaf(-n, dot, e * w[v]);
-        if (p.r) dx[v] += rv[v];
-    }
-    write8(static_cast<T *>(p.dx) + at, dx);
-    if (p.z) write8(static_cast<T *>(p.dz) + at, dz);
-}
+// Rows arrive in a ring of stages in shared memory, a bulk copy a row of each input, as far ahead as there is room; a
+// CTA takes every gridDim-th token, thread i its pieces i, i + threads, .. (U at most).
+constexpr int RING_NT = 256, MAX_STAGES = 8;
+constexpr size_t RING_BYTES = 100 * 1024;  // of a CTA, two of which share an SM
 
-// A CTA takes every gridDim-th token: thread i holds pieces i, i + threads, .. of it (U at most).
-template <typename T, int U>
-__global__ void __launch_bounds__(512) norm_token_backward_kernel(const RmsNormParams p, int lanes) {
+template <typename T, int U, int NT>
+__global__ void __launch_bounds__(NT, 2 * RING_NT / NT) norm_ring_backward_kernel(const RmsNormParams p, int lanes, int stages) {
     dependent_prologue();
-    __shared__ float2 buf[2][16];
-    const int n = p.H * p.d, pieces = n / V, threads = blockDim.x;
-    float part[U][V] = {}, w[U][V];
+    extern __shared__ __align__(128) unsigned char raw[];
+    __shared__ float2 buf[2][32];
+    __shared__ uint64_t full[MAX_STAGES];
+    const int n = p.H * p.d, pieces = n / V, threads = blockDim.x, arrays = 2 + (p.r != nullptr) + (p.z != nullptr);
+    const uint32_t row_bytes = (uint32_t)n * sizeof(T);
+    T *ring = reinterpret_cast<T *>(raw);
+    auto fetch = [&](int stage, long long t) {
+        T *dst = ring + (long long)stage * arrays * n;
+        ptx::mbar_arrive_expect_tx(&full[stage], row_bytes * arrays);
+        ptx::bulk_g2s(dst, static_cast<const T *>(p.x) + t * p.x_stride, row_bytes, &full[stage]);
+        ptx::bulk_g2s(dst += n, static_cast<const T *>(p.dy) + t * p.dy_stride, row_bytes, &full[stage]);
+        if (p.r) ptx::bulk_g2s(dst += n, static_cast<const T *>(p.r) + t * p.r_stride, row_bytes, &full[stage]);
+        if (p.z) ptx::bulk_g2s(dst += n, static_cast<const T *>(p.z) + t * p.z_stride, row_bytes, &full[stage]);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[s], 1);
+        ptx::fence_mbar_init();
+        for (int s = 0; s < stages; ++s) {
+            const long long t = blockIdx.x + (long long)s * gridDim.x;
+            if (t < p.T) fetch(s, t);
+        }
+    }
+    F2 part[U][V / 2], w[U][V / 2];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int i = threadIdx.x + k * threads;
 #pragma unroll
-        for (int v = 0; v < V; ++v) w[k][v] = 1.f;
+        for (int v = 0; v < V / 2; ++v) part[k][v] = F2(0.f), w[k][v] = F2(1.f);
         if (p.w && i < pieces) {
-            read8(p.w + i * V % p.d, w[k]);
+            Piece<float> pw;
+            pw.load(p.w + i * V % p.d);
+            pw.to(w[k]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) w[k][v] += p.offset;
+            for (int v = 0; v < V / 2; ++v) w[k][v] = add2(w[k][v], F2(p.offset));
         }
     }
-    int turn = 0;
+    __syncthreads();
+    const float mean = 1.f / (float)p.d;
+    int stage = 0, turn = 0;
+    uint32_t parity = 0;
     for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
-        Piece<T> px[U], pdy[U], z[U], r[U];
-        float x[U][V], dy[U][V];
+        ptx::mbar_wait_bounded(&full[stage], parity, 2000000000ll);
+        const T *src = ring + (long long)stage * arrays * n;
+        Piece<T> x[U], dy[U], r[U], z[U];
+        float2 sum[U], all = make_float2(0.f, 0.f);  // of s^2 and of e w s: mean(e w n) = rstd mean(e w s)
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int i = threadIdx.x + k * threads;
-            px[k].zero();
-            pdy[k].zero();
-            z[k].zero();
-            if (i >= pieces) continue;
-            px[k].load(static_cast<const T *>(p.x) + t * p.x_stride + i * V);
-            pdy[k].load(static_cast<const T *>(p.dy) + t * p.dy_stride + i * V);
-            if (p.z) z[k].load(static_cast<const T *>(p.z) + t * p.z_stride + i * V);
-            if (p.r) r[k].load(static_cast<const T *>(p.r) + t * p.r_stride + i * V);
-        }
-        // the sums of s^2 and of e w s together: mean(e w n) = rstd mean(e w s)
-        float2 sum[U], all = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            float zv[V];
-            px[k].to(x[k]);
-            pdy[k].to(dy[k]);
-            z[k].to(zv);
             sum[k] = make_float2(0.f, 0.f);
+            if (i < pieces) {
+                const T *at = src + i * V;
+                F2 xf[V / 2], e[V / 2];
+                x[k].load(at);
+                dy[k].load(at += n);
+                if (p.r) r[k].load(at += n);
+                x[k].to(xf);
+                dy[k].to(e);
+                if (p.z) {
+                    F2 zf[V / 2];
+                    z[k].load(at += n);
+                    z[k].to(zf);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float e = dy[k][v];
-                if (p.z) e *= silu(zv[v]);
-                sum[k].x = fmaf(x[k][v], x[k][v], sum[k].x);
-                sum[k].y = fmaf(e * w[k][v], x[k][v], sum[k].y);
+                    for (int v = 0; v < V / 2; ++v) e[v] = mul2(e[v], silu(zf[v]));
+                }
+                F2 dot(0.f);
+#pragma unroll
+                for (int v = 0; v < V / 2; ++v) dot = fma2(mul2(e[v], w[k][v]), xf[v], dot);
+                float a, b;
+                dot.get(a, b);
+                sum[k] = make_float2(squares(xf), a + b);
             }
             all.x += sum[k].x;
             all.y += sum[k].y;
@@ -513,13 +518,15 @@ __global__ void __launch_bounds__(512) norm_token_backward_kernel(const RmsNormP
         } else {
             all = make_float2(lanes_sum(all.x, 32), lanes_sum(all.y, 32));
             turn ^= 1;
-            const int lane = threadIdx.x % 32, warps = (threads + 31) / 32;
-            if (lane == 0) buf[turn][threadIdx.x / 32] = all;
-            __syncthreads();
-            all = lane < warps ? buf[turn][lane] : make_float2(0.f, 0.f);
-            all = make_float2(lanes_sum(all.x, 16), lanes_sum(all.y, 16));
-            all.x = __shfl_sync(0xffffffffu, all.x, 0);
-            all.y = __shfl_sync(0xffffffffu, all.y, 0);
+            if (threadIdx.x % 32 == 0) buf[turn][threadIdx.x / 32] = all;
+        }
+        __syncthreads();  // every thread has its pieces: the stage can be filled again
+        if (threadIdx.x == 0 && t + (long long)stages * gridDim.x < p.T) fetch(stage, t + (long long)stages * gridDim.x);
+        if (++stage == stages) stage = 0, parity ^= 1;
+        if (!lanes) {
+            const int lane = threadIdx.x % 32;
+            all = lane < threads / 32 ? buf[turn][lane] : make_float2(0.f, 0.f);
+            all = make_float2(lanes_sum(all.x, 32), lanes_sum(all.y, 32));
 #pragma unroll
             for (int k = 0; k < U; ++k) sum[k] = all;
         }
@@ -527,8 +534,36 @@ __global__ void __launch_bounds__(512) norm_token_backward_kernel(const RmsNormP
         for (int k = 0; k < U; ++k) {
             const int i = threadIdx.x + k * threads;
             if (i >= pieces) continue;
-            const float rstd = rsqrtf(sum[k].x / (float)p.d + p.eps), dot = sum[k].y * rstd / (float)p.d;
-            finish8<T>(p, t * n + i * V, r[k], z[k], x[k], dy[k], w[k], rstd, dot, part[k]);
+            const float rs = rsqrtf(sum[k].x * mean + p.eps);
+            const F2 rstd(rs), minus_dot(-sum[k].y * rs * mean);
+            F2 xf[V / 2], e[V / 2], add[V / 2];
+            x[k].to(xf);
+            dy[k].to(e);
+            if (p.r) r[k].to(add);
+            if (p.z) {
+                F2 zf[V / 2];
+                z[k].to(zf);
+#pragma unroll
+                for (int v = 0; v < V / 2; ++v) {
+                    // silu = z sig, silu' = sig (1 + z (1 - sig))
+                    float a, b;
+                    zf[v].get(a, b);
+                    const F2 sig(sigmoid(a), sigmoid(b));
+                    const F2 slope = mul2(sig, fma2(zf[v], fma2(sig, F2(-1.f), F2(1.f)), F2(1.f)));
+                    const F2 dyn = mul2(e[v], mul2(xf[v], rstd));
+                    e[v] = mul2(e[v], mul2(zf[v], sig));
+                    zf[v] = mul2(mul2(dyn, w[k][v]), slope);
+                }
+                write8(static_cast<T *>(p.dz) + t * n + i * V, zf);
+            }
+#pragma unroll
+            for (int v = 0; v < V / 2; ++v) {
+                const F2 nx = mul2(xf[v], rstd);
+                part[k][v] = fma2(e[v], nx, part[k][v]);
+                xf[v] = mul2(rstd, fma2(nx, minus_dot, mul2(e[v], w[k][v])));
+                if (p.r) xf[v] = add2(xf[v], add[v]);
+            }
+            write8(static_cast<T *>(p.dx) + t * n + i * V, xf);
         }
     }
     if (p.dw) {
@@ -618,8 +653,16 @@ int head_lanes(int d) { return d % V == 0 && d / V <= 32 && power_of_two(d / V) 
 // Threads of a CTA that takes a token of `pieces`, U each: whole warps, as even as can be.
 int token_threads(int pieces, int U) { return ((pieces + U - 1) / U + 31) / 32 * 32; }
 
+// Threads of a CTA of the ring: as many as a token has pieces up to RING_NT, which may have two each; twice that beyond.
+int ring_threads(long long pieces) {
+    return pieces > 2 * RING_NT ? 2 * RING_NT : (int)std::min<long long>(RING_NT, (pieces + 31) / 32 * 32);
+}
+
 // CTAs that walk over the tokens backwards: what is resident at once, or one a token.
-int backward_ctas(int T) { return (int)std::min<long long>(T, 4LL * current_device_sms()); }
+int backward_ctas(int T, long long n) {
+    const int a_sm = std::min(8, 2 * RING_NT / ring_threads(n / V + 1));
+    return (int)std::min<long long>(T, (long long)a_sm * current_device_sms());
+}
 
 template <typename T, int OUT>
 cudaError_t forward_typed(const RmsNormParams &p, int out_dtype, cudaStream_t stream) {
@@ -664,22 +707,35 @@ cudaError_t forward_out(const RmsNormParams &p, int out_dtype, cudaStream_t stre
     }
 }
 
+template <typename T, int U, int NT>
+cudaError_t launch_ring(const RmsNormParams &p, int ctas, int threads, int lanes, size_t stage, cudaStream_t stream) {
+    // (two CTAs of RING_NT threads share an SM; more, smaller ones share it too)
+    const size_t room = std::max(stage * 2, RING_BYTES * 2 * (size_t)threads / (2 * RING_NT));
+    const int stages = (int)std::min<size_t>(MAX_STAGES, room / stage);
+    auto kernel = norm_ring_backward_kernel<T, U, NT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (int)RING_BYTES);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3((unsigned)ctas), dim3((unsigned)threads), stages * stage, stream, p, lanes, stages);
+}
+
 template <typename T>
 cudaError_t backward_typed(const RmsNormParams &p, cudaStream_t stream) {
     const long long n = (long long)p.H * p.d, pieces = n / V;
-    const int lanes = head_lanes(p.d), ctas = backward_ctas(p.T);
+    const int lanes = p.H > 1 ? head_lanes(p.d) : 0, ctas = backward_ctas(p.T, n);
+    const size_t stage = (size_t)(2 + (p.r != nullptr) + (p.z != nullptr)) * n * sizeof(T);
     cudaError_t e = cudaSuccess;
     if (p.T > 0) {
-        const bool vec = n % V == 0 && p.d % V == 0 && whole(p.x, p.x_stride, sizeof(T)) && whole(p.dy, p.dy_stride, sizeof(T)) &&
+        const bool vec = p.d % V == 0 && whole(p.x, p.x_stride, sizeof(T)) && whole(p.dy, p.dy_stride, sizeof(T)) &&
                          whole(p.r, p.r_stride, sizeof(T)) && whole(p.z, p.z_stride, sizeof(T)) && whole(p.w, 0, 4) &&
                          whole(p.dx, n, sizeof(T)) && whole(p.dz, n, sizeof(T));
-        const dim3 grid((unsigned)ctas);
-        if (vec && (p.H == 1 || lanes) && pieces <= 512)
-            e = launch_dependent(norm_token_backward_kernel<T, 1>, grid, dim3(token_threads((int)pieces, 1)), 0, stream, p, p.H > 1 ? lanes : 0);
-        else if (vec && (p.H == 1 || lanes) && pieces <= 1024)
-            e = launch_dependent(norm_token_backward_kernel<T, 2>, grid, dim3(token_threads((int)pieces, 2)), 0, stream, p, p.H > 1 ? lanes : 0);
-        else
-            e = launch_dependent(norm_any_backward_kernel<T>, grid, dim3(ANY_NT), 0, stream, p);
+        if (vec && (p.H == 1 || lanes) && pieces <= 4 * RING_NT && stage <= RING_BYTES) {
+            const int threads = ring_threads(pieces);
+            if (pieces <= RING_NT) e = launch_ring<T, 1, RING_NT>(p, ctas, threads, lanes, stage, stream);
+            else if (pieces <= 2 * RING_NT) e = launch_ring<T, 2, RING_NT>(p, ctas, threads, lanes, stage, stream);
+            else e = launch_ring<T, 2, 2 * RING_NT>(p, ctas, threads, lanes, stage, stream);
+        } else {
+            e = launch_dependent(norm_any_backward_kernel<T>, dim3((unsigned)ctas), dim3(ANY_NT), 0, stream, p);
+        }
     }
     if (e != cudaSuccess || !p.dw) return e;
     return launch_dependent(norm_sums_kernel, dim3((unsigned)((p.d + 31) / 32)), dim3(32 * SUM_WARPS), 0, stream, p, ctas);
@@ -687,7 +743,7 @@ cudaError_t backward_typed(const RmsNormParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t rms_norm_backward_workspace_bytes(int T, int H, int d) { return 4 * (size_t)backward_ctas(T) * H * d; }
+size_t rms_norm_backward_workspace_bytes(int T, int H, int d) { return 4 * (size_t)backward_ctas(T, (long long)H * d) * H * d; }
 
 cudaError_t launch_rms_norm(const RmsNormParams &p, int io_dtype, int out_dtype, cudaStream_t stream) {
     switch (io_dtype) {
