@@ -99,35 +99,42 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
 
         // every token's state and decay with nothing in front of the half-warp's tokens
         const unsigned reset = bits_of<TT>(tokens.reset, sub), loads = bits_of<TT>(tokens.load, sub);
+        const unsigned valid = bits_of<TT>(tokens.valid, sub), lasts = bits_of<TT>(tokens.last, sub);
+        // most runs lie inside a sequence
+        const bool plain = __all_sync(0xffffffffu, (reset | lasts) == 0 && valid == (1u << TT) - 1);
         F2 h[TT][PAIRS], P[TT][PAIRS];
+        auto scan = [&](auto inside_a_sequence) {
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            const int r = sub * TT + i;
-            float x[VC], a[VC], b[VC] = {};
-            read<T, VC>(sm.x + r * SLAB + lane * VC, x);
-            read<G, VC>(sm.a + r * SLAB + lane * VC, a);
-            if (has_b) read<G, VC>(sm.b + r * SLAB + lane * VC, b);
-            const bool cut = reset >> i & 1;
-            F2 front[PAIRS];
+            for (int i = 0; i < TT; ++i) {
+                const int r = sub * TT + i;
+                float x[VC], a[VC], b[VC] = {};
+                read<T, VC>(sm.x + r * SLAB + lane * VC, x);
+                read<G, VC>(sm.a + r * SLAB + lane * VC, a);
+                if (has_b) read<G, VC>(sm.b + r * SLAB + lane * VC, b);
+                F2 front[PAIRS];
 #pragma unroll
-            for (int v = 0; v < PAIRS; ++v) {
-                front[v] = F2(0.f);
-                if (i > 0 && !cut) front[v] = h[i - 1][v];
+                for (int v = 0; v < PAIRS; ++v) {
+                    front[v] = F2(0.f);
+                    if (i > 0 && (inside_a_sequence || !(reset >> i & 1))) front[v] = h[i - 1][v];
+                }
+                if (!inside_a_sequence && (loads >> i & 1) && p.init) {
+                    float h0[VC];
+                    load<VC>(p.init + (long long)tokens.slot[r] * p.C + c0, h0, inside, false);
+#pragma unroll
+                    for (int v = 0; v < PAIRS; ++v) front[v] = F2(h0[2 * v], h0[2 * v + 1]);
+                }
+#pragma unroll
+                for (int v = 0; v < PAIRS; ++v) {
+                    F2 g, w;
+                    gate_pair<MODE>(F2(a[2 * v], a[2 * v + 1]), F2(b[2 * v], b[2 * v + 1]), rate[v], dt[v], has_b, g, w);
+                    const F2 u = mul2(w, F2(x[2 * v], x[2 * v + 1]));
+                    h[i][v] = i == 0 && inside_a_sequence ? u : fma2(g, front[v], u);
+                    P[i][v] = i == 0 ? g : mul2(g, P[i - 1][v]);
+                }
             }
-            if ((loads >> i & 1) && p.init) {
-                float h0[VC];
-                load<VC>(p.init + (long long)tokens.slot[r] * p.C + c0, h0, inside, false);
-#pragma unroll
-                for (int v = 0; v < PAIRS; ++v) front[v] = F2(h0[2 * v], h0[2 * v + 1]);
-            }
-#pragma unroll
-            for (int v = 0; v < PAIRS; ++v) {
-                F2 g, w;
-                gate_pair<MODE>(F2(a[2 * v], a[2 * v + 1]), F2(b[2 * v], b[2 * v + 1]), rate[v], dt[v], has_b, g, w);
-                h[i][v] = fma2(g, front[v], mul2(w, F2(x[2 * v], x[2 * v + 1])));
-                P[i][v] = i == 0 ? g : mul2(g, P[i - 1][v]);
-            }
-        }
+        };
+        if (plain) scan(std::true_type());
+        else scan(std::false_type());
         {
             Pack<float, VC> A, B;
 #pragma unroll
@@ -192,20 +199,29 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
         F2 front2[PAIRS];
 #pragma unroll
         for (int v = 0; v < PAIRS; ++v) front2[v] = F2(front[2 * v], front[2 * v + 1]);
-        const unsigned valid = bits_of<TT>(tokens.valid, sub), lasts = bits_of<TT>(tokens.last, sub);
         T *y = static_cast<T *>(p.y) + (long long)first * p.C + c0;
+        if (plain && access.y) {
 #pragma unroll
-        for (int i = 0; i < TT; ++i, y += p.C) {
-            float out[VC];
-            const bool open = !(reset & ((2u << i) - 1));
+            for (int i = 0; i < TT; ++i, y += p.C) {
+                float out[VC];
 #pragma unroll
-            for (int v = 0; v < PAIRS; ++v) {
-                if (open) h[i][v] = fma2(P[i][v], front2[v], h[i][v]);
-                h[i][v].get(out[2 * v], out[2 * v + 1]);
+                for (int v = 0; v < PAIRS; ++v) fma2(P[i][v], front2[v], h[i][v]).get(out[2 * v], out[2 * v + 1]);
+                if (inside > 0) store<T, VC>(y, out, VC, true);
             }
-            if (valid >> i & 1) store<T, VC>(y, out, inside, access.y);
-            if ((lasts >> i & 1) && p.final_state)
-                store<float, VC>(p.final_state + (long long)tokens.slot[sub * TT + i] * p.C + c0, out, inside, false);
+        } else {
+#pragma unroll
+            for (int i = 0; i < TT; ++i, y += p.C) {
+                float out[VC];
+                const bool open = !(reset & ((2u << i) - 1));
+#pragma unroll
+                for (int v = 0; v < PAIRS; ++v) {
+                    if (open) h[i][v] = fma2(P[i][v], front2[v], h[i][v]);
+                    h[i][v].get(out[2 * v], out[2 * v + 1]);
+                }
+                if (valid >> i & 1) store<T, VC>(y, out, inside, access.y);
+                if ((lasts >> i & 1) && p.final_state)
+                    store<float, VC>(p.final_state + (long long)tokens.slot[sub * TT + i] * p.C + c0, out, inside, false);
+            }
         }
     }
 

@@ -189,8 +189,17 @@ __device__ __forceinline__ void read(const E *src, float (&f)[VC]) {
     else if constexpr (sizeof(E) * VC == 8) v.u2 = *reinterpret_cast<const uint2 *>(src);
     else if constexpr (sizeof(E) * VC == 4) v.u1 = *reinterpret_cast<const uint32_t *>(src);
     else v.e[0] = *src;
+    if constexpr (std::is_same<E, __nv_bfloat16>::value && VC % 2 == 0) {
+        // (an instruction a number: BF16 is the upper half of FP32)
 #pragma unroll
-    for (int i = 0; i < VC; ++i) f[i] = to_f32(v.e[i]);
+        for (int i = 0; i < VC; i += 2) {
+            f[i] = __uint_as_float(v.words[i / 2] << 16);
+            f[i + 1] = __uint_as_float(v.words[i / 2] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VC; ++i) f[i] = to_f32(v.e[i]);
+    }
 }
 
 template <int VC>
