@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
 
     const int step = cluster * TILE, rounds = (p.T + step - 1) / step;
     fetch(rank * TILE);
-    tokens_of(sm.tokens[0], p, rank * TILE, slab == 0, tid - (NT - TILE));
+    tokens_of(sm.tokens[0], p, rank * TILE, slab == 0, tid / 32 - (NT - TILE) / 32);
     if (blockIdx.x == 0) check_packing(p);
     if (cluster > 1) cluster_sync();  // every CTA has its barriers before another writes to its shared memory
     float run = 0.f;  // the state in front of the cluster's tiles, channel tid of the slab
@@ -98,10 +98,11 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
         __syncthreads();
 
         // every token's state and decay with nothing in front of the half-warp's tokens
-        const unsigned reset = bits_of<TT>(tokens.reset, sub), loads = bits_of<TT>(tokens.load, sub);
-        const unsigned valid = bits_of<TT>(tokens.valid, sub), lasts = bits_of<TT>(tokens.last, sub);
-        // most runs lie inside a sequence
-        const bool plain = __all_sync(0xffffffffu, (reset | lasts) == 0 && valid == (1u << TT) - 1);
+        const bool plain = tokens.plain;  // as most are
+        const unsigned reset = plain ? 0 : bits_of<TT>(tokens.reset, sub), loads = plain ? 0 : bits_of<TT>(tokens.load, sub);
+        const unsigned valid = plain ? (1u << TT) - 1 : bits_of<TT>(tokens.valid, sub);
+        const unsigned lasts = plain ? 0 : bits_of<TT>(tokens.last, sub);
+        const bool quick = plain || __all_sync(0xffffffffu, (reset | lasts) == 0 && valid == (1u << TT) - 1);  // the warp's tokens
         F2 h[TT][PAIRS], P[TT][PAIRS];
         auto scan = [&](auto inside_a_sequence) {
 #pragma unroll
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
                 }
             }
         };
-        if (plain) scan(std::true_type());
+        if (quick) scan(std::true_type());
         else scan(std::false_type());
         {
             Pack<float, VC> A, B;
@@ -159,10 +160,13 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
             for (int s = 0; s < SUBS; ++s) {
                 sm.A[s][tid] = A;
                 sm.B[s][tid] = B;
-                const bool cut = bits_of<TT>(tokens.reset, s);
-                B = cut ? b[s] : fmaf(a[s], B, b[s]);
-                A = cut ? 0.f : a[s] * A;
-                closed |= cut;
+                B = fmaf(a[s], B, b[s]);
+                A *= a[s];
+                if (!plain && bits_of<TT>(tokens.reset, s)) {
+                    B = b[s];
+                    A = 0.f;
+                    closed = true;
+                }
             }
             if (cluster > 1) {
                 uint64_t *bar = &sm.maps[buf];
@@ -180,13 +184,15 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
                 run = closed ? B : fmaf(A, run, B);
             }
         }
-        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 + step, slab == 0, tid - (NT - TILE));  // (not by the threads above)
+        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 + step, slab == 0, tid / 32 - (NT - TILE) / 32);  // (not by the threads above)
         __syncthreads();
 
-        // whether a reset stands before the half-warp's tokens in the tile
-        unsigned before = tokens.reset[sub * TT / 32] & ((1u << (sub * TT % 32)) - 1);
+        unsigned before = 0;  // whether a reset stands before the half-warp's tokens in the tile
+        if (!plain) {
+            before = tokens.reset[sub * TT / 32] & ((1u << (sub * TT % 32)) - 1);
 #pragma unroll
-        for (int w = 0; w < TILE / 32 - 1; ++w) before |= w < sub * TT / 32 ? tokens.reset[w] : 0;
+            for (int w = 0; w < TILE / 32 - 1; ++w) before |= w < sub * TT / 32 ? tokens.reset[w] : 0;
+        }
         float front[VC], A[VC], B[VC], carry[VC];
         read<float, VC>(&sm.A[sub][lane * VC], A);
         read<float, VC>(&sm.B[sub][lane * VC], B);
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
 #pragma unroll
         for (int v = 0; v < PAIRS; ++v) front2[v] = F2(front[2 * v], front[2 * v + 1]);
         T *y = static_cast<T *>(p.y) + (long long)first * p.C + c0;
-        if (plain && access.y) {
+        if (quick && access.y) {
 #pragma unroll
             for (int i = 0; i < TT; ++i, y += p.C) {
                 float out[VC];

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
     const int step = cluster * TILE, rounds = (p.T + step - 1) / step;
     if (rounds > 0) {  // (a call without tokens has none)
         fetch((rounds - 1) * step + rank * TILE, 0);
-        tokens_of(sm.tokens[0], p, (rounds - 1) * step + rank * TILE, slab == 0, tid - (NT - TILE));
+        tokens_of(sm.tokens[0], p, (rounds - 1) * step + rank * TILE, slab == 0, tid / 32 - (NT - TILE) / 32);
     }
     if (blockIdx.x == 0) check_packing(p);
     if (cluster > 1) cluster_sync();  // every CTA has its barriers before another writes to its shared memory
@@ -112,10 +112,12 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         copies_done();
         __syncthreads();
         const bool more = n + 1 < rounds;
-        const unsigned reset = bits_of<TT>(tokens.reset, sub), loads = bits_of<TT>(tokens.load, sub);
-        const unsigned valid = bits_of<TT>(tokens.valid, sub), lasts = bits_of<TT>(tokens.last, sub);
+        constexpr unsigned ALL = (1u << TT) - 1;
+        const bool plain = tokens.plain;  // as most are
+        const unsigned reset = plain ? 0 : bits_of<TT>(tokens.reset, sub), loads = plain ? 0 : bits_of<TT>(tokens.load, sub);
+        const unsigned valid = plain ? ALL : bits_of<TT>(tokens.valid, sub), lasts = plain ? 0 : bits_of<TT>(tokens.last, sub);
         // Backwards a sequence's last token cuts off what stands behind it, and so does one of no sequence.
-        const unsigned cuts = lasts | (~valid & ((1u << TT) - 1));
+        const unsigned cuts = lasts | (~valid & ALL);
         const int place = sub * TT * SLAB + lane * VC;
         auto row = [&](int i) { return (long long)tokens.slot[sub * TT + i] * p.C + c0; };
 
@@ -179,10 +181,13 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
             for (int s = SUBS - 1; s >= 0; --s) {
                 sm.RA[s][tid] = A;
                 sm.RB[s][tid] = B;
-                const bool cut = bits_of<TT>(tokens.last, s) | (bits_of<TT>(tokens.valid, s) ^ ((1u << TT) - 1));
-                B = cut ? b[s] : fmaf(a[s], B, b[s]);
-                A = cut ? 0.f : a[s] * A;
-                closed |= cut;
+                B = fmaf(a[s], B, b[s]);
+                A *= a[s];
+                if (!plain && (bits_of<TT>(tokens.last, s) | (bits_of<TT>(tokens.valid, s) ^ ALL))) {
+                    B = b[s];
+                    A = 0.f;
+                    closed = true;
+                }
             }
             if (cluster > 1) {
                 uint64_t *bar = &sm.maps[buf];
@@ -207,10 +212,10 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
             for (int s = 0; s < SUBS; ++s) {
                 const float a = sm.FA[s][c], b = sm.FB[s][c];
                 sm.FB[s][c] = h;
-                h = bits_of<TT>(tokens.reset, s) ? b : fmaf(a, h, b);
+                h = !plain && bits_of<TT>(tokens.reset, s) ? b : fmaf(a, h, b);
             }
         }
-        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 - step, slab == 0, tid - (NT - TILE));  // (not by the threads above)
+        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 - step, slab == 0, tid / 32 - (NT - TILE) / 32);  // (not by the threads above)
         __syncthreads();
 
         // the states again, each before its token
@@ -236,11 +241,13 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         }
         // whether something cuts off what stands behind the half-warp's tokens within the tile
         bool cut = false;
+        if (!plain) {
 #pragma unroll
-        for (int w = 0; w < TILE / 32; ++w) {
-            const unsigned c = tokens.last[w] | ~tokens.valid[w];
-            const int own = sub * TT / 32;
-            cut |= w > own ? c != 0 : w == own ? (c >> (sub * TT % 32) >> TT) != 0 : false;
+            for (int w = 0; w < TILE / 32; ++w) {
+                const unsigned c = tokens.last[w] | ~tokens.valid[w];
+                const int own = sub * TT / 32;
+                cut |= w > own ? c != 0 : w == own ? (c >> (sub * TT % 32) >> TT) != 0 : false;
+            }
         }
         float m[VC], sum_A[VC] = {}, sum_dt[VC] = {};
         {

@@ -39,9 +39,9 @@ __device__ __forceinline__ int last_start(const int32_t *cu, int hi, int t) {
     return lo;
 }
 
-// What token t is, and its sequence's slot.
-__device__ __forceinline__ int token_of(const RecurrenceParams &p, int t, bool flag, int &slot) {
-    slot = 0;
+// What token t is, its sequence's slot, and the tokens from it to its sequence's end.
+__device__ __forceinline__ int token_of(const RecurrenceParams &p, int t, bool flag, int &slot, int &rest) {
+    slot = rest = 0;
     if (t >= p.T || p.B == 0) return RESET;
     int b, begin, end;
     if (p.cu) {
@@ -53,37 +53,44 @@ __device__ __forceinline__ int token_of(const RecurrenceParams &p, int t, bool f
         begin = b * p.S;
         end = begin + p.S;
     }
-    if (t < begin || t >= end) return RESET;
+    if (t < begin || t >= end || end > p.T) return RESET;  // (the last: a packing out of order)
     slot = p.slots ? p.slots[b] : b;
     if (slot < 0 || slot >= p.num_slots) {
         if (flag) flag_error(p.status, GDN_DEVERR_STATE_SLOT);
         slot = 0;
         return RESET;
     }
+    rest = end - t;
     return VALID | (t == begin ? RESET | LOAD : 0) | (t == end - 1 ? LAST : 0);
 }
 
 // Which of a tile's tokens are what, a bit a token, and their slots.
 template <int TILE>
 struct Tokens {
+    int plain;  // the tile lies inside a sequence, without its first and last token: the rest is not set
     unsigned reset[TILE / 32], load[TILE / 32], last[TILE / 32], valid[TILE / 32];
     int slot[TILE];
 };
 
-// Fills them for the tile at t0 (whole warps of TILE threads i).
+// Fills them for the tile at t0 (TILE / 32 warps, w: which of them).
 template <int TILE>
-__device__ __forceinline__ void tokens_of(Tokens<TILE> &k, const RecurrenceParams &p, int t0, bool flag, int i) {
-    if (i < 0 || i >= TILE) return;
-    int slot;
-    const int what = token_of(p, t0 + i, flag, slot);
-    k.slot[i] = slot;
+__device__ __forceinline__ void tokens_of(Tokens<TILE> &k, const RecurrenceParams &p, int t0, bool flag, int w) {
+    if (w < 0) return;
+    const int lane = threadIdx.x % 32;
+    int slot, rest;
+    int what = token_of(p, t0, flag, slot, rest);
+    const bool plain = what == VALID && rest > TILE;
+    if (w == 0 && lane == 0) k.plain = plain;
+    if (plain) return;
+    what = token_of(p, t0 + 32 * w + lane, flag, slot, rest);
+    k.slot[32 * w + lane] = slot;
     const unsigned reset = __ballot_sync(0xffffffffu, what & RESET), load = __ballot_sync(0xffffffffu, what & LOAD);
     const unsigned last = __ballot_sync(0xffffffffu, what & LAST), valid = __ballot_sync(0xffffffffu, what & VALID);
-    if (i % 32 == 0) {
-        k.reset[i / 32] = reset;
-        k.load[i / 32] = load;
-        k.last[i / 32] = last;
-        k.valid[i / 32] = valid;
+    if (lane == 0) {
+        k.reset[w] = reset;
+        k.load[w] = load;
+        k.last[w] = last;
+        k.valid[w] = valid;
     }
 }
 
