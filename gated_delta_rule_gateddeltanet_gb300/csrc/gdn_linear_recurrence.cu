@@ -126,11 +126,11 @@ __global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParam
                 }
 #pragma unroll
                 for (int v = 0; v < PAIRS; ++v) {
-                    F2 g, w;
-                    gate_pair<MODE>(F2(a[2 * v], a[2 * v + 1]), F2(b[2 * v], b[2 * v + 1]), rate[v], dt[v], has_b, g, w);
-                    const F2 u = mul2(w, F2(x[2 * v], x[2 * v + 1]));
-                    h[i][v] = i == 0 && inside_a_sequence ? u : fma2(g, front[v], u);
-                    P[i][v] = i == 0 ? g : mul2(g, P[i - 1][v]);
+                    const GatePair q =
+                        gate_pair<MODE>(F2(a[2 * v], a[2 * v + 1]), F2(b[2 * v], b[2 * v + 1]), rate[v], dt[v], has_b);
+                    const F2 u = mul2(weight_of<MODE>(q), F2(x[2 * v], x[2 * v + 1]));
+                    h[i][v] = i == 0 && inside_a_sequence ? u : fma2(q.g, front[v], u);
+                    P[i][v] = i == 0 ? q.g : mul2(q.g, P[i - 1][v]);
                 }
             }
         };

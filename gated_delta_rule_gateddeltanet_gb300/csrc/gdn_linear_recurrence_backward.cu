@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
     dependent_prologue();
     using S = Shape<T, MODE>;
     using G = typename S::G;
-    constexpr int VC = S::VC, SLAB = S::SLAB;
+    constexpr int VC = S::VC, SLAB = S::SLAB, PAIRS = VC / 2;
     constexpr bool RAW = MODE != RECUR_PRECOMPUTED;
     extern __shared__ __align__(128) unsigned char raw[];
     typename S::Shared &sm = *reinterpret_cast<typename S::Shared *>(raw);
@@ -59,11 +59,16 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
     const int s0 = slab * SLAB, c0 = s0 + lane * VC, inside = p.C - c0;
     const bool has_b = p.b != nullptr;
 
-    float rate[VC], dt[VC];
+    F2 rate[PAIRS], dt[PAIRS];
 #pragma unroll
-    for (int v = 0; v < VC; ++v) {
-        rate[v] = RAW && v < inside ? expf(p.A_log[c0 + v]) : 0.f;
-        dt[v] = RAW && v < inside ? p.dt_bias[c0 + v] : 0.f;
+    for (int v = 0; v < PAIRS; ++v) {
+        float r[2] = {}, d[2] = {};
+        if (RAW)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (2 * v + k < inside) r[k] = -LOG2E * expf(p.A_log[c0 + 2 * v + k]), d[k] = p.dt_bias[c0 + 2 * v + k];
+        rate[v] = F2(r[0], r[1]);
+        dt[v] = F2(d[0], d[1]);
     }
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -121,52 +126,62 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         const int place = sub * TT * SLAB + lane * VC;
         auto row = [&](int i) { return (long long)tokens.slot[sub * TT + i] * p.C + c0; };
 
-        Gate q[TT][VC];
-        {
-            Pack<float, VC> A, B;  // forwards
+        auto state_of = [&](const float *pool, int i, F2 (&f)[PAIRS]) {
+            float g[VC];
+            load<VC>(pool + row(i), g, inside, false);
 #pragma unroll
-            for (int v = 0; v < VC; ++v) A.e[v] = 1.f, B.e[v] = 0.f;
+            for (int v = 0; v < PAIRS; ++v) f[v] = F2(g[2 * v], g[2 * v + 1]);
+        };
+        auto put = [&](float *dst, const F2 (&f)[PAIRS]) {
+            Pack<float, VC> v;
+#pragma unroll
+            for (int k = 0; k < PAIRS; ++k) f[k].get(v.e[2 * k], v.e[2 * k + 1]);
+            put_pack(dst + lane * VC, v);
+        };
+        GatePair q[TT][PAIRS];
+        {
+            F2 A[PAIRS], B[PAIRS];  // forwards
+#pragma unroll
+            for (int v = 0; v < PAIRS; ++v) A[v] = F2(1.f), B[v] = F2(0.f);
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
-                float x[VC], a[VC], b[VC] = {}, front[VC];
-                read<T, VC>(tile.x + place + i * SLAB, x);
-                read<G, VC>(tile.a + place + i * SLAB, a);
-                if (has_b) read<G, VC>(tile.b + place + i * SLAB, b);
+                F2 x[PAIRS], a[PAIRS], b[PAIRS];
+                pairs_of(tile.x + place + i * SLAB, x);
+                pairs_of(tile.a + place + i * SLAB, a);
+                if (has_b) pairs_of(tile.b + place + i * SLAB, b);
+                if (reset >> i & 1) {
 #pragma unroll
-                for (int v = 0; v < VC; ++v) {
-                    q[i][v] = gate_of<MODE>(a[v], b[v], rate[v], dt[v], has_b);
-                    front[v] = reset >> i & 1 ? 0.f : B.e[v];
+                    for (int v = 0; v < PAIRS; ++v) B[v] = F2(0.f);
+                    if ((loads >> i & 1) && p.init) state_of(p.init, i, B);
                 }
-                if ((loads >> i & 1) && p.init) load<VC>(p.init + row(i), front, inside, false);
 #pragma unroll
-                for (int v = 0; v < VC; ++v) {
-                    B.e[v] = fmaf(q[i][v].g, front[v], q[i][v].w() * x[v]);
-                    A.e[v] *= q[i][v].g;
+                for (int v = 0; v < PAIRS; ++v) {
+                    q[i][v] = gate_pair<MODE>(a[v], b[v], rate[v], dt[v], has_b);
+                    B[v] = fma2(q[i][v].g, B[v], mul2(weight_of<MODE>(q[i][v]), x[v]));
+                    A[v] = mul2(A[v], q[i][v].g);
                 }
             }
-            put_pack(&sm.FA[sub][lane * VC], A);
-            put_pack(&sm.FB[sub][lane * VC], B);
+            put(sm.FA[sub], A);
+            put(sm.FB[sub], B);
 #pragma unroll
-            for (int v = 0; v < VC; ++v) B.e[v] = 0.f;  // backwards
+            for (int v = 0; v < PAIRS; ++v) B[v] = F2(0.f);  // backwards
 #pragma unroll
             for (int i = TT - 1; i >= 0; --i) {
-                float dy[VC];
-                read<T, VC>(tile.dy + place + i * SLAB, dy);
+                F2 dy[PAIRS];
+                pairs_of(tile.dy + place + i * SLAB, dy);
                 if (cuts >> i & 1) {
 #pragma unroll
-                    for (int v = 0; v < VC; ++v) B.e[v] = 0.f;
-                    if ((lasts >> i & 1) && p.dfinal) {
-                        float d[VC];
-                        load<VC>(p.dfinal + row(i), d, inside, false);
-#pragma unroll
-                        for (int v = 0; v < VC; ++v) B.e[v] = d[v];
-                    }
+                    for (int v = 0; v < PAIRS; ++v) B[v] = F2(0.f);
+                    if ((lasts >> i & 1) && p.dfinal) state_of(p.dfinal, i, B);
                 }
 #pragma unroll
-                for (int v = 0; v < VC; ++v) B.e[v] = valid >> i & 1 ? q[i][v].g * (dy[v] + B.e[v]) : 0.f;
+                for (int v = 0; v < PAIRS; ++v) B[v] = mul2(q[i][v].g, add2(dy[v], B[v]));
+                if (!(valid >> i & 1))
+#pragma unroll
+                    for (int v = 0; v < PAIRS; ++v) B[v] = F2(0.f);
             }
-            put_pack(&sm.RA[sub][lane * VC], A);
-            put_pack(&sm.RB[sub][lane * VC], B);
+            put(sm.RA[sub], A);
+            put(sm.RB[sub], B);
         }
         __syncthreads();
 
@@ -219,23 +234,23 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         __syncthreads();
 
         // the states again, each before its token
-        float before[TT][VC];
+        F2 before[TT][PAIRS];
         {
-            float h[VC];
-            read<float, VC>(&sm.FB[sub][lane * VC], h);
+            F2 h[PAIRS];
+            pairs_of(&sm.FB[sub][lane * VC], h);
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
-                float x[VC];
-                read<T, VC>(tile.x + place + i * SLAB, x);
+                F2 x[PAIRS];
+                pairs_of(tile.x + place + i * SLAB, x);
                 if (reset >> i & 1) {
 #pragma unroll
-                    for (int v = 0; v < VC; ++v) h[v] = 0.f;
-                    if ((loads >> i & 1) && p.init) load<VC>(p.init + row(i), h, inside, false);
+                    for (int v = 0; v < PAIRS; ++v) h[v] = F2(0.f);
+                    if ((loads >> i & 1) && p.init) state_of(p.init, i, h);
                 }
 #pragma unroll
-                for (int v = 0; v < VC; ++v) {
+                for (int v = 0; v < PAIRS; ++v) {
                     before[i][v] = h[v];
-                    h[v] = fmaf(q[i][v].g, h[v], q[i][v].w() * x[v]);
+                    h[v] = fma2(q[i][v].g, h[v], mul2(weight_of<MODE>(q[i][v]), x[v]));
                 }
             }
         }
@@ -249,50 +264,59 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
                 cut |= w > own ? c != 0 : w == own ? (c >> (sub * TT % 32) >> TT) != 0 : false;
             }
         }
-        float m[VC], sum_A[VC] = {}, sum_dt[VC] = {};
+        F2 m[PAIRS], sum_A[PAIRS], sum_dt[PAIRS];
         {
-            float A[VC], B[VC], carry[VC];
-            read<float, VC>(&sm.RA[sub][lane * VC], A);
-            read<float, VC>(&sm.RB[sub][lane * VC], B);
-            read<float, VC>(&sm.carry[lane * VC], carry);
+            F2 A[PAIRS], B[PAIRS], carry[PAIRS];
+            pairs_of(&sm.RA[sub][lane * VC], A);
+            pairs_of(&sm.RB[sub][lane * VC], B);
+            pairs_of(&sm.carry[lane * VC], carry);
 #pragma unroll
-            for (int v = 0; v < VC; ++v) m[v] = cut ? B[v] : fmaf(A[v], carry[v], B[v]);
+            for (int v = 0; v < PAIRS; ++v) {
+                m[v] = B[v];
+                if (!cut) m[v] = fma2(A[v], carry[v], B[v]);
+                sum_A[v] = sum_dt[v] = F2(0.f);
+            }
         }
         long long at = (long long)(t0 + sub * TT + TT - 1) * p.C + c0;
 #pragma unroll
         for (int i = TT - 1; i >= 0; --i, at -= p.C) {
-            float x[VC], a[VC], dy[VC], dx[VC], da[VC], db[VC];
-            read<T, VC>(tile.x + place + i * SLAB, x);
-            read<G, VC>(tile.a + place + i * SLAB, a);
-            read<T, VC>(tile.dy + place + i * SLAB, dy);
             if (cuts >> i & 1) {
 #pragma unroll
-                for (int v = 0; v < VC; ++v) m[v] = 0.f;
-                if ((lasts >> i & 1) && p.dfinal) load<VC>(p.dfinal + row(i), m, inside, false);
+                for (int v = 0; v < PAIRS; ++v) m[v] = F2(0.f);
+                if ((lasts >> i & 1) && p.dfinal) state_of(p.dfinal, i, m);
+                if (!(valid >> i & 1)) continue;
             }
-            if (!(valid >> i & 1)) continue;
+            F2 x[PAIRS], a[PAIRS], dy[PAIRS];
+            float dx[VC], da[VC], db[VC];
+            pairs_of(tile.x + place + i * SLAB, x);
+            pairs_of(tile.a + place + i * SLAB, a);
+            pairs_of(tile.dy + place + i * SLAB, dy);
 #pragma unroll
-            for (int v = 0; v < VC; ++v) {
-                const float l = m[v] + dy[v];
-                const GateGrad d = gate_grad<MODE>(q[i][v], a[v], l * before[i][v], l * x[v], rate[v], dt[v]);
-                dx[v] = l * q[i][v].w();
-                da[v] = d.da;
-                db[v] = d.db;
-                sum_A[v] += d.dA;
-                sum_dt[v] += d.da;
-                m[v] = q[i][v].g * l;
+            for (int v = 0; v < PAIRS; ++v) {
+                const F2 l = add2(m[v], dy[v]);
+                const GradPair d = grad_pair<MODE>(q[i][v], a[v], mul2(l, before[i][v]), mul2(l, x[v]), rate[v], dt[v]);
+                mul2(l, weight_of<MODE>(q[i][v])).get(dx[2 * v], dx[2 * v + 1]);
+                d.da.get(da[2 * v], da[2 * v + 1]);
+                d.db.get(db[2 * v], db[2 * v + 1]);
+                if (RAW) {
+                    sum_A[v] = add2(sum_A[v], d.dA);
+                    sum_dt[v] = add2(sum_dt[v], d.da);
+                }
+                m[v] = mul2(q[i][v].g, l);
             }
             store<T, VC>(static_cast<T *>(p.dx) + at, dx, inside, access.dx);
             store<G, VC>(static_cast<G *>(p.da) + at, da, inside, access.da);
             if (has_b) store<G, VC>(static_cast<G *>(p.db) + at, db, inside, access.db);
-            if ((loads >> i & 1) && p.dinit) store<float, VC>(p.dinit + row(i), m, inside, false);
+            if ((loads >> i & 1) && p.dinit) {
+                float first[VC];
+#pragma unroll
+                for (int v = 0; v < PAIRS; ++v) m[v].get(first[2 * v], first[2 * v + 1]);
+                store<float, VC>(p.dinit + row(i), first, inside, false);
+            }
         }
         if constexpr (RAW) {
-            Pack<float, VC> A, B;
-#pragma unroll
-            for (int v = 0; v < VC; ++v) A.e[v] = sum_A[v], B.e[v] = sum_dt[v];
-            put_pack(&sm.sum_A[sub][lane * VC], A);
-            put_pack(&sm.sum_dt[sub][lane * VC], B);
+            put(sm.sum_A[sub], sum_A);
+            put(sm.sum_dt[sub], sum_dt);
             __syncthreads();
             if (tid < SLAB) {
                 float a = 0.f, d = 0.f;
@@ -319,7 +343,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
             }
         }
         if (rank == 0 && tid < SLAB && s0 + tid < p.C) {
-            if (p.dA_log) p.dA_log[s0 + tid] = total_A;
+            if (p.dA_log) p.dA_log[s0 + tid] = LN2 * total_A;  // (from base-2 logarithms)
             if (p.ddt_bias) p.ddt_bias[s0 + tid] = total_dt;
         }
     }

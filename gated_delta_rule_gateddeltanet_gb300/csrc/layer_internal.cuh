@@ -76,7 +76,7 @@ struct Gate {
 
 // The gates' arithmetic is that of FP32 to a few units in the last place, in the fewest instructions: the
 // recurrence moves 8 bytes a channel of a token at 16 bits, which leaves an SM time for 44 instructions.
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718056f;
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -165,70 +165,96 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     return d;
 }
 
-// gate_of's decays and input weights of two channels, with the same results; minus_rate: -log2(e) exp(A_log).
+__device__ __forceinline__ F2 exp2_approx(F2 a) {
+    float x, y;
+    a.get(x, y);
+    return F2(exp2_approx(x), exp2_approx(y));
+}
+__device__ __forceinline__ F2 rcp_approx(F2 a) {
+    float x, y;
+    a.get(x, y);
+    return F2(rcp_approx(x), rcp_approx(y));
+}
+// e^-|a|
+__device__ __forceinline__ F2 exp_minus_abs(F2 a) {
+    float x, y;
+    a.get(x, y);
+    return F2(exp2_approx(-LOG2E * fabsf(x)), exp2_approx(-LOG2E * fabsf(y)));
+}
+__device__ __forceinline__ F2 log1p_over(F2 e) {
+    F2 y;
+    GDN_LOG1P(fma2, F2)
+    return y;
+}
+
+// gate_of for two channels, with the same results; exponent: the base-2 logarithm of g; minus_rate: -log2(e) exp(A_log).
+struct GatePair {
+    F2 g, exponent, sig_b, factor;
+};
 template <int MODE>
-__device__ __forceinline__ void gate_pair(F2 a, F2 b, F2 minus_rate, F2 dt_bias, bool has_b, F2 &g, F2 &w) {
+__device__ __forceinline__ F2 weight_of(const GatePair &q) {
+    return MODE == RECUR_RAW_UNIT ? mul2(q.sig_b, q.factor) : q.sig_b;
+}
+template <int MODE>
+__device__ __forceinline__ GatePair gate_pair(F2 a, F2 b, F2 minus_rate, F2 dt_bias, bool has_b) {
+    GatePair r;
     if constexpr (MODE == RECUR_PRECOMPUTED) {
-        g = a;
-        w = has_b ? b : F2(1.f);
+        r.g = a;
+        r.sig_b = has_b ? b : F2(1.f);
     } else {
         float x, y;
-        add2(a, dt_bias).get(x, y);
-        const F2 e(exp2_approx(-LOG2E * fabsf(x)), exp2_approx(-LOG2E * fabsf(y)));
-        F2 q;
-        {
-            F2 y;
-            GDN_LOG1P(fma2, F2)
-            q = y;
-        }
-        const F2 exponent = mul2(minus_rate, fma2(q, e, F2(fmaxf(x, 0.f), fmaxf(y, 0.f))));
-        exponent.get(x, y);
-        g = F2(exp2_approx(x), exp2_approx(y));
-        w = F2(1.f);
-        if (has_b) {
-            mul2(b, F2(-LOG2E)).get(x, y);
-            add2(F2(exp2_approx(x), exp2_approx(y)), F2(1.f)).get(x, y);
-            w = F2(rcp_approx(x), rcp_approx(y));
-        }
+        const F2 v = add2(a, dt_bias), e = exp_minus_abs(v);
+        v.get(x, y);
+        r.exponent = mul2(minus_rate, fma2(log1p_over(e), e, F2(fmaxf(x, 0.f), fmaxf(y, 0.f))));
+        r.g = exp2_approx(r.exponent);
+        r.sig_b = F2(1.f);
+        if (has_b) r.sig_b = rcp_approx(add2(exp2_approx(mul2(b, F2(-LOG2E))), F2(1.f)));
         if constexpr (MODE == RECUR_RAW_UNIT) {
-            // 1 - g^2, as one_minus_square
-            const F2 t = mul2(exponent, F2(-0.69314718056f)), t2 = mul2(t, t);
-            const F2 s = mul2(fma2(fma2(t2, F2(1.f / 120.f), F2(1.f / 6.f)), t2, F2(1.f)), mul2(t, add2(g, g)));
+            // as one_minus_square
+            const F2 t = mul2(r.exponent, F2(-LN2)), t2 = mul2(t, t);
+            const F2 s = mul2(fma2(fma2(t2, F2(1.f / 120.f), F2(1.f / 6.f)), t2, F2(1.f)), mul2(t, add2(r.g, r.g)));
             float g1, g2, t1, t2s, s1, s2;
-            g.get(g1, g2);
+            r.g.get(g1, g2);
             t.get(t1, t2s);
             s.get(s1, s2);
             s1 = t1 < SMALL_T ? s1 : fmaf(-g1, g1, 1.f);
             s2 = t2s < SMALL_T ? s2 : fmaf(-g2, g2, 1.f);
-            w = mul2(w, F2(sqrt_approx(s1), sqrt_approx(s2)));
+            r.factor = F2(sqrt_approx(s1), sqrt_approx(s2));
         }
     }
+    return r;
 }
 
-// The gradients of a and b (and their parameters) from those of g and w.
-struct GateGrad {
-    float da, db, dA;  // dA: that of A_log; dt_bias has a's
+// The gradients of a, b and A_log (da_log, up to a factor of -ln 2) from those of g and w; dt_bias has a's.
+struct GradPair {
+    F2 da, db, dA;
 };
-
 template <int MODE>
-__device__ __forceinline__ GateGrad gate_grad(const Gate &r, float a, float dg, float dw, float rate, float dt_bias) {
-    GateGrad o;
+__device__ __forceinline__ GradPair grad_pair(const GatePair &q, F2 a, F2 dg, F2 dw, F2 minus_rate, F2 dt_bias) {
+    GradPair o;
     if constexpr (MODE == RECUR_PRECOMPUTED) {
         o.da = dg;
         o.db = dw;
-        o.dA = 0.f;
     } else {
-        const float v = a + dt_bias, e = exp2_approx(-LOG2E * fabsf(v));
-        const float sig_a = (v >= 0.f ? 1.f : e) * rcp_approx(1.f + e);
-        float dlg = dg * r.g;
-        const float di = dw * r.sig_b;
+        // sigmoid(v) = 1 / (1 + e^-|v|), or 1 minus that
+        const F2 v = add2(a, dt_bias), e = exp_minus_abs(v), r = rcp_approx(add2(e, F2(1.f))), er = mul2(e, r);
+        float x, y, r1, r2, e1, e2;
+        v.get(x, y);
+        r.get(r1, r2);
+        er.get(e1, e2);
+        const F2 sig_a(x >= 0.f ? r1 : e1, y >= 0.f ? r2 : e2);
+        F2 dlg = mul2(dg, q.g), di = mul2(dw, q.sig_b);
         if constexpr (MODE == RECUR_RAW_UNIT) {
-            const float k = r.g * r.g * rcp_approx(r.factor);
-            dlg -= r.factor > 0.f ? di * k : 0.f;
+            // -g^2 / factor, 0 where the factor is
+            float f1, f2;
+            q.factor.get(f1, f2);
+            const F2 k = mul2(mul2(q.g, q.g), F2(f1 > 0.f ? -rcp_approx(f1) : 0.f, f2 > 0.f ? -rcp_approx(f2) : 0.f));
+            dlg = fma2(di, k, dlg);
+            di = mul2(di, q.factor);
         }
-        o.da = -dlg * (rate * sig_a);
-        o.dA = dlg * r.lg;
-        o.db = di * r.factor * (1.f - r.sig_b);
+        o.da = mul2(mul2(dlg, sig_a), mul2(minus_rate, F2(LN2)));
+        o.dA = mul2(dlg, q.exponent);
+        o.db = fma2(mul2(di, q.sig_b), F2(-1.f), di);
     }
     return o;
 }

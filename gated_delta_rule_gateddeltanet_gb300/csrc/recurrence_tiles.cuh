@@ -209,6 +209,14 @@ __device__ __forceinline__ void read(const E *src, float (&f)[VC]) {
     }
 }
 
+template <typename E, int PAIRS>
+__device__ __forceinline__ void pairs_of(const E *src, F2 (&f)[PAIRS]) {
+    float g[2 * PAIRS];
+    read<E, 2 * PAIRS>(src, g);
+#pragma unroll
+    for (int v = 0; v < PAIRS; ++v) f[v] = F2(g[2 * v], g[2 * v + 1]);
+}
+
 template <int VC>
 __device__ __forceinline__ void put_pack(float *dst, const Pack<float, VC> &v) {
     if constexpr (VC == 4) *reinterpret_cast<uint4 *>(dst) = v.u4;
