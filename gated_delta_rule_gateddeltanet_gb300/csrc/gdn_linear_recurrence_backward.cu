@@ -117,6 +117,9 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         copies_done();
         __syncthreads();
         const bool more = n + 1 < rounds;
+        float checkpoint = 0.f;  // channel tid - SLAB's, on its way while the gates are worked out
+        if (tid >= SLAB && tid < 2 * SLAB && s0 + tid - SLAB < p.C && t0 < p.T)
+            checkpoint = p.states[(long long)(t0 / CHECK) * p.C + s0 + tid - SLAB];
         constexpr unsigned ALL = (1u << TT) - 1;
         const bool plain = tokens.plain;  // as most are
         const unsigned reset = plain ? 0 : bits_of<TT>(tokens.reset, sub), loads = plain ? 0 : bits_of<TT>(tokens.load, sub);
@@ -124,6 +127,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         // Backwards a sequence's last token cuts off what stands behind it, and so does one of no sequence.
         const unsigned cuts = lasts | (~valid & ALL);
         const int place = sub * TT * SLAB + lane * VC;
+        const bool quick = plain || __all_sync(0xffffffffu, (reset | cuts) == 0);  // the warp's tokens lie inside a sequence
         auto row = [&](int i) { return (long long)tokens.slot[sub * TT + i] * p.C + c0; };
 
         auto state_of = [&](const float *pool, int i, F2 (&f)[PAIRS]) {
@@ -139,7 +143,8 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
             put_pack(dst + lane * VC, v);
         };
         GatePair q[TT][PAIRS];
-        {
+        F2 u[TT][PAIRS];  // a token's w x, and later the state before it
+        auto gates = [&](auto inside_a_sequence) {
             F2 A[PAIRS], B[PAIRS];  // forwards
 #pragma unroll
             for (int v = 0; v < PAIRS; ++v) A[v] = F2(1.f), B[v] = F2(0.f);
@@ -149,7 +154,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
                 pairs_of(tile.x + place + i * SLAB, x);
                 pairs_of(tile.a + place + i * SLAB, a);
                 if (has_b) pairs_of(tile.b + place + i * SLAB, b);
-                if (reset >> i & 1) {
+                if (!inside_a_sequence && (reset >> i & 1)) {
 #pragma unroll
                     for (int v = 0; v < PAIRS; ++v) B[v] = F2(0.f);
                     if ((loads >> i & 1) && p.init) state_of(p.init, i, B);
@@ -157,7 +162,8 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
 #pragma unroll
                 for (int v = 0; v < PAIRS; ++v) {
                     q[i][v] = gate_pair<MODE>(a[v], b[v], rate[v], dt[v], has_b);
-                    B[v] = fma2(q[i][v].g, B[v], mul2(weight_of<MODE>(q[i][v]), x[v]));
+                    u[i][v] = mul2(weight_of<MODE>(q[i][v]), x[v]);
+                    B[v] = fma2(q[i][v].g, B[v], u[i][v]);
                     A[v] = mul2(A[v], q[i][v].g);
                 }
             }
@@ -169,20 +175,22 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
             for (int i = TT - 1; i >= 0; --i) {
                 F2 dy[PAIRS];
                 pairs_of(tile.dy + place + i * SLAB, dy);
-                if (cuts >> i & 1) {
+                if (!inside_a_sequence && (cuts >> i & 1)) {
 #pragma unroll
                     for (int v = 0; v < PAIRS; ++v) B[v] = F2(0.f);
                     if ((lasts >> i & 1) && p.dfinal) state_of(p.dfinal, i, B);
                 }
 #pragma unroll
                 for (int v = 0; v < PAIRS; ++v) B[v] = mul2(q[i][v].g, add2(dy[v], B[v]));
-                if (!(valid >> i & 1))
+                if (!inside_a_sequence && !(valid >> i & 1))
 #pragma unroll
                     for (int v = 0; v < PAIRS; ++v) B[v] = F2(0.f);
             }
             put(sm.RA[sub], A);
             put(sm.RB[sub], B);
-        }
+        };
+        if (quick) gates(std::true_type());
+        else gates(std::false_type());
         __syncthreads();
 
         if (more) fetch(t0 - step, buf ^ 1);
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         } else if (tid < 2 * SLAB) {
             // the state in front of each half-warp's tokens
             const int c = tid - SLAB;
-            float h = s0 + c < p.C && t0 < p.T ? p.states[(long long)(t0 / CHECK) * p.C + s0 + c] : 0.f;
+            float h = checkpoint;
 #pragma unroll
             for (int s = 0; s < SUBS; ++s) {
                 const float a = sm.FA[s][c], b = sm.FB[s][c];
@@ -233,27 +241,6 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
         if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 - step, slab == 0, tid / 32 - (NT - TILE) / 32);  // (not by the threads above)
         __syncthreads();
 
-        // the states again, each before its token
-        F2 before[TT][PAIRS];
-        {
-            F2 h[PAIRS];
-            pairs_of(&sm.FB[sub][lane * VC], h);
-#pragma unroll
-            for (int i = 0; i < TT; ++i) {
-                F2 x[PAIRS];
-                pairs_of(tile.x + place + i * SLAB, x);
-                if (reset >> i & 1) {
-#pragma unroll
-                    for (int v = 0; v < PAIRS; ++v) h[v] = F2(0.f);
-                    if ((loads >> i & 1) && p.init) state_of(p.init, i, h);
-                }
-#pragma unroll
-                for (int v = 0; v < PAIRS; ++v) {
-                    before[i][v] = h[v];
-                    h[v] = fma2(q[i][v].g, h[v], mul2(weight_of<MODE>(q[i][v]), x[v]));
-                }
-            }
-        }
         // whether something cuts off what stands behind the half-warp's tokens within the tile
         bool cut = false;
         if (!plain) {
@@ -277,43 +264,72 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
                 sum_A[v] = sum_dt[v] = F2(0.f);
             }
         }
-        long long at = (long long)(t0 + sub * TT + TT - 1) * p.C + c0;
+        auto gradients = [&](auto inside_a_sequence) {
+            // the states again
+            F2 h[PAIRS];
+            pairs_of(&sm.FB[sub][lane * VC], h);
 #pragma unroll
-        for (int i = TT - 1; i >= 0; --i, at -= p.C) {
-            if (cuts >> i & 1) {
+            for (int i = 0; i < TT; ++i) {
+                if (!inside_a_sequence && (reset >> i & 1)) {
 #pragma unroll
-                for (int v = 0; v < PAIRS; ++v) m[v] = F2(0.f);
-                if ((lasts >> i & 1) && p.dfinal) state_of(p.dfinal, i, m);
-                if (!(valid >> i & 1)) continue;
-            }
-            F2 x[PAIRS], a[PAIRS], dy[PAIRS];
-            float dx[VC], da[VC], db[VC];
-            pairs_of(tile.x + place + i * SLAB, x);
-            pairs_of(tile.a + place + i * SLAB, a);
-            pairs_of(tile.dy + place + i * SLAB, dy);
-#pragma unroll
-            for (int v = 0; v < PAIRS; ++v) {
-                const F2 l = add2(m[v], dy[v]);
-                const GradPair d = grad_pair<MODE>(q[i][v], a[v], mul2(l, before[i][v]), mul2(l, x[v]), rate[v], dt[v]);
-                mul2(l, weight_of<MODE>(q[i][v])).get(dx[2 * v], dx[2 * v + 1]);
-                d.da.get(da[2 * v], da[2 * v + 1]);
-                d.db.get(db[2 * v], db[2 * v + 1]);
-                if (RAW) {
-                    sum_A[v] = add2(sum_A[v], d.dA);
-                    sum_dt[v] = add2(sum_dt[v], d.da);
+                    for (int v = 0; v < PAIRS; ++v) h[v] = F2(0.f);
+                    if ((loads >> i & 1) && p.init) state_of(p.init, i, h);
                 }
-                m[v] = mul2(q[i][v].g, l);
-            }
-            store<T, VC>(static_cast<T *>(p.dx) + at, dx, inside, access.dx);
-            store<G, VC>(static_cast<G *>(p.da) + at, da, inside, access.da);
-            if (has_b) store<G, VC>(static_cast<G *>(p.db) + at, db, inside, access.db);
-            if ((loads >> i & 1) && p.dinit) {
-                float first[VC];
 #pragma unroll
-                for (int v = 0; v < PAIRS; ++v) m[v].get(first[2 * v], first[2 * v + 1]);
-                store<float, VC>(p.dinit + row(i), first, inside, false);
+                for (int v = 0; v < PAIRS; ++v) {
+                    const F2 next = fma2(q[i][v].g, h[v], u[i][v]);
+                    u[i][v] = h[v];
+                    h[v] = next;
+                }
             }
-        }
+            long long at = (long long)(t0 + sub * TT + TT - 1) * p.C + c0;
+#pragma unroll
+            for (int i = TT - 1; i >= 0; --i, at -= p.C) {
+                if (!inside_a_sequence && (cuts >> i & 1)) {
+#pragma unroll
+                    for (int v = 0; v < PAIRS; ++v) m[v] = F2(0.f);
+                    if ((lasts >> i & 1) && p.dfinal) state_of(p.dfinal, i, m);
+                    if (!(valid >> i & 1)) continue;
+                }
+                F2 x[PAIRS], a[PAIRS], dy[PAIRS];
+                float dx[VC], da[VC], db[VC];
+                pairs_of(tile.x + place + i * SLAB, x);
+                pairs_of(tile.a + place + i * SLAB, a);
+                pairs_of(tile.dy + place + i * SLAB, dy);
+#pragma unroll
+                for (int v = 0; v < PAIRS; ++v) {
+                    const F2 l = add2(m[v], dy[v]);
+                    const GradPair d = grad_pair<MODE>(q[i][v], a[v], mul2(l, u[i][v]), mul2(l, x[v]), rate[v], dt[v]);
+                    mul2(l, d.w).get(dx[2 * v], dx[2 * v + 1]);
+                    d.da.get(da[2 * v], da[2 * v + 1]);
+                    d.db.get(db[2 * v], db[2 * v + 1]);
+                    if (RAW) {
+                        sum_A[v] = add2(sum_A[v], d.dA);
+                        sum_dt[v] = add2(sum_dt[v], d.da);
+                    }
+                    m[v] = mul2(q[i][v].g, l);
+                }
+                if (inside_a_sequence) {
+                    if (inside > 0) {
+                        store<T, VC>(static_cast<T *>(p.dx) + at, dx, VC, true);
+                        store<G, VC>(static_cast<G *>(p.da) + at, da, VC, true);
+                        if (has_b) store<G, VC>(static_cast<G *>(p.db) + at, db, VC, true);
+                    }
+                } else {
+                    store<T, VC>(static_cast<T *>(p.dx) + at, dx, inside, access.dx);
+                    store<G, VC>(static_cast<G *>(p.da) + at, da, inside, access.da);
+                    if (has_b) store<G, VC>(static_cast<G *>(p.db) + at, db, inside, access.db);
+                    if ((loads >> i & 1) && p.dinit) {
+                        float first[VC];
+#pragma unroll
+                        for (int v = 0; v < PAIRS; ++v) m[v].get(first[2 * v], first[2 * v + 1]);
+                        store<float, VC>(p.dinit + row(i), first, inside, false);
+                    }
+                }
+            }
+        };
+        if (quick && access.dx && access.da && access.db) gradients(std::true_type());
+        else gradients(std::false_type());
         if constexpr (RAW) {
             put(sm.sum_A[sub], sum_A);
             put(sm.sum_dt[sub], sum_dt);

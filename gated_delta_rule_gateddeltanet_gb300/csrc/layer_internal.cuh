@@ -189,12 +189,8 @@ __device__ __forceinline__ F2 log1p_over(F2 e) {
 
 // gate_of for two channels, with the same results; exponent: the base-2 logarithm of g; minus_rate: -log2(e) exp(A_log).
 struct GatePair {
-    F2 g, exponent, sig_b, factor;
+    F2 g, exponent, sig_b;
 };
-template <int MODE>
-__device__ __forceinline__ F2 weight_of(const GatePair &q) {
-    return MODE == RECUR_RAW_UNIT ? mul2(q.sig_b, q.factor) : q.sig_b;
-}
 template <int MODE>
 __device__ __forceinline__ GatePair gate_pair(F2 a, F2 b, F2 minus_rate, F2 dt_bias, bool has_b) {
     GatePair r;
@@ -209,29 +205,35 @@ __device__ __forceinline__ GatePair gate_pair(F2 a, F2 b, F2 minus_rate, F2 dt_b
         r.g = exp2_approx(r.exponent);
         r.sig_b = F2(1.f);
         if (has_b) r.sig_b = rcp_approx(add2(exp2_approx(mul2(b, F2(-LOG2E))), F2(1.f)));
-        if constexpr (MODE == RECUR_RAW_UNIT) {
-            // as one_minus_square
-            const F2 t = mul2(r.exponent, F2(-LN2)), t2 = mul2(t, t);
-            const F2 s = mul2(fma2(fma2(t2, F2(1.f / 120.f), F2(1.f / 6.f)), t2, F2(1.f)), mul2(t, add2(r.g, r.g)));
-            float g1, g2, t1, t2s, s1, s2;
-            r.g.get(g1, g2);
-            t.get(t1, t2s);
-            s.get(s1, s2);
-            s1 = t1 < SMALL_T ? s1 : fmaf(-g1, g1, 1.f);
-            s2 = t2s < SMALL_T ? s2 : fmaf(-g2, g2, 1.f);
-            r.factor = F2(sqrt_approx(s1), sqrt_approx(s2));
-        }
     }
     return r;
+}
+// sqrt(1 - g^2) (RECUR_RAW_UNIT)
+__device__ __forceinline__ F2 factor_pair(const GatePair &q) {
+    // as one_minus_square
+    const F2 t = mul2(q.exponent, F2(-LN2)), t2 = mul2(t, t);
+    const F2 s = mul2(fma2(fma2(t2, F2(1.f / 120.f), F2(1.f / 6.f)), t2, F2(1.f)), mul2(t, add2(q.g, q.g)));
+    float g1, g2, t1, t2s, s1, s2;
+    q.g.get(g1, g2);
+    t.get(t1, t2s);
+    s.get(s1, s2);
+    s1 = t1 < SMALL_T ? s1 : fmaf(-g1, g1, 1.f);
+    s2 = t2s < SMALL_T ? s2 : fmaf(-g2, g2, 1.f);
+    return F2(sqrt_approx(s1), sqrt_approx(s2));
+}
+template <int MODE>
+__device__ __forceinline__ F2 weight_of(const GatePair &q) {
+    return MODE == RECUR_RAW_UNIT ? mul2(q.sig_b, factor_pair(q)) : q.sig_b;
 }
 
 // The gradients of a, b and A_log (da_log, up to a factor of -ln 2) from those of g and w; dt_bias has a's.
 struct GradPair {
-    F2 da, db, dA;
+    F2 da, db, dA, w;  // w: the input's weight
 };
 template <int MODE>
 __device__ __forceinline__ GradPair grad_pair(const GatePair &q, F2 a, F2 dg, F2 dw, F2 minus_rate, F2 dt_bias) {
     GradPair o;
+    o.w = q.sig_b;
     if constexpr (MODE == RECUR_PRECOMPUTED) {
         o.da = dg;
         o.db = dw;
@@ -247,10 +249,12 @@ __device__ __forceinline__ GradPair grad_pair(const GatePair &q, F2 a, F2 dg, F2
         if constexpr (MODE == RECUR_RAW_UNIT) {
             // -g^2 / factor, 0 where the factor is
             float f1, f2;
-            q.factor.get(f1, f2);
+            const F2 factor = factor_pair(q);
+            factor.get(f1, f2);
             const F2 k = mul2(mul2(q.g, q.g), F2(f1 > 0.f ? -rcp_approx(f1) : 0.f, f2 > 0.f ? -rcp_approx(f2) : 0.f));
             dlg = fma2(di, k, dlg);
-            di = mul2(di, q.factor);
+            di = mul2(di, factor);
+            o.w = mul2(q.sig_b, factor);
         }
         o.da = mul2(mul2(dlg, sig_a), mul2(minus_rate, F2(LN2)));
         o.dA = mul2(dlg, q.exponent);
