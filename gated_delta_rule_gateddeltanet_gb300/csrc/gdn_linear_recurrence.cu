@@ -21,10 +21,10 @@ struct Maps {
     CUtensorMap x, a, b;  // of what is copied 16 bytes at a time
 };
 
-template <typename T, int MODE>
+template <typename T, int MODE, int VC_>
 struct Shape {
     using G = typename GateType<T, MODE>::type;
-    static constexpr int VC = sizeof(G) == 4 ? 2 : 4, SLAB = LANES * VC;
+    static constexpr int VC = VC_, SLAB = LANES * VC;
     struct Shared {
         alignas(128) T x[TILE * SLAB];
         alignas(128) G a[TILE * SLAB], b[TILE * SLAB];
@@ -36,13 +36,13 @@ struct Shape {
     };
 };
 
-template <typename T, int MODE>
-__global__ void __launch_bounds__(NT, 2) recurrence_kernel(const RecurrenceParams p, const Access access,
+template <typename T, int MODE, int VC>
+__global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const RecurrenceParams p, const Access access,
                                                            const __grid_constant__ Maps maps, int cluster) {
     dependent_prologue();
-    using S = Shape<T, MODE>;
+    using S = Shape<T, MODE, VC>;
     using G = typename S::G;
-    constexpr int VC = S::VC, SLAB = S::SLAB, PAIRS = VC / 2;
+    constexpr int SLAB = S::SLAB, PAIRS = VC / 2;
     extern __shared__ __align__(128) unsigned char raw[];
     typename S::Shared &sm = *reinterpret_cast<typename S::Shared *>(raw);
     const int tid = threadIdx.x, lane = tid % LANES, sub = tid / LANES;
@@ -319,10 +319,9 @@ cudaError_t launch_short(const RecurrenceParams &p, cudaStream_t stream) {
     return launch_dependent(recurrence_short_kernel<T, MODE, 1>, grid, dim3(SHORT_NT), 0, stream, p);
 }
 
-template <typename T, int MODE>
-cudaError_t launch_typed(const RecurrenceParams &p, int longest, cudaStream_t stream) {
-    if (longest <= SHORT_LEN) return launch_short<T, MODE>(p, stream);
-    using S = Shape<T, MODE>;
+template <typename T, int MODE, int VC>
+cudaError_t launch_tiles(const RecurrenceParams &p, cudaStream_t stream) {
+    using S = Shape<T, MODE, VC>;
     using G = typename S::G;
     Access access;
     access.x = whole_bytes(p.x, p.x_stride, p.C, sizeof(T));
@@ -332,17 +331,24 @@ cudaError_t launch_typed(const RecurrenceParams &p, int longest, cudaStream_t st
     if (access.x == 16 && !tile_map<T, S::SLAB, TILE>(&maps.x, p.x, p.x_stride, p.T, p.C)) access.x = 4;
     if (access.a == 16 && !tile_map<G, S::SLAB, TILE>(&maps.a, p.a, p.a_stride, p.T, p.C)) access.a = 4;
     if (p.b && access.b == 16 && !tile_map<G, S::SLAB, TILE>(&maps.b, p.b, p.b_stride, p.T, p.C)) access.b = 4;
-    access.y = whole_rows(p.y, p.C, sizeof(T), S::VC * sizeof(T));
-    access.state = whole_rows(p.init, p.C, 4, S::VC * 4) && whole_rows(p.final_state, p.C, 4, S::VC * 4) &&
-                   whole_rows(p.checkpoints, p.C, 4, S::VC * 4);
+    access.y = whole_rows(p.y, p.C, sizeof(T), VC * sizeof(T));
+    access.state = whole_rows(p.init, p.C, 4, VC * 4) && whole_rows(p.final_state, p.C, 4, VC * 4) &&
+                   whole_rows(p.checkpoints, p.C, 4, VC * 4);
     constexpr size_t smem = sizeof(typename S::Shared);
-    auto kernel = recurrence_kernel<T, MODE>;
+    auto kernel = recurrence_kernel<T, MODE, VC>;
     const Resident *resident;
-    const cudaError_t e = prepare_clusters<T, MODE>(kernel, NT, smem, &resident);
+    const cudaError_t e = prepare_clusters<T, MODE, VC>(kernel, NT, smem, &resident);
     if (e != cudaSuccess) return e;
     const long long slabs = ((long long)p.C + S::SLAB - 1) / S::SLAB, tiles = ((long long)p.T + TILE - 1) / TILE;
     const int size = cluster_size(*resident, slabs, tiles);
     return launch_clusters(kernel, (unsigned)slabs, (unsigned)size, NT, smem, stream, p, access, maps, size);
+}
+
+template <typename T, int MODE>
+cudaError_t launch_typed(const RecurrenceParams &p, int longest, cudaStream_t stream) {
+    if (longest <= SHORT_LEN) return launch_short<T, MODE>(p, stream);
+    if constexpr (sizeof(typename GateType<T, MODE>::type) == 4) return launch_tiles<T, MODE, 2>(p, stream);
+    else return narrow_slabs(p.C) ? launch_tiles<T, MODE, 2>(p, stream) : launch_tiles<T, MODE, 4>(p, stream);
 }
 
 template <typename T>

@@ -20,10 +20,10 @@ struct Maps {
     CUtensorMap x, a, b, dy;  // of what is copied 16 bytes at a time
 };
 
-template <typename T, int MODE>
+template <typename T, int MODE, int VC_>
 struct Shape {
     using G = typename GateType<T, MODE>::type;
-    static constexpr int VC = sizeof(G) == 4 ? 2 : 4, SLAB = LANES * VC;
+    static constexpr int VC = VC_, SLAB = LANES * VC;
     struct Tile {
         alignas(128) T x[TILE * SLAB];
         alignas(128) T dy[TILE * SLAB];
@@ -44,13 +44,13 @@ struct Shape {
     };
 };
 
-template <typename T, int MODE>
-__global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const RecurrenceParams p, const Access access,
+template <typename T, int MODE, int VC>
+__global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kernel(const RecurrenceParams p, const Access access,
                                                                     const __grid_constant__ Maps maps, int cluster) {
     dependent_prologue();
-    using S = Shape<T, MODE>;
+    using S = Shape<T, MODE, VC>;
     using G = typename S::G;
-    constexpr int VC = S::VC, SLAB = S::SLAB, PAIRS = VC / 2;
+    constexpr int SLAB = S::SLAB, PAIRS = VC / 2;
     constexpr bool RAW = MODE != RECUR_PRECOMPUTED;
     extern __shared__ __align__(128) unsigned char raw[];
     typename S::Shared &sm = *reinterpret_cast<typename S::Shared *>(raw);
@@ -378,11 +378,10 @@ __global__ void __launch_bounds__(NT, 2) recurrence_backward_kernel(const Recurr
     }
 }
 
-template <typename T, int MODE>
-cudaError_t launch_typed(const RecurrenceParams &p, cudaStream_t stream) {
-    using S = Shape<T, MODE>;
+template <typename T, int MODE, int VC>
+cudaError_t launch_tiles(const RecurrenceParams &p, cudaStream_t stream) {
+    using S = Shape<T, MODE, VC>;
     using G = typename S::G;
-    constexpr int VC = S::VC;
     Access access;
     access.x = whole_bytes(p.x, p.x_stride, p.C, sizeof(T));
     access.dy = whole_bytes(p.dy, p.dy_stride, p.C, sizeof(T));
@@ -398,13 +397,19 @@ cudaError_t launch_typed(const RecurrenceParams &p, cudaStream_t stream) {
     access.db = whole_rows(p.db, p.C, sizeof(G), VC * sizeof(G));
     access.state = whole_rows(p.dfinal, p.C, 4, VC * 4) && whole_rows(p.dinit, p.C, 4, VC * 4);
     constexpr size_t smem = sizeof(typename S::Shared);
-    auto kernel = recurrence_backward_kernel<T, MODE>;
+    auto kernel = recurrence_backward_kernel<T, MODE, VC>;
     const Resident *resident;
-    const cudaError_t e = prepare_clusters<T, MODE>(kernel, NT, smem, &resident);
+    const cudaError_t e = prepare_clusters<T, MODE, VC>(kernel, NT, smem, &resident);
     if (e != cudaSuccess) return e;
     const long long slabs = ((long long)p.C + S::SLAB - 1) / S::SLAB, tiles = ((long long)p.T + TILE - 1) / TILE;
     const int size = cluster_size(*resident, slabs, tiles);
     return launch_clusters(kernel, (unsigned)slabs, (unsigned)size, NT, smem, stream, p, access, maps, size);
+}
+
+template <typename T, int MODE>
+cudaError_t launch_typed(const RecurrenceParams &p, cudaStream_t stream) {
+    if constexpr (sizeof(typename GateType<T, MODE>::type) == 4) return launch_tiles<T, MODE, 2>(p, stream);
+    else return narrow_slabs(p.C) ? launch_tiles<T, MODE, 2>(p, stream) : launch_tiles<T, MODE, 4>(p, stream);
 }
 
 template <typename T>
