@@ -32,6 +32,7 @@ struct Shape {
         alignas(16) float4 map[2][MAX_CLUSTER][SLAB];  // the cluster's tiles' maps (A, B, whether it holds a reset)
         alignas(16) float carry[SLAB];
         Tokens<TILE> tokens[2];
+        Packing packing;
         alignas(8) uint64_t full, maps[2];
     };
 };
@@ -67,6 +68,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
         ptx::mbar_init(&sm.maps[1], 1);
         ptx::fence_mbar_init();
     }
+    const Lookup lookup = stage_packing(p, sm.packing);
     __syncthreads();
 
     const bool bulk = access.x == 16 || access.a == 16 || (has_b && access.b == 16);
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
 
     const int step = cluster * TILE, rounds = (p.T + step - 1) / step;
     fetch(rank * TILE);
-    tokens_of(sm.tokens[0], p, rank * TILE, slab == 0, tid / 32 - (NT - TILE) / 32);
+    tokens_of(sm.tokens[0], p, lookup, rank * TILE, slab == 0, tid / 32 - (NT - TILE) / 32);
     if (blockIdx.x == 0) check_packing(p);
     if (cluster > 1) cluster_sync();  // every CTA has its barriers before another writes to its shared memory
     float run = 0.f;  // the state in front of the cluster's tiles, channel tid of the slab
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
                 run = closed ? B : fmaf(A, run, B);
             }
         }
-        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 + step, slab == 0, tid / 32 - (NT - TILE) / 32);  // (not by the threads above)
+        if (more) tokens_of(sm.tokens[buf ^ 1], p, lookup, t0 + step, slab == 0, tid / 32 - (NT - TILE) / 32);  // (not by the threads above)
         __syncthreads();
 
         unsigned before = 0;  // whether a reset stands before the half-warp's tokens in the tile
@@ -328,9 +330,9 @@ cudaError_t launch_tiles(const RecurrenceParams &p, cudaStream_t stream) {
     access.a = whole_bytes(p.a, p.a_stride, p.C, sizeof(G));
     access.b = whole_bytes(p.b, p.b_stride, p.C, sizeof(G));
     Maps maps{};
-    if (access.x == 16 && !tile_map<T, S::SLAB, TILE>(&maps.x, p.x, p.x_stride, p.T, p.C)) access.x = 4;
-    if (access.a == 16 && !tile_map<G, S::SLAB, TILE>(&maps.a, p.a, p.a_stride, p.T, p.C)) access.a = 4;
-    if (p.b && access.b == 16 && !tile_map<G, S::SLAB, TILE>(&maps.b, p.b, p.b_stride, p.T, p.C)) access.b = 4;
+    if (access.x == 16 && !tile_map<T, S::SLAB, TILE>(&maps.x, p.x, p.x_stride, p.T, p.C)) access.x = 8;
+    if (access.a == 16 && !tile_map<G, S::SLAB, TILE>(&maps.a, p.a, p.a_stride, p.T, p.C)) access.a = 8;
+    if (p.b && access.b == 16 && !tile_map<G, S::SLAB, TILE>(&maps.b, p.b, p.b_stride, p.T, p.C)) access.b = 8;
     access.y = whole_rows(p.y, p.C, sizeof(T), VC * sizeof(T));
     access.state = whole_rows(p.init, p.C, 4, VC * 4) && whole_rows(p.final_state, p.C, 4, VC * 4) &&
                    whole_rows(p.checkpoints, p.C, 4, VC * 4);

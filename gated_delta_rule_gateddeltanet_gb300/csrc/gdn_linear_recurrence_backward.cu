@@ -40,6 +40,7 @@ struct Shape {
         alignas(16) float carry[SLAB];
         alignas(16) float2 sums[MAX_CLUSTER][SLAB];
         Tokens<TILE> tokens[2];
+        Packing packing;
         alignas(8) uint64_t full[2], maps[2];
     };
 };
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
         }
         ptx::fence_mbar_init();
     }
+    const Lookup lookup = stage_packing(p, sm.packing);
     __syncthreads();
 
     const bool bulk = access.x == 16 || access.dy == 16 || access.a == 16 || (has_b && access.b == 16);
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
     const int step = cluster * TILE, rounds = (p.T + step - 1) / step;
     if (rounds > 0) {  // (a call without tokens has none)
         fetch((rounds - 1) * step + rank * TILE, 0);
-        tokens_of(sm.tokens[0], p, (rounds - 1) * step + rank * TILE, slab == 0, tid / 32 - (NT - TILE) / 32);
+        tokens_of(sm.tokens[0], p, lookup, (rounds - 1) * step + rank * TILE, slab == 0, tid / 32 - (NT - TILE) / 32);
     }
     if (blockIdx.x == 0) check_packing(p);
     if (cluster > 1) cluster_sync();  // every CTA has its barriers before another writes to its shared memory
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
                 h = !plain && bits_of<TT>(tokens.reset, s) ? b : fmaf(a, h, b);
             }
         }
-        if (more) tokens_of(sm.tokens[buf ^ 1], p, t0 - step, slab == 0, tid / 32 - (NT - TILE) / 32);  // (not by the threads above)
+        if (more) tokens_of(sm.tokens[buf ^ 1], p, lookup, t0 - step, slab == 0, tid / 32 - (NT - TILE) / 32);  // (not by the threads above)
         __syncthreads();
 
         // whether something cuts off what stands behind the half-warp's tokens within the tile
@@ -388,10 +390,10 @@ cudaError_t launch_tiles(const RecurrenceParams &p, cudaStream_t stream) {
     access.a = whole_bytes(p.a, p.a_stride, p.C, sizeof(G));
     access.b = whole_bytes(p.b, p.b_stride, p.C, sizeof(G));
     Maps maps{};
-    if (access.x == 16 && !tile_map<T, S::SLAB, TILE>(&maps.x, p.x, p.x_stride, p.T, p.C)) access.x = 4;
-    if (access.dy == 16 && !tile_map<T, S::SLAB, TILE>(&maps.dy, p.dy, p.dy_stride, p.T, p.C)) access.dy = 4;
-    if (access.a == 16 && !tile_map<G, S::SLAB, TILE>(&maps.a, p.a, p.a_stride, p.T, p.C)) access.a = 4;
-    if (p.b && access.b == 16 && !tile_map<G, S::SLAB, TILE>(&maps.b, p.b, p.b_stride, p.T, p.C)) access.b = 4;
+    if (access.x == 16 && !tile_map<T, S::SLAB, TILE>(&maps.x, p.x, p.x_stride, p.T, p.C)) access.x = 8;
+    if (access.dy == 16 && !tile_map<T, S::SLAB, TILE>(&maps.dy, p.dy, p.dy_stride, p.T, p.C)) access.dy = 8;
+    if (access.a == 16 && !tile_map<G, S::SLAB, TILE>(&maps.a, p.a, p.a_stride, p.T, p.C)) access.a = 8;
+    if (p.b && access.b == 16 && !tile_map<G, S::SLAB, TILE>(&maps.b, p.b, p.b_stride, p.T, p.C)) access.b = 8;
     access.dx = whole_rows(p.dx, p.C, sizeof(T), VC * sizeof(T));
     access.da = whole_rows(p.da, p.C, sizeof(G), VC * sizeof(G));
     access.db = whole_rows(p.db, p.C, sizeof(G), VC * sizeof(G));

@@ -39,22 +39,44 @@ __device__ __forceinline__ int last_start(const int32_t *cu, int hi, int t) {
     return lo;
 }
 
+// The packing, in shared memory if it is short: every tile looks its tokens up in it.  (Room for 512 sequences took the
+// L1 cache down a step, and rows that are copied 4 bytes at a time from 33 to 44 us.)
+constexpr int STAGED = 64;
+struct Packing {
+    int cu[STAGED + 1], slots[STAGED];
+};
+struct Lookup {
+    const int32_t *cu, *slots;
+};
+// (the caller synchronises the CTA after it)
+__device__ __forceinline__ Lookup stage_packing(const RecurrenceParams &p, Packing &k) {
+    Lookup l = {p.cu, p.slots};
+    if (!p.cu || p.B > STAGED) return l;
+    for (int b = threadIdx.x; b <= p.B; b += blockDim.x) {
+        k.cu[b] = p.cu[b];
+        if (p.slots && b < p.B) k.slots[b] = p.slots[b];
+    }
+    l.cu = k.cu;
+    if (p.slots) l.slots = k.slots;
+    return l;
+}
+
 // What token t is, its sequence's slot, and the tokens from it to its sequence's end.
-__device__ __forceinline__ int token_of(const RecurrenceParams &p, int t, bool flag, int &slot, int &rest) {
+__device__ __forceinline__ int token_of(const RecurrenceParams &p, const Lookup &l, int t, bool flag, int &slot, int &rest) {
     slot = rest = 0;
     if (t >= p.T || p.B == 0) return RESET;
     int b, begin, end;
-    if (p.cu) {
-        b = last_start(p.cu, p.B - 1, t);
-        begin = p.cu[b];
-        end = p.cu[b + 1];
+    if (l.cu) {
+        b = last_start(l.cu, p.B - 1, t);
+        begin = l.cu[b];
+        end = l.cu[b + 1];
     } else {
         b = t / p.S;
         begin = b * p.S;
         end = begin + p.S;
     }
     if (t < begin || t >= end || end > p.T) return RESET;  // (the last: a packing out of order)
-    slot = p.slots ? p.slots[b] : b;
+    slot = l.slots ? l.slots[b] : b;
     if (slot < 0 || slot >= p.num_slots) {
         if (flag) flag_error(p.status, GDN_DEVERR_STATE_SLOT);
         slot = 0;
@@ -74,15 +96,15 @@ struct Tokens {
 
 // Fills them for the tile at t0 (TILE / 32 warps, w: which of them).
 template <int TILE>
-__device__ __forceinline__ void tokens_of(Tokens<TILE> &k, const RecurrenceParams &p, int t0, bool flag, int w) {
+__device__ __forceinline__ void tokens_of(Tokens<TILE> &k, const RecurrenceParams &p, const Lookup &l, int t0, bool flag, int w) {
     if (w < 0) return;
     const int lane = threadIdx.x % 32;
     int slot, rest;
-    int what = token_of(p, t0, flag, slot, rest);
+    int what = token_of(p, l, t0, flag, slot, rest);
     const bool plain = what == VALID && rest > TILE;
     if (w == 0 && lane == 0) k.plain = plain;
     if (plain) return;
-    what = token_of(p, t0 + 32 * w + lane, flag, slot, rest);
+    what = token_of(p, l, t0 + 32 * w + lane, flag, slot, rest);
     k.slot[32 * w + lane] = slot;
     const unsigned reset = __ballot_sync(0xffffffffu, what & RESET), load = __ballot_sync(0xffffffffu, what & LOAD);
     const unsigned last = __ballot_sync(0xffffffffu, what & LAST), valid = __ballot_sync(0xffffffffu, what & VALID);
@@ -115,6 +137,8 @@ __device__ __forceinline__ void copy(void *dst, const void *src, bool in) {
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
+    else if constexpr (BYTES == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(in ? 8 : 0) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
@@ -142,17 +166,19 @@ __device__ __forceinline__ void copy_tile(E *dst, const E *base, long long strid
 }
 
 // A tile of E's, [TILE][SLAB], from rows `stride` apart; zeros past T and C.  bytes: what base, stride and C are whole
-// multiples of (16, 4, or less).
+// multiples of (16: where no tensor map takes them, 8, 4, or less).
 template <typename E, int SLAB, int TILE, int NT>
 __device__ __forceinline__ void load_tile(E *dst, const void *base, long long stride, int t0, int T, int c0, int C, int bytes) {
     const E *src = static_cast<const E *>(base);
     if (bytes == 16) {
         copy_tile<E, SLAB, TILE, NT, 16>(dst, src, stride, t0, T, c0, C);
+    } else if (bytes == 8) {
+        copy_tile<E, SLAB, TILE, NT, 8>(dst, src, stride, t0, T, c0, C);
     } else if (bytes == 4) {
         copy_tile<E, SLAB, TILE, NT, 4>(dst, src, stride, t0, T, c0, C);
     } else {
         src += (long long)t0 * stride + c0;
-#pragma unroll 8
+#pragma unroll 16
         for (int i = threadIdx.x; i < TILE * SLAB; i += NT) {
             const int r = i / SLAB, c = i % SLAB;
             dst[i] = t0 + r < T && c0 + c < C ? src[r * stride + c] : from_f32<E>(0.f);
@@ -167,10 +193,10 @@ bool tile_map(CUtensorMap *map, const void *base, long long stride, int T, long 
     else return encode_rows_f32_strided(map, static_cast<const float *>(base), C, stride, T, SLAB, TILE);
 }
 
-// 16 or 4 if address and rows are whole multiples of it, else 2; for rows of C elements `stride` apart.
+// 16, 8 or 4 if address and rows are whole multiples of it, else 2; for rows of C elements `stride` apart.
 inline int whole_bytes(const void *ptr, long long stride, long long C, size_t elem) {
     const unsigned long long all = reinterpret_cast<uintptr_t>(ptr) | (unsigned long long)stride * elem | (unsigned long long)C * elem;
-    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
+    return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
 }
 // Whether rows of C elements without gaps can be accessed `bytes` at a time.
 inline bool whole_rows(const void *ptr, long long C, size_t elem, size_t bytes) {
