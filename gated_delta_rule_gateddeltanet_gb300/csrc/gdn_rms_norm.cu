@@ -566,13 +566,29 @@ __global__ void __launch_bounds__(NT, 2 * RING_NT / NT) norm_ring_backward_kerne
             write8(static_cast<T *>(p.dx) + t * n + i * V, xf);
         }
     }
-    if (p.dw) {
-        float *out = p.partials + (long long)blockIdx.x * n;
+    if (!p.dw) return;
+    float *out = p.partials + (long long)blockIdx.x * p.d;
+    if (p.H == 1) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int i = threadIdx.x + k * threads;
             if (i < pieces) write8(out + i * V, part[k]);
         }
+        return;
+    }
+    // the heads' parts are summed in order; the ring has room for them, and no copy is on its way any more
+    float *heads = reinterpret_cast<float *>(raw);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int i = threadIdx.x + k * threads;
+        if (i < pieces) write8(heads + i * V, part[k]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.d; c += threads) {
+        float sum = 0.f;
+        for (int h = 0; h < p.H; ++h) sum += heads[h * p.d + c];
+        out[c] = sum;
     }
 }
 
@@ -581,10 +597,9 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_backward_kernel(const RmsNorm
     dependent_prologue();
     __shared__ float buf[2][32];
     const long long n = (long long)p.H * p.d;
-    float *part = p.dw ? p.partials + (long long)blockIdx.x * n : nullptr;
+    float *part = p.dw ? p.partials + (long long)blockIdx.x * p.d : nullptr;
     if (part)
-        for (int i = threadIdx.x; i < p.d; i += ANY_NT)
-            for (int h = 0; h < p.H; ++h) part[(long long)h * p.d + i] = 0.f;
+        for (int i = threadIdx.x; i < p.d; i += ANY_NT) part[i] = 0.f;
     int turn = 0;
     for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
         for (int h = 0; h < p.H; ++h) {
@@ -608,7 +623,7 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_backward_kernel(const RmsNorm
                 float dx = rstd * fmaf(-nx, dot, e * weight(i));
                 if (r) dx += to_f32(r[i]);
                 static_cast<T *>(p.dx)[t * n + at + i] = from_f32<T>(dx);
-                if (part) part[at + i] += e * nx;
+                if (part) part[i] += e * nx;
                 if (z) {
                     const float zv = to_f32(z[i]), sig = sigmoid(zv);
                     static_cast<T *>(p.dz)[t * n + at + i] = from_f32<T>(to_f32(dy[i]) * nx * weight(i) * (sig * fmaf(zv, 1.f - sig, 1.f)));
@@ -624,11 +639,10 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) norm_sums_kernel(const RmsNorm
     dependent_prologue();
     __shared__ float buf[SUM_WARPS][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
-    const long long rows = (long long)parts * p.H;
     float sum = 0.f;
     if (c < p.d) {
 #pragma unroll 8
-        for (long long k = warp; k < rows; k += SUM_WARPS) sum += p.partials[k * p.d + c];
+        for (int k = warp; k < parts; k += SUM_WARPS) sum += p.partials[(long long)k * p.d + c];
     }
     buf[warp][lane] = sum;
     __syncthreads();
@@ -743,7 +757,7 @@ cudaError_t backward_typed(const RmsNormParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t rms_norm_backward_workspace_bytes(int T, int H, int d) { return 4 * (size_t)backward_ctas(T, (long long)H * d) * H * d; }
+size_t rms_norm_backward_workspace_bytes(int T, int H, int d) { return 4 * (size_t)backward_ctas(T, (long long)H * d) * d; }
 
 cudaError_t launch_rms_norm(const RmsNormParams &p, int io_dtype, int out_dtype, cudaStream_t stream) {
     switch (io_dtype) {
