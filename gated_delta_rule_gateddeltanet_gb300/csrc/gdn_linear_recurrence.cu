@@ -154,20 +154,24 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
         if (more) fetch(t0 + step);
         if (tid < SLAB) {
             // the map of the tile, and on the way that of what stands in front of each half-warp's tokens
-            float A = 1.f, B = 0.f, a[SUBS], b[SUBS];
+            float A = 1.f, B = 0.f;
             bool closed = false;
+#pragma unroll 1
+            for (int s0 = 0; s0 < SUBS; s0 += 8) {
+                float a[8], b[8];
 #pragma unroll
-            for (int s = 0; s < SUBS; ++s) a[s] = sm.A[s][tid], b[s] = sm.B[s][tid];
+                for (int s = 0; s < 8; ++s) a[s] = sm.A[s0 + s][tid], b[s] = sm.B[s0 + s][tid];
 #pragma unroll
-            for (int s = 0; s < SUBS; ++s) {
-                sm.A[s][tid] = A;
-                sm.B[s][tid] = B;
-                B = fmaf(a[s], B, b[s]);
-                A *= a[s];
-                if (!plain && bits_of<TT>(tokens.reset, s)) {
-                    B = b[s];
-                    A = 0.f;
-                    closed = true;
+                for (int s = 0; s < 8; ++s) {
+                    sm.A[s0 + s][tid] = A;
+                    sm.B[s0 + s][tid] = B;
+                    B = fmaf(a[s], B, b[s]);
+                    A *= a[s];
+                    if (!plain && bits_of<TT>(tokens.reset, s0 + s)) {
+                        B = b[s];
+                        A = 0.f;
+                        closed = true;
+                    }
                 }
             }
             if (cluster > 1) {

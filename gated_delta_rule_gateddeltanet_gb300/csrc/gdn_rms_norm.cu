@@ -195,10 +195,14 @@ constexpr int SAME = GDN_F32;
 
 // ---------------------------------------------------------------- forward
 
+// Threads of a CTA of it at most: four pieces of FP32 a thread take more registers than 1024 threads have.
+template <typename T>
+constexpr int token_limit(int U) { return sizeof(T) == 4 && U > 1 ? 512 : 1024; }
+
 // What a row's sum is taken over: `lanes` neighbouring threads (heads of at most 256 channels), or the CTA.
 // A CTA takes one token: thread i holds pieces i, i + threads, .. of it (U at most).
 template <typename T, int OUT, int U>
-__global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p, int lanes) {
+__global__ void __launch_bounds__(token_limit<T>(U)) norm_token_kernel(const RmsNormParams p, int lanes) {
     dependent_prologue();
     __shared__ float buf[3][32];
     const int n = p.H * p.d, pieces = n / V, threads = blockDim.x;
@@ -213,6 +217,8 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
         if (p.r) r[k].load(static_cast<const T *>(p.r) + t * p.r_stride + i * V);
         if (p.z) z[k].load(static_cast<const T *>(p.z) + t * p.z_stride + i * V);
     }
+    Piece<float> weight;  // (of one piece, ahead of its use; of four it would take too many registers)
+    if (U == 1 && p.w && threadIdx.x < pieces) weight.load(p.w + (lanes ? threadIdx.x * V % p.d : threadIdx.x * V));
     float sum[U], all = 0.f;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -250,9 +256,8 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const RmsNormParams p,
         if (i >= pieces) continue;
         if (p.w) {
             F2 w[V / 2];
-            Piece<float> pw;
-            pw.load(p.w + i * V % p.d);
-            pw.to(w);
+            if (U > 1) weight.load(p.w + (lanes ? i * V % p.d : i * V));
+            weight.to(w);
 #pragma unroll
             for (int v = 0; v < V / 2; ++v) s[k][v] = mul2(s[k][v], mul2(rstd, add2(w[v], offset)));
         } else {
@@ -700,7 +705,7 @@ cudaError_t forward_typed(const RmsNormParams &p, int out_dtype, cudaStream_t st
             }
         }
     }
-    if (vec && (p.H == 1 || lanes) && pieces <= 4096) {
+    if (vec && (p.H == 1 || lanes) && pieces <= 4 * token_limit<T>(4)) {
         // Few tokens: as many threads as there are pieces, for latency.  Many: four pieces a thread, whose loads are all
         // on their way at once, and fewer threads to wait for one another.
         const dim3 grid((unsigned)p.T);
