@@ -29,10 +29,21 @@ __device__ __forceinline__ float max_or_nan(float a, float b, float c) {
     return y;
 }
 
-// The scale of 8-bit values whose largest magnitude is top (its reciprocal is a normal number); one_most: 1 / 448 or 1 / 127.
-__device__ __forceinline__ float scale_of(float top, float one_most) {
-    if (!(top <= 3.402823466e38f)) return __int_as_float(0x7fc00000);
-    return top == 0.f ? 1.f : fmaxf(top * one_most, 0x1p-120f);
+// 8-bit values stand for y = t f with f a factor of the whole row (the norm's, or 1), which does not enter the quotients:
+// they are t times the one number `times`, with fewer roundings than y / scale has.  scale: max|y| / 448 (or 127), with a
+// normal reciprocal.
+struct Scale {
+    float scale, times;
+};
+__device__ __forceinline__ Scale scale_of(float top, float factor, float most) {
+    const float largest = top * factor;
+    if (!(largest <= 3.402823466e38f)) return {__int_as_float(0x7fc00000), __int_as_float(0x7fc00000)};
+    if (largest == 0.f) return {1.f, factor};
+    const float scale = largest * (1.f / most);
+    if (scale < 0x1p-120f || top < 0x1p-100f || top > 0x1p100f) return {fmaxf(scale, 0x1p-120f), __fdiv_rn(factor, fmaxf(scale, 0x1p-120f))};
+    // most / top: the approximate quotient and its remainder's share (both numbers are far from the ends of the range)
+    const float r = rcp_approx(top), q = most * r;
+    return {scale, fmaf(fmaf(-q, top, most), r, q)};
 }
 
 // (0 for z below -88, where e^-z is infinite)
@@ -116,7 +127,6 @@ __device__ __forceinline__ void write8(T *p, const F (&f)[M]) {
     v.store(p);
 }
 
-// 8-bit values of y / scale, as products with the scale's reciprocal (two roundings in FP32 instead of one).
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
     uint16_t v;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
@@ -124,11 +134,11 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
 }
 __device__ __forceinline__ int int8_of(float q) { return min(127, max(-127, __float2int_rn(q))); }
 template <int OUT>
-__device__ __forceinline__ void quantise8(uint8_t *p, const F2 (&f)[V / 2], float scale) {
+__device__ __forceinline__ void quantise8(uint8_t *p, const F2 (&f)[V / 2], float times) {
     float q[V];
-    const F2 inv(rcp_approx(scale));
+    const F2 m(times);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) mul2(f[i], inv).get(q[2 * i], q[2 * i + 1]);
+    for (int i = 0; i < V / 2; ++i) mul2(f[i], m).get(q[2 * i], q[2 * i + 1]);
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -141,8 +151,8 @@ __device__ __forceinline__ void quantise8(uint8_t *p, const F2 (&f)[V / 2], floa
     }
     *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
-__device__ __forceinline__ uint8_t quantise1(float y, float scale, int out) {
-    const float q = y * rcp_approx(scale);
+__device__ __forceinline__ uint8_t quantise1(float y, float times, int out) {
+    const float q = y * times;
     return out == GDN_INT8 ? (uint8_t)int8_of(q) : (uint8_t)e4m3x2(q, 0.f);
 }
 
@@ -179,14 +189,14 @@ __device__ __forceinline__ float cta_sum(float v, float *buf) {
     v = lanes_sum(v, 32);
     if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
     __syncthreads();
-    const int warps = (blockDim.x + 31) / 32, lane = threadIdx.x % 32;
+    const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
     return lanes_sum(lane < warps ? buf[lane] : 0.f, 32);
 }
 __device__ __forceinline__ float cta_max(float v, float *buf) {
     v = lanes_max(v, 32);
     if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
     __syncthreads();
-    const int warps = (blockDim.x + 31) / 32, lane = threadIdx.x % 32;
+    const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
     return lanes_max(lane < warps ? buf[lane] : 0.f, 32);
 }
 
@@ -251,7 +261,8 @@ __global__ void __launch_bounds__(token_limit<T>(U)) norm_token_kernel(const Rms
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int i = threadIdx.x + k * threads;
-        const F2 rstd(rsqrtf(sum[k] * mean + p.eps)), offset(p.offset);
+        const float rs = rsqrtf(sum[k] * mean + p.eps);
+        const F2 rstd(OUT != SAME && !lanes ? 1.f : rs), offset(p.offset);  // (8 bits of one row: the factor goes to the scale)
         x[k].to(s[k]);
         if (i >= pieces) continue;
         if (p.w) {
@@ -274,20 +285,21 @@ __global__ void __launch_bounds__(token_limit<T>(U)) norm_token_kernel(const Rms
         else top = largest(s[k], top);
     }
     if constexpr (OUT != SAME) {
-        constexpr float ONE_MOST = OUT == GDN_INT8 ? 1.f / 127.f : 1.f / 448.f;
-        float scale = 0.f;
+        constexpr float MOST = OUT == GDN_INT8 ? 127.f : 448.f;
+        const float factor = lanes ? 1.f : rsqrtf(all * mean + p.eps);
+        Scale scale;
         if (p.group == 0) {
-            scale = scale_of(cta_max(top, buf[1]), ONE_MOST);
-            if (threadIdx.x == 0) p.scale[t] = scale;
+            scale = scale_of(cta_max(top, buf[1]), factor, MOST);
+            if (threadIdx.x == 0) p.scale[t] = scale.scale;
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int i = threadIdx.x + k * threads;
             if (p.group) {  // (whole groups of lanes are past the end together)
-                scale = scale_of(lanes_max(largest(s[k], 0.f), p.group / V), ONE_MOST);
-                if (i < pieces && (i & (p.group / V - 1)) == 0) p.scale[(t * n + i * V) >> (31 - __clz(p.group))] = scale;
+                scale = scale_of(lanes_max(largest(s[k], 0.f), p.group / V), factor, MOST);
+                if (i < pieces && (i & (p.group / V - 1)) == 0) p.scale[(t * n + i * V) >> (31 - __clz(p.group))] = scale.scale;
             }
-            if (i < pieces) quantise8<OUT>(static_cast<uint8_t *>(p.y) + t * n + i * V, s[k], scale);
+            if (i < pieces) quantise8<OUT>(static_cast<uint8_t *>(p.y) + t * n + i * V, s[k], scale.times);
         }
     }
 }
@@ -341,9 +353,10 @@ __global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams 
             x[k].to(s);
             x[k].store(static_cast<T *>(p.s_out) + at);
         }
-        const F2 rstd(rsqrtf(lanes_sum(squares(s), LANES) * (1.f / (LANES * V)) + p.eps));
+        const float rs = rsqrtf(lanes_sum(squares(s), LANES) * (1.f / (LANES * V)) + p.eps);
+        const F2 rstd(rs);
 #pragma unroll
-        for (int v = 0; v < V / 2; ++v) s[v] = mul2(s[v], mul2(rstd, w[v]));
+        for (int v = 0; v < V / 2; ++v) s[v] = mul2(s[v], OUT == SAME ? mul2(rstd, w[v]) : w[v]);
         if (p.z) {
             F2 gate[V / 2];
             z[k].to(gate);
@@ -353,11 +366,10 @@ __global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams 
         if constexpr (OUT == SAME) {
             if (in(k)) write8(static_cast<T *>(p.y) + at, s);
         } else {
-            constexpr float ONE_MOST = OUT == GDN_INT8 ? 1.f / 127.f : 1.f / 448.f;
-            const float scale = scale_of(lanes_max(largest(s, 0.f), group), ONE_MOST);
+            const Scale scale = scale_of(lanes_max(largest(s, 0.f), group), rs, OUT == GDN_INT8 ? 127.f : 448.f);
             if (in(k)) {
-                if ((j & (group - 1)) == 0) p.scale[at >> shift] = scale;
-                quantise8<OUT>(static_cast<uint8_t *>(p.y) + at, s, scale);
+                if ((j & (group - 1)) == 0) p.scale[at >> shift] = scale.scale;
+                quantise8<OUT>(static_cast<uint8_t *>(p.y) + at, s, scale.times);
             }
         }
     }
@@ -376,16 +388,16 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_kernel(const RmsNormParams p,
     const T *z = p.z ? static_cast<const T *>(p.z) + t * p.z_stride : nullptr;
     T *s_out = r ? static_cast<T *>(p.s_out) + t * n : nullptr;
     const bool eight = out_dtype == GDN_FP8_E4M3 || out_dtype == GDN_INT8;
-    const float most = out_dtype == GDN_INT8 ? 1.f / 127.f : 1.f / 448.f;
+    const float most = out_dtype == GDN_INT8 ? 127.f : 448.f;
     const T *s = r ? s_out : x;
     float top = 0.f;
     int turn = 0;
     // pass 0: 16 or 32 bits are written, or a token's largest magnitude found; pass 1: 8 bits
     for (int pass = 0; pass < (eight ? 2 : 1); ++pass) {
-        float token_scale = 0.f;
+        Scale token_scale = {};
         if (pass && p.group == 0) {
-            token_scale = scale_of(cta_max(top, buf[turn ^= 1]), most);
-            if (threadIdx.x == 0) p.scale[t] = token_scale;
+            token_scale = scale_of(cta_max(top, buf[turn ^= 1]), 1.f, most);
+            if (threadIdx.x == 0) p.scale[t] = token_scale.scale;
         }
         for (int h = 0; h < p.H; ++h) {
             const long long at = (long long)h * p.d;
@@ -411,16 +423,16 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_kernel(const RmsNormParams p,
                 // (a thread's channels of s are its own: what it added, it reads)
                 uint8_t *y = static_cast<uint8_t *>(p.y) + t * n + at;
                 if (p.group == 0) {
-                    for (int i = threadIdx.x; i < p.d; i += ANY_NT) y[i] = quantise1(value(i), token_scale, out_dtype);
+                    for (int i = threadIdx.x; i < p.d; i += ANY_NT) y[i] = quantise1(value(i), token_scale.times, out_dtype);
                 } else {
                     for (int g0 = threadIdx.x / 32 * 32; g0 < p.d; g0 += ANY_NT) {
                         // a warp's 32 channels; groups of 64 and 128 look at those of the other warps as well
                         const int start = g0 / p.group * p.group;
                         float m = 0.f;
                         for (int i = start + threadIdx.x % 32; i < start + p.group; i += 32) m = max_or_nan(m, fabsf(value(i)));
-                        const float scale = scale_of(lanes_max(m, 32), most);
-                        if (g0 == start && threadIdx.x % 32 == 0) p.scale[(t * n + at + start) / p.group] = scale;
-                        y[g0 + threadIdx.x % 32] = quantise1(value(g0 + threadIdx.x % 32), scale, out_dtype);
+                        const Scale scale = scale_of(lanes_max(m, 32), 1.f, most);
+                        if (g0 == start && threadIdx.x % 32 == 0) p.scale[(t * n + at + start) / p.group] = scale.scale;
+                        y[g0 + threadIdx.x % 32] = quantise1(value(g0 + threadIdx.x % 32), scale.times, out_dtype);
                     }
                 }
             }
@@ -436,26 +448,28 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_kernel(const RmsNormParams p,
 // second kernel in the order of the CTAs.
 
 // Rows arrive in a ring of stages in shared memory, a bulk copy a row of each input, as far ahead as there is room; a
-// CTA takes every gridDim-th token, thread i its pieces i, i + threads, .. (U at most).
+// CTA takes `cols` channels of every gridDim.x-th token (whole tokens, or whole heads of them: blockIdx.y), thread i the
+// pieces i, i + threads, .. of them (U at most).
 constexpr int RING_NT = 256, MAX_STAGES = 8;
 constexpr size_t RING_BYTES = 100 * 1024;  // of a CTA, two of which share an SM
 
 template <typename T, int U, int NT>
-__global__ void __launch_bounds__(NT, 2 * RING_NT / NT) norm_ring_backward_kernel(const RmsNormParams p, int lanes, int stages) {
+__global__ void __launch_bounds__(NT, 2 * RING_NT / NT) norm_ring_backward_kernel(const RmsNormParams p, int lanes, int cols, int stages) {
     dependent_prologue();
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ float2 buf[2][32];
     __shared__ uint64_t full[MAX_STAGES];
-    const int n = p.H * p.d, pieces = n / V, threads = blockDim.x, arrays = 2 + (p.r != nullptr) + (p.z != nullptr);
+    const int all_cols = p.H * p.d, c0 = blockIdx.y * cols, n = min(cols, all_cols - c0), pieces = n / V;
+    const int threads = blockDim.x, arrays = 2 + (p.r != nullptr) + (p.z != nullptr);
     const uint32_t row_bytes = (uint32_t)n * sizeof(T);
     T *ring = reinterpret_cast<T *>(raw);
     auto fetch = [&](int stage, long long t) {
         T *dst = ring + (long long)stage * arrays * n;
         ptx::mbar_arrive_expect_tx(&full[stage], row_bytes * arrays);
-        ptx::bulk_g2s(dst, static_cast<const T *>(p.x) + t * p.x_stride, row_bytes, &full[stage]);
-        ptx::bulk_g2s(dst += n, static_cast<const T *>(p.dy) + t * p.dy_stride, row_bytes, &full[stage]);
-        if (p.r) ptx::bulk_g2s(dst += n, static_cast<const T *>(p.r) + t * p.r_stride, row_bytes, &full[stage]);
-        if (p.z) ptx::bulk_g2s(dst += n, static_cast<const T *>(p.z) + t * p.z_stride, row_bytes, &full[stage]);
+        ptx::bulk_g2s(dst, static_cast<const T *>(p.x) + t * p.x_stride + c0, row_bytes, &full[stage]);
+        ptx::bulk_g2s(dst += n, static_cast<const T *>(p.dy) + t * p.dy_stride + c0, row_bytes, &full[stage]);
+        if (p.r) ptx::bulk_g2s(dst += n, static_cast<const T *>(p.r) + t * p.r_stride + c0, row_bytes, &full[stage]);
+        if (p.z) ptx::bulk_g2s(dst += n, static_cast<const T *>(p.z) + t * p.z_stride + c0, row_bytes, &full[stage]);
     };
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[s], 1);
@@ -559,7 +573,7 @@ __global__ void __launch_bounds__(NT, 2 * RING_NT / NT) norm_ring_backward_kerne
                     e[v] = mul2(e[v], mul2(zf[v], sig));
                     zf[v] = mul2(mul2(dyn, w[k][v]), slope);
                 }
-                write8(static_cast<T *>(p.dz) + t * n + i * V, zf);
+                write8(static_cast<T *>(p.dz) + t * all_cols + c0 + i * V, zf);
             }
 #pragma unroll
             for (int v = 0; v < V / 2; ++v) {
@@ -568,11 +582,11 @@ __global__ void __launch_bounds__(NT, 2 * RING_NT / NT) norm_ring_backward_kerne
                 xf[v] = mul2(rstd, fma2(nx, minus_dot, mul2(e[v], w[k][v])));
                 if (p.r) xf[v] = add2(xf[v], add[v]);
             }
-            write8(static_cast<T *>(p.dx) + t * n + i * V, xf);
+            write8(static_cast<T *>(p.dx) + t * all_cols + c0 + i * V, xf);
         }
     }
     if (!p.dw) return;
-    float *out = p.partials + (long long)blockIdx.x * p.d;
+    float *out = p.partials + ((long long)blockIdx.y * gridDim.x + blockIdx.x) * p.d;
     if (p.H == 1) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -592,7 +606,7 @@ __global__ void __launch_bounds__(NT, 2 * RING_NT / NT) norm_ring_backward_kerne
     __syncthreads();
     for (int c = threadIdx.x; c < p.d; c += threads) {
         float sum = 0.f;
-        for (int h = 0; h < p.H; ++h) sum += heads[h * p.d + c];
+        for (int h = 0; h < n; h += p.d) sum += heads[h + c];
         out[c] = sum;
     }
 }
@@ -672,15 +686,23 @@ int head_lanes(int d) { return d % V == 0 && d / V <= 32 && power_of_two(d / V) 
 // Threads of a CTA that takes a token of `pieces`, U each: whole warps, as even as can be.
 int token_threads(int pieces, int U) { return ((pieces + U - 1) / U + 31) / 32 * 32; }
 
-// Threads of a CTA of the ring: as many as a token has pieces up to RING_NT, which may have two each; twice that beyond.
-int ring_threads(long long pieces) {
-    return pieces > 2 * RING_NT ? 2 * RING_NT : (int)std::min<long long>(RING_NT, (pieces + 31) / 32 * 32);
-}
-
-// CTAs that walk over the tokens backwards: what is resident at once, or one a token.
-int backward_ctas(int T, long long n) {
-    const int a_sm = std::min(8, 2 * RING_NT / ring_threads(n / V + 1));
-    return (int)std::min<long long>(T, (long long)a_sm * current_device_sms());
+// How the backward pass is cut: CTAs over the tokens (what is resident at once, or one a token) and over the channels.
+struct Cut {
+    int cols, threads, tokens, parts;  // parts: of the channels
+};
+Cut backward_cut(int T, int H, int d) {
+    const long long n = (long long)H * d;
+    Cut c;
+    // heads of a few lanes need nothing of one another: as many of them a CTA as its threads have a piece each of
+    const bool heads = H > 1 && head_lanes(d);
+    c.cols = (int)(heads ? std::min<long long>(n, RING_NT * V) : n);
+    c.parts = (int)((n + c.cols - 1) / c.cols);
+    const long long pieces = (c.cols + V - 1) / V;
+    // (up to two pieces a thread; twice the threads beyond)
+    c.threads = pieces > 2 * RING_NT ? 2 * RING_NT : (int)std::min<long long>(RING_NT, (pieces + 31) / 32 * 32);
+    const int slots = std::min(8, 2 * RING_NT / c.threads) * current_device_sms();
+    c.tokens = std::min(T, std::max(1, slots / c.parts));
+    return c;
 }
 
 template <typename T, int OUT>
@@ -727,42 +749,49 @@ cudaError_t forward_out(const RmsNormParams &p, int out_dtype, cudaStream_t stre
 }
 
 template <typename T, int U, int NT>
-cudaError_t launch_ring(const RmsNormParams &p, int ctas, int threads, int lanes, size_t stage, cudaStream_t stream) {
+cudaError_t launch_ring(const RmsNormParams &p, const Cut &cut, int lanes, size_t stage, cudaStream_t stream) {
     // (two CTAs of RING_NT threads share an SM; more, smaller ones share it too)
-    const size_t room = std::max(stage * 2, RING_BYTES * 2 * (size_t)threads / (2 * RING_NT));
+    const size_t room = std::max(stage * 2, RING_BYTES * 2 * (size_t)cut.threads / (2 * RING_NT));
     const int stages = (int)std::min<size_t>(MAX_STAGES, room / stage);
     auto kernel = norm_ring_backward_kernel<T, U, NT>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (int)RING_BYTES);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3((unsigned)ctas), dim3((unsigned)threads), stages * stage, stream, p, lanes, stages);
+    return launch_dependent(kernel, dim3((unsigned)cut.tokens, (unsigned)cut.parts), dim3((unsigned)cut.threads), stages * stage, stream,
+                            p, lanes, cut.cols, stages);
 }
 
 template <typename T>
 cudaError_t backward_typed(const RmsNormParams &p, cudaStream_t stream) {
-    const long long n = (long long)p.H * p.d, pieces = n / V;
-    const int lanes = p.H > 1 ? head_lanes(p.d) : 0, ctas = backward_ctas(p.T, n);
-    const size_t stage = (size_t)(2 + (p.r != nullptr) + (p.z != nullptr)) * n * sizeof(T);
+    const long long n = (long long)p.H * p.d;
+    const int lanes = p.H > 1 ? head_lanes(p.d) : 0;
+    const Cut cut = backward_cut(p.T, p.H, p.d);
+    const size_t stage = (size_t)(2 + (p.r != nullptr) + (p.z != nullptr)) * cut.cols * sizeof(T);
+    int parts = cut.tokens * cut.parts;
     cudaError_t e = cudaSuccess;
     if (p.T > 0) {
         const bool vec = p.d % V == 0 && whole(p.x, p.x_stride, sizeof(T)) && whole(p.dy, p.dy_stride, sizeof(T)) &&
                          whole(p.r, p.r_stride, sizeof(T)) && whole(p.z, p.z_stride, sizeof(T)) && whole(p.w, 0, 4) &&
                          whole(p.dx, n, sizeof(T)) && whole(p.dz, n, sizeof(T));
-        if (vec && (p.H == 1 || lanes) && pieces <= 4 * RING_NT && stage <= RING_BYTES) {
-            const int threads = ring_threads(pieces);
-            if (pieces <= RING_NT) e = launch_ring<T, 1, RING_NT>(p, ctas, threads, lanes, stage, stream);
-            else if (pieces <= 2 * RING_NT) e = launch_ring<T, 2, RING_NT>(p, ctas, threads, lanes, stage, stream);
-            else e = launch_ring<T, 2, 2 * RING_NT>(p, ctas, threads, lanes, stage, stream);
+        const int pieces = cut.cols / V;
+        if (vec && (p.H == 1 || lanes) && pieces <= 4 * RING_NT && stage <= RING_BYTES && cut.parts <= 65535) {
+            if (pieces <= RING_NT) e = launch_ring<T, 1, RING_NT>(p, cut, lanes, stage, stream);
+            else if (pieces <= 2 * RING_NT) e = launch_ring<T, 2, RING_NT>(p, cut, lanes, stage, stream);
+            else e = launch_ring<T, 2, 2 * RING_NT>(p, cut, lanes, stage, stream);
         } else {
-            e = launch_dependent(norm_any_backward_kernel<T>, dim3((unsigned)ctas), dim3(ANY_NT), 0, stream, p);
+            parts = cut.tokens;
+            e = launch_dependent(norm_any_backward_kernel<T>, dim3((unsigned)parts), dim3(ANY_NT), 0, stream, p);
         }
     }
     if (e != cudaSuccess || !p.dw) return e;
-    return launch_dependent(norm_sums_kernel, dim3((unsigned)((p.d + 31) / 32)), dim3(32 * SUM_WARPS), 0, stream, p, ctas);
+    return launch_dependent(norm_sums_kernel, dim3((unsigned)((p.d + 31) / 32)), dim3(32 * SUM_WARPS), 0, stream, p, parts);
 }
 
 }  // namespace
 
-size_t rms_norm_backward_workspace_bytes(int T, int H, int d) { return 4 * (size_t)backward_ctas(T, (long long)H * d) * d; }
+size_t rms_norm_backward_workspace_bytes(int T, int H, int d) {
+    const Cut cut = backward_cut(T, H, d);
+    return 4 * (size_t)cut.tokens * cut.parts * d;
+}
 
 cudaError_t launch_rms_norm(const RmsNormParams &p, int io_dtype, int out_dtype, cudaStream_t stream) {
     switch (io_dtype) {
