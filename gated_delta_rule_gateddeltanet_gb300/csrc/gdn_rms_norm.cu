@@ -451,10 +451,12 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_kernel(const RmsNormParams p,
 // CTA takes `cols` channels of every gridDim.x-th token (whole tokens, or whole heads of them: blockIdx.y), thread i the
 // pieces i, i + threads, .. of them (U at most).
 constexpr int RING_NT = 256, MAX_STAGES = 8;
-constexpr size_t RING_BYTES = 100 * 1024;  // of a CTA, two of which share an SM
+constexpr size_t RING_BYTES = 200 * 1024;  // of an SM
+// CTAs of RING_NT threads that share an SM (three of two pieces a thread would not have the registers).
+constexpr int ring_blocks(int U) { return U == 1 ? 3 : 2; }
 
 template <typename T, int U, int NT>
-__global__ void __launch_bounds__(NT, 2 * RING_NT / NT) norm_ring_backward_kernel(const RmsNormParams p, int lanes, int cols, int stages) {
+__global__ void __launch_bounds__(NT, ring_blocks(U) * RING_NT / NT) norm_ring_backward_kernel(const RmsNormParams p, int lanes, int cols, int stages) {
     dependent_prologue();
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ float2 buf[2][32];
@@ -700,7 +702,7 @@ Cut backward_cut(int T, int H, int d) {
     const long long pieces = (c.cols + V - 1) / V;
     // (up to two pieces a thread; twice the threads beyond)
     c.threads = pieces > 2 * RING_NT ? 2 * RING_NT : (int)std::min<long long>(RING_NT, (pieces + 31) / 32 * 32);
-    const int slots = std::min(8, 2 * RING_NT / c.threads) * current_device_sms();
+    const int slots = std::min(8, ring_blocks(pieces > RING_NT ? 2 : 1) * RING_NT / c.threads) * current_device_sms();
     c.tokens = std::min(T, std::max(1, slots / c.parts));
     return c;
 }
@@ -750,11 +752,11 @@ cudaError_t forward_out(const RmsNormParams &p, int out_dtype, cudaStream_t stre
 
 template <typename T, int U, int NT>
 cudaError_t launch_ring(const RmsNormParams &p, const Cut &cut, int lanes, size_t stage, cudaStream_t stream) {
-    // (two CTAs of RING_NT threads share an SM; more, smaller ones share it too)
-    const size_t room = std::max(stage * 2, RING_BYTES * 2 * (size_t)cut.threads / (2 * RING_NT));
+    // (smaller CTAs share an SM with more)
+    const size_t room = std::max(stage * 2, RING_BYTES / ring_blocks(U) * (size_t)cut.threads / RING_NT);
     const int stages = (int)std::min<size_t>(MAX_STAGES, room / stage);
     auto kernel = norm_ring_backward_kernel<T, U, NT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (int)RING_BYTES);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES);
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, dim3((unsigned)cut.tokens, (unsigned)cut.parts), dim3((unsigned)cut.threads), stages * stage, stream,
                             p, lanes, cut.cols, stages);
@@ -773,7 +775,7 @@ cudaError_t backward_typed(const RmsNormParams &p, cudaStream_t stream) {
                          whole(p.r, p.r_stride, sizeof(T)) && whole(p.z, p.z_stride, sizeof(T)) && whole(p.w, 0, 4) &&
                          whole(p.dx, n, sizeof(T)) && whole(p.dz, n, sizeof(T));
         const int pieces = cut.cols / V;
-        if (vec && (p.H == 1 || lanes) && pieces <= 4 * RING_NT && stage <= RING_BYTES && cut.parts <= 65535) {
+        if (vec && (p.H == 1 || lanes) && pieces <= 4 * RING_NT && stage * 2 <= RING_BYTES && cut.parts <= 65535) {
             if (pieces <= RING_NT) e = launch_ring<T, 1, RING_NT>(p, cut, lanes, stage, stream);
             else if (pieces <= 2 * RING_NT) e = launch_ring<T, 2, RING_NT>(p, cut, lanes, stage, stream);
             else e = launch_ring<T, 2, 2 * RING_NT>(p, cut, lanes, stage, stream);
