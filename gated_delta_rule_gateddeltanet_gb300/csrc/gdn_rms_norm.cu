@@ -3,11 +3,20 @@
 //
 //   s = x (+ r),  y = s / sqrt(mean s^2 + eps) * (w + offset) * silu(z)
 //
-// Both directions are HBM streams: a row is read once into registers, 8 channels a
-// thread and piece, and everything about it is worked out there.  What a row needs of
-// other threads is one sum (two backwards) and, for 8 bits, a maximum.  A CTA takes
-// a token at a time (whole-token norms and scales), or tokens are cut into runs of
-// pieces of heads whose sums are shuffles inside a warp.
+// Both directions are HBM streams: a row is read once, 8 channels a thread and piece, and
+// everything about it is worked out in registers.  What a row needs of other threads is one
+// sum (two backwards) and, for 8 bits, a maximum.
+//   forward   a CTA a token (whole-token norms and scales), four pieces a thread so that
+//             enough loads are on their way; heads of 32 to 256 channels without any
+//             barrier, their sums being shuffles of a few lanes.  8192 BF16 tokens of 4096,
+//             residual added, to e4m3: 39.5 us (5.9 TB/s, 0.88 of a copy's rate; a piece a thread
+//             55 us).  4099 FP16 tokens of 48 gated heads of 128 to e4m3, a scale a head: 25.9 us
+//             (4.9 TB/s; the gate's exponentials and the scales are half of its instructions).
+//             One token of 2048: 1.5 us, a launch.
+//   backward  CTAs walk over the tokens behind a ring of bulk copies, so that a channel's part
+//             of dweight stays in one thread.  8192 BF16 tokens of 4096: 45 us (5.9 TB/s),
+//             FP32 70 us (7.7 TB/s: part of it comes from L2); 8192 FP16 tokens of 40 gated heads of 128:
+//             97 us (4.3 TB/s, 0.64: 34 instructions a channel).
 #include <type_traits>
 
 #include "layer_internal.cuh"
@@ -444,8 +453,7 @@ __global__ void __launch_bounds__(ANY_NT) norm_any_kernel(const RmsNormParams p,
 // ---------------------------------------------------------------- backward
 
 // With e = dy silu(z): dx = rstd (e w - n mean(e w n)) + dr, dw = sum e n, dz = dy n w silu'(z), n = s rstd.
-// CTAs walk over tokens, so that a thread's channels and their part of dw stay the same; the parts are summed by a
-// second kernel in the order of the CTAs.
+// The CTAs' parts of dw are summed by a second kernel in order.
 
 // Rows arrive in a ring of stages in shared memory, a bulk copy a row of each input, as far ahead as there is room; a
 // CTA takes `cols` channels of every gridDim.x-th token (whole tokens, or whole heads of them: blockIdx.y), thread i the
