@@ -24,7 +24,7 @@ gdn_status check_recurrence_sizes(const Args *a) {
     if (!valid_io(a->io_dtype)) return GDN_ERR_DTYPE;
     if (a->gate_mode != GDN_GATES_RAW && a->gate_mode != GDN_GATES_PRECOMPUTED) return GDN_ERR_ARG;
     if ((a->unit_input != 0 && a->unit_input != 1) || (a->unit_input && a->gate_mode != GDN_GATES_RAW)) return GDN_ERR_ARG;
-    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->total_tokens < 0 || a->channels < 1 || a->channels > (1 << 24)) return GDN_ERR_SHAPE;
+    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->total_tokens < 0 || a->total_tokens > (1 << 30) || a->channels < 1 || a->channels > (1 << 24)) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
 

@@ -17,7 +17,7 @@ using namespace recur;
 
 // ---------------------------------------------------------------- long sequences
 
-// (8 BF16 prompts of 9078 tokens and 4096 channels, raw: 77 us.  512 threads of 4 tokens a half-warp 99 us, 256 of 4
+// (Packed BF16 prompts, 9078 tokens of 4096 channels, raw: 77 us.  512 threads of 4 tokens a half-warp 99 us, 256 of 4
 // and three CTAs an SM 81 us, 128 of 8 and four 82 us: as many elements on an SM, with more to exchange for each.)
 constexpr int NT = 256, SUBS = NT / LANES;
 constexpr int TT = 8, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA

@@ -123,12 +123,6 @@ struct Piece {
         }
     }
 };
-template <typename T>
-__device__ __forceinline__ void read8(const T *p, float (&f)[V]) {
-    Piece<T> v;
-    v.load(p);
-    v.to(f);
-}
 template <typename T, typename F, int M>
 __device__ __forceinline__ void write8(T *p, const F (&f)[M]) {
     Piece<T> v;
@@ -218,8 +212,8 @@ constexpr int SAME = GDN_F32;
 template <typename T>
 constexpr int token_limit(int U) { return sizeof(T) == 4 && U > 1 ? 512 : 1024; }
 
-// What a row's sum is taken over: `lanes` neighbouring threads (heads of at most 256 channels), or the CTA.
-// A CTA takes one token: thread i holds pieces i, i + threads, .. of it (U at most).
+// A CTA takes one token; a row's sum is over `lanes` neighbouring threads (heads of 8 to 256 channels), or over the
+// CTA (lanes 0: one head).  Thread i holds pieces i, i + threads, .. of it (U at most).
 template <typename T, int OUT, int U>
 __global__ void __launch_bounds__(token_limit<T>(U)) norm_token_kernel(const RmsNormParams p, int lanes) {
     dependent_prologue();
@@ -314,7 +308,7 @@ __global__ void __launch_bounds__(token_limit<T>(U)) norm_token_kernel(const Rms
 }
 
 // Heads of 32 to 256 channels (a power of two), no scale over whole tokens.  A CTA's threads lie side by side over the
-// pieces of `rows` tokens (blockIdx.x: over the parts of a long token); each takes its piece of U tokens, `rows` apart.
+// pieces of `rows` tokens (blockIdx.x: over the parts of a long token; y and z: over the tokens); each takes its piece of U tokens, `rows` apart.
 constexpr int HEAD_NT = 128, HEAD_U = 4;
 
 template <typename T, int OUT, int LANES>
@@ -323,7 +317,7 @@ __global__ void __launch_bounds__(HEAD_NT) norm_head_kernel(const RmsNormParams 
     constexpr int U = HEAD_U;
     const int n = p.H * p.d, pieces = n / V;
     const int j = blockIdx.x * blockDim.x + threadIdx.x, row = j / pieces, c = (j - row * pieces) * V;
-    const long long t0 = (long long)blockIdx.y * (rows * U) + row;
+    const long long t0 = ((long long)blockIdx.z * gridDim.y + blockIdx.y) * (rows * U) + row;
     const bool column = row < rows;
     auto in = [&](int k) { return column && t0 + k * rows < p.T; };
     Piece<T> x[U], z[U];
@@ -727,14 +721,13 @@ cudaError_t forward_typed(const RmsNormParams &p, int out_dtype, cudaStream_t st
         const int rows = (int)std::max<long long>(1, HEAD_NT / pieces), parts = (int)((pieces * rows + HEAD_NT - 1) / HEAD_NT);
         const int threads = (int)((pieces * rows + parts * 32 - 1) / (parts * 32)) * 32;
         const long long runs = ((long long)p.T + rows * HEAD_U - 1) / (rows * HEAD_U);
-        if (runs <= 65535) {
-            const dim3 grid((unsigned)parts, (unsigned)runs), block((unsigned)threads);
-            switch (lanes) {
-                case 4: return launch_dependent(norm_head_kernel<T, OUT, 4>, grid, block, 0, stream, p, rows);
-                case 8: return launch_dependent(norm_head_kernel<T, OUT, 8>, grid, block, 0, stream, p, rows);
-                case 16: return launch_dependent(norm_head_kernel<T, OUT, 16>, grid, block, 0, stream, p, rows);
-                default: return launch_dependent(norm_head_kernel<T, OUT, 32>, grid, block, 0, stream, p, rows);
-            }
+        const long long deep = (runs + 65534) / 65535;
+        const dim3 grid((unsigned)parts, (unsigned)((runs + deep - 1) / deep), (unsigned)deep), block((unsigned)threads);
+        switch (lanes) {
+            case 4: return launch_dependent(norm_head_kernel<T, OUT, 4>, grid, block, 0, stream, p, rows);
+            case 8: return launch_dependent(norm_head_kernel<T, OUT, 8>, grid, block, 0, stream, p, rows);
+            case 16: return launch_dependent(norm_head_kernel<T, OUT, 16>, grid, block, 0, stream, p, rows);
+            default: return launch_dependent(norm_head_kernel<T, OUT, 32>, grid, block, 0, stream, p, rows);
         }
     }
     if (vec && (p.H == 1 || lanes) && pieces <= 4 * token_limit<T>(4)) {

@@ -69,7 +69,7 @@ struct GateType<T, RECUR_PRECOMPUTED> {
 
 // What the gates of one (token, channel) come to.
 struct Gate {
-    float g, lg;          // decay and its logarithm
+    float g;              // decay
     float sig_b, factor;  // sigmoid(b); sqrt(1 - g^2) (1 without unit_input)
     __device__ __forceinline__ float w() const { return sig_b * factor; }  // the input's weight
 };
@@ -125,13 +125,11 @@ __device__ __forceinline__ Gate gate_of(float a, float b, float rate, float dt_b
     if constexpr (MODE == RECUR_PRECOMPUTED) {
         r.g = a;
         r.sig_b = has_b ? b : 1.f;
-        r.lg = 0.f;
         r.factor = 1.f;
     } else {
         const float v = a + dt_bias;
         const float e = exp2_approx(-LOG2E * fabsf(v));
         const float t = rate * fmaf(log1p_over(e), e, fmaxf(v, 0.f));
-        r.lg = -t;
         r.g = exp2_approx(-LOG2E * t);
         r.sig_b = has_b ? rcp_approx(1.f + exp2_approx(-LOG2E * b)) : 1.f;
         r.factor = MODE == RECUR_RAW_UNIT ? sqrt_approx(one_minus_square(r.g, t)) : 1.f;
@@ -226,7 +224,7 @@ __device__ __forceinline__ F2 weight_of(const GatePair &q) {
     return MODE == RECUR_RAW_UNIT ? mul2(q.sig_b, factor_pair(q)) : q.sig_b;
 }
 
-// The gradients of a, b and A_log (da_log, up to a factor of -ln 2) from those of g and w; dt_bias has a's.
+// The gradients of a, b and A_log (dA up to a factor of ln 2) from those of g and w; dt_bias has a's.
 struct GradPair {
     F2 da, db, dA, w;  // w: the input's weight
 };
@@ -257,7 +255,9 @@ __device__ __forceinline__ GradPair grad_pair(const GatePair &q, F2 a, F2 dg, F2
             o.w = mul2(q.sig_b, factor);
         }
         o.da = mul2(mul2(dlg, sig_a), mul2(minus_rate, F2(LN2)));
-        o.dA = mul2(dlg, q.exponent);
+        // (an infinite gate's exponent too is multiplied by a dlg of 0)
+        q.exponent.get(x, y);
+        o.dA = mul2(dlg, F2(fmaxf(x, -3.402823466e38f), fmaxf(y, -3.402823466e38f)));
         o.db = fma2(mul2(di, q.sig_b), F2(-1.f), di);
     }
     return o;

@@ -135,9 +135,7 @@ __device__ __forceinline__ void check_packing(const RecurrenceParams &p) {
 template <int BYTES>
 __device__ __forceinline__ void copy(void *dst, const void *src, bool in) {
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
-    else if constexpr (BYTES == 8)
+    if constexpr (BYTES == 8)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(in ? 8 : 0) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(in ? 4 : 0) : "memory");
@@ -166,13 +164,11 @@ __device__ __forceinline__ void copy_tile(E *dst, const E *base, long long strid
 }
 
 // A tile of E's, [TILE][SLAB], from rows `stride` apart; zeros past T and C.  bytes: what base, stride and C are whole
-// multiples of (16: where no tensor map takes them, 8, 4, or less).
+// multiples of: 8, 4, or less (what 16 divides comes by tensor copies, or 8 bytes at a time).
 template <typename E, int SLAB, int TILE, int NT>
 __device__ __forceinline__ void load_tile(E *dst, const void *base, long long stride, int t0, int T, int c0, int C, int bytes) {
     const E *src = static_cast<const E *>(base);
-    if (bytes == 16) {
-        copy_tile<E, SLAB, TILE, NT, 16>(dst, src, stride, t0, T, c0, C);
-    } else if (bytes == 8) {
+    if (bytes == 8) {
         copy_tile<E, SLAB, TILE, NT, 8>(dst, src, stride, t0, T, c0, C);
     } else if (bytes == 4) {
         copy_tile<E, SLAB, TILE, NT, 4>(dst, src, stride, t0, T, c0, C);

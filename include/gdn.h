@@ -734,7 +734,8 @@ gdn_status gdn_paged_attention(const gdn_paged_attention_args *args, gdn_stream_
  *   GDN_GATES_RAW          g = exp(-exp(A_log) softplus(a + dt_bias)), w = sigmoid(b) (1 if b is NULL);
  *                          with unit_input, w is that times sqrt(1 - g^2), which keeps
  *                          the state's variance at the input's
- *   GDN_GATES_PRECOMPUTED  g = a, w = b (1 if b is NULL); any finite values
+ *   GDN_GATES_PRECOMPUTED  g = a, w = b (1 if b is NULL): finite, of either sign, and so that the
+ *                          product of any 128 consecutive decays is finite too (as for |g| < 2)
  *   x             device [T, C] io_dtype; token stride x_stride elements (0 = C)
  *   a, b          device [T, C], strides a_stride, b_stride (0 = C): io_dtype if RAW, FP32
  *                 if PRECOMPUTED (16 bits cannot hold a decay next to 1)
@@ -757,7 +758,7 @@ gdn_status gdn_paged_attention(const gdn_paged_attention_args *args, gdn_stream_
  */
 typedef struct gdn_linear_recurrence_args {
     int32_t num_seqs;        /* B, at most 65535 */
-    int32_t total_tokens;    /* T */
+    int32_t total_tokens;    /* T, at most 2^30 */
     int32_t channels;        /* C, 1 to 2^24 */
     int32_t num_state_slots;
     int32_t io_dtype;        /* GDN_F32, GDN_F16 or GDN_BF16 */
@@ -816,7 +817,8 @@ gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_a
  * channels that is normalised by itself (num_heads = 1: the whole token):
  *   s = x (+ residual, rounded to io_dtype as it is stored)
  *   y = s / sqrt(mean(s^2) + eps) * (weight + weight_offset) * silu(gate)
- * without the factors whose pointer is NULL.
+ * without the factors whose pointer is NULL.  (silu of a gate below -88 is 0: its values there
+ * are below 1e-36.)
  *   x, residual, gate  device [T, num_heads, head_dim] io_dtype, heads and channels contiguous
  *                 inside a token; x_stride, residual_stride, gate_stride elements between tokens
  *                 (0 = num_heads * head_dim)

@@ -64,7 +64,7 @@ def test_null_argument_structs(lib):
 RECURRENCE_REFUSALS = [
     (dict(io_dtype=3), DTYPE), (dict(io_dtype=-1), DTYPE), (dict(gate_mode=2), ARG), (dict(unit_input=2), ARG),
     (dict(unit_input=1, gate_mode=1), ARG), (dict(num_seqs=-1), SHAPE), (dict(num_seqs=65536), SHAPE),
-    (dict(total_tokens=-1), SHAPE), (dict(channels=0), SHAPE), (dict(channels=(1 << 24) + 1), SHAPE),
+    (dict(total_tokens=-1), SHAPE), (dict(total_tokens=(1 << 30) + 1), SHAPE), (dict(channels=0), SHAPE), (dict(channels=(1 << 24) + 1), SHAPE),
     (dict(num_state_slots=0), SHAPE), (dict(state_slots=None, num_state_slots=1), SHAPE),
     (dict(cu_seqlens=None, total_tokens=101), SHAPE), (dict(x_stride=63), SHAPE), (dict(a_stride=1), SHAPE),
     (dict(b_stride=-64), SHAPE), (dict(x=None), NULL), (dict(a=None), NULL), (dict(A_log=None), NULL),
