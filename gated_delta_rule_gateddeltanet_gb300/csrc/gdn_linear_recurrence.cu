@@ -40,11 +40,11 @@ struct Shape {
         alignas(128) T x[TILE * SLAB];
         alignas(128) G a[TILE * SLAB], b[TILE * SLAB];
         alignas(16) float A[SUBS][SLAB], B[SUBS][SLAB];  // the half-warps' maps, then those of what stands in front of each
-        alignas(16) float4 map[2][MAX_CLUSTER][SLAB];  // the cluster's tiles' maps (A, B, whether it holds a reset)
+        Exchange<SLAB> exchange;
         alignas(16) float carry[SLAB];
         Tokens<TILE> tokens[2];
         Packing packing;
-        alignas(8) uint64_t full, maps[2];
+        alignas(8) uint64_t full;
     };
 };
 
@@ -75,14 +75,15 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
     }
     if (tid == 0) {
         ptx::mbar_init(&sm.full, 1);
-        ptx::mbar_init(&sm.maps[0], 1);
-        ptx::mbar_init(&sm.maps[1], 1);
+        ptx::mbar_init(&sm.exchange.full[0], 1);
+        ptx::mbar_init(&sm.exchange.full[1], 1);
         ptx::fence_mbar_init();
     }
     const Lookup lookup = stage_packing(p, sm.packing);
     __syncthreads();
 
     const bool bulk = access.x == 16 || access.a == 16 || (has_b && access.b == 16);
+    const bool own = access.x != 16 || access.a != 16 || (has_b && access.b != 16);  // copies of the threads' own
     auto fetch = [&](int t0) {
         if (bulk && tid == COPIER && t0 < p.T) {
             constexpr uint32_t XB = sizeof(T) * TILE * SLAB, GB = sizeof(G) * TILE * SLAB;
@@ -102,13 +103,16 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
     tokens_of(sm.tokens[0], p, lookup, rank * TILE, slab == 0, tid / 32 - (NT - TILE) / 32);
     if (blockIdx.x == 0) check_packing(p);
     if (cluster > 1) cluster_sync();  // every CTA has its barriers before another writes to its shared memory
+    else __syncthreads();
     float run = 0.f;  // the state in front of the cluster's tiles, channel tid of the slab
     for (int n = 0, buf = 0; n < rounds; ++n, buf ^= 1) {
         const int t0 = n * step + rank * TILE;
         const Tokens<TILE> &tokens = sm.tokens[buf];
         if (bulk && t0 < p.T) wait(&sm.full, n & 1, p.status);
-        copies_done();
-        __syncthreads();
+        if (own) {
+            copies_done();
+            __syncthreads();
+        }
 
         // every token's state and decay with nothing in front of the half-warp's tokens
         const bool plain = tokens.plain;  // as most are
@@ -187,16 +191,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
                 }
             }
             if (cluster > 1) {
-                uint64_t *bar = &sm.maps[buf];
-                if (tid == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)cluster * SLAB * 16);
-                for (int r = 0; r < cluster; ++r)
-                    store_async(in_cta(&sm.map[buf][rank][tid], r), in_cta(bar, r), A, B, closed ? 1.f : 0.f);
-                wait_cluster(bar, n >> 1 & 1, p.status);
-                for (int r = 0; r < cluster; ++r) {
-                    const float4 m = sm.map[buf][r][tid];
-                    if (r == rank) sm.carry[tid] = run;
-                    run = m.z != 0.f ? m.y : fmaf(m.x, run, m.y);
-                }
+                sm.carry[tid] = exchange<true>(sm.exchange, n, cluster, rank, tid, A, B, closed, run, p.status);
             } else {
                 sm.carry[tid] = run;
                 run = closed ? B : fmaf(A, run, B);

@@ -49,12 +49,11 @@ struct Shape {
         // what stands behind each in the tile (RA, RB)
         alignas(16) float FA[SUBS][SLAB], FB[SUBS][SLAB], RA[SUBS][SLAB], RB[SUBS][SLAB];
         alignas(16) float sum_A[SUBS][SLAB], sum_dt[SUBS][SLAB];
-        alignas(16) float4 map[2][MAX_CLUSTER][SLAB];  // the cluster's tiles' maps backwards (A, B, whether a sequence ends in it)
+        Exchange<SLAB> exchange;
         alignas(16) float carry[SLAB];
-        alignas(16) float2 sums[MAX_CLUSTER][SLAB];
         Tokens<TILE> tokens[2];
         Packing packing;
-        alignas(8) uint64_t full[2], maps[2];
+        alignas(8) uint64_t full[2];
     };
 };
 
@@ -87,7 +86,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sm.full[i], 1);
-            ptx::mbar_init(&sm.maps[i], 1);
+            ptx::mbar_init(&sm.exchange.full[i], 1);
         }
         ptx::fence_mbar_init();
     }
@@ -95,6 +94,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
     __syncthreads();
 
     const bool bulk = access.x == 16 || access.dy == 16 || access.a == 16 || (has_b && access.b == 16);
+    const bool own = access.x != 16 || access.dy != 16 || access.a != 16 || (has_b && access.b != 16);  // the threads' own copies
     auto fetch = [&](int t0, int buf) {
         typename S::Tile &tile = sm.tile[buf];
         if (bulk && tid == COPIER && t0 < p.T) {
@@ -121,16 +121,25 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
     }
     if (blockIdx.x == 0) check_packing(p);
     if (cluster > 1) cluster_sync();  // every CTA has its barriers before another writes to its shared memory
+    else __syncthreads();
     float run = 0.f;                     // what reaches the state behind the cluster's tiles, channel tid of the slab
-    float total_A = 0.f, total_dt = 0.f;  // channel tid's sums
+    if constexpr (RAW) {
+        Pack<float, VC> zero;
+#pragma unroll
+        for (int v = 0; v < VC; ++v) zero.e[v] = 0.f;
+        put_pack(&sm.sum_A[sub][lane * VC], zero);
+        put_pack(&sm.sum_dt[sub][lane * VC], zero);
+    }
     const int skipped = (rounds - 1) * step + rank * TILE >= p.T;  // a tile behind the last token is not copied
     for (int n = 0, buf = 0; n < rounds; ++n, buf ^= 1) {
         const int t0 = (rounds - 1 - n) * step + rank * TILE;
         const Tokens<TILE> &tokens = sm.tokens[buf];
         const typename S::Tile &tile = sm.tile[buf];
         if (bulk && t0 < p.T) wait(&sm.full[buf], (n >> 1) - (buf ? 0 : skipped) & 1, p.status);
-        copies_done();
-        __syncthreads();
+        if (own) {
+            copies_done();
+            __syncthreads();
+        }
         const bool more = n + 1 < rounds;
         float checkpoint = 0.f;  // channel tid - SLAB's, on its way while the gates are worked out
         if (tid >= SLAB && tid < 2 * SLAB && s0 + tid - SLAB < p.C && t0 < p.T)
@@ -228,16 +237,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
                 }
             }
             if (cluster > 1) {
-                uint64_t *bar = &sm.maps[buf];
-                if (tid == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)cluster * SLAB * 16);
-                for (int r = 0; r < cluster; ++r)
-                    store_async(in_cta(&sm.map[buf][rank][tid], r), in_cta(bar, r), A, B, closed ? 1.f : 0.f);
-                wait_cluster(bar, n >> 1 & 1, p.status);
-                for (int r = cluster - 1; r >= 0; --r) {
-                    const float4 m = sm.map[buf][r][tid];
-                    if (r == rank) sm.carry[tid] = run;
-                    run = m.z != 0.f ? m.y : fmaf(m.x, run, m.y);
-                }
+                sm.carry[tid] = exchange<false>(sm.exchange, n, cluster, rank, tid, A, B, closed, run, p.status);
             } else {
                 sm.carry[tid] = run;
                 run = closed ? B : fmaf(A, run, B);
@@ -346,28 +346,34 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
         if (quick && access.dx && access.da && access.db) gradients(std::true_type());
         else gradients(std::false_type());
         if constexpr (RAW) {
-            put(sm.sum_A[sub], sum_A);
-            put(sm.sum_dt[sub], sum_dt);
-            __syncthreads();
-            if (tid < SLAB) {
-                float a = 0.f, d = 0.f;
+            // (in shared memory, since registers are short; a thread's entries are its own)
+            F2 before[PAIRS];
+            pairs_of(&sm.sum_A[sub][lane * VC], before);
 #pragma unroll
-                for (int s = 0; s < SUBS; ++s) a += sm.sum_A[s][tid], d += sm.sum_dt[s][tid];
-                total_A += a;
-                total_dt += d;
-            }
+            for (int v = 0; v < PAIRS; ++v) sum_A[v] = add2(before[v], sum_A[v]);
+            put(sm.sum_A[sub], sum_A);
+            pairs_of(&sm.sum_dt[sub][lane * VC], before);
+#pragma unroll
+            for (int v = 0; v < PAIRS; ++v) sum_dt[v] = add2(before[v], sum_dt[v]);
+            put(sm.sum_dt[sub], sum_dt);
         }
     }
 
     if constexpr (RAW) {
-        // the cluster's sums, in the order of its CTAs
+        __syncthreads();
+        float total_A = 0.f, total_dt = 0.f;  // channel tid's sums
+        if (tid < SLAB)
+            for (int s = 0; s < SUBS; ++s) total_A += sm.sum_A[s][tid], total_dt += sm.sum_dt[s][tid];
+        // the cluster's sums, in the order of its CTAs (where the maps of the last round but one were: whoever has the
+        // last round's has them from CTAs that are past that one)
         if (cluster > 1) {
-            if (tid < SLAB) store_cluster(in_cta(&sm.sums[rank][tid], 0), total_A, total_dt);
+            float2(*sums)[SLAB] = sm.exchange.map[rounds & 1];
+            if (tid < SLAB) store_cluster(in_cta(&sums[rank][tid], 0), total_A, total_dt);
             cluster_sync();
             if (rank == 0 && tid < SLAB) {
                 total_A = total_dt = 0.f;
                 for (int r = 0; r < cluster; ++r) {
-                    const float2 s = sm.sums[r][tid];
+                    const float2 s = sums[r][tid];
                     total_A += s.x;
                     total_dt += s.y;
                 }

@@ -25,7 +25,7 @@ namespace recur {
 
 constexpr int CHECK = GDN_RECURRENCE_CHECKPOINT;
 constexpr int LANES = 16;  // lanes beside one another along the channels
-constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_CLUSTER = 16;  // (8 is what every device takes)
 enum { RESET = 1, LOAD = 2, LAST = 4, VALID = 8 };  // LOAD: a sequence begins here; RESET: so, or no sequence's token
 
 // The largest b in [0, hi] with cu[b] <= t (0 if there is none).
@@ -308,12 +308,19 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, int rank) {
 __device__ __forceinline__ void store_cluster(uint32_t a, float x, float y) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
 }
-// 16 bytes to another CTA's shared memory, counted by the barrier there.
-__device__ __forceinline__ void store_async(uint32_t a, uint32_t bar, float x, float y, float z) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a), "f"(x), "f"(y),
-                 "f"(z), "f"(0.f), "r"(bar)
+// 8 bytes to another CTA's shared memory, counted by the barrier there.
+__device__ __forceinline__ void store_async(uint32_t a, uint32_t bar, float x, float y) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(a), "f"(x), "f"(y), "r"(bar)
                  : "memory");
 }
+
+// What the CTAs of a cluster tell one another about their tiles: each channel's map (A, B), or A = NaN if a reset
+// closes the tile, so that nothing from in front of it comes through (where an A is NaN by itself, B is too).  Twice, for a round and the next.
+template <int SLAB>
+struct Exchange {
+    alignas(16) float2 map[2][MAX_CLUSTER][SLAB];
+    alignas(8) uint64_t full[2];
+};
 
 // Waits for a phase of `bar`; after about a second without it the caller goes on and the status word says so.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, int32_t *status) {
@@ -336,6 +343,37 @@ __device__ __forceinline__ void wait_cluster(uint64_t *bar, uint32_t parity, int
         if (clock64() - t0 > 2000000000ll) break;
     }
     flag_error(status, GDN_DEVERR_TIMEOUT);
+}
+
+// Thread c of SLAB: channel c's map of this CTA's tile to every CTA; returns what stands in front of the tile, given what
+// stands in front of the cluster's (`run`, which becomes what stands behind them).  FORWARD: tiles in the order of the ranks.
+template <bool FORWARD, int SLAB>
+__device__ __forceinline__ float exchange(Exchange<SLAB> &x, int n, int cluster, int rank, int c, float A, float B, bool closed,
+                                          float &run, int32_t *status) {
+    const int buf = n & 1;
+    uint64_t *bar = &x.full[buf];
+    if (c == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)cluster * SLAB * 8);
+    if (closed) A = __int_as_float(0x7fc00000);
+#pragma unroll 1
+    for (int r = 0; r < cluster; ++r) store_async(in_cta(&x.map[buf][rank][c], r), in_cta(bar, r), A, B);
+    wait_cluster(bar, n >> 1 & 1, status);
+    float front = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < cluster; k0 += 4) {  // four loads at once: their latency is what a round waits for
+        float2 m[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = min(k0 + k, cluster - 1);
+            m[k] = x.map[buf][FORWARD ? r : cluster - 1 - r][c];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k0 + k >= cluster) break;
+            if ((FORWARD ? k0 + k : cluster - 1 - k0 - k) == rank) front = run;
+            run = isnan(m[k].x) ? m[k].y : fmaf(m[k].x, run, m[k].y);
+        }
+    }
+    return front;
 }
 
 // A cluster's launch as a programmatic dependent (launch_dependent with clusters).
@@ -381,19 +419,22 @@ cudaError_t resident_clusters(Kernel kernel, unsigned threads, size_t smem, Resi
     return cudaSuccess;
 }
 
-// CTAs a cluster: the largest size at which all clusters are resident at once, and no more than there are tiles.
+// CTAs a cluster: the largest size at which all clusters are resident at once and has no more CTAs than tiles, or the least
+// of as few rounds.  (A size at which some clusters wait for others: 1.4 times as long.)
 inline int cluster_size(const Resident &r, long long slabs, long long tiles) {
     int size = 1;
     for (int s = 2; s <= MAX_CLUSTER && s <= tiles; ++s)
         if (slabs <= r.most[s]) size = s;
-    return size;
+    const long long rounds = (tiles + size - 1) / size;
+    return tiles ? (int)((tiles + rounds - 1) / rounds) : 1;
 }
 
-// Two channels a lane instead of four where clusters of slabs of four would leave SMs without a CTA (1024 channels of
-// BF16: 45 us instead of 63 us forwards over 16,384 tokens, 105 us instead of 139 us backwards; 2560: 85 and 88 us, 197 and 193 us).
+// Two channels a lane instead of four where slabs of four are few (16,384 tokens of BF16, forwards and backwards: 512
+// channels 31 instead of 38 us and 73 instead of 84, 1024 41 instead of 46 and 96 instead of 105, 1536 54 instead of 57 and 132 instead of 129,
+// but 2048 72 instead of 67 and 173 instead of 155).
 inline bool narrow_slabs(long long C) {
     constexpr int SLAB = 4 * LANES;
-    return (C + SLAB - 1) / SLAB * MAX_CLUSTER <= current_device_sms();
+    return (C + SLAB - 1) / SLAB * 6 <= current_device_sms();
 }
 
 // A kernel's shared memory set and its residency looked up, once a device (as current_device_sms); a template of
@@ -410,6 +451,7 @@ cudaError_t prepare_clusters(Kernel kernel, unsigned threads, size_t smem, const
     if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
         Resident r;
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
         if ((e = resident_clusters(kernel, threads, smem, r)) != cudaSuccess) return e;
         known[dev] = r;  // (two threads that come here at once write the same)
         __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
