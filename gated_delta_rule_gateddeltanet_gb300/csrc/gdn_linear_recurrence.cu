@@ -3,8 +3,8 @@
 // An HBM stream where the gates come ready (x, a, b read and y written once), and where
 // they are worked out here a matter of instructions: 30 a channel of a token, of which an
 // SM has 44 to spend at 8 bytes a channel.  Over 16,384 tokens of 4096 channels: FP32
-// gates 161 us at FP32 (6.7 TB/s, 0.98 of a copy's rate) and 124 us at BF16 (6.5 TB/s); raw
-// gates 167 us at FP32 (6.4 TB/s) and 119 us at BF16 (4.5 TB/s, issue slots 45% busy, four
+// gates 163 us at FP32 (6.6 TB/s, 0.97 of a copy's rate) and 124 us at BF16 (6.5 TB/s); raw
+// gates 166 us at FP32 (6.5 TB/s) and 118 us at BF16 (4.6 TB/s, issue slots 45% busy, four
 // warps a scheduler), with unit_input 142 us.  The latter are bound by the dependent
 // instructions of the gates: (A, B) and the 8 x 4 states and decays of a lane's tokens are
 // 64 registers, which leaves 16 warps an SM.  One token of 64 sequences of 2560 channels: 1.9 us, a launch.
@@ -17,8 +17,8 @@ using namespace recur;
 
 // ---------------------------------------------------------------- long sequences
 
-// (Packed BF16 prompts, 9078 tokens of 4096 channels, raw: 77 us.  512 threads of 4 tokens a half-warp 99 us, 256 of 4
-// and three CTAs an SM 81 us, 128 of 8 and four 82 us: as many elements on an SM, with more to exchange for each.)
+// (Packed BF16 prompts, 9078 tokens of 4096 channels, raw: 74 us.  When it was 77, 512 threads of 4 tokens a half-warp
+// took 99 us, 256 of 4 and three CTAs an SM 81 us, 128 of 8 and four 82 us: as many elements on an SM, with more to exchange for each.)
 constexpr int NT = 256, SUBS = NT / LANES;
 constexpr int TT = 8, TILE = TT * SUBS;  // tokens of a half-warp, and of a CTA
 constexpr int COPIER = 96;  // a thread that has nothing else to do between the two halves of a round

@@ -430,7 +430,7 @@ inline int cluster_size(const Resident &r, long long slabs, long long tiles) {
 }
 
 // Two channels a lane instead of four where slabs of four are few (16,384 tokens of BF16, forwards and backwards: 512
-// channels 31 instead of 38 us and 73 instead of 84, 1024 41 instead of 46 and 96 instead of 105, 1536 54 instead of 57 and 132 instead of 129,
+// channels 31 instead of 38 us and 70 instead of 84, 1024 41 instead of 46 and 96 instead of 105, 1536 54 instead of 57 and 132 instead of 129,
 // but 2048 72 instead of 67 and 173 instead of 155).
 inline bool narrow_slabs(long long C) {
     constexpr int SLAB = 4 * LANES;
