@@ -9,7 +9,7 @@
 //
 // Over 16,384 tokens of 4096 channels: FP32 gates 312 us at FP32 (6.0 TB/s, 0.89 of a copy's
 // rate) and 236 us at BF16 (6.2 TB/s); raw gates 384 us at FP32 and 267 us at BF16 (3.5 TB/s),
-// with unit_input 322 us.  The raw ones are bound by their instructions (about 70 a channel of a
+// with unit_input 325 us.  The raw ones are bound by their instructions (about 70 a channel of a
 // token) at 16 warps an SM.  What counted: no spills (beside tiles that fill the shared
 // memory, the L1 cache is too small for them: 394 -> 278 us), and code for tokens inside a
 // sequence apart from the rest, which the instruction cache then holds.

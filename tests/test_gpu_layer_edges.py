@@ -108,3 +108,20 @@ def test_more_heads_than_a_grid_dimension_holds(out):
         part = gdn.rms_norm(x[lo:hi], w, **kw)
         for e, p in zip(every, part if isinstance(part, tuple) else (part,)):
             assert torch.equal(e[lo:hi].view(torch.uint8), p.view(torch.uint8))
+
+
+@pytest.mark.parametrize("lo", [-9, -7, -5])
+def test_decays_next_to_one_are_not_off_to_one_side(lo):
+    """A long memory multiplies a decay's mean error by its length while the random part grows with the root of it, so the
+    mean is held to 0.2 units of 2^-24, well inside a rounding's half (65,536 decays have a mean good to 0.01 units)."""
+    C = 1 << 16
+    g = torch.Generator("cpu").manual_seed(5)
+    a, A_log = lo + 2 * torch.rand(1, C, generator=g), torch.log(1 + 15 * torch.rand(C, generator=g))
+    want = np.exp(-np.exp(A_log.double().numpy()) * np.log1p(np.exp(a.double().numpy())))
+    zero = torch.zeros(C, device=dev())
+    for T in (1, 17):  # a decay alone, by a thread and by a tile: the tokens after the first keep the state
+        rows = torch.full((T, C), -200.0)
+        rows[0] = a[0]
+        _, final = gdn.linear_recurrence(torch.zeros(T, C, device=dev()), rows.to(dev()), None, None, A_log=A_log.to(dev()),
+                                         dt_bias=zero, initial_state=torch.ones(1, C, device=dev()), num_seqs=1)
+        assert abs(((final.double().cpu().numpy() - want) / 2.0 ** -24).mean()) < 0.2
