@@ -112,6 +112,9 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
         if (own) {
             copies_done();
             __syncthreads();
+            if (access.x == 2) prefetch_tile<T, SLAB, TILE, NT>(p.x, p.x_stride, t0 + step, p.T, s0, p.C);
+            if (access.a == 2) prefetch_tile<G, SLAB, TILE, NT>(p.a, p.a_stride, t0 + step, p.T, s0, p.C);
+            if (has_b && access.b == 2) prefetch_tile<G, SLAB, TILE, NT>(p.b, p.b_stride, t0 + step, p.T, s0, p.C);
         }
 
         // every token's state and decay with nothing in front of the half-warp's tokens

@@ -139,6 +139,12 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
         if (own) {
             copies_done();
             __syncthreads();
+            if (n + 1 < rounds) {
+                if (access.x == 2) prefetch_tile<T, SLAB, TILE, NT>(p.x, p.x_stride, t0 - step, p.T, s0, p.C);
+                if (access.dy == 2) prefetch_tile<T, SLAB, TILE, NT>(p.dy, p.dy_stride, t0 - step, p.T, s0, p.C);
+                if (access.a == 2) prefetch_tile<G, SLAB, TILE, NT>(p.a, p.a_stride, t0 - step, p.T, s0, p.C);
+                if (has_b && access.b == 2) prefetch_tile<G, SLAB, TILE, NT>(p.b, p.b_stride, t0 - step, p.T, s0, p.C);
+            }
         }
         const bool more = n + 1 < rounds;
         float checkpoint = 0.f;  // channel tid - SLAB's, on its way while the gates are worked out

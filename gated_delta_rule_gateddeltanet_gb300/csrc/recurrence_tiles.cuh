@@ -182,6 +182,18 @@ __device__ __forceinline__ void load_tile(E *dst, const void *base, long long st
     }
 }
 
+// Brings such a tile's rows to L2 (the first and the last channel's line of each) for plain loads, which wait for what they load
+// (65,536 BF16 tokens of 1001 channels backwards: 1080 -> 932 us).
+template <typename E, int SLAB, int TILE, int NT>
+__device__ __forceinline__ void prefetch_tile(const void *base, long long stride, int t0, int T, int c0, int C) {
+    const int last = min(SLAB, C - c0) - 1;
+    for (int i = threadIdx.x; i < 2 * TILE; i += NT) {
+        if (t0 + i / 2 >= T) break;
+        const E *p = static_cast<const E *>(base) + (long long)(t0 + i / 2) * stride + c0 + (i % 2 ? last : 0);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+    }
+}
+
 // Tensor map of such rows for boxes of a tile; false if the driver does not take it.
 template <typename E, int SLAB, int TILE>
 bool tile_map(CUtensorMap *map, const void *base, long long stride, int T, long long C) {
