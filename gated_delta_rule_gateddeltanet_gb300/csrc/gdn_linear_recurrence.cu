@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_kernel(const R
                 for (int v = 0; v < PAIRS; ++v) {
                     const GatePair q =
                         gate_pair<MODE>(F2(a[2 * v], a[2 * v + 1]), F2(b[2 * v], b[2 * v + 1]), rate[v], dt[v], has_b);
-                    const F2 u = mul2(weight_of<MODE>(q), F2(x[2 * v], x[2 * v + 1]));
+                    const F2 u = mul2(weight_of<MODE>(q, has_b), F2(x[2 * v], x[2 * v + 1]));
                     h[i][v] = i == 0 && inside_a_sequence ? u : fma2(q.g, front[v], u);
                     P[i][v] = i == 0 ? q.g : mul2(q.g, P[i - 1][v]);
                 }

@@ -192,22 +192,22 @@ __device__ __forceinline__ F2 log1p_over(F2 e) {
 
 // gate_of for two channels, with the same results; exponent: the base-2 logarithm of g; minus_rate: -log2(e) exp(A_log).
 struct GatePair {
-    F2 g, exponent, sig_b;
+    F2 g, exponent;
+    F2 b;  // e^-b (0 without b); RECUR_PRECOMPUTED: the input's weight
 };
 template <int MODE>
 __device__ __forceinline__ GatePair gate_pair(F2 a, F2 b, F2 minus_rate, F2 dt_bias, bool has_b) {
     GatePair r;
     if constexpr (MODE == RECUR_PRECOMPUTED) {
         r.g = a;
-        r.sig_b = has_b ? b : F2(1.f);
+        r.b = has_b ? b : F2(1.f);
     } else {
         float x, y;
         const F2 v = add2(a, dt_bias), e = exp_minus_abs(v);
         v.get(x, y);
         r.exponent = mul2(minus_rate, fma2(log1p_over(e), e, F2(fmaxf(x, 0.f), fmaxf(y, 0.f))));
         r.g = exp2_approx(add2(r.exponent, F2(DECAY_UP)));
-        r.sig_b = F2(1.f);
-        if (has_b) r.sig_b = rcp_approx(add2(exp2_approx(mul2(b, F2(-LOG2E))), F2(1.f)));
+        r.b = has_b ? exp2_approx(mul2(b, F2(-LOG2E))) : F2(0.f);
     }
     return r;
 }
@@ -224,9 +224,16 @@ __device__ __forceinline__ F2 factor_pair(const GatePair &q) {
     s2 = t2s < SMALL_T ? s2 : fmaf(-g2, g2, 1.f);
     return F2(sqrt_approx(s1), sqrt_approx(s2));
 }
+// sigmoid(b), or the weight itself
 template <int MODE>
-__device__ __forceinline__ F2 weight_of(const GatePair &q) {
-    return MODE == RECUR_RAW_UNIT ? mul2(q.sig_b, factor_pair(q)) : q.sig_b;
+__device__ __forceinline__ F2 input_gate(const GatePair &q, bool has_b) {
+    if constexpr (MODE == RECUR_PRECOMPUTED) return q.b;
+    else return has_b ? rcp_approx(add2(q.b, F2(1.f))) : F2(1.f);
+}
+template <int MODE>
+__device__ __forceinline__ F2 weight_of(const GatePair &q, bool has_b) {
+    const F2 sig_b = input_gate<MODE>(q, has_b);
+    return MODE == RECUR_RAW_UNIT ? mul2(sig_b, factor_pair(q)) : sig_b;
 }
 
 // The gradients of a, b and A_log (dA up to a factor of ln 2) from those of g and w; dt_bias has a's.
@@ -234,21 +241,18 @@ struct GradPair {
     F2 da, db, dA, w;  // w: the input's weight
 };
 template <int MODE>
-__device__ __forceinline__ GradPair grad_pair(const GatePair &q, F2 a, F2 dg, F2 dw, F2 minus_rate, F2 dt_bias) {
+__device__ __forceinline__ GradPair grad_pair(const GatePair &q, F2 a, F2 dg, F2 dw, F2 minus_rate, F2 dt_bias, bool has_b) {
     GradPair o;
-    o.w = q.sig_b;
+    const F2 sig_b = input_gate<MODE>(q, has_b);
+    o.w = sig_b;
     if constexpr (MODE == RECUR_PRECOMPUTED) {
         o.da = dg;
         o.db = dw;
     } else {
-        // sigmoid(v) = 1 / (1 + e^-|v|), or 1 minus that
-        const F2 v = add2(a, dt_bias), e = exp_minus_abs(v), r = rcp_approx(add2(e, F2(1.f))), er = mul2(e, r);
-        float x, y, r1, r2, e1, e2;
-        v.get(x, y);
-        r.get(r1, r2);
-        er.get(e1, e2);
-        const F2 sig_a(x >= 0.f ? r1 : e1, y >= 0.f ? r2 : e2);
-        F2 dlg = mul2(dg, q.g), di = mul2(dw, q.sig_b);
+        // (1 / (1 + e^-v) is good to a few units relative for either sign: nothing here takes it from 1)
+        float x, y;
+        const F2 sig_a = rcp_approx(add2(exp2_approx(mul2(add2(a, dt_bias), F2(-LOG2E))), F2(1.f)));
+        F2 dlg = mul2(dg, q.g), di = mul2(dw, sig_b);
         if constexpr (MODE == RECUR_RAW_UNIT) {
             // -g^2 / factor, 0 where the factor is
             float f1, f2;
@@ -257,13 +261,18 @@ __device__ __forceinline__ GradPair grad_pair(const GatePair &q, F2 a, F2 dg, F2
             const F2 k = mul2(mul2(q.g, q.g), F2(f1 > 0.f ? -rcp_approx(f1) : 0.f, f2 > 0.f ? -rcp_approx(f2) : 0.f));
             dlg = fma2(di, k, dlg);
             di = mul2(di, factor);
-            o.w = mul2(q.sig_b, factor);
+            o.w = mul2(sig_b, factor);
         }
         o.da = mul2(mul2(dlg, sig_a), mul2(minus_rate, F2(LN2)));
         // (an infinite gate's exponent too is multiplied by a dlg of 0)
         q.exponent.get(x, y);
         o.dA = mul2(dlg, F2(fmaxf(x, -3.402823466e38f), fmaxf(y, -3.402823466e38f)));
-        o.db = fma2(mul2(di, q.sig_b), F2(-1.f), di);
+        // 1 - sigmoid(b) = e^-b sigmoid(b), which keeps its digits where the sigmoid is next to 1 (where e^-b is infinite,
+        // the sigmoid is 0, and so is this)
+        if (has_b) {
+            q.b.get(x, y);
+            o.db = mul2(di, mul2(F2(fminf(x, 3.402823466e38f), fminf(y, 3.402823466e38f)), sig_b));
+        }
     }
     return o;
 }

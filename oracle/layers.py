@@ -45,6 +45,7 @@ class Gates:
         self.lg = -self.rate * softplus(v)
         self.g = np.exp(self.lg)
         self.sig_b = np.ones_like(a) if b is None else sigmoid(b)
+        self.b = b
         self.factor = np.sqrt(-np.expm1(2 * self.lg)) if unit else np.ones_like(a)
         self.w = self.sig_b * self.factor
         self.rel_lg = (2 * np.abs(v) + 12) * U
@@ -107,10 +108,10 @@ def linear_recurrence_backward(x, gates, spans, before, err_before, dy, d_final)
     da_err = dlg_err * slope + np.abs(da) * ((2 * np.abs(gates.v) + 16) * U)
     out["da"] = (da, da_err)
     if gates.has_b:
-        s = gates.sig_b * (1 - gates.sig_b)
-        # 1 - sigmoid loses what the sigmoid was rounded by
-        out["db"] = (dw * gates.factor * s, gates.factor * s * dw_err + np.abs(dw * gates.factor * s) * (gates.rel_f + 4 * U) +
-                     np.abs(dw * gates.factor * gates.sig_b) * gates.rel_b * 2)
+        s = gates.sig_b * sigmoid(-gates.b)
+        db = dw * gates.factor * s
+        # the sigmoid, and 1 less it as e^-b times it: each is relative, (|b| + 4) u the exponential's
+        out["db"] = (db, gates.factor * s * dw_err + np.abs(db) * (gates.rel_f + 2 * gates.rel_b + (np.abs(gates.b) + 10) * U))
     dA = dlg * gates.lg
     dA_err = dlg_err * np.abs(gates.lg) + np.abs(dA) * (gates.rel_lg + 2 * U)
     own = np.zeros(x.shape[0], bool)
