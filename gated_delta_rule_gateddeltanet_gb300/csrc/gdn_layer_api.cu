@@ -74,8 +74,9 @@ gdn_status check_forward_sizes(const gdn_linear_recurrence_args *a) {
     return a->max_seqlen < 0 ? GDN_ERR_SHAPE : GDN_OK;
 }
 
-// The longest sequence, as far as the host knows.
+// The longest sequence, as far as the host knows (num_seqs > 0).
 int longest(const gdn_linear_recurrence_args *a) {
+    if (!a->cu_seqlens) return a->total_tokens / a->num_seqs;
     int n = a->total_tokens;
     if (a->max_seqlen > 0 && a->max_seqlen < n) n = a->max_seqlen;
     return n;

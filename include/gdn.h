@@ -765,7 +765,8 @@ typedef struct gdn_linear_recurrence_args {
     int32_t gate_mode;       /* GDN_GATES_* */
     int32_t unit_input;      /* 0 or 1 (RAW only) */
     int32_t max_seqlen;      /* upper bound on the longest sequence, 0 = unknown; a hint: up to 16
-                                a thread carries its channels through a sequence's tokens */
+                                a thread carries its channels through a sequence's tokens
+                                (not read without cu_seqlens, where T / B is known) */
     int64_t x_stride, a_stride, b_stride;
     const void *x, *a, *b;
     const float *A_log, *dt_bias;
