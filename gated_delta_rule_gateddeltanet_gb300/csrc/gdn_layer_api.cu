@@ -84,7 +84,8 @@ int longest(const gdn_linear_recurrence_args *a) {
 
 gdn_status check_norm_sizes(int T, int H, int d, int io, float eps, float offset) {
     if (!valid_io(io)) return GDN_ERR_DTYPE;
-    if (T < 0 || H < 1 || d < 1 || (int64_t)H * d > INT32_MAX) return GDN_ERR_SHAPE;
+    // (the kernels count a row's channels in steps of up to 128 with 32-bit counters)
+    if (T < 0 || H < 1 || d < 1 || (int64_t)H * d > INT32_MAX - 255) return GDN_ERR_SHAPE;
     if (!(eps > 0.f) || isinf(eps) || !isfinite(offset)) return GDN_ERR_ARG;
     return GDN_OK;
 }

@@ -838,7 +838,7 @@ gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_a
 typedef struct gdn_rms_norm_args {
     int32_t total_tokens; /* T */
     int32_t num_heads;    /* >= 1 */
-    int32_t head_dim;     /* >= 1 */
+    int32_t head_dim;     /* >= 1; num_heads * head_dim at most 2^31 - 256 */
     int32_t io_dtype;     /* GDN_F32, GDN_F16 or GDN_BF16 */
     int32_t out_dtype;    /* io_dtype, GDN_FP8_E4M3 or GDN_INT8 */
     int32_t scale_group;  /* 0, or 32, 64 or 128 that divides head_dim */
