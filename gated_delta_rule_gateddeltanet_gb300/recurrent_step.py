@@ -42,8 +42,8 @@ class RecurrentStep:
         dev, (slots, C, _) = conv_bank.device, conv_bank.shape
         if C % head_dim:
             raise ValueError(f"head_dim must divide the {C} channels, got {head_dim}")
-        if seqs > slots:
-            raise ValueError(f"{seqs} sequences need as many state slots, got {slots}")
+        if seqs > min(slots, bank.shape[0]):
+            raise ValueError(f"{seqs} sequences need as many state slots, got {slots} and {bank.shape[0]}")
         T = seqs * tokens
         self.device, self.conv_bank, self.bank = dev, conv_bank, bank
         self.projection = torch.zeros((T, 4 * C), dtype=conv_bank.dtype, device=dev)
