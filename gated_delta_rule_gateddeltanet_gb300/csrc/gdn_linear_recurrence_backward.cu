@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
 #pragma unroll
                 for (int v = 0; v < PAIRS; ++v) {
                     q[i][v] = gate_pair<MODE>(a[v], b[v], rate[v], dt[v], has_b);
-                    u[i][v] = mul2(weight_of<MODE>(q[i][v], has_b), x[v]);
+                    u[i][v] = mul2(weight_of<MODE>(q[i][v]), x[v]);
                     B[v] = fma2(q[i][v].g, B[v], u[i][v]);
                     A[v] = mul2(A[v], q[i][v].g);
                 }
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(NT, VC == 2 ? 3 : 2) recurrence_backward_kerne
 #pragma unroll
                 for (int v = 0; v < PAIRS; ++v) {
                     const F2 l = add2(m[v], dy[v]);
-                    const GradPair d = grad_pair<MODE>(q[i][v], a[v], mul2(l, u[i][v]), mul2(l, x[v]), rate[v], dt[v], has_b);
+                    const GradPair d = grad_pair<MODE>(q[i][v], a[v], mul2(l, u[i][v]), mul2(l, x[v]), rate[v], dt[v]);
                     mul2(l, d.w).get(dx[2 * v], dx[2 * v + 1]);
                     d.da.get(da[2 * v], da[2 * v + 1]);
                     d.db.get(db[2 * v], db[2 * v + 1]);
