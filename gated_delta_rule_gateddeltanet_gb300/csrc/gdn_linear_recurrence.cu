@@ -4,10 +4,11 @@
 // they are worked out here a matter of instructions: 30 a channel of a token, of which an
 // SM has 44 to spend at 8 bytes a channel.  Over 16,384 tokens of 4096 channels: FP32
 // gates 163 us at FP32 (6.6 TB/s, 0.97 of a copy's rate) and 124 us at BF16 (6.5 TB/s); raw
-// gates 166 us at FP32 (6.5 TB/s) and 118 us at BF16 (4.6 TB/s, issue slots 45% busy, four
-// warps a scheduler), with unit_input 144 us.  The latter are bound by the dependent
-// instructions of the gates: (A, B) and the 8 x 4 states and decays of a lane's tokens are
-// 64 registers, which leaves 16 warps an SM.  One token of 64 sequences of 2560 channels: 1.9 us, a launch.
+// gates 166 us at FP32 (6.5 TB/s) and 118 us at BF16 (4.5 TB/s), with unit_input 144 us.
+// The latter are bound by latency: the issue slots are 45% busy, and the largest stalls are the
+// chains of dependent instructions and the barrier at which most warps stand while a thread a channel
+// folds the half-warps' maps and waits for the cluster's; the 8 x 4 states and decays of a lane's tokens are 64 registers, so that only
+// two CTAs share an SM to cover for one another.  One token of 64 sequences of 2560 channels: 1.9 us, a launch.
 #include "recurrence_tiles.cuh"
 
 namespace gdn {

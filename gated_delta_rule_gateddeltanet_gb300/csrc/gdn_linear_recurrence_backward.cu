@@ -4,15 +4,17 @@
 // The same scan as forwards, from the last tokens to the first, with m_t = g_t l_t as its
 // state; the forward states, which dg needs, are worked out again inside each tile from the
 // checkpoint in front of it (a tile is GDN_RECURRENCE_CHECKPOINT tokens).  x, a, b, dy are
-// read once and dx, da, db written once; the parameters' gradients stay in registers until
-// the last tile and are summed over a cluster's CTAs in order.
+// read once and dx, da, db written once; the parameters' gradients are added up tile by tile
+// in shared memory, a thread's in its own entries, and summed over a cluster's CTAs in order.
 //
-// Over 16,384 tokens of 4096 channels: FP32 gates 312 us at FP32 (6.0 TB/s, 0.89 of a copy's
-// rate) and 236 us at BF16 (6.2 TB/s); raw gates 384 us at FP32 and 267 us at BF16 (3.5 TB/s),
-// with unit_input 325 us.  The raw ones are bound by their instructions (about 70 a channel of a
-// token) at 16 warps an SM.  What counted: no spills (beside tiles that fill the shared
-// memory, the L1 cache is too small for them: 394 -> 278 us), and code for tokens inside a
-// sequence apart from the rest, which the instruction cache then holds.
+// Over 16,384 tokens of 4096 channels: FP32 gates 313 us at FP32 (6.0 TB/s, 0.89 of a copy's
+// rate) and 237 us at BF16 (6.2 TB/s); raw gates 379 us at FP32 and 256 us at BF16 (3.7 TB/s),
+// with unit_input 314 us.  The 16-bit raw ones are bound by latency as forwards: 67 instructions a
+// channel of a token, of which an SM has time for 77 at 14 bytes, but the issue slots are 48% busy; half
+// of the warps stand at a barrier while the others fold and exchange.  What counted: no spills (beside
+// tiles that fill the shared memory, the L1 cache is too small for them: 394 -> 278 us), code for tokens
+// inside a sequence apart from the rest, which the instruction cache then holds, and no branches in
+// the unrolled gradients (274 -> 257 us).
 #include "recurrence_tiles.cuh"
 
 namespace gdn {

@@ -10,8 +10,8 @@
 //             enough loads are on their way; heads of 32 to 256 channels without any
 //             barrier, their sums being shuffles of a few lanes.  8192 BF16 tokens of 4096,
 //             residual added, to e4m3: 39.5 us (5.9 TB/s, 0.88 of a copy's rate; a piece a thread
-//             55 us).  4099 FP16 tokens of 48 gated heads of 128 to e4m3, a scale a head: 25.9 us
-//             (4.9 TB/s; the gate's exponentials and the scales are half of its instructions).
+//             55 us).  4099 FP16 tokens of 48 gated heads of 128 to e4m3, a scale a head: 26.0 us
+//             (4.9 TB/s; 29 instructions a channel, gate and scales among them, fill 74% of the issue slots).
 //             One token of 2048: 1.5 us, a launch.
 //   backward  CTAs walk over the tokens behind a ring of bulk copies, so that a channel's part
 //             of dweight stays in one thread.  8192 BF16 tokens of 4096: 45 us (5.9 TB/s),
@@ -50,7 +50,8 @@ __device__ __forceinline__ Scale scale_of(float top, float factor, float most) {
     if (largest == 0.f) return {1.f, factor};
     const float scale = largest * (1.f / most);
     if (scale < 0x1p-120f || top < 0x1p-100f || top > 0x1p100f) return {fmaxf(scale, 0x1p-120f), __fdiv_rn(factor, fmaxf(scale, 0x1p-120f))};
-    // most / top: the approximate quotient and its remainder's share (both numbers are far from the ends of the range)
+    // most / top: the approximate quotient and its remainder's share, one step of Markstein's refinement of a quotient (IBM
+    // J. Res. Develop. 34, 1990); both numbers are far from the ends of the range
     const float r = rcp_approx(top), q = most * r;
     return {scale, fmaf(fmaf(-q, top, most), r, q)};
 }

@@ -74,8 +74,9 @@ struct Gate {
     __device__ __forceinline__ float w() const { return sig_b * factor; }  // the input's weight
 };
 
-// The gates' arithmetic is that of FP32 to a few units in the last place, in the fewest instructions: the
-// recurrence moves 8 bytes a channel of a token at 16 bits, which leaves an SM time for 44 instructions.
+// The gates' arithmetic is FP32 in the fewest instructions: the recurrence moves 8 bytes a channel of a token at 16 bits, which
+// leaves an SM time for 44.  With u = 2^-24, relative: e^-|v| is good to (2 |v| + 4) u, a sigmoid of b to (|b| + 8) u
+// (the exponent is rounded: 3e-6 at |b| = 50), since the special functions are the approximate ones.
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718056f;
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -111,7 +112,7 @@ __device__ __forceinline__ float log1p_over(float e) {
 }
 
 // 1 - g^2 for g = e^-t: for small t 2 g sinh(t), whose series keeps its digits (t^6 / 5040 off); beyond, g^2 is 0.67 at
-// most, and 1 - g^2 has lost no more than twice g's own error.
+// most, and the relative error of 1 - g^2 is four times g's (2 x 0.67 / 0.33), that of its root twice.
 constexpr float SMALL_T = 0.2f;
 __device__ __forceinline__ float one_minus_square(float g, float t) {
     const float q = t * t, s = fmaf(fmaf(q, 1.f / 120.f, 1.f / 6.f), q, 1.f);
@@ -120,7 +121,7 @@ __device__ __forceinline__ float one_minus_square(float g, float t) {
 
 // A decay from its base-2 logarithm x.  For results next to 1 the approximate exponential lies 0.22 to 0.35 units of 2^-24
 // low on average (65,536 logarithms in each of three ranges), which a memory of 1000 tokens adds up to 2e-5; its
-// argument makes up for 0.27 of them.
+// argument makes up for 0.27 of them.  (It is fitted there: decays near 0.06 come out 0.06 units of their own high on average.)
 constexpr float DECAY_UP = 0.27f * 0x1p-24f * LOG2E;
 
 // rate = exp(A_log); b absent: has_b 0.
@@ -190,7 +191,8 @@ __device__ __forceinline__ F2 log1p_over(F2 e) {
     return y;
 }
 
-// gate_of for two channels, with the same results; exponent: the base-2 logarithm of g; minus_rate: -log2(e) exp(A_log).
+// gate_of for two channels, up to roundings (log2(e) is multiplied into the rate first); exponent: the base-2 logarithm of g;
+// minus_rate: -log2(e) exp(A_log).
 struct GatePair {
     F2 g, exponent;
     F2 b;  // e^-b (0 without b); RECUR_PRECOMPUTED: the input's weight

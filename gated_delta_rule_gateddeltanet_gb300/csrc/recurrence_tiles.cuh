@@ -441,9 +441,13 @@ inline int cluster_size(const Resident &r, long long slabs, long long tiles) {
     return tiles ? (int)((tiles + rounds - 1) / rounds) : 1;
 }
 
-// Two channels a lane instead of four where slabs of four are few (16,384 tokens of BF16, forwards and backwards: 512
-// channels 31 instead of 38 us and 70 instead of 84, 1024 41 instead of 46 and 96 instead of 105, 1536 54 instead of 57 and 132 instead of 129,
-// but 2048 72 instead of 67 and 173 instead of 155).
+// Two channels a lane instead of four where slabs of four are few: up to 1600 channels.  BF16, raw, us forwards / backwards
+// with two and with four:
+//   16,384 tokens   512: 32 / 70 and 37 / 77, 1024: 42 / 93 and 46 / 96, 1536: 55 / 126 and 56 / 118,
+//                   2048: 72 / 163 and 66 / 141, 2560: 83 / 192 and 85 / 180, 4096: 128 / 302 and 118 / 256
+//   2048 tokens     1024: 9.7 / 17.9 and 11.7 / 18.2, 1536: 10.9 / 21.3 and 12.2 / 21.7, 2048: 14.1 / 27.7 and 12.5 / 23.1
+// The rule looks at the channels alone and takes the slower form in places: backwards at 1536 from 4000 tokens on (39.0 instead
+// of 35.6 at 4131), forwards with unit input past 1600 (4131 tokens: 2048 28.3 instead of 26.0, 4096 45.6 instead of 42.9).
 inline bool narrow_slabs(long long C) {
     constexpr int SLAB = 4 * LANES;
     return (C + SLAB - 1) / SLAB * 6 <= current_device_sms();

@@ -129,8 +129,9 @@ class LinearRecurrenceCall(_Call):
     input weight by sqrt(1 - decay^2).  cu_seqlens: [B + 1] int32, or None with
     ``num_seqs`` sequences of equal length.  ``initial_state`` [slots, C] fp32 or
     None (zeros); ``final_state`` may be the same tensor (in place);
-    ``write_final_state=False`` writes none.  ``return_checkpoints`` keeps what the
-    backward pass needs.  ``outputs`` is (output, final_state), or (output,
+    ``write_final_state=False`` writes none.  A launch writes the batch's slots only:
+    the other rows of a ``final_state`` that this object allocated are ``initial_state``'s at
+    its construction.  ``return_checkpoints`` keeps what the backward pass needs.  ``outputs`` is (output, final_state), or (output,
     final_state, checkpoints)."""
 
     def __init__(self, x, a, b=None, cu_seqlens=None, *, A_log=None, dt_bias=None, gate_mode="raw", unit_input=False,
@@ -168,7 +169,9 @@ class LinearRecurrenceBackwardCall(_Call):
     ``checkpoints`` from the forward call; ``d_final_state`` [slots, C] fp32 or None
     (zeros); everything else as that call was given it (its initial states must not
     have been overwritten in place).  ``outputs`` is (dx, da, db, d_initial_state),
-    and (.., dA_log, ddt_bias) with raw gates; db is None without b."""
+    and (.., dA_log, ddt_bias) with raw gates; db is None without b.  A launch writes the
+    batch's slots of d_initial_state only.  ``max_seqlen`` is taken so that the forward call's keywords can be
+    passed on; nothing depends on it."""
 
     def __init__(self, dy, x, a, b, checkpoints, cu_seqlens=None, *, A_log=None, dt_bias=None, gate_mode="raw",
                  unit_input=False, initial_state=None, state_slots=None, num_seqs=None, num_state_slots=None,

@@ -27,8 +27,8 @@ from .recurrence import LinearRecurrenceCall
 
 class RecurrentStep:
     """``seqs`` sequences, ``tokens`` new tokens each.  conv_weight: [C, K] fp32;
-    ``conv_bank`` [slots, C, K-1] (fp16 or fp32, the I/O type) and ``bank`` [slots,
-    C] fp32 hold the states; A_log, dt_bias: [C] fp32; norm_weight: [head_dim] fp32
+    ``conv_bank`` [slots, C, K-1] (fp16 or fp32, the I/O type: the convolution takes
+    no bf16) and ``bank`` [slots, C] fp32 hold the states; A_log, dt_bias: [C] fp32; norm_weight: [head_dim] fp32
     or None.
 
     Buffers, device tensors owned by this object: ``projection`` [seqs * tokens,

@@ -739,20 +739,21 @@ gdn_status gdn_paged_attention(const gdn_paged_attention_args *args, gdn_stream_
  *   x             device [T, C] io_dtype; token stride x_stride elements (0 = C)
  *   a, b          device [T, C], strides a_stride, b_stride (0 = C): io_dtype if RAW, FP32
  *                 if PRECOMPUTED (16 bits cannot hold a decay next to 1)
- *   A_log, dt_bias device [C] FP32 (RAW only)
+ *   A_log, dt_bias device [C] FP32 (RAW only); A_log at most 88 (an infinite exp(A_log) times a softplus or a
+ *                 gradient of 0 is NaN)
  *   cu_seqlens    device [B+1] int32, or NULL: B sequences of T / B tokens each
  *   state_slots   device [B] int32, or NULL for slot b = b
  *   initial_state device [num_state_slots, C] FP32, or NULL for zeros
  *   final_state   device, same shape, or NULL (not written); may equal initial_state.  Only
  *                 the batch's slots are written; that of a sequence without tokens gets its initial state.
- *   output        device [T, C] io_dtype, contiguous
+ *   output        device [T, C] io_dtype, contiguous; no output but final_state may overlap an input
  *   checkpoints   device [ceil(T / GDN_RECURRENCE_CHECKPOINT), C] FP32 or NULL: the state
  *                 before every GDN_RECURRENCE_CHECKPOINT-th packed token (unspecified where that token
  *                 begins a sequence or belongs to none), for gdn_linear_recurrence_backward
  * Sequences in one call must use distinct state slots (checked by the debug
  * build).  A sequence whose slot is out of range is skipped; tokens past cu[B]
  * are flagged and left as they were; of a cu_seqlens that is out of order, which is
- * flagged, any sequences may be skipped or computed.
+ * flagged, any sequences may be skipped or computed.  A call without sequences does nothing.
  * Long sequences are split over time: a call gives the same bits every time, and
  * those of another batching or max_seqlen up to FP32 rounding.
  */
@@ -795,8 +796,9 @@ gdn_status gdn_linear_recurrence(const gdn_linear_recurrence_args *args, gdn_str
  *                 with b); all contiguous
  *   dA_log, ddt_bias device [C] FP32 or NULL (RAW only): summed over all tokens
  *   d_initial_state device [num_state_slots, C] FP32 or NULL; only the batch's slots are written
- * Outputs must not overlap inputs (also d_initial_state not d_final_state).  Where unit_input meets a decay that rounds to 1
- * (its factor is 0), that factor's part of da is 0, its limit.
+ * Outputs must not overlap inputs (also d_initial_state not d_final_state).  unit_input's factor comes from the decay's
+ * exponent, so that it and its part of da keep their digits where the decay rounds to 1; where the exponent underflows (below
+ * 1e-38), the factor is 0 and its part of da too, its limit.  db keeps its digits for any b.
  */
 typedef struct gdn_linear_recurrence_backward_args {
     int32_t num_seqs, total_tokens, channels, num_state_slots;
@@ -818,8 +820,12 @@ gdn_status gdn_linear_recurrence_backward(const gdn_linear_recurrence_backward_a
  * channels that is normalised by itself (num_heads = 1: the whole token):
  *   s = x (+ residual, rounded to io_dtype as it is stored)
  *   y = s / sqrt(mean(s^2) + eps) * (weight + weight_offset) * silu(gate)
- * without the factors whose pointer is NULL.  (silu of a gate below -88 is 0: its values there
- * are below 1e-36.)
+ * without the factors whose pointer is NULL.  (silu of a finite gate below -88 is 0: its values there
+ * are below 1e-36; of -infinity it is NaN, as z / (1 + e^-z) is.)  The squares are summed in FP32: a row whose squares add
+ * up to more than 3.4e38 comes out as zeros.
+ * Fast are whole tokens (num_heads = 1, head_dim a multiple of 8, up to 32,768 channels of 16 bits and 16,384 of FP32;
+ * backwards up to 8192, FP32 with both gate and d_residual up to 6400) and heads of 8 to 256 channels, a power of two, all on
+ * 16-byte boundaries.  Any other call runs on kernels for all sizes, which take 6 to 60 times what their bytes would.
  *   x, residual, gate  device [T, num_heads, head_dim] io_dtype, heads and channels contiguous
  *                 inside a token; x_stride, residual_stride, gate_stride elements between tokens
  *                 (0 = num_heads * head_dim)
